@@ -66,7 +66,7 @@
 extern "C" {
 #endif
 
-#define MXQ_ABI_VERSION 7
+#define MXQ_ABI_VERSION 8
 #define MXQ_BLOCK 32          /* elements per MX block; fixed */
 #define MXQ_MAX_GROUPS 1024   /* largest G the grouped entry points accept */
 /* E4M3 GEMM reductions of at most this many elements (dense and ragged M: K;
@@ -344,6 +344,157 @@ mxq_status mxq_grouped_gemm(mxq_gg_mode mode, const uint8_t* A, const uint8_t* s
  */
 mxq_status mxq_validate_group_end(const int32_t* group_end, int32_t G, int64_t T,
                                   int32_t* flag, hipStream_t st);
+
+/* ------------------------------------------------------------------ around the expert GEMMs
+ * Routing, the move between token order and expert order, and the optimiser
+ * step of an MoE layer.  T = 0 tokens (and tensors without elements) are
+ * valid; pointers of empty arrays may then be NULL. */
+
+/* element type of a float tensor argument */
+typedef enum { MXQ_DT_F32 = 0, MXQ_DT_BF16 = 1, MXQ_DT_MAX_ENUM = 0x7FFFFFFF } mxq_dtype;
+
+typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1, MXQ_SCORE_MAX_ENUM = 0x7FFFFFFF } mxq_score;
+
+#define MXQ_MAX_TOPK 32          /* largest top_k */
+#define MXQ_MAX_ROUTE_GROUPS 64  /* largest n_group */
+
+/* How a token's experts are chosen among E (<= MXQ_MAX_GROUPS) experts.
+ *  - score: s = softmax of the row's logits, or their sigmoid.
+ *  - A logit at or below the lowest finite bf16 value (-3.3895314e38, so
+ *    -inf and both types' lowest values) masks its expert: score 0, never
+ *    chosen, not counted by a softmax.
+ *  - An expert ranks by its key: s + bias[e], or its logit where bias is
+ *    NULL.  A NaN key ranks below every number.
+ *  - n_group > 1 splits the experts into n_group equal runs; a group's total
+ *    is the sum of its best `group_top` (1 or 2) s + bias (s without bias)
+ *    over unmasked experts; only the topk_group best groups' experts can be
+ *    chosen.  E must be a multiple of n_group.
+ *  - The top_k largest keys are chosen, largest first; ties go to the lowest
+ *    index (experts and groups).  Order is that of the keys and totals in
+ *    64-bit arithmetic.  A row with fewer available experts than top_k ends
+ *    in index -1 with weight 0.
+ *  - The weight of a chosen expert is scale * s, or with renormalise
+ *    scale * s / (sum of the chosen s) (0 if that sum is 0).  The bias has
+ *    no part in it.  NaN and +inf logits follow the arithmetic. */
+typedef struct {
+    int32_t score;       /* mxq_score */
+    int32_t top_k;       /* 1 .. min(E, MXQ_MAX_TOPK) */
+    int32_t n_group;     /* 1 .. MXQ_MAX_ROUTE_GROUPS */
+    int32_t topk_group;  /* 1 .. n_group */
+    int32_t group_top;   /* 1 or 2 */
+    int32_t renormalise; /* 0 or 1 */
+    float scale;         /* finite */
+} mxq_route_config;
+
+/* Workspace bytes of mxq_route with expert order, or of mxq_expert_order.
+ * Pure host arithmetic; 0 for arguments those would refuse.  The workspace
+ * needs no initialisation and holds nothing between calls. */
+int64_t mxq_expert_order_workspace(int64_t T, int32_t top_k, int32_t E);
+
+/* Route T tokens: logits [T][E] (type dt, row stride ld >= E elements) ->
+ * idx int32 [T][top_k] and weights fp32 [T][top_k].  bias fp32 [E] or NULL.
+ * group_end, row_token, slot: all NULL, or all given (then also a 16-byte
+ * aligned workspace of mxq_expert_order_workspace bytes) to have the expert
+ * order of mxq_expert_order too.  T * top_k < 2^31. */
+mxq_status mxq_route(const void* logits, mxq_dtype dt, int64_t T, int32_t E, int64_t ld, const float* bias,
+                     const mxq_route_config* cfg, int32_t* idx, float* weights, int32_t* group_end,
+                     int32_t* row_token, int32_t* slot, void* workspace, int64_t workspace_bytes,
+                     hipStream_t st);
+
+/* Expert order of a routing: the pairs (t, k) sorted by expert, pairs of one
+ * expert in the order of t * top_k + k (so the result does not depend on
+ * timing).  idx int32 [T][top_k]; entries outside [0, E) are dropped.
+ *  group_end int32 [E]: the cumulative ends that the grouped entry points take.
+ *  row_token int32 [T * top_k]: the token of each expert-ordered row, -1 for
+ *    rows past the last.
+ *  slot int32 [T][top_k]: the row of each pair, -1 for a dropped one. */
+mxq_status mxq_expert_order(const int32_t* idx, int64_t T, int32_t top_k, int32_t E, int32_t* group_end,
+                            int32_t* row_token, int32_t* slot, void* workspace, int64_t workspace_bytes,
+                            hipStream_t st);
+
+/* Gradient of the weights of mxq_route with respect to the logits for the
+ * chosen experts idx (entries of a row distinct; outside [0, E): no
+ * gradient): dweights fp32 [T][top_k] -> dlogits [T][E] (type dt, row stride
+ * ldd), every element written, 0 at masked experts.  cfg: score, top_k,
+ * renormalise and scale are used. */
+mxq_status mxq_route_backward(const void* logits, mxq_dtype dt, int64_t T, int32_t E, int64_t ld,
+                              const mxq_route_config* cfg, const int32_t* idx, const float* dweights,
+                              void* dlogits, int64_t ldd, hipStream_t st);
+
+/* out[t] = sum_k weights[t][k] * y[slot[t][k]]: the experts' rows back in
+ * token order.  y [rows][H] (row stride ldy), slot int32 [T][top_k] (entries
+ * outside [0, rows) take no part; a token with none gets zeros), weights fp32
+ * [T][top_k] or NULL for 1 (then also the gradient of a dispatch), out
+ * [T][H] (row stride ldo).  Sums in fp32 in the order of k, rounded once.
+ * top_k <= MXQ_MAX_TOPK, rows < 2^31. */
+mxq_status mxq_combine(const void* y, mxq_dtype ydt, int64_t rows, int64_t ldy, const int32_t* slot,
+                       const float* weights, int64_t T, int32_t top_k, int64_t H, void* out, mxq_dtype odt,
+                       int64_t ldo, hipStream_t st);
+
+/* Gradient of mxq_combine: dy[slot[t][k]] = weights[t][k] * dout[t] and
+ * dweights[t][k] = <dout[t], y[slot[t][k]]> (0 for a dropped pair; sums in
+ * fp32, in an order that does not depend on timing).  weights NULL: 1.
+ * dweights NULL: not computed, y is not read and may be NULL.  dy NULL: not
+ * computed.  No two pairs may share a row; rows that no pair names are not
+ * written.  With weights and dweights NULL this is the dispatch of tokens
+ * into expert order: dy[slot[t][k]] = dout[t]. */
+mxq_status mxq_combine_backward(const void* dout, mxq_dtype dt, int64_t ldd, const void* y, mxq_dtype ydt,
+                                int64_t ldy, const int32_t* slot, const float* weights, int64_t T, int32_t top_k,
+                                int64_t H, int64_t rows, void* dy, mxq_dtype dydt, int64_t lddy, float* dweights,
+                                hipStream_t st);
+
+/* State format of mxq_adamw: fp32, or MXFP8: E4M3 codes with an E8M0 scale
+ * byte for every 32 consecutive elements of the tensor. */
+typedef enum { MXQ_ADAMW_F32 = 0, MXQ_ADAMW_MXFP8 = 1, MXQ_ADAMW_MAX_ENUM = 0x7FFFFFFF } mxq_adamw_format;
+
+/* One tensor of n contiguous elements.  fp32 arrays 4-byte aligned, bf16 2. */
+typedef struct {
+    void* param;           /* fp32 or bf16, updated */
+    const void* grad;      /* fp32 or bf16 */
+    void* m;               /* first moment: fp32 [n], or E4M3 codes [n]; updated */
+    void* v;               /* second moment v: fp32 [n], or E4M3 codes of sqrt(v) [n]; updated */
+    uint8_t* m_scale;      /* MXFP8: E8M0 bytes [ceil(n / 32)], else NULL */
+    uint8_t* v_scale;      /* likewise */
+    void* copy;            /* bf16 [n]: the new parameters rounded to bf16, or NULL */
+    int64_t n;             /* elements, >= 0 */
+    double decay_scale;    /* times weight_decay (0: none for this tensor) */
+} mxq_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps > 0 */
+    double grad_scale;                          /* multiplies every gradient */
+    int64_t step;                               /* of this update, 1 for the first */
+    uint32_t seed;                              /* of the stochastic rounding */
+} mxq_adamw_config;
+
+/* What changes from step to step, in device memory (16 bytes, 16-byte aligned), so that a
+ * captured step can be replayed with new values: where given to mxq_adamw, it
+ * replaces the config's lr, grad_scale, step and seed. */
+typedef struct {
+    float lr;
+    float grad_scale;
+    int32_t step;
+    uint32_t seed;
+} mxq_adamw_control;
+
+/* One AdamW step of n_tensors tensors (a host array, read before the call
+ * returns), all of one parameter, gradient and state type:
+ *   g' = grad_scale g;  m' = beta1 m + (1 - beta1) g';  v' = beta2 v + (1 - beta2) g'^2
+ *   p' = p (1 - lr wd) - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
+ * in fp32, the products and sums in this order without contraction; p'
+ * rounded to nearest for bf16.  A grad_scale that is not finite (a gradient
+ * norm or loss scale that overflowed) skips the step: nothing changes.
+ * MXFP8 states hold m and r = sqrt(v); the block's scale is the smallest
+ * power of two (2^(byte-127), byte >= 1) that keeps its largest finite
+ * magnitude at or below 448, 0 for a block of zeros; elements are rounded
+ * stochastically, y -> step * floor(y / step + u) with u in (0, 1) from a
+ * counter hash of (seed, step, index of the tensor in the call, element), so
+ * that moments whose change in one step is below half an E4M3 step still
+ * move; a positive r stays positive; a moment that is not finite becomes NaN.  Zero codes
+ * and scales are the state before the first step. */
+mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dtype param_dt, mxq_dtype grad_dt,
+                     mxq_adamw_format format, const mxq_adamw_config* cfg, const mxq_adamw_control* control,
+                     hipStream_t st);
 
 #ifdef __cplusplus
 }

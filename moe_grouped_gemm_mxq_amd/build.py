@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxq.so")
-SOURCES = ["mxq_api.hip", "quant_mxfp8.hip", "qdq_mxfp4.hip", "gemm_mxfp8.hip"]
+SOURCES = ["mxq_api.hip", "quant_mxfp8.hip", "qdq_mxfp4.hip", "gemm_mxfp8.hip", "route.hip", "combine.hip",
+           "adamw.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "../../include/mxq.h"
+#include "mxq_host.h"
 #include "mxq_internal.h"
 
 namespace mxq {
@@ -16,6 +17,8 @@ static_assert(kIlvMaxK == MXQ_EXACT_GROUPS_MAX_K, "the header states the kernels
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
 
 mxq_status fail(mxq_status st, const char* fmt, ...) {
   char buf[512];
@@ -31,6 +34,8 @@ mxq_status ok() {
   g_last_error.clear();
   return MXQ_OK;
 }
+
+namespace {
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_arch_state[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
@@ -55,6 +60,8 @@ mxq_status check_device_id(int dev) {
   return MXQ_OK;
 }
 
+}  // namespace
+
 mxq_status check_current_device() {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) {
@@ -69,8 +76,8 @@ mxq_status launched(hipError_t e, const char* what) {
   return ok();
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
+namespace {
+bool aligned16(const void* p) { return aligned_to(p, 16); }
 }  // namespace
 
 int device_cu_count() {
@@ -88,17 +95,6 @@ int device_cu_count() {
 }  // namespace mxq
 
 using namespace mxq;
-
-#define MXQ_REQUIRE(cond, ...) \
-  do {                         \
-    if (!(cond)) return fail(MXQ_ERR_INVALID_ARGUMENT, __VA_ARGS__); \
-  } while (0)
-
-#define MXQ_REQUIRE_DEVICE()                     \
-  do {                                           \
-    mxq_status _s = check_current_device();      \
-    if (_s != MXQ_OK) return _s;                 \
-  } while (0)
 
 extern "C" {
 

@@ -17,8 +17,11 @@ rows r, r+32, r+64, r+96 of a 128-row group for one block).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -39,16 +42,45 @@ MXQ_FMT_E4M3 = 0
 MXQ_FMT_E2M1 = 1
 MXQ_GG_RAGGED_M = 0
 MXQ_GG_RAGGED_K = 1
+MXQ_DT_F32 = 0
+MXQ_DT_BF16 = 1
+MXQ_SCORE_SOFTMAX = 0
+MXQ_SCORE_SIGMOID = 1
+MXQ_ADAMW_F32 = 0
+MXQ_ADAMW_MXFP8 = 1
 BLOCK = 32
 MAX_GROUPS = 1024
+MAX_TOPK = 32  # MXQ_MAX_TOPK
 MAX_ROW_BYTES = 1 << 23  # MXQ_GEMM_MAX_ROW_BYTES: GEMM code rows (K, or K/2 for E2M1) stay below this
 
 EXPORTED = [
     "mxq_abi_version", "mxq_last_error", "mxq_device_check", "mxq_grouped_cols_max", "mxq_operand_sizes",
     "mxq_quantize", "mxq_quantize_batched", "mxq_quantize_grouped", "mxq_qdq_fp4", "mxq_qdq_fp4_ex",
     "mxq_ste_backward_fp4", "mxq_fp4_scale_threshold", "mxq_quantize_fp4", "mxq_gemm", "mxq_grouped_gemm",
-    "mxq_validate_group_end", "mxq_quantize_fp4_grouped",
+    "mxq_validate_group_end", "mxq_quantize_fp4_grouped", "mxq_expert_order_workspace", "mxq_route",
+    "mxq_expert_order", "mxq_route_backward", "mxq_combine", "mxq_combine_backward", "mxq_adamw",
 ]
+
+
+class RouteConfig(ctypes.Structure):
+    """mxq_route_config."""
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """mxq_adamw_tensor."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("decay_scale", ctypes.c_double)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """mxq_adamw_config."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint32)]
 
 
 def _load(path: str = LIB_PATH):
@@ -76,6 +108,13 @@ def _load(path: str = LIB_PATH):
         "mxq_grouped_gemm": ([I, P, P, P, P, P, I64, I64, I64, P, I32, I, P], I),
         "mxq_validate_group_end": ([P, I32, I64, P, P], I),
         "mxq_quantize_fp4_grouped": ([P, I64, I64, I64, P, I32, I64, ctypes.c_float, P, P, P], I),
+        "mxq_expert_order_workspace": ([I64, I32, I32], I64),
+        "mxq_route": ([P, I, I64, I32, I64, P, P, P, P, P, P, P, P, I64, P], I),
+        "mxq_expert_order": ([P, I64, I32, I32, P, P, P, P, I64, P], I),
+        "mxq_route_backward": ([P, I, I64, I32, I64, P, P, P, P, I64, P], I),
+        "mxq_combine": ([P, I, I64, I64, P, P, I64, I32, I64, P, I, I64, P], I),
+        "mxq_combine_backward": ([P, I, I64, P, I, I64, P, P, I64, I32, I64, I64, P, I, I64, P, P], I),
+        "mxq_adamw": ([P, I32, I, I, I, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -84,7 +123,7 @@ def _load(path: str = LIB_PATH):
     return lib
 
 
-ABI_VERSION = 7  # MXQ_ABI_VERSION of include/mxq.h this binding is written against
+ABI_VERSION = 8  # MXQ_ABI_VERSION of include/mxq.h this binding is written against
 
 _lib = _load()
 if _lib.mxq_abi_version() != ABI_VERSION:
@@ -361,6 +400,159 @@ def mxq_validate_group_end(group_end, T, flag, stream=None):
                                        _stream(stream, group_end.device)), "mxq_validate_group_end")
 
 
+# ---- around the expert GEMMs: routing, combine, optimiser
+_DTYPES = {torch.float32: MXQ_DT_F32, torch.bfloat16: MXQ_DT_BF16}
+_SCORES = {"softmax": MXQ_SCORE_SOFTMAX, "sigmoid": MXQ_SCORE_SIGMOID, 0: MXQ_SCORE_SOFTMAX, 1: MXQ_SCORE_SIGMOID}
+
+
+def _need_float(t, name, dim=2):
+    """Type code of a float matrix with unit stride along its last dim."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dims, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dim")
+    return dt
+
+
+def _need_array(t, name, dtype, shape):
+    """Device tensor of this type and shape, contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _row_stride(t):
+    """Row stride the C entry points take (the stride of a dim of size 1 or 0 says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def route_config(top_k, score="softmax", n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0):
+    """mxq_route_config; score "softmax" or "sigmoid"."""
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r}; one of 'softmax', 'sigmoid'")
+    return RouteConfig(_SCORES[score], top_k, n_group, topk_group, group_top, int(bool(renormalise)), float(scale))
+
+
+def mxq_expert_order_workspace(T: int, top_k: int, E: int) -> int:
+    return _lib.mxq_expert_order_workspace(T, top_k, E)
+
+
+def mxq_route(logits, cfg, idx, weights, bias=None, group_end=None, row_token=None, slot=None, workspace=None,
+              stream=None):
+    """logits fp32 or bf16 [T][E] (unit column stride) -> idx int32, weights fp32 [T][top_k]; with group_end int32
+    [E], row_token int32 [T * top_k], slot int32 [T][top_k] and a uint8 workspace the expert order too."""
+    dt = _need_float(logits, "logits")
+    T, E = logits.shape
+    K = cfg.top_k
+    _need_array(idx, "idx", torch.int32, (T, K))
+    _need_array(weights, "weights", torch.float32, (T, K))
+    if bias is not None:
+        _need_array(bias, "bias", torch.float32, (E,))
+    nbytes = _need_order(group_end, row_token, slot, workspace, T, K, E) if group_end is not None else 0
+    _check(_lib.mxq_route(logits.data_ptr(), dt, T, E, _row_stride(logits), _raw(bias), ctypes.byref(cfg), idx.data_ptr(),
+                          weights.data_ptr(), _raw(group_end), _raw(row_token), _raw(slot), _raw(workspace), nbytes,
+                          _stream(stream, logits.device)), "mxq_route")
+
+
+def _need_order(group_end, row_token, slot, workspace, T, K, E):
+    _need_array(group_end, "group_end", torch.int32, (E,))
+    _need_array(row_token, "row_token", torch.int32, (T * K,))
+    _need_array(slot, "slot", torch.int32, (T, K))
+    _need(workspace, torch.uint8, "workspace", 1)
+    return workspace.numel()
+
+
+def mxq_expert_order(idx, E, group_end, row_token, slot, workspace, stream=None):
+    """idx int32 [T][top_k] (entries outside [0, E) dropped) -> group_end [E], row_token [T * top_k], slot [T][top_k]."""
+    _need(idx, torch.int32, "idx", 2)
+    T, K = idx.shape
+    _need_array(idx, "idx", torch.int32, (T, K))
+    nbytes = _need_order(group_end, row_token, slot, workspace, T, K, E)
+    _check(_lib.mxq_expert_order(idx.data_ptr(), T, K, E, group_end.data_ptr(), row_token.data_ptr(), slot.data_ptr(),
+                                 workspace.data_ptr(), nbytes, _stream(stream, idx.device)), "mxq_expert_order")
+
+
+def mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream=None):
+    """dweights fp32 [T][top_k] -> dlogits [T][E] of the logits' type, every element written."""
+    dt = _need_float(logits, "logits")
+    T, E = logits.shape
+    if _need_float(dlogits, "dlogits") != dt or dlogits.shape != logits.shape:
+        raise ValueError("dlogits must have the logits' type and shape")
+    _need_array(idx, "idx", torch.int32, (T, cfg.top_k))
+    _need_array(dweights, "dweights", torch.float32, (T, cfg.top_k))
+    _check(_lib.mxq_route_backward(logits.data_ptr(), dt, T, E, _row_stride(logits), ctypes.byref(cfg), idx.data_ptr(),
+                                   dweights.data_ptr(), dlogits.data_ptr(), _row_stride(dlogits),
+                                   _stream(stream, logits.device)), "mxq_route_backward")
+
+
+def _need_pairs(slot, weights):
+    _need(slot, torch.int32, "slot", 2)
+    _need_array(slot, "slot", torch.int32, slot.shape)
+    if weights is not None:
+        _need_array(weights, "weights", torch.float32, slot.shape)
+    return slot.shape
+
+
+def mxq_combine(y, slot, weights, out, stream=None):
+    """out[t] = sum_k weights[t][k] * y[slot[t][k]]; y [rows][H], slot int32 [T][top_k], weights fp32 or None, out
+    [T][H]; y and out fp32 or bf16 with unit column stride."""
+    ydt, odt = _need_float(y, "y"), _need_float(out, "out")
+    T, K = _need_pairs(slot, weights)
+    if out.shape != (T, y.shape[1]):
+        raise ValueError(f"out must have shape {(T, y.shape[1])}, got {tuple(out.shape)}")
+    _check(_lib.mxq_combine(y.data_ptr(), ydt, y.shape[0], _row_stride(y), slot.data_ptr(), _raw(weights), T, K, y.shape[1],
+                            out.data_ptr(), odt, _row_stride(out), _stream(stream, out.device)), "mxq_combine")
+
+
+def mxq_combine_backward(dout, slot, rows, dy=None, dweights=None, weights=None, y=None, stream=None):
+    """dy[slot[t][k]] = weights[t][k] * dout[t] ([rows][H]); dweights[t][k] = <dout[t], y[slot[t][k]]> (needs y)."""
+    dt = _need_float(dout, "dout")
+    T, K = _need_pairs(slot, weights)
+    H = dout.shape[1]
+    if dout.shape[0] != T:
+        raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
+    ydt = gdt = dt
+    if y is not None:
+        ydt = _need_float(y, "y")
+        if y.shape != (rows, H):
+            raise ValueError(f"y must have shape {(rows, H)}, got {tuple(y.shape)}")
+    if dy is not None:
+        gdt = _need_float(dy, "dy")
+        if dy.shape != (rows, H):
+            raise ValueError(f"dy must have shape {(rows, H)}, got {tuple(dy.shape)}")
+    if dweights is not None:
+        _need_array(dweights, "dweights", torch.float32, (T, K))
+        if y is None:
+            raise ValueError("dweights needs y")
+    _check(_lib.mxq_combine_backward(dout.data_ptr(), dt, _row_stride(dout), _raw(y), ydt, 0 if y is None else _row_stride(y),
+                                     slot.data_ptr(), _raw(weights), T, K, H, rows, _raw(dy), gdt,
+                                     0 if dy is None else _row_stride(dy), _raw(dweights), _stream(stream, dout.device)),
+           "mxq_combine_backward")
+
+
+def mxq_adamw(tensors, n_tensors, param_dt, grad_dt, fmt, cfg, control=None, stream=None, device=None):
+    """tensors: a ctypes array of AdamWTensor (see the AdamW class, which fills one from torch tensors)."""
+    _check(_lib.mxq_adamw(tensors, n_tensors, param_dt, grad_dt, fmt, ctypes.byref(cfg), _raw(control),
+                          _stream(stream, device)), "mxq_adamw")
+
+
 # ------------------------------------------------------------------ allocate-and-call helpers
 def _u8(shape, device):
     return torch.empty(shape, dtype=torch.uint8, device=device)
@@ -476,3 +668,154 @@ def grouped_gemm(mode, A, sA, B, sB, group_end, stream=None, fmt=MXQ_FMT_E4M3):
         C = torch.empty((group_end.numel(), A.shape[0], B.shape[0]), dtype=torch.float32, device=A.device)
     mxq_grouped_gemm(mode, A, sA, B, sB, C, group_end, stream, fmt)
     return C
+
+
+def _on(stream):
+    """Context in which temporaries belong to the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _workspace(T, top_k, E, device, stream):
+    with _on(stream):
+        return torch.empty(mxq_expert_order_workspace(T, top_k, E), dtype=torch.uint8, device=device)
+
+
+def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0,
+          order=True, out=None, stream=None):
+    """Route tokens: {"idx", "weights"} and, with order, {"group_end", "row_token", "slot"} (the expert order the grouped
+    entry points and combine take).  out: a dict of such buffers to write to ("workspace" may be among them)."""
+    cfg = route_config(top_k, score, n_group, topk_group, group_top, renormalise, scale)
+    T, E = logits.shape
+    if out is None:
+        i32 = functools.partial(torch.empty, dtype=torch.int32, device=logits.device)
+        out = {"idx": i32((T, top_k)), "weights": torch.empty((T, top_k), dtype=torch.float32, device=logits.device)}
+        if order:
+            out.update(group_end=i32((E,)), row_token=i32((T * top_k,)), slot=i32((T, top_k)))
+    if not order:
+        mxq_route(logits, cfg, out["idx"], out["weights"], bias, stream=stream)
+        return out
+    ws = out.get("workspace")
+    if ws is None:
+        ws = _workspace(T, top_k, E, logits.device, stream)
+    mxq_route(logits, cfg, out["idx"], out["weights"], bias, out["group_end"], out["row_token"], out["slot"], ws, stream)
+    return out
+
+
+def expert_order(idx, E, stream=None):
+    """Expert order of chosen experts idx int32 [T][top_k]: {"group_end", "row_token", "slot"}."""
+    T, K = idx.shape
+    i32 = functools.partial(torch.empty, dtype=torch.int32, device=idx.device)
+    out = {"group_end": i32((E,)), "row_token": i32((T * K,)), "slot": i32((T, K))}
+    mxq_expert_order(idx, E, out["group_end"], out["row_token"], out["slot"], _workspace(T, K, E, idx.device, stream), stream)
+    return out
+
+
+def route_backward(logits, idx, dweights, *, score="softmax", renormalise=True, scale=1.0, stream=None):
+    """Gradient of route's weights with respect to the logits."""
+    cfg = route_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream)
+    return dlogits
+
+
+def combine(y, slot, weights=None, dtype=torch.bfloat16, stream=None):
+    """The experts' rows y [rows][H] back in token order: [T][H] of `dtype`."""
+    out = torch.empty((slot.shape[0], y.shape[1]), dtype=dtype, device=y.device)
+    mxq_combine(y, slot, weights, out, stream)
+    return out
+
+
+def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=None):
+    """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights."""
+    dy = torch.empty((rows, dout.shape[1]), dtype=dtype or dout.dtype, device=dout.device)
+    dw = None
+    if y is not None and weights is not None:
+        dw = torch.empty(slot.shape, dtype=torch.float32, device=dout.device)
+    mxq_combine_backward(dout, slot, rows, dy, dw, weights, y if dw is not None else None, stream)
+    return dy, dw
+
+
+def dispatch(x, slot, rows, dtype=None, stream=None):
+    """Tokens x [T][H] in expert order: row slot[t][k] of the result is x[t].  Its gradient is combine without weights."""
+    return combine_backward(x, slot, rows, dtype=dtype, stream=stream)[0]
+
+
+def adamw_state(param, fmt=MXQ_ADAMW_MXFP8):
+    """One moment of a parameter before the first step: fp32 zeros, or (codes, scales) of MXFP8."""
+    if fmt == MXQ_ADAMW_F32:
+        return torch.zeros(param.shape, dtype=torch.float32, device=param.device)
+    zeros = functools.partial(torch.zeros, dtype=torch.uint8, device=param.device)
+    return zeros(param.shape), zeros((ceil32(param.numel()) // BLOCK,))
+
+
+def adamw_control(lr, step, seed=0, grad_scale=1.0, out=None, device="cuda"):
+    """mxq_adamw_control in device memory (int32 [4]); `out`: such a tensor to overwrite, as between graph replays."""
+    host = torch.tensor(struct.unpack("4i", struct.pack("2fiI", lr, grad_scale, step, seed)), dtype=torch.int32)
+    return host.to(device) if out is None else out.copy_(host)
+
+
+class AdamW:
+    """AdamW steps of a list of tensors (mxq_adamw).
+
+    params fp32 or bf16, grads fp32 or bf16, m and v the moments: fp32 tensors, or (codes, scales) pairs of uint8 tensors
+    (MXFP8; v holds sqrt of the second moment) as adamw_state makes them.  copies: bf16 tensors that get the new
+    parameters too, or None.  decay_scales: per tensor, times the weight decay.  The tensors stay the caller's: they are
+    read and written where they are, so a gradient that moves to other storage needs a new AdamW."""
+
+    def __init__(self, params, grads, m, v, copies=None, decay_scales=None):
+        n = len(params)
+        if not (len(grads) == len(m) == len(v) == n) or any(x is not None and len(x) != n for x in (copies, decay_scales)):
+            raise ValueError("params, grads, m, v, copies and decay_scales must be of one length")
+        self.device = params[0].device if n else None
+        self.param_dt = self.grad_dt = MXQ_DT_F32
+        self.fmt = MXQ_ADAMW_MXFP8 if n and isinstance(m[0], (tuple, list)) else MXQ_ADAMW_F32
+        self.tensors = (AdamWTensor * max(n, 1))()
+        self.n = n
+        self.keep = (list(params), list(grads), list(m), list(v), copies and list(copies))
+        for i, p in enumerate(params):
+            name = f"tensor {i}: "
+            pdt = self._need(p, name + "param", p, _DTYPES)
+            gdt = self._need(grads[i], name + "grad", p, _DTYPES)
+            if i == 0:
+                self.param_dt, self.grad_dt = pdt, gdt
+            elif (pdt, gdt) != (self.param_dt, self.grad_dt):
+                raise TypeError(name + "all parameters must be of one type, and all gradients")
+            d = self.tensors[i]
+            for field, x in (("m", m[i]), ("v", v[i])):
+                if isinstance(x, (tuple, list)) != (self.fmt == MXQ_ADAMW_MXFP8):
+                    raise TypeError(name + "all states must be of one format")
+                if self.fmt == MXQ_ADAMW_MXFP8:
+                    x, scale = x
+                    _need_array(scale, name + field + " scales", torch.uint8, (ceil32(p.numel()) // BLOCK,))
+                    setattr(d, field + "_scale", scale.data_ptr())
+                self._need(x, name + field, p, {torch.uint8 if self.fmt == MXQ_ADAMW_MXFP8 else torch.float32: 0})
+                setattr(d, field, x.data_ptr())
+            if copies is not None and copies[i] is not None:
+                self._need(copies[i], name + "copy", p, {torch.bfloat16: 0})
+                d.copy = copies[i].data_ptr()
+            d.param, d.grad, d.n = p.data_ptr(), grads[i].data_ptr(), p.numel()
+            d.decay_scale = 1.0 if decay_scales is None else float(decay_scales[i])
+
+    @staticmethod
+    def _need(t, name, like, types):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype not in types:
+            raise TypeError(f"{name} must be {' or '.join(str(k) for k in types)}, got {t.dtype}")
+        if not t.is_cuda or t.device != like.device:
+            raise ValueError(f"{name} must be a device tensor, on its parameter's device")
+        if t.numel() != like.numel() or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with {like.numel()} elements")
+        return types[t.dtype]
+
+    def step(self, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1, grad_scale=1.0, seed=0, control=None,
+             stream=None):
+        """One step.  control: an adamw_control tensor whose lr, step, seed and grad_scale replace these (for graphs)."""
+        if control is not None:
+            _need_array(control, "control", torch.int32, (4,))
+        if not self.n:
+            return
+        cfg = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, seed & 0xFFFFFFFF)
+        mxq_adamw(self.tensors, self.n, self.param_dt, self.grad_dt, self.fmt, cfg, control, stream, self.device)

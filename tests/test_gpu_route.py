@@ -1,0 +1,303 @@
+"""Router, expert order and the gradient of the weights against 64-bit references.
+
+Weights: relative error at most (4 R + 40) half steps of fp32, R the spread of the row's logits: exp of a
+difference x - max costs R from the difference and R from its scaling, in the numerator and in the sum, two
+steps each for exp and for the quotient, and at most 22 additions follow one another in the sum (16 of a
+lane's own, 6 across lanes)."""
+import numpy as np
+import pytest
+import torch
+
+import moe_reference as ref
+from gpu_util import host, mxq
+
+pytestmark = pytest.mark.gpu
+
+U = ref.U32
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def logits_of(T, E, dtype, seed, masked=0.0, std=1.5):
+    g = torch.Generator().manual_seed(seed)
+    x = (std * torch.randn(T, E, generator=g)).to(dtype)
+    if masked and T:
+        x[torch.rand(T, E, generator=g) < masked] = -float("inf")
+        x[T // 2] = torch.finfo(dtype).min
+    return x.cuda()
+
+
+def spread(l):
+    fine = np.where(np.isfinite(l) & (l > ref.LOWEST), l, np.nan)
+    with np.errstate(all="ignore"):
+        import warnings
+        with warnings.catch_warnings():
+            warnings.simplefilter("ignore")
+            r = np.nanmax(fine, 1) - np.nanmin(fine, 1)
+    return np.nan_to_num(r)[:, None] + np.nan_to_num(np.nanmax(np.abs(np.nan_to_num(fine)), 1, initial=0))[:, None]
+
+
+def check_route(x, K, bias=None, **kw):
+    m = mxq()
+    E = x.shape[1]
+    got = m.route(x, K, bias=bias, **kw)
+    idx, w = ref.route(f64(x), K, bias=None if bias is None else f64(bias), **kw)
+    assert np.array_equal(host(got["idx"]), idx)
+    gw = f64(got["weights"])
+    assert np.array_equal(np.isnan(gw), np.isnan(w))
+    fine = np.isfinite(w)
+    tol = (4 * spread(f64(x)) + 40) * U * np.abs(w) + 2.0 ** -126
+    assert np.all(np.abs(np.where(fine, gw - w, 0)) <= np.where(fine, tol, 0))
+    ends, token, slot = ref.expert_order(idx, E)
+    assert np.array_equal(host(got["group_end"]), ends)
+    assert np.array_equal(host(got["row_token"]), token)
+    assert np.array_equal(host(got["slot"]), slot)
+    again = m.route(x, K, bias=bias, **kw)
+    for k in got:
+        if not (k == "weights" and np.isnan(gw).any()):
+            assert torch.equal(got[k], again[k]), k
+
+
+SIZES = [(0, 8, 2), (1, 1, 1), (1, 2, 2), (2, 31, 5), (3, 32, 32), (5, 33, 8), (63, 64, 1), (64, 65, 6), (65, 100, 3),
+         (7, 160, 6), (129, 256, 8), (17, 500, 9), (9, 512, 8), (4, 1000, 32), (33, 1024, 16), (1000, 32, 8)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,K", SIZES)
+def test_route_sizes(T, E, K, score, dtype):
+    x = logits_of(T, E, dtype, 7 * T + E)
+    bias = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))).cuda()
+    for b in (None, bias, torch.zeros_like(bias)):
+        check_route(x, K, b, score=score, renormalise=True, scale=2.5)
+    check_route(x, K, bias, score=score, renormalise=False, scale=1.0)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,K", [(256, 8, 4, 8), (256, 8, 1, 8), (96, 3, 2, 7), (64, 64, 5, 5), (30, 2, 2, 4),
+                                                   (1024, 16, 3, 12), (48, 6, 4, 20), (36, 4, 2, 3), (160, 8, 3, 6)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups(E, n_group, topk_group, K, group_top, score):
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+    for dtype, masked in ((torch.float32, 0.0), (torch.bfloat16, 0.0), (torch.float32, 0.3), (torch.bfloat16, 0.6)):
+        x = logits_of(41, E, dtype, E + K, masked)
+        bias = (0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E))).cuda()
+        for b in (None, bias, torch.zeros_like(bias)):
+            check_route(x, K, b, renormalise=True, scale=1.0, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_route_masks(score, renormalise):
+    """Masked experts, rows with fewer experts than top_k, none at all, and the lowest values of both types."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x = logits_of(64, 40, dtype, 3, 0.85)
+        x[5] = -float("inf")
+        x[6, 1:] = torch.finfo(torch.bfloat16).min
+        bias = torch.linspace(-0.5, 0.5, 40).cuda()
+        for b in (None, bias):
+            check_route(x, 8, b, score=score, renormalise=renormalise)
+            check_route(x, 8, b, score=score, renormalise=renormalise, n_group=5, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_not_finite(score):
+    x = logits_of(8, 50, torch.float32, 4)
+    x[1, 7] = float("nan")
+    x[2, :] = float("nan")
+    x[3, 9] = float("inf")
+    x[4, 3] = float("nan")
+    x[4, 20] = -float("inf")
+    x[5, 10:12] = float("inf")
+    bias = torch.linspace(0.3, -0.3, 50).cuda()
+    for b in (None, bias):
+        check_route(x, 6, b, score=score, renormalise=False)
+        check_route(x, 6, b, score=score, renormalise=True, n_group=5, topk_group=3, group_top=2)
+
+
+def test_route_ties_go_to_the_lowest_index():
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.zeros(5, 96, dtype=dtype, device="cuda")
+        x[1, 40:] = 1.0
+        x[2, ::3] = 2.0
+        x[3] = torch.arange(96, device="cuda") // 7
+        x[4, 95] = 1e-3
+        for kw in ({}, {"n_group": 8, "topk_group": 3, "group_top": 2}, {"n_group": 4, "topk_group": 2}):
+            for b in (None, torch.zeros(96, device="cuda"), torch.full((96,), 0.25, device="cuda")):
+                for score in ("softmax", "sigmoid"):
+                    check_route(x, 8, b, score=score, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_close_keys(score):
+    """Keys that differ by less than fp32 resolves: the bias undoes the scores' differences up to its own rounding."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(1, 64, generator=g)
+    s = torch.sigmoid(x.double()) if score == "sigmoid" else torch.softmax(x.double(), 1)
+    bias = (1.0 - s[0]).float()
+    key = np.sort(f64(s[0]) + f64(bias))
+    assert np.min(np.diff(key)) > 1e-13 and np.max(np.diff(key)) < 1e-7  # apart in 64 bits, not in 32
+    check_route(x.cuda(), 8, bias.cuda(), score=score)
+    check_route(x.cuda(), 8, bias.cuda(), score=score, n_group=8, topk_group=3, group_top=2)
+    # among ordinary rows, and far-off scores
+    rows = logits_of(33, 64, torch.float32, 5)
+    rows[::4] = x.cuda()
+    check_route(rows, 8, bias.cuda(), score=score, n_group=4, topk_group=2, group_top=2)
+    check_route(rows * 40, 8, bias.cuda(), score=score)
+
+
+def test_route_strides_and_alignment():
+    base = logits_of(20, 200, torch.float32, 9)
+    for lo, hi in ((0, 128), (1, 129), (3, 60), (8, 200)):
+        for x in (base[:, lo:hi], base.to(torch.bfloat16)[:, lo:hi]):
+            check_route(x, 4)
+    check_route(base.to(torch.bfloat16)[::2, 5:37], 4)
+
+
+def test_route_far_rows():
+    """A row stride that takes the last row's offset past 32 bits."""
+    x = torch.empty_strided((3, 64), (1 << 30, 1), dtype=torch.float32, device="cuda")
+    x.copy_(logits_of(3, 64, torch.float32, 2))
+    check_route(x, 8, score="sigmoid")
+    d = torch.empty_strided((3, 64), (1 << 30, 1), dtype=torch.float32, device="cuda")
+    m = mxq()
+    idx = m.route(x, 8, order=False)["idx"]
+    dw = torch.ones(3, 8, device="cuda")
+    dw[:, 0] = 2.0
+    m.mxq_route_backward(x, m.route_config(8), idx, dw, d)
+    assert torch.equal(d, m.route_backward(x.contiguous(), idx, dw))
+
+
+def test_route_on_another_stream():
+    m = mxq()
+    x = logits_of(500, 64, torch.float32, 8)
+    want = m.route(x, 8)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        out = {k: torch.empty_like(v) for k, v in want.items()}
+    got = m.route(x, 8, out=out, stream=st)
+    st.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+# ------------------------------------------------------------------ expert order
+@pytest.mark.parametrize("T,K,E", [(0, 1, 1), (1, 1, 1), (1, 8, 8), (127, 8, 3), (128, 8, 256), (129, 8, 256), (1024, 1, 1024),
+                                  (2049, 5, 7), (5003, 8, 32), (40000, 2, 1000)])
+def test_expert_order(T, K, E):
+    m = mxq()
+    g = torch.Generator().manual_seed(T + E)
+    for kind in ("random", "one", "dropped"):
+        if kind == "one":
+            idx = torch.full((T, K), E - 1, dtype=torch.int32)
+        elif kind == "random":
+            idx = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)
+        else:  # out of range on both sides
+            idx = torch.randint(-2, E + 3, (T, K), generator=g, dtype=torch.int32)
+            if T:
+                idx[0, 0] = -2 ** 31
+                idx[-1, -1] = 2 ** 31 - 1
+        got = m.expert_order(idx.cuda(), E)
+        for name, want in zip(("group_end", "row_token", "slot"), ref.expert_order(idx.numpy(), E)):
+            assert np.array_equal(host(got[name]), want), (kind, name)
+
+
+def test_expert_order_of_many_chunks():
+    m = mxq()
+    idx = torch.randint(0, 77, (120000, 8), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    got = m.expert_order(idx.cuda(), 77)
+    flat = idx.reshape(-1).numpy()
+    order = np.argsort(flat, kind="stable")
+    assert np.array_equal(host(got["row_token"]), order // 8)
+    slot = np.empty_like(order)
+    slot[order] = np.arange(len(order))
+    assert np.array_equal(host(got["slot"]).reshape(-1), slot)
+    assert np.array_equal(host(got["group_end"]), np.cumsum(np.bincount(flat, minlength=77)))
+
+
+# ------------------------------------------------------------------ gradient
+def check_backward(x, idx, dw, score, renormalise, scale=1.0):
+    """|err| <= (6 R + 64) half steps of s_e (sum_k |g_k| p_k + |g_e|): the factors of the weights' bound, with the
+    sum over the chosen experts and two products more; bf16 results another half step of theirs."""
+    m = mxq()
+    got = f64(m.route_backward(x, idx, dw, score=score, renormalise=renormalise, scale=scale))
+    l, i, g = f64(x), host(idx), f64(dw)
+    want = ref.route_backward(l, i, g, score, renormalise, scale)
+    E = l.shape[1]
+    with np.errstate(all="ignore"):
+        off = l <= ref.LOWEST
+        s = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - np.max(np.where(off, -np.inf, l), 1, keepdims=True))
+    s = np.where(off, 0, s)
+    if score == "softmax":
+        s = s / np.maximum(s.sum(1, keepdims=True), 1e-300)
+    G = np.zeros_like(l)
+    for t in range(len(l)):
+        for k in range(i.shape[1]):
+            if 0 <= i[t, k] < E and not off[t, i[t, k]]:
+                G[t, i[t, k]] = abs(g[t, k]) * scale
+    p = np.where(G > 0, s, 0)
+    size = p * G if score == "sigmoid" and not renormalise else s * (G + (s * G).sum(1, keepdims=True))
+    if renormalise:
+        p = p / np.maximum(p.sum(1, keepdims=True), 1e-300)
+        size = p * (G + (p * G).sum(1, keepdims=True))
+    tol = (6 * spread(l) + 64) * U * size + 2.0 ** -126
+    if x.dtype == torch.bfloat16:
+        tol = tol + ref.UBF16 * np.abs(want)
+    assert np.all(np.abs(got - want) <= tol)
+    return got
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("T,E,K", SIZES)
+def test_route_backward(T, E, K, score, renormalise):
+    m = mxq()
+    for dtype, masked in ((torch.float32, 0.0), (torch.bfloat16, 0.0), (torch.float32, 0.4)):
+        x = logits_of(T, E, dtype, T + E, masked)
+        idx = m.route(x, K, score=score, order=False)["idx"]
+        dw = torch.randn(T, K, generator=torch.Generator().manual_seed(E)).cuda()
+        check_backward(x, idx, dw, score, renormalise, 2.5)
+
+
+def test_route_backward_drops_bad_indexes():
+    x = logits_of(6, 20, torch.float32, 1)
+    idx = torch.tensor([[0, -1, 5], [20, 3, 1], [-2 ** 31, 2 ** 31 - 1, 19], [-1, -1, -1], [7, 8, 9], [1, 2, 40]], dtype=torch.int32).cuda()
+    dw = torch.randn(6, 3, generator=torch.Generator().manual_seed(2)).cuda()
+    for score in ("softmax", "sigmoid"):
+        for renormalise in (False, True):
+            check_backward(x, idx, dw, score, renormalise)
+
+
+def test_route_backward_strides():
+    m = mxq()
+    base = logits_of(9, 100, torch.bfloat16, 3)
+    x = base[:, 3:80]
+    idx = m.route(x, 5, order=False)["idx"]
+    dw = torch.randn(9, 5, generator=torch.Generator().manual_seed(2)).cuda()
+    out = torch.full((9, 90), 7.0, dtype=torch.bfloat16, device="cuda")
+    m.mxq_route_backward(x, m.route_config(5), idx, dw, out[:, 5:82])
+    assert torch.equal(out[:, 5:82], m.route_backward(x.contiguous(), idx, dw))
+    assert bool((out[:, :5] == 7).all()) and bool((out[:, 82:] == 7).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_route_backward_against_differences(score, renormalise):
+    """Central differences of the forward kernel.  Every weight's third derivative along one logit is below 6, so the
+    difference is off by h^2 times sum |dw|, and by the weights' rounding over h."""
+    m = mxq()
+    E, K, h = 24, 4, 2.0 ** -7
+    x = logits_of(1, E, torch.float32, 12)
+    idx = m.route(x, K, score=score, order=False)["idx"]
+    dw = torch.randn(1, K, generator=torch.Generator().manual_seed(3)).cuda()
+    step = h * torch.eye(E, device="cuda")
+    pinned = torch.zeros(E, device="cuda")
+    pinned[idx[0].long()] = torch.arange(K, 0, -1, device="cuda") * 10.0  # the choice stays, whatever the logits
+    w = [m.route(x + s * step, K, score=score, bias=pinned, renormalise=renormalise, order=False) for s in (1, -1)]
+    assert all(bool((v["idx"] == idx).all()) for v in w)
+    diff = ((w[0]["weights"].double() - w[1]["weights"].double()) * dw.double()).sum(1).cpu().numpy() / (2 * h)
+    got = check_backward(x, idx, dw, score, renormalise)[0]
+    total = float(dw.abs().sum())
+    assert np.all(np.abs(diff - got) <= total * (h * h + (4 * 10 + 40) * U / h + 1e-5))
