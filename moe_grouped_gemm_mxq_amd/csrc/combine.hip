@@ -6,6 +6,8 @@
 // a tile of its columns (the gradient's dot products need the whole token, so
 // there it walks the tiles), a thread eight consecutive columns, and the loads
 // of up to kRows rows are issued before the first of them is used.
+#include <type_traits>
+
 #include "mxq_device.h"
 #include "mxq_host.h"
 #include "mxq_vec.h"
@@ -15,28 +17,29 @@ namespace mxq {
 namespace {
 
 constexpr int kWave = 64;
-constexpr int kThreads = 256;
-constexpr int kTile = 8 * kThreads;
-constexpr int kRows = 8;  // rows in flight
-#ifndef NTV
-#define NTV true
-#endif
-constexpr bool kNT = NTV;
+constexpr int kMaxThreads = 512;
+constexpr int kCols = 8;  // columns of a thread in a tile of kCols * blockDim.x
+// Rows in flight.  A thread's sums are the same few registers however many rows
+// feed them, so combine takes eight; the gradient also writes eight rows then,
+// and measured 5.25 TB/s with eight, 5.35 with four (16384 x 8 x 4096, fp32 y).
+constexpr int kRows = 8, kRowsBackward = 4;
 
 // workgroups for `units` units of work, one each while a grid can hold them
 // (a grid has fewer than 2^32 threads); the kernels walk the rest
-unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 23) ? units : 1 << 23); }
+unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 22) ? units : 1 << 22); }
 
-// Rows k0 .. k0 + kRows - 1 of a token (uniform over the workgroup); -1: none
+// Rows k0 .. k0 + N - 1 of a token (uniform over the workgroup); -1: none
+template <int N>
 struct Rows {
-  int32_t row[kRows];
-  float w[kRows];
+  int32_t row[N];
+  float w[N];
 };
-__device__ __forceinline__ Rows token_rows(const int32_t* __restrict__ slot, const float* __restrict__ weights, int64_t t,
-                                           int K, int k0, int32_t rows) {
-  Rows r;
+template <int N>
+__device__ __forceinline__ Rows<N> token_rows(const int32_t* __restrict__ slot, const float* __restrict__ weights,
+                                              int64_t t, int K, int k0, int32_t rows) {
+  Rows<N> r;
 #pragma unroll
-  for (int j = 0; j < kRows; j++) {
+  for (int j = 0; j < N; j++) {
     r.row[j] = -1;
     r.w[j] = 1.f;
     if (k0 + j < K) {
@@ -48,161 +51,148 @@ __device__ __forceinline__ Rows token_rows(const int32_t* __restrict__ slot, con
   return r;
 }
 
-// Columns of a thread in a tile: kTile / kThreads, in pieces of W consecutive ones, so
-// that each load of a wave is one unbroken run: 16 bytes a lane for fp32 (W = 4)
-// and for bf16 alone (W = 8), 8 for bf16 beside fp32 (W = 4).
+// A thread's columns lie in kCols / W pieces of W, piece p at p * blockDim.x * W, so
+// that each load of a wave is one unbroken run of 16 bytes a lane for fp32 (W = 4)
+// and for bf16 alone (W = 8), 8 for bf16 beside fp32 (W = 4).  (Eight fp32
+// columns as two loads 32 bytes apart from lane to lane measured 5.1 against
+// 5.9 TB/s.)  Only the row's last piece can be a part of W columns: it is
+// taken one column at a time.
 template <typename A, typename B>
 constexpr int width() {
   return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4;
 }
 
 template <typename YT, typename OT>
-__global__ __launch_bounds__(kThreads) void combine_kernel(const YT* __restrict__ y, int32_t rows, int64_t ldy,
-                                                          const int32_t* __restrict__ slot,
-                                                          const float* __restrict__ weights, int32_t K, int64_t H,
-                                                          OT* __restrict__ out, int64_t ldo, int64_t T, uint32_t tiles) {
-  constexpr int W = width<YT, OT>(), P = kTile / kThreads / W;
+__global__ __launch_bounds__(kMaxThreads) void combine_kernel(const YT* __restrict__ y, int32_t rows, int64_t ldy,
+                                                             const int32_t* __restrict__ slot,
+                                                             const float* __restrict__ weights, int32_t K, int64_t H,
+                                                             OT* __restrict__ out, int64_t ldo, int64_t T,
+                                                             uint32_t tiles) {
+  constexpr int W = width<YT, OT>(), P = kCols / W;
+  const int step = blockDim.x * W;
   for (int64_t u = blockIdx.x; u < T * tiles; u += gridDim.x) {
     const int64_t t = u / tiles;
-    const int64_t h0 = (u - t * tiles) * kTile + threadIdx.x * W;
+    const int64_t h0 = (u - t * tiles) * (P * step) + threadIdx.x * W;
     float acc[P][W] = {};
     for (int k0 = 0; k0 < K; k0 += kRows) {
-      const Rows r = token_rows(slot, weights, t, K, k0, rows);
-      if (h0 + (P - 1) * kThreads * W + W <= H) {
-        Raw<YT, W> v[kRows][P];
+      const Rows<kRows> r = token_rows<kRows>(slot, weights, t, K, k0, rows);
+      Raw<YT, W> v[kRows][P];
 #pragma unroll
-        for (int j = 0; j < kRows; j++)
-          if (r.row[j] >= 0)
+      for (int j = 0; j < kRows; j++)
+        if (r.row[j] >= 0)
 #pragma unroll
-            for (int p = 0; p < P; p++) v[j][p] = load_raw<W, kNT>(y + r.row[j] * ldy + h0 + p * kThreads * W);
+          for (int p = 0; p < P; p++)
+            if (h0 + p * step + W <= H) v[j][p] = load_raw<W, true>(y + r.row[j] * ldy + h0 + p * step);
 #pragma unroll
-        for (int j = 0; j < kRows; j++)
-          if (r.row[j] >= 0)
+      for (int j = 0; j < kRows; j++)
+        if (r.row[j] >= 0)
 #pragma unroll
-            for (int p = 0; p < P; p++) {
-              float f[W];
+          for (int p = 0; p < P; p++) {
+            const int64_t h = h0 + p * step;
+            float f[W];
+            if (h + W <= H)
               unpack(v[j][p], f);
+            else
+              load_some<W>(y + r.row[j] * ldy + h, (int)max(H - h, (int64_t)0), f);
 #pragma unroll
-              for (int i = 0; i < W; i++) acc[p][i] += r.w[j] * f[i];
-            }
-      } else {
-#pragma unroll
-        for (int p = 0; p < P; p++) {
-          const int64_t h = h0 + p * kThreads * W;
-          const int n = (int)min((int64_t)W, H - h);
-          if (n > 0)
-#pragma unroll
-            for (int j = 0; j < kRows; j++)
-              if (r.row[j] >= 0) {
-                float f[W];
-                load_some<W>(y + r.row[j] * ldy + h, n, f);
-#pragma unroll
-                for (int i = 0; i < W; i++) acc[p][i] += r.w[j] * f[i];
-              }
-        }
-      }
+            for (int i = 0; i < W; i++) acc[p][i] += r.w[j] * f[i];
+          }
     }
 #pragma unroll
     for (int p = 0; p < P; p++) {
-      const int64_t h = h0 + p * kThreads * W;
-      const int n = (int)min((int64_t)W, H - h);
-      if (n == W)
-        store_vec<W, kNT>(out + t * ldo + h, acc[p]);
-      else if (n > 0)
-        store_some<W>(out + t * ldo + h, n, acc[p]);
+      const int64_t h = h0 + p * step;
+      if (h + W <= H)
+        store_vec<W, true>(out + t * ldo + h, acc[p]);
+      else
+        store_some<W>(out + t * ldo + h, (int)max(H - h, (int64_t)0), acc[p]);
     }
   }
 }
 
-// kRows columns of sums over the workgroup; the result is in the first thread
-__device__ __forceinline__ void block_sums(float (&s)[kRows], float (*part)[kRows]) {
-#pragma unroll
-  for (int j = 0; j < kRows; j++)
-#pragma unroll
-    for (int o = 32; o; o >>= 1) s[j] += __shfl_xor(s[j], o);
-  const int wave = threadIdx.x / kWave;
-  if ((threadIdx.x & (kWave - 1)) == 0)
-#pragma unroll
-    for (int j = 0; j < kRows; j++) part[wave][j] = s[j];
-}
-
-// DW: with the gradient of the weights, a token per workgroup; else a tile per workgroup
+// DW: with the gradient of the weights, whose dot products need a whole token per
+// workgroup; else a tile per workgroup.
 template <typename DT, typename YT, typename GT, bool DW>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(
+__global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const DT* __restrict__ dout, int64_t ldd, const YT* __restrict__ y, int32_t rows, int64_t ldy,
     const int32_t* __restrict__ slot, const float* __restrict__ weights, int32_t K, int64_t H, GT* __restrict__ dy,
     int64_t lddy, float* __restrict__ dweights, int64_t T, uint32_t tiles) {
-  __shared__ float part[kThreads / kWave][kRows];
-  constexpr int W = width<DT, YT>(), P = kTile / kThreads / W;  // dy's type has no part in the order of the dot products
+  constexpr int N = kRowsBackward;
+  constexpr int W = width<DT, YT>(), P = kCols / W;  // dy's type has no part in the order of the dot products
+  __shared__ float part[kMaxThreads / kWave][N];
+  const int step = blockDim.x * W;
   const int64_t units = DW ? T : T * tiles;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t t = DW ? u : u / tiles;
-    const int64_t h0 = DW ? 0 : (u - t * tiles) * kTile, h1 = DW ? H : min(H, h0 + kTile);
-    for (int k0 = 0; k0 < K; k0 += kRows) {
-      const Rows r = token_rows(slot, weights, t, K, k0, rows);
-      float dot[kRows] = {};
-      for (int64_t hb = h0 + threadIdx.x * W; hb < h1; hb += kTile) {
-        if (hb + (P - 1) * kThreads * W + W <= H) {
+    const int64_t h0 = DW ? 0 : (u - t * tiles) * (P * step), h1 = DW ? H : min(H, h0 + P * step);
+    for (int k0 = 0; k0 < K; k0 += N) {
+      const Rows<N> r = token_rows<N>(slot, weights, t, K, k0, rows);
+      float dot[N] = {};
+      for (int64_t hb = h0 + threadIdx.x * W; hb < h1; hb += P * step) {
+        auto move = [&](auto inside) {
+          auto whole = [&](int p) { return inside || hb + p * step + W <= H; };
+          auto left = [&](int p) { return (int)max(H - hb - p * step, (int64_t)0); };
           Raw<DT, W> dr[P];
-          Raw<YT, W> v[kRows][P];
+          Raw<YT, W> v[N][P];
 #pragma unroll
-          for (int p = 0; p < P; p++) dr[p] = load_raw<W, false>(dout + t * ldd + hb + p * kThreads * W);
+          for (int p = 0; p < P; p++)
+            if (whole(p)) dr[p] = load_raw<W, false>(dout + t * ldd + hb + p * step);
           if (DW)
 #pragma unroll
-            for (int j = 0; j < kRows; j++)
+            for (int j = 0; j < N; j++)
               if (r.row[j] >= 0)
 #pragma unroll
-                for (int p = 0; p < P; p++) v[j][p] = load_raw<W, kNT>(y + r.row[j] * ldy + hb + p * kThreads * W);
+                for (int p = 0; p < P; p++)
+                  if (whole(p)) v[j][p] = load_raw<W, true>(y + r.row[j] * ldy + hb + p * step);
+          float d[P][W];
 #pragma unroll
-          for (int j = 0; j < kRows; j++)
+          for (int p = 0; p < P; p++) {
+            if (whole(p))
+              unpack(dr[p], d[p]);
+            else
+              load_some<W>(dout + t * ldd + hb + p * step, left(p), d[p]);
+          }
+#pragma unroll
+          for (int j = 0; j < N; j++)
             if (r.row[j] >= 0)
 #pragma unroll
               for (int p = 0; p < P; p++) {
-                float d[W], f[W];
-                unpack(dr[p], d);
+                const int64_t h = hb + p * step;
+                float f[W];
                 if (DW) {
-                  unpack(v[j][p], f);
+                  if (whole(p))
+                    unpack(v[j][p], f);
+                  else
+                    load_some<W>(y + r.row[j] * ldy + h, left(p), f);
 #pragma unroll
-                  for (int i = 0; i < W; i++) dot[j] += d[i] * f[i];
+                  for (int i = 0; i < W; i++) dot[j] += d[p][i] * f[i];
                 }
                 if (dy) {
 #pragma unroll
-                  for (int i = 0; i < W; i++) d[i] *= r.w[j];
-                  store_vec<W, kNT>(dy + r.row[j] * lddy + hb + p * kThreads * W, d);
+                  for (int i = 0; i < W; i++) f[i] = d[p][i] * r.w[j];
+                  if (whole(p))
+                    store_vec<W, true>(dy + r.row[j] * lddy + h, f);
+                  else
+                    store_some<W>(dy + r.row[j] * lddy + h, left(p), f);
                 }
               }
-        } else {
-#pragma unroll
-          for (int p = 0; p < P; p++) {
-            const int64_t h = hb + p * kThreads * W;
-            const int n = (int)min((int64_t)W, H - h);
-            if (n <= 0) continue;
-#pragma unroll
-            for (int j = 0; j < kRows; j++)
-              if (r.row[j] >= 0) {
-                float d[W], f[W];
-                load_some<W>(dout + t * ldd + h, n, d);
-                if (DW) {
-                  load_some<W>(y + r.row[j] * ldy + h, n, f);
-#pragma unroll
-                  for (int i = 0; i < W; i++) dot[j] += d[i] * f[i];
-                }
-                if (dy) {
-#pragma unroll
-                  for (int i = 0; i < W; i++) d[i] *= r.w[j];
-                  store_some<W>(dy + r.row[j] * lddy + h, n, d);
-                }
-              }
-          }
-        }
+        };
+        if (hb + (P - 1) * step + W <= H)
+          move(std::true_type{});
+        else
+          move(std::false_type{});
       }
-      if (DW) {
-        block_sums(dot, part);
-        __syncthreads();
-        if (threadIdx.x < kRows && k0 + (int)threadIdx.x < K) {
-          float s = 0.f;
+      if (DW) {  // sums over the workgroup, always in the same order
 #pragma unroll
-          for (int w = 0; w < kThreads / kWave; w++) s += part[w][threadIdx.x];
+        for (int j = 0; j < N; j++)
+#pragma unroll
+          for (int o = 32; o; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
+        if ((threadIdx.x & (kWave - 1)) == 0)
+#pragma unroll
+          for (int j = 0; j < N; j++) part[threadIdx.x / kWave][j] = dot[j];
+        __syncthreads();
+        if (threadIdx.x < N && k0 + (int)threadIdx.x < K) {
+          float s = 0.f;
+          for (int w = 0; w < (int)blockDim.x / kWave; w++) s += part[w][threadIdx.x];
           dweights[t * K + k0 + threadIdx.x] = s;
         }
         __syncthreads();
@@ -231,14 +221,27 @@ mxq_status check_pairs(const char* what, const int32_t* slot, const float* weigh
   return MXQ_OK;
 }
 
-uint32_t tiles_of(int64_t H) { return (uint32_t)((H + kTile - 1) / kTile); }
+// Tiles of a row and threads of a workgroup.  As few tiles as up to 512 threads
+// allow (16384 x 8 x 4096 fp32 rows: 372 us with 512, 385 with 256 and two
+// tiles), then as few whole waves as the tiles need, so that most threads have
+// all their columns inside the row.  Few tokens: half as large, to reach more CUs.
+struct Shape {
+  unsigned threads;
+  uint32_t tiles;
+};
+Shape shape_of(int64_t T, int64_t H) {
+  const int64_t most = T >= 256 ? kMaxThreads : kMaxThreads / 2;
+  const int64_t tiles = (H + most * kCols - 1) / (most * kCols);
+  const int64_t waves = (H + tiles * kWave * kCols - 1) / (tiles * kWave * kCols);
+  return {(unsigned)waves * kWave, (uint32_t)tiles};
+}
 
 template <typename YT, typename OT>
 hipError_t combine(const void* y, int64_t rows, int64_t ldy, const int32_t* slot, const float* weights, int64_t T,
                    int32_t K, int64_t H, void* out, int64_t ldo, hipStream_t st) {
-  const uint32_t tiles = tiles_of(H);
-  combine_kernel<<<grid_of(T * tiles), kThreads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (OT*)out,
-                                                         ldo, T, tiles);
+  const Shape s = shape_of(T, H);
+  combine_kernel<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (OT*)out,
+                                                         ldo, T, s.tiles);
   return hipGetLastError();
 }
 
@@ -246,13 +249,13 @@ template <typename DT, typename YT, typename GT>
 hipError_t combine_backward(const void* dout, int64_t ldd, const void* y, int64_t ldy, const int32_t* slot,
                             const float* weights, int64_t T, int32_t K, int64_t H, int64_t rows, void* dy,
                             int64_t lddy, float* dweights, hipStream_t st) {
-  const uint32_t tiles = tiles_of(H);
+  const Shape s = shape_of(T, H);
   if (dweights)
-    combine_backward_kernel<DT, YT, GT, true><<<grid_of(T), kThreads, 0, st>>>(
-        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, tiles);
+    combine_backward_kernel<DT, YT, GT, true><<<grid_of(T), s.threads, 0, st>>>(
+        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, s.tiles);
   else
-    combine_backward_kernel<DT, YT, GT, false><<<grid_of(T * tiles), kThreads, 0, st>>>(
-        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, tiles);
+    combine_backward_kernel<DT, YT, GT, false><<<grid_of(T * s.tiles), s.threads, 0, st>>>(
+        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, s.tiles);
   return hipGetLastError();
 }
 
