@@ -426,7 +426,7 @@ mxq_status mxq_route_backward(const void* logits, mxq_dtype dt, int64_t T, int32
  * outside [0, rows) take no part; a token with none gets zeros), weights fp32
  * [T][top_k] or NULL for 1 (then also the gradient of a dispatch), out
  * [T][H] (row stride ldo).  Sums in fp32 in the order of k, rounded once.
- * top_k <= MXQ_MAX_TOPK, rows < 2^31. */
+ * top_k <= MXQ_MAX_TOPK, T and rows < 2^31, H < 2^29. */
 mxq_status mxq_combine(const void* y, mxq_dtype ydt, int64_t rows, int64_t ldy, const int32_t* slot,
                        const float* weights, int64_t T, int32_t top_k, int64_t H, void* out, mxq_dtype odt,
                        int64_t ldo, hipStream_t st);

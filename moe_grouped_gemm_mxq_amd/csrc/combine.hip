@@ -6,8 +6,6 @@
 // a tile of its columns (the gradient's dot products need the whole token, so
 // there it walks the tiles), a thread eight consecutive columns, and the loads
 // of up to kRows rows are issued before the first of them is used.
-#include <type_traits>
-
 #include "mxq_device.h"
 #include "mxq_host.h"
 #include "mxq_vec.h"
@@ -28,10 +26,14 @@ constexpr int kRows = 8, kRowsBackward = 4;
 // (a grid has fewer than 2^32 threads); the kernels walk the rest
 unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 22) ? units : 1 << 22); }
 
-// Rows k0 .. k0 + N - 1 of a token (uniform over the workgroup); -1: none
+// Rows k0 .. k0 + N - 1 of a token, uniform over the workgroup.  in[j]: pair k0 + j
+// exists and names a row; where it does not, row[j] is one that the token reads
+// anyway (or row 0), so that the loads need no branch between them: with one, each
+// load was waited for before the next.
 template <int N>
 struct Rows {
   int32_t row[N];
+  bool in[N];
   float w[N];
 };
 template <int N>
@@ -39,147 +41,126 @@ __device__ __forceinline__ Rows<N> token_rows(const int32_t* __restrict__ slot, 
                                               int64_t t, int K, int k0, int32_t rows) {
   Rows<N> r;
 #pragma unroll
+  for (int j = 0; j < N; j++) r.row[j] = slot[t * K + min(k0 + j, K - 1)];
+#pragma unroll
+  for (int j = 0; j < N; j++) r.w[j] = weights ? weights[t * K + min(k0 + j, K - 1)] : 1.f;
+  int32_t some = 0;
+#pragma unroll
   for (int j = 0; j < N; j++) {
-    r.row[j] = -1;
-    r.w[j] = 1.f;
-    if (k0 + j < K) {
-      const int32_t s = slot[t * K + k0 + j];
-      r.row[j] = s < 0 || s >= rows ? -1 : s;
-      if (weights) r.w[j] = weights[t * K + k0 + j];
-    }
+    r.in[j] = k0 + j < K && r.row[j] >= 0 && r.row[j] < rows;
+    some = r.in[j] ? r.row[j] : some;
+    r.row[j] = some;
   }
   return r;
 }
 
-// A thread's columns lie in kCols / W pieces of W, piece p at p * blockDim.x * W, so
+// A thread's columns lie in P = kCols / W pieces of W, piece p at p * blockDim.x * W, so
 // that each load of a wave is one unbroken run of 16 bytes a lane for fp32 (W = 4)
 // and for bf16 alone (W = 8), 8 for bf16 beside fp32 (W = 4).  (Eight fp32
 // columns as two loads 32 bytes apart from lane to lane measured 5.1 against
-// 5.9 TB/s.)  Only the row's last piece can be a part of W columns: it is
-// taken one column at a time.
-template <typename A, typename B>
-constexpr int width() {
-  return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4;
+// 5.9 TB/s.)  A piece that would pass the row's end moves back to it; the columns
+// it then shares with its neighbour are written twice with one value and counted
+// once.  Rows shorter than a piece take W = 1.
+constexpr int width(size_t a, size_t b) { return a == 2 && b == 2 ? 8 : 4; }
+
+// element h of a row whose address is the same for the whole workgroup (H < 2^29: 32-bit byte offsets)
+template <typename T>
+__device__ __forceinline__ T* at(T* row, uint32_t h) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(row) + h * (uint32_t)sizeof(T));
 }
 
-template <typename YT, typename OT>
+template <typename YT, typename OT, int W, int N>
 __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const YT* __restrict__ y, int32_t rows, int64_t ldy,
                                                              const int32_t* __restrict__ slot,
-                                                             const float* __restrict__ weights, int32_t K, int64_t H,
+                                                             const float* __restrict__ weights, int32_t K, uint32_t H,
                                                              OT* __restrict__ out, int64_t ldo, int64_t T,
                                                              uint32_t tiles) {
-  constexpr int W = width<YT, OT>(), P = kCols / W;
-  const int step = blockDim.x * W;
+  constexpr int P = kCols / W;
+  const uint32_t step = blockDim.x * W;
   for (int64_t u = blockIdx.x; u < T * tiles; u += gridDim.x) {
     const int64_t t = u / tiles;
-    const int64_t h0 = (u - t * tiles) * (P * step) + threadIdx.x * W;
+    const uint32_t h0 = (uint32_t)(u - t * tiles) * (P * step) + threadIdx.x * W;
+    uint32_t h[P];
+#pragma unroll
+    for (int p = 0; p < P; p++) h[p] = min(h0 + p * step, H - W);
     float acc[P][W] = {};
-    for (int k0 = 0; k0 < K; k0 += kRows) {
-      const Rows<kRows> r = token_rows<kRows>(slot, weights, t, K, k0, rows);
-      Raw<YT, W> v[kRows][P];
+    if (rows > 0)
+      for (int k0 = 0; k0 < K; k0 += N) {
+        const Rows<N> r = token_rows<N>(slot, weights, t, K, k0, rows);
+        Raw<YT, W> v[N][P];
 #pragma unroll
-      for (int j = 0; j < kRows; j++)
-        if (r.row[j] >= 0)
+        for (int j = 0; j < N; j++)
 #pragma unroll
-          for (int p = 0; p < P; p++)
-            if (h0 + p * step + W <= H) v[j][p] = load_raw<W, true>(y + r.row[j] * ldy + h0 + p * step);
+          for (int p = 0; p < P; p++) v[j][p] = load_raw<W, true>(at(y + r.row[j] * ldy, h[p]));
 #pragma unroll
-      for (int j = 0; j < kRows; j++)
-        if (r.row[j] >= 0)
+        for (int j = 0; j < N; j++)
+          if (r.in[j])
 #pragma unroll
-          for (int p = 0; p < P; p++) {
-            const int64_t h = h0 + p * step;
-            float f[W];
-            if (h + W <= H)
+            for (int p = 0; p < P; p++) {
+              float f[W];
               unpack(v[j][p], f);
-            else
-              load_some<W>(y + r.row[j] * ldy + h, (int)max(H - h, (int64_t)0), f);
 #pragma unroll
-            for (int i = 0; i < W; i++) acc[p][i] += r.w[j] * f[i];
-          }
-    }
+              for (int i = 0; i < W; i++) acc[p][i] += r.w[j] * f[i];
+            }
+      }
 #pragma unroll
-    for (int p = 0; p < P; p++) {
-      const int64_t h = h0 + p * step;
-      if (h + W <= H)
-        store_vec<W, true>(out + t * ldo + h, acc[p]);
-      else
-        store_some<W>(out + t * ldo + h, (int)max(H - h, (int64_t)0), acc[p]);
-    }
+    for (int p = 0; p < P; p++)
+      if (h0 + p * step < H) store_vec<W, true>(at(out + t * ldo, h[p]), acc[p]);
   }
 }
 
 // DW: with the gradient of the weights, whose dot products need a whole token per
 // workgroup; else a tile per workgroup.
-template <typename DT, typename YT, typename GT, bool DW>
+template <typename DT, typename YT, typename GT, int W, int N, bool DW>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const DT* __restrict__ dout, int64_t ldd, const YT* __restrict__ y, int32_t rows, int64_t ldy,
-    const int32_t* __restrict__ slot, const float* __restrict__ weights, int32_t K, int64_t H, GT* __restrict__ dy,
+    const int32_t* __restrict__ slot, const float* __restrict__ weights, int32_t K, uint32_t H, GT* __restrict__ dy,
     int64_t lddy, float* __restrict__ dweights, int64_t T, uint32_t tiles) {
-  constexpr int N = kRowsBackward;
-  constexpr int W = width<DT, YT>(), P = kCols / W;  // dy's type has no part in the order of the dot products
+  constexpr int P = kCols / W;
   __shared__ float part[kMaxThreads / kWave][N];
-  const int step = blockDim.x * W;
+  const uint32_t step = blockDim.x * W;
   const int64_t units = DW ? T : T * tiles;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t t = DW ? u : u / tiles;
-    const int64_t h0 = DW ? 0 : (u - t * tiles) * (P * step), h1 = DW ? H : min(H, h0 + P * step);
+    const uint32_t first = DW ? 0 : (uint32_t)(u - t * tiles) * (P * step), last = DW ? H : min(H, first + P * step);
     for (int k0 = 0; k0 < K; k0 += N) {
       const Rows<N> r = token_rows<N>(slot, weights, t, K, k0, rows);
       float dot[N] = {};
-      for (int64_t hb = h0 + threadIdx.x * W; hb < h1; hb += P * step) {
-        auto move = [&](auto inside) {
-          auto whole = [&](int p) { return inside || hb + p * step + W <= H; };
-          auto left = [&](int p) { return (int)max(H - hb - p * step, (int64_t)0); };
-          Raw<DT, W> dr[P];
-          Raw<YT, W> v[N][P];
+      if (rows > 0)
+      for (uint32_t h0 = first + threadIdx.x * W; h0 < last; h0 += P * step) {
+        uint32_t h[P];
 #pragma unroll
-          for (int p = 0; p < P; p++)
-            if (whole(p)) dr[p] = load_raw<W, false>(dout + t * ldd + hb + p * step);
-          if (DW)
+        for (int p = 0; p < P; p++) h[p] = min(h0 + p * step, H - W);
+        Raw<DT, W> dr[P];
+        Raw<YT, W> v[N][P];
 #pragma unroll
-            for (int j = 0; j < N; j++)
-              if (r.row[j] >= 0)
-#pragma unroll
-                for (int p = 0; p < P; p++)
-                  if (whole(p)) v[j][p] = load_raw<W, true>(y + r.row[j] * ldy + hb + p * step);
-          float d[P][W];
-#pragma unroll
-          for (int p = 0; p < P; p++) {
-            if (whole(p))
-              unpack(dr[p], d[p]);
-            else
-              load_some<W>(dout + t * ldd + hb + p * step, left(p), d[p]);
-          }
+        for (int p = 0; p < P; p++) dr[p] = load_raw<W, false>(at(dout + t * ldd, h[p]));
+        if (DW)
 #pragma unroll
           for (int j = 0; j < N; j++)
-            if (r.row[j] >= 0)
 #pragma unroll
-              for (int p = 0; p < P; p++) {
-                const int64_t h = hb + p * step;
-                float f[W];
-                if (DW) {
-                  if (whole(p))
-                    unpack(v[j][p], f);
-                  else
-                    load_some<W>(y + r.row[j] * ldy + h, left(p), f);
+            for (int p = 0; p < P; p++) v[j][p] = load_raw<W, true>(at(y + r.row[j] * ldy, h[p]));
+        float d[P][W];
 #pragma unroll
-                  for (int i = 0; i < W; i++) dot[j] += d[p][i] * f[i];
-                }
-                if (dy) {
+        for (int p = 0; p < P; p++) unpack(dr[p], d[p]);
 #pragma unroll
-                  for (int i = 0; i < W; i++) f[i] = d[p][i] * r.w[j];
-                  if (whole(p))
-                    store_vec<W, true>(dy + r.row[j] * lddy + h, f);
-                  else
-                    store_some<W>(dy + r.row[j] * lddy + h, left(p), f);
-                }
+        for (int j = 0; j < N; j++)
+          if (r.in[j])
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+              float f[W];
+              if (DW) {
+                unpack(v[j][p], f);
+#pragma unroll
+                for (int i = 0; i < W; i++)
+                  if (h[p] + i >= h0 + p * step) dot[j] += d[p][i] * f[i];
               }
-        };
-        if (hb + (P - 1) * step + W <= H)
-          move(std::true_type{});
-        else
-          move(std::false_type{});
+              if (dy && h0 + p * step < H) {
+#pragma unroll
+                for (int i = 0; i < W; i++) f[i] = d[p][i] * r.w[j];
+                store_vec<W, true>(at(dy + r.row[j] * lddy, h[p]), f);
+              }
+            }
       }
       if (DW) {  // sums over the workgroup, always in the same order
 #pragma unroll
@@ -214,7 +195,7 @@ mxq_status check_pairs(const char* what, const int32_t* slot, const float* weigh
                        int64_t rows) {
   MXQ_REQUIRE(T >= 0 && T <= INT32_MAX, "%s: T must be in [0, 2^31)", what);
   MXQ_REQUIRE(rows >= 0 && rows <= INT32_MAX, "%s: rows must be in [0, 2^31)", what);
-  MXQ_REQUIRE(H >= 1 && H <= INT32_MAX, "%s: H must be in [1, 2^31)", what);
+  MXQ_REQUIRE(H >= 1 && H < (1 << 29), "%s: H must be in [1, 2^29)", what);
   MXQ_REQUIRE(K >= 1 && K <= MXQ_MAX_TOPK, "%s: top_k must be in [1, %d] (got %d)", what, MXQ_MAX_TOPK, K);
   MXQ_REQUIRE(slot != nullptr || T == 0, "%s: slot is NULL", what);
   MXQ_REQUIRE(aligned_to(slot, 4) && aligned_to(weights, 4), "%s: slot and weights must be 4-byte aligned", what);
@@ -240,8 +221,13 @@ template <typename YT, typename OT>
 hipError_t combine(const void* y, int64_t rows, int64_t ldy, const int32_t* slot, const float* weights, int64_t T,
                    int32_t K, int64_t H, void* out, int64_t ldo, hipStream_t st) {
   const Shape s = shape_of(T, H);
-  combine_kernel<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (OT*)out,
-                                                         ldo, T, s.tiles);
+  constexpr int W = width(sizeof(YT), sizeof(OT));
+  auto f = H < W    ? combine_kernel<YT, OT, 1, 2>
+           : K <= 2 ? combine_kernel<YT, OT, W, 2>
+           : K <= 4 ? combine_kernel<YT, OT, W, 4>
+                    : combine_kernel<YT, OT, W, kRows>;
+  f<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, (uint32_t)H, (OT*)out, ldo, T,
+                                                s.tiles);
   return hipGetLastError();
 }
 
@@ -250,12 +236,15 @@ hipError_t combine_backward(const void* dout, int64_t ldd, const void* y, int64_
                             const float* weights, int64_t T, int32_t K, int64_t H, int64_t rows, void* dy,
                             int64_t lddy, float* dweights, hipStream_t st) {
   const Shape s = shape_of(T, H);
-  if (dweights)
-    combine_backward_kernel<DT, YT, GT, true><<<grid_of(T), s.threads, 0, st>>>(
-        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, s.tiles);
-  else
-    combine_backward_kernel<DT, YT, GT, false><<<grid_of(T * s.tiles), s.threads, 0, st>>>(
-        (const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot, weights, K, H, (GT*)dy, lddy, dweights, T, s.tiles);
+  // dy's type has no part in W, hence none in the order of the dot products
+  constexpr int W = width(sizeof(DT), sizeof(YT));
+  auto f = dweights ? (H < W    ? combine_backward_kernel<DT, YT, GT, 1, 2, true>
+                       : K <= 2 ? combine_backward_kernel<DT, YT, GT, W, 2, true>
+                                : combine_backward_kernel<DT, YT, GT, W, kRowsBackward, true>)
+                    : (H < W ? combine_backward_kernel<DT, YT, GT, 1, kRowsBackward, false>
+                             : combine_backward_kernel<DT, YT, GT, W, kRowsBackward, false>);
+  f<<<grid_of(dweights ? T : T * s.tiles), s.threads, 0, st>>>((const DT*)dout, ldd, (const YT*)y, (int32_t)rows, ldy, slot,
+                                                              weights, K, (uint32_t)H, (GT*)dy, lddy, dweights, T, s.tiles);
   return hipGetLastError();
 }
 

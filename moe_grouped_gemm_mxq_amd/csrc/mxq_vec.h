@@ -25,10 +25,14 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
 __device__ __forceinline__ void store_f(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void store_f(uint16_t* p, int64_t i, float v) { p[i] = bf16_of(v); }
 
-// W consecutive elements as they lie in memory: fp32 four at a time, bf16 four
-// or eight (8 or 16 bytes, one instruction).
+// W consecutive elements as they lie in memory, one instruction's worth: fp32
+// one or four at a time, bf16 one, four or eight.
 template <typename T, int W>
 struct Raw;
+template <typename T>
+struct Raw<T, 1> {
+  T a;
+};
 template <>
 struct Raw<float, 4> {
   u32x4 a;
@@ -43,6 +47,10 @@ struct Raw<uint16_t, 8> {
 };
 template <typename T, int W>
 struct RawPtr;
+template <typename T>
+struct RawPtr<T, 1> {
+  typedef T type;
+};
 template <>
 struct RawPtr<float, 4> {
   typedef u32x4_any type;
@@ -68,6 +76,8 @@ __device__ __forceinline__ void unpack(const Raw<float, 4>& r, float* f) {
 #pragma unroll
   for (int j = 0; j < 4; j++) f[j] = __uint_as_float(r.a[j]);
 }
+__device__ __forceinline__ void unpack(const Raw<float, 1>& r, float* f) { f[0] = r.a; }
+__device__ __forceinline__ void unpack(const Raw<uint16_t, 1>& r, float* f) { f[0] = __uint_as_float((uint32_t)r.a << 16); }
 template <int W>
 __device__ __forceinline__ void unpack(const Raw<uint16_t, W>& r, float* f) {
 #pragma unroll
@@ -79,6 +89,10 @@ __device__ __forceinline__ void unpack(const Raw<uint16_t, W>& r, float* f) {
 
 template <int W, bool NT>
 __device__ __forceinline__ void store_vec(float* p, const float* f) {
+  if constexpr (W == 1) {
+    *p = f[0];
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < W / 4; k++) {
     u32x4 a;
@@ -93,27 +107,18 @@ __device__ __forceinline__ void store_vec(float* p, const float* f) {
 }
 template <int W, bool NT>
 __device__ __forceinline__ void store_vec(uint16_t* p, const float* f) {
-  Raw<uint16_t, W> r;
+  if constexpr (W == 1) {
+    *p = bf16_of(f[0]);
+  } else {
+    Raw<uint16_t, W> r;
 #pragma unroll
-  for (int j = 0; j < W / 2; j++) r.a[j] = bf16x2_of(f[2 * j], f[2 * j + 1]);
-  typename RawPtr<uint16_t, W>::type* q = reinterpret_cast<typename RawPtr<uint16_t, W>::type*>(p);
-  if (NT)
-    __builtin_nontemporal_store(r.a, q);
-  else
-    *q = r.a;
-}
-
-// the first n (0 .. W) of W elements, zeros after them
-template <int W, typename T>
-__device__ __forceinline__ void load_some(const T* p, int n, float* f) {
-#pragma unroll
-  for (int j = 0; j < W; j++) f[j] = j < n ? load_f(p, j) : 0.f;
-}
-template <int W, typename T>
-__device__ __forceinline__ void store_some(T* p, int n, const float* f) {
-#pragma unroll
-  for (int j = 0; j < W; j++)
-    if (j < n) store_f(p, j, f[j]);
+    for (int j = 0; j < W / 2; j++) r.a[j] = bf16x2_of(f[2 * j], f[2 * j + 1]);
+    typename RawPtr<uint16_t, W>::type* q = reinterpret_cast<typename RawPtr<uint16_t, W>::type*>(p);
+    if (NT)
+      __builtin_nontemporal_store(r.a, q);
+    else
+      *q = r.a;
+  }
 }
 
 }  // namespace mxq
