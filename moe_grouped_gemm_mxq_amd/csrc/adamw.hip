@@ -4,15 +4,19 @@
 
 #include "mxq_device.h"
 #include "mxq_host.h"
+#include "mxq_vec.h"
 
 namespace mxq {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;   // elements per workgroup, a multiple of the 32-element blocks
-constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
+constexpr int kTile = 4096;    // elements of a workgroup's pass
+constexpr int kPieces = kTile / (4 * kThreads);
 constexpr int kTensors = 40;   // per launch: the descriptors travel as a kernel argument (< 4 KB)
+static_assert(kTensors <= 64, "a wave looks its workgroup's tensor up, a tensor per lane");
+constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
+constexpr int64_t kMaxElements = kMaxGrid * kTile;
 
 struct Tensor {
   void* p;
@@ -39,16 +43,11 @@ struct Hyper {
 struct Args {
   Tensor t[kTensors];
   int32_t count;
+  int32_t chunk;  // elements of a workgroup, a multiple of kTile
   Hyper h;
   double log2_b1, log2_b2;
   const mxq_adamw_control* control;
 };
-
-__device__ __forceinline__ float load_f(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load_f(const uint16_t* p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
-__device__ __forceinline__ uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-__device__ __forceinline__ void store_f(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store_f(uint16_t* p, int64_t i, float v) { p[i] = bf16_of(v); }
 
 // ------------------------------------------------------------------ random bits
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -77,10 +76,14 @@ __device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t u16) {
   return (b + (u16 << 4) + 8u) >> 20;
 }
 
-__device__ __forceinline__ float e4m3_decode(uint32_t c) {
-  if ((c & 0x7F) == 0x7F) return NAN;
-  const float a = __uint_as_float((c & 0x7F) << 20) * 0x1p120f;
-  return c & 0x80 ? -a : a;
+// four codes times their scale; 0x7F and 0xFF are NaN
+__device__ __forceinline__ void e4m3_decode4(uint32_t c, float scale, float (&f)[4]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+  f[0] = lo[0] * scale;
+  f[1] = lo[1] * scale;
+  f[2] = hi[0] * scale;
+  f[3] = hi[1] * scale;
 }
 
 // scale byte of a block whose largest finite magnitude has these bits:
@@ -91,22 +94,180 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
   return e < 1 ? 1u : (uint32_t)e;
 }
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
-// 2^(127 - byte) by powf, which on this GPU is off by one step for some
-// exponents.  torch.ldexp and torch.pow take it the same way, so the states are
-// bit for bit those of this formula in torch operations; one step of the scaled
-// value changes a probability of rounding up by at most 2^-20.
-__device__ __forceinline__ float scale_inverse(uint32_t byte) { return powf(2.0f, 127.0f - (float)byte); }
 
-__device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-  return v;
+// largest of the eight lanes that hold a block
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  v = quad_max_u32(v);
+  return max(v, dpp_half_mirror(v));
 }
 
-// one element per lane, 32 lanes per block
+template <typename PT, typename GT, bool MX>
+struct Step {
+  PT* p;
+  const GT* g;
+  void *m, *v;
+  uint8_t *ms, *vs;
+  uint16_t* copy;
+  int64_t n;
+  float keep;
+  uint32_t key;
+
+  // Elements i0 + 1024 j + 4 threadIdx.x .. + 3 for j < kPieces.  INSIDE: all of them are
+  // elements of the tensor, so the loads are whole and need no branch between them.
+  template <bool INSIDE>
+  __device__ __forceinline__ void tile(int64_t i0, const Hyper& h, const float* inverse) const {
+#pragma clang fp contract(off)
+    float pr[kPieces][4], gr[kPieces][4], mr[kPieces][4], vr[kPieces][4];
+    uint32_t mc[kPieces], vc[kPieces], mb[kPieces], vb[kPieces];
+    Raw<PT, 4> pw[kPieces];
+    Raw<GT, 4> gw[kPieces];
+    Raw<float, 4> mw[kPieces], vw[kPieces];
+    int64_t at[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; j++) at[j] = i0 + j * 4 * kThreads + threadIdx.x * 4;
+    if constexpr (INSIDE) {
+#pragma unroll
+      for (int j = 0; j < kPieces; j++) {
+        const int64_t i = at[j];
+        gw[j] = load_raw<4, true>(g + i);
+        pw[j] = load_raw<4, true>(p + i);
+        if constexpr (MX) {
+          mc[j] = load_u32((const uint8_t*)m + i);
+          vc[j] = load_u32((const uint8_t*)v + i);
+          mb[j] = ms[i >> 5];
+          vb[j] = vs[i >> 5];
+        } else {
+          mw[j] = load_raw<4, true>((const float*)m + i);
+          vw[j] = load_raw<4, true>((const float*)v + i);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; j++) {
+        unpack(gw[j], gr[j]);
+        unpack(pw[j], pr[j]);
+        if constexpr (!MX) {
+          unpack(mw[j], mr[j]);
+          unpack(vw[j], vr[j]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPieces; j++) {
+        mc[j] = vc[j] = mb[j] = vb[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int64_t i = at[j] + k;
+          const bool in = i < n;
+          gr[j][k] = in ? load_f(g, i) : 0.f;
+          pr[j][k] = in ? load_f(p, i) : 0.f;
+          if constexpr (MX) {
+            mc[j] |= in ? (uint32_t)((const uint8_t*)m)[i] << (8 * k) : 0;
+            vc[j] |= in ? (uint32_t)((const uint8_t*)v)[i] << (8 * k) : 0;
+          } else {
+            mr[j][k] = in ? ((const float*)m)[i] : 0.f;
+            vr[j][k] = in ? ((const float*)v)[i] : 0.f;
+          }
+        }
+        if (MX && at[j] < n) {
+          mb[j] = ms[at[j] >> 5];
+          vb[j] = vs[at[j] >> 5];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; j++) {
+      const int64_t i = at[j];
+      if constexpr (MX) {
+        e4m3_decode4(mc[j], scale_value(mb[j]), mr[j]);
+        e4m3_decode4(vc[j], scale_value(vb[j]), vr[j]);
+#pragma unroll
+        for (int k = 0; k < 4; k++) vr[j][k] = vr[j][k] * vr[j][k];
+      }
+      float rr[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float gs = gr[j][k] * h.grad_scale;
+        mr[j][k] = mr[j][k] * h.b1 + gs * h.c1;
+        vr[j][k] = vr[j][k] * h.b2 + gs * h.c2 * gs;
+        rr[k] = sqrtf(vr[j][k]);
+        pr[j][k] = pr[j][k] * keep - h.alpha * (mr[j][k] / (rr[k] * h.rs + h.eps));
+      }
+      if constexpr (MX) {
+        uint32_t ma = 0, ra = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const uint32_t x = __float_as_uint(mr[j][k]) & 0x7FFFFFFFu, y = __float_as_uint(rr[k]);  // r >= 0 or NaN
+          ma = max(ma, x < 0x7F800000u ? x : 0u);
+          ra = max(ra, y < 0x7F800000u ? y : 0u);
+        }
+        mb[j] = scale_byte(block_max(ma));
+        vb[j] = scale_byte(block_max(ra));
+        const float mi = inverse[mb[j]], vi = inverse[vb[j]];
+        mc[j] = vc[j] = 0;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          const uint64_t bits = pair_bits(key, (i >> 1) + q);
+          const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32);
+          const uint32_t um[2] = {lo & 0xFFFFu, hi & 0xFFFFu}, ur[2] = {lo >> 16, (hi >> 8) & 0xFFFFu};
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int k = 2 * q + e;
+            const uint32_t mbits = __float_as_uint(mr[j][k]);
+            uint32_t x = e4m3_stochastic(__uint_as_float(mbits & 0x7FFFFFFFu) * mi, um[e]);
+            x = (mbits & 0x7FFFFFFFu) < 0x7F800000u ? x : 0x7Fu;
+            mc[j] |= (x | (mbits >> 31 << 7)) << (8 * k);
+            uint32_t y = e4m3_stochastic(rr[k] * vi, ur[e]);
+            y = rr[k] > 0.f ? max(y, 1u) : y;
+            y = __float_as_uint(rr[k]) < 0x7F800000u ? y : 0x7Fu;
+            vc[j] |= y << (8 * k);
+          }
+        }
+      }
+      if constexpr (INSIDE) {
+        store_vec<4, true>(p + i, pr[j]);
+        if (copy) store_vec<4, true>(copy + i, pr[j]);
+        if constexpr (MX) {
+          store_u32((uint8_t*)m + i, mc[j]);
+          store_u32((uint8_t*)v + i, vc[j]);
+        } else {
+          store_vec<4, true>((float*)m + i, mr[j]);
+          store_vec<4, true>((float*)v + i, vr[j]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (i + k < n) {
+            store_f(p, i + k, pr[j][k]);
+            if (copy) copy[i + k] = bf16_of(pr[j][k]);
+            if constexpr (MX) {
+              ((uint8_t*)m)[i + k] = (uint8_t)(mc[j] >> (8 * k));
+              ((uint8_t*)v)[i + k] = (uint8_t)(vc[j] >> (8 * k));
+            } else {
+              ((float*)m)[i + k] = mr[j][k];
+              ((float*)v)[i + k] = vr[j][k];
+            }
+          }
+      }
+      if (MX && (threadIdx.x & 7) == 0 && (INSIDE || i < n)) {
+        ms[i >> 5] = (uint8_t)mb[j];
+        vs[i >> 5] = (uint8_t)vb[j];
+      }
+    }
+  }
+
+  static __device__ __forceinline__ uint32_t load_u32(const uint8_t* q) {
+    typedef uint32_t u32_any __attribute__((aligned(1)));
+    return __builtin_nontemporal_load(reinterpret_cast<const u32_any*>(q));
+  }
+  static __device__ __forceinline__ void store_u32(uint8_t* q, uint32_t x) {
+    typedef uint32_t u32_any __attribute__((aligned(1)));
+    __builtin_nontemporal_store(x, reinterpret_cast<u32_any*>(q));
+  }
+};
+
 template <typename PT, typename GT, bool MX>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
-#pragma clang fp contract(off)
+  __shared__ float inverse[MX ? 256 : 1];
   Hyper h = a.h;
   if (a.control) {
     const mxq_adamw_control c = *a.control;
@@ -118,64 +279,26 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
     h.alpha = (float)(h.lr / (1.0 - exp2(c.step * a.log2_b1)));
   }
   if (!isfinite(h.grad_scale)) return;
-  int k = 0;
-  while (k + 1 < a.count && a.t[k + 1].first_wg <= blockIdx.x) k++;
-  const Tensor& t = a.t[k];
-  const int64_t begin = (int64_t)(blockIdx.x - t.first_wg) * kChunk;
-  const int64_t end = min(begin + kChunk, t.n);
-  const float keep = (float)(1.0 - h.lr * t.decay);
-  const uint32_t key = mix(h.key + 0xBB67AE85u * (t.index + 1));
-  PT* p = (PT*)t.p;
-  const GT* g = (const GT*)t.g;
-  for (int64_t i0 = begin; i0 < end; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool in = i < end;
-    float m = 0.f, v = 0.f, gr = 0.f, pr = 0.f;
-    if (in) {
-      gr = load_f(g, i) * h.grad_scale;
-      pr = load_f(p, i);
-      if constexpr (MX) {
-        m = e4m3_decode(((const uint8_t*)t.m)[i]) * scale_value(t.ms[i >> 5]);
-        const float r = e4m3_decode(((const uint8_t*)t.v)[i]) * scale_value(t.vs[i >> 5]);
-        v = r * r;
-      } else {
-        m = ((const float*)t.m)[i];
-        v = ((const float*)t.v)[i];
-      }
-    }
-    m = m * h.b1 + gr * h.c1;
-    v = v * h.b2 + gr * h.c2 * gr;
-    const float r = sqrtf(v);
-    pr = pr * keep - h.alpha * (m / (r * h.rs + h.eps));
-    if constexpr (MX) {
-      const uint32_t mb = __float_as_uint(m) & 0x7FFFFFFFu, rb = __float_as_uint(r) & 0x7FFFFFFFu;
-      const bool mf = mb < 0x7F800000u, rf = rb < 0x7F800000u;
-      const uint32_t mscale = scale_byte(half_wave_max(in && mf ? mb : 0));
-      const uint32_t rscale = scale_byte(half_wave_max(in && rf ? rb : 0));
-      if (in) {
-        const uint64_t bits = pair_bits(key, i >> 1);
-        const uint32_t um = (uint32_t)(bits >> (i & 1 ? 32 : 0)) & 0xFFFFu;
-        const uint32_t ur = (uint32_t)(bits >> (i & 1 ? 40 : 16)) & 0xFFFFu;
-        uint32_t mc = mf ? e4m3_stochastic(fabsf(m) * scale_inverse(mscale), um) : 0x7Fu;
-        mc |= (__float_as_uint(m) >> 24) & 0x80u;
-        uint32_t rc = rf ? e4m3_stochastic(r * scale_inverse(rscale), ur) : 0x7Fu;
-        if (rc == 0 && r > 0.f) rc = 1;
-        ((uint8_t*)t.m)[i] = (uint8_t)mc;
-        ((uint8_t*)t.v)[i] = (uint8_t)rc;
-        if ((i & 31) == 0) {
-          t.ms[i >> 5] = (uint8_t)mscale;
-          t.vs[i >> 5] = (uint8_t)rscale;
-        }
-      }
-    } else if (in) {
-      ((float*)t.m)[i] = m;
-      ((float*)t.v)[i] = v;
-    }
-    if (in) {
-      store_f(p, i, pr);
-      if (t.copy) t.copy[i] = bf16_of(pr);
-    }
+  // 2^(127 - byte) by powf, which on this GPU is off by one step for some
+  // exponents.  torch.ldexp and torch.pow take it the same way, so the states are
+  // bit for bit those of these formulas in torch operations; one step of the scaled
+  // value changes a probability of rounding up by at most 2^-20.
+  if constexpr (MX) {
+    static_assert(kThreads == 256, "one entry per thread");
+    inverse[threadIdx.x] = powf(2.0f, 127.0f - (float)threadIdx.x);
+    __syncthreads();
   }
+  const int lane = threadIdx.x & 63;
+  const bool before = lane < a.count && a.t[lane < a.count ? lane : 0].first_wg <= blockIdx.x;
+  const int k = __popcll(__ballot(before)) - 1;  // workgroups of the tensors follow one another
+  const Tensor& t = a.t[k];
+  const Step<PT, GT, MX> s = {(PT*)t.p, (const GT*)t.g, t.m, t.v, t.ms, t.vs, t.copy, t.n, (float)(1.0 - h.lr * t.decay),
+                              mix(h.key + 0xBB67AE85u * (t.index + 1))};
+  const int64_t begin = (int64_t)(blockIdx.x - t.first_wg) * a.chunk;
+  const int64_t end = min(begin + a.chunk, t.n);
+  int64_t i = begin;
+  for (; i + kTile <= end; i += kTile) s.template tile<true>(i, h, inverse);
+  if (i < end) s.template tile<false>(i, h, inverse);
 }
 
 template <typename PT, typename GT>
@@ -219,7 +342,7 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
     MXQ_REQUIRE(aligned_to(t.param, pa) && aligned_to(t.grad, ga) && aligned_to(t.copy, 2) &&
                     (mx || (aligned_to(t.m, 4) && aligned_to(t.v, 4))),
                 "mxq_adamw: tensor %d: a pointer is not aligned to its type", i);
-    MXQ_REQUIRE((t.n - 1) / kChunk < kMaxGrid, "mxq_adamw: tensor %d has too many elements", i);
+    MXQ_REQUIRE(t.n <= kMaxElements, "mxq_adamw: tensor %d has too many elements", i);
   }
   MXQ_REQUIRE_DEVICE();
   if (!control && !isfinite(cfg->grad_scale)) return ok();
@@ -239,18 +362,28 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
   a.h.key = cfg->seed + 0x9E3779B9u * (uint32_t)cfg->step;
   int32_t i = 0;
   while (i < n_tensors) {
+    int32_t end = i;  // the launch takes tensors i .. end - 1
+    int64_t tiles = 0;
+    for (int32_t count = 0; end < n_tensors && count < kTensors; end++) {
+      const int64_t w = (tensors[end].n + kTile - 1) / kTile;
+      if (tiles + w > kMaxGrid) break;
+      tiles += w;
+      count += w > 0;
+    }
+    // One tile per workgroup until the grid is many times the card; then longer
+    // runs, over which a workgroup's table and descriptors cost less.
+    a.chunk = kTile;
+    while (a.chunk < 16 * kTile && tiles * kTile / a.chunk > 16384) a.chunk *= 2;
     int64_t wgs = 0;
     a.count = 0;
-    for (; i < n_tensors && a.count < kTensors; i++) {
+    for (; i < end; i++) {
       const mxq_adamw_tensor& t = tensors[i];
       if (t.n == 0) continue;
-      const int64_t w = (t.n + kChunk - 1) / kChunk;
-      if (wgs + w > kMaxGrid) break;
       a.t[a.count++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, (uint16_t*)t.copy, t.n,
                         cfg->weight_decay * t.decay_scale, (uint32_t)wgs, (uint32_t)i};
-      wgs += w;
+      wgs += (t.n + a.chunk - 1) / a.chunk;
     }
-    if (a.count == 0) break;
+    if (a.count == 0) continue;
     const unsigned grid = (unsigned)wgs;
     if (param_dt == MXQ_DT_F32)
       grad_dt == MXQ_DT_F32 ? launch<float, float>(mx, grid, a, st) : launch<float, uint16_t>(mx, grid, a, st);
