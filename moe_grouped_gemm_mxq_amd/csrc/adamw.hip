@@ -2,6 +2,8 @@
 // states in fp32 or in MXFP8 blocks.
 #include <math.h>
 
+#include <type_traits>
+
 #include "mxq_device.h"
 #include "mxq_host.h"
 #include "mxq_vec.h"
@@ -76,23 +78,32 @@ __device__ __forceinline__ uint64_t pair_bits(uint32_t key, int64_t q) {
 }
 
 // ------------------------------------------------------------------ MXFP8 states
-// y >= 0, y <= 448, with 16 random bits -> E4M3 magnitude code.  Times 2^-120
-// an fp32 number's exponent field is the E4M3 one and its top three mantissa
-// bits the E4M3 mantissa, subnormals included, so adding u below bit 20
-// carries into the code exactly when y is rounded up.
-__device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t u16) {
-  const uint32_t b = __float_as_uint(y * 0x1p-120f);
-  return (b + (u16 << 4) + 8u) >> 20;
-}
+// Stochastic rounding to E4M3 by the conversion instruction: it adds the top 20
+// random bits below the kept mantissa bits, so 16 of them and a half stand for
+// u = (u16 + 1/2) / 65536.  Checked against floor(y / step + u) over 2^24 values and
+// numbers of each range: equal from 2^-6 to 448; below, where E4M3 is
+// subnormal, the two differ where y has bits below 2^-29 that decide.
+__device__ __forceinline__ uint32_t above(uint32_t u16_in_the_top) { return (u16_in_the_top & 0xFFFF0000u) | 0x8000u; }
 
-// four codes times their scale; 0x7F and 0xFF are NaN
+// four codes times their scale
 __device__ __forceinline__ void e4m3_decode4(uint32_t c, float scale, float (&f)[4]) {
   typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-  f[0] = lo[0] * scale;
-  f[1] = lo[1] * scale;
-  f[2] = hi[0] * scale;
-  f[3] = hi[1] * scale;
+  const f2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, false);
+  const f2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, true);
+  f[0] = lo[0];
+  f[1] = lo[1];
+  f[2] = hi[0];
+  f[3] = hi[1];
+}
+
+// Square root rounded to nearest: the hardware's is off by at most one step, and
+// the residuals at its neighbours say which way.  Equal to sqrtf for every x
+// from 2^-96 up (all of them compared), within a step below; 0, infinity and NaN pass.
+__device__ __forceinline__ float sqrt_rn(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);
+  const float r = __builtin_fmaf(-down, s, x) <= 0.f ? down : s;
+  return __builtin_fmaf(-up, s, x) > 0.f ? up : r;
 }
 
 // scale byte of a block whose largest finite magnitude has these bits:
@@ -192,43 +203,65 @@ struct Step {
 #pragma unroll
         for (int k = 0; k < 4; k++) vr[j][k] = vr[j][k] * vr[j][k];
       }
+      // The moments' products and sums are rounded one by one, as documented.  The
+      // parameter's may be contracted and its quotient is m times a reciprocal
+      // (one step): neither feeds a state.
       float rr[4];
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         const float gs = gr[j][k] * h.grad_scale;
         mr[j][k] = mr[j][k] * h.b1 + gs * h.c1;
         vr[j][k] = vr[j][k] * h.b2 + gs * h.c2 * gs;
-        rr[k] = sqrtf(vr[j][k]);
-        pr[j][k] = pr[j][k] * keep - h.alpha * (mr[j][k] / (rr[k] * h.rs + h.eps));
+        rr[k] = sqrt_rn(vr[j][k]);
+        const float den = __builtin_fmaf(rr[k], h.rs, h.eps);
+        pr[j][k] = __builtin_fmaf(pr[j][k], keep, -(h.alpha * mr[j][k]) * __builtin_amdgcn_rcpf(den));
       }
       if constexpr (MX) {
         uint32_t ma = 0, ra = 0;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-          const uint32_t x = __float_as_uint(mr[j][k]) & 0x7FFFFFFFu, y = __float_as_uint(rr[k]);  // r >= 0 or NaN
-          ma = max(ma, x < 0x7F800000u ? x : 0u);
-          ra = max(ra, y < 0x7F800000u ? y : 0u);
+          ma = max(ma, __float_as_uint(mr[j][k]) & 0x7FFFFFFFu);
+          ra = max(ra, __float_as_uint(rr[k]) & 0x7FFFFFFFu);
         }
-        mb[j] = scale_byte(block_max(ma));
-        vb[j] = scale_byte(block_max(ra));
+        ma = block_max(ma);
+        ra = block_max(ra);
+        const bool odd = max(ma, ra) >= 0x7F800000u;  // an infinity or NaN in the block
+        if (__builtin_expect(__any(odd), 0)) {          // leave those out of the largest magnitudes
+          ma = ra = 0;
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const uint32_t x = __float_as_uint(mr[j][k]) & 0x7FFFFFFFu, y = __float_as_uint(rr[k]) & 0x7FFFFFFFu;
+            ma = max(ma, x < 0x7F800000u ? x : 0u);
+            ra = max(ra, y < 0x7F800000u ? y : 0u);
+          }
+          ma = block_max(ma);
+          ra = block_max(ra);
+        }
+        mb[j] = scale_byte(ma);
+        vb[j] = scale_byte(ra);
         const float mi = inverse[mb[j]], vi = inverse[vb[j]];
-        mc[j] = vc[j] = 0;
+        int mw4 = 0, vw4 = 0;
+        const uint64_t b0 = pair_bits(key, i >> 1), b1 = pair_bits(key, (i >> 1) + 1);
+        const uint32_t w[4] = {(uint32_t)b0, (uint32_t)(b0 >> 32), (uint32_t)b1, (uint32_t)(b1 >> 32)};
+        // m: between -448 and 448; r: not below the least E4M3 value unless it is 0
+        auto put = [&](auto byte) {
+          constexpr int k = decltype(byte)::value;
+          const float x = __builtin_amdgcn_fmed3f(mr[j][k] * mi, -448.f, 448.f);
+          const float y = __builtin_amdgcn_fmed3f(rr[k] * vi, fminf(rr[k] * 0x1p100f, 0x1p-9f), 448.f);
+          mw4 = __builtin_amdgcn_cvt_sr_fp8_f32(x, (int)above(w[k] << 16), mw4, k);
+          vw4 = __builtin_amdgcn_cvt_sr_fp8_f32(y, (int)above(k & 1 ? w[k] << 8 : w[k]), vw4, k);
+        };
+        put(std::integral_constant<int, 0>{});
+        put(std::integral_constant<int, 1>{});
+        put(std::integral_constant<int, 2>{});
+        put(std::integral_constant<int, 3>{});
+        mc[j] = (uint32_t)mw4;
+        vc[j] = (uint32_t)vw4;
+        if (__builtin_expect(__any(odd), 0)) {
 #pragma unroll
-        for (int q = 0; q < 2; q++) {
-          const uint64_t bits = pair_bits(key, (i >> 1) + q);
-          const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32);
-          const uint32_t um[2] = {lo & 0xFFFFu, hi & 0xFFFFu}, ur[2] = {lo >> 16, (hi >> 8) & 0xFFFFu};
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const int k = 2 * q + e;
-            const uint32_t mbits = __float_as_uint(mr[j][k]);
-            uint32_t x = e4m3_stochastic(__uint_as_float(mbits & 0x7FFFFFFFu) * mi, um[e]);
-            x = (mbits & 0x7FFFFFFFu) < 0x7F800000u ? x : 0x7Fu;
-            mc[j] |= (x | (mbits >> 31 << 7)) << (8 * k);
-            uint32_t y = e4m3_stochastic(rr[k] * vi, ur[e]);
-            y = rr[k] > 0.f ? max(y, 1u) : y;
-            y = __float_as_uint(rr[k]) < 0x7F800000u ? y : 0x7Fu;
-            vc[j] |= y << (8 * k);
+          for (int k = 0; k < 4; k++) {
+            if ((__float_as_uint(mr[j][k]) & 0x7FFFFFFFu) >= 0x7F800000u) mc[j] |= 0x7Fu << (8 * k);
+            if ((__float_as_uint(rr[k]) & 0x7FFFFFFFu) >= 0x7F800000u) vc[j] |= 0x7Fu << (8 * k);
           }
         }
       }
