@@ -24,6 +24,9 @@ __device__ __forceinline__ uint32_t dpp_xor2(uint32_t v) {
 __device__ __forceinline__ uint32_t dpp_half_mirror(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);
 }
+__device__ __forceinline__ uint32_t dpp_mirror(uint32_t v) {  // lane i of each 16-lane row reads lane 15-i
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);
+}
 // max over the 4 lanes of a quad (unsigned)
 __device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
   v = max(v, dpp_xor1(v));

@@ -3,11 +3,14 @@
 //
 // The choice has to be that of exact arithmetic: two keys of a row that fp32
 // cannot tell apart would come out in an order that depends on how exp is
-// evaluated.  Keys and group totals are therefore taken in fp64.
+// evaluated.  The fast kernel chooses in fp32, knows how far its keys can be
+// off, and takes what that leaves open to fp64: the order of the candidates
+// alone where that decides, the whole row (route_row64) where it does not.
 #include <math.h>
 
 #include "mxq_device.h"
 #include "mxq_host.h"
+#include "mxq_vec.h"
 
 namespace mxq {
 
@@ -21,13 +24,6 @@ struct RouteParams {
   int32_t E, K, n_group, topk_group, group_top, renorm, sigmoid;
   float scale;
 };
-
-__device__ __forceinline__ float load_f(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load_f(const uint16_t* p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
-__device__ __forceinline__ void store_f(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store_f(uint16_t* p, int64_t i, float v) {
-  p[i] = __builtin_bit_cast(uint16_t, (__bf16)v);  // to nearest even
-}
 
 __device__ __forceinline__ double wave_max(double v) {
 #pragma unroll
@@ -154,9 +150,10 @@ unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 20) ? units : 
 
 // one wave per token
 template <typename LT>
-__global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const LT* __restrict__ logits, int64_t T, int64_t ld,
-                                                                  const float* __restrict__ bias, RouteParams p,
-                                                                  int32_t* __restrict__ idx, float* __restrict__ weights) {
+__global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel64(const LT* __restrict__ logits, int64_t T, int64_t ld,
+                                                                    const float* __restrict__ bias, RouteParams p,
+                                                                    int32_t* __restrict__ idx,
+                                                                    float* __restrict__ weights) {
   extern __shared__ double lds_keys[];
   const int wave = threadIdx.x / kWave;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < T; t += (int64_t)gridDim.x * kRouteWaves)
@@ -165,79 +162,46 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const LT* __r
 
 // ------------------------------------------------------------------ expert order
 // A stable counting sort of the N = T * K pairs by expert.  The pairs are cut
-// into chunks; hist_kernel counts each chunk's pairs by expert, order_kernel
-// adds up the counts before its chunk and ranks the chunk's pairs segment by
-// segment: within a wave by ballots over the bits of the expert, across waves
-// by their counts.  No atomics order anything, so the result is always the same.
-constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / kWave;
-constexpr int kMaxChunks = 256;
+// into chunks whose pairs are counted by expert (by route_fast_kernel for its own
+// tokens, or by hist_kernel); order_kernel adds up the counts before its chunks
+// and ranks its pairs segment by segment: within a wave by ballots over the bits
+// of the expert, across waves by their counts.  No atomics order anything, so the
+// result is always the same.
+constexpr int kMaxOrderThreads = 1024, kMaxOrderWaves = kMaxOrderThreads / kWave;
+constexpr int kMaxChunks = 512;         // while a chunk then has at most
+constexpr int kMaxChunkPairs = 1 << 15;  // this many pairs: counts are 16-bit
+static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
-struct OrderPlan {
-  int chunks;
-  int64_t chunk;  // pairs per chunk, a multiple of kOrderThreads
-};
+// LDS of the ranking: counts of up to kMaxOrderWaves waves, rows of E
+constexpr size_t order_lds(int waves, int E) { return (size_t)waves * E * sizeof(uint16_t); }
 
-OrderPlan order_plan(int64_t N) {
-  int64_t per = (N + kMaxChunks - 1) / kMaxChunks;
-  per = (per + kOrderThreads - 1) / kOrderThreads * kOrderThreads;
-  if (per < kOrderThreads) per = kOrderThreads;
-  int64_t c = (N + per - 1) / per;
-  return {(int)(c < 1 ? 1 : c), per};
-}
-
-__global__ __launch_bounds__(kOrderThreads) void hist_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                            int32_t E, int32_t* __restrict__ counts) {
-  __shared__ int32_t h[MXQ_MAX_GROUPS];
-  const int t = threadIdx.x;
-  if (t < E) h[t] = 0;
-  __syncthreads();
-  const int64_t b = blockIdx.x * chunk, e = min(b + chunk, N);
-  for (int64_t i = b + t; i < e; i += kOrderThreads) {
-    const int32_t x = idx[i];
-    if (x >= 0 && x < E) atomicAdd(&h[x], 1);  // a count: the order does not matter
-  }
-  __syncthreads();
-  if (t < E) counts[(int64_t)blockIdx.x * E + t] = h[t];
-}
-
-__global__ __launch_bounds__(kOrderThreads) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                             int32_t E, int32_t K, const int32_t* __restrict__ counts,
-                                                             int32_t* __restrict__ group_end,
-                                                             int32_t* __restrict__ row_token,
-                                                             int32_t* __restrict__ slot) {
-  __shared__ uint16_t wave_count[kOrderWaves][MXQ_MAX_GROUPS];
-  __shared__ int32_t base[MXQ_MAX_GROUPS];
-  __shared__ int32_t scan[kOrderWaves];
-  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
-  // of expert t: pairs in all chunks and in those before this one
-  int32_t all = 0, before = 0;
-  if (t < E)
-    for (int c = 0; c < (int)gridDim.x; c++) {
-      const int32_t n = counts[(int64_t)c * E + t];
-      all += n;
-      if (c < (int)blockIdx.x) before += n;
-    }
-  int32_t incl = all;
+// exclusive sums of one value per thread over the workgroup; total: of all
+__device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int32_t& total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+  int32_t incl = v;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
-    const int32_t v = __shfl_up(incl, o);
-    if (lane >= o) incl += v;
+    const int32_t u = __shfl_up(incl, o);
+    if (lane >= o) incl += u;
   }
-  if (lane == kWave - 1) scan[wave] = incl;
+  if (lane == kWave - 1) part[wave] = incl;
   __syncthreads();
-  int32_t off = 0, total = 0;
-  for (int w = 0; w < kOrderWaves; w++) {
-    if (w < wave) off += scan[w];
-    total += scan[w];
+  int32_t off = 0;
+  total = 0;
+  for (int w = 0; w < waves; w++) {
+    if (w < wave) off += part[w];
+    total += part[w];
   }
-  incl += off;
-  if (t < E) {
-    base[t] = incl - all + before;
-    if (blockIdx.x == 0) group_end[t] = incl;
-  }
-  const int64_t b = blockIdx.x * chunk, e = min(b + chunk, N);
-  for (int64_t s = b; s < e; s += kOrderThreads) {
-    for (int i = t; i < kOrderWaves * E; i += kOrderThreads) wave_count[i / E][i % E] = 0;
+  __syncthreads();
+  return off + incl - v;
+}
+
+// Ranks pairs [b, e): base[x] is the next row of expert x (moved on), `count` order_lds() bytes.
+__device__ void order_pairs(const int32_t* idx, int64_t b, int64_t e, int32_t E, int32_t K, int32_t* base,
+                            uint16_t* count, int32_t* __restrict__ row_token, int32_t* __restrict__ slot) {
+  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave, threads = blockDim.x, waves = threads / kWave;
+  for (int64_t s = b; s < e; s += threads) {
+    for (int i = t; i < waves * E; i += threads) count[i] = 0;
     __syncthreads();
     const int64_t i = s + t;
     int32_t x = i < e ? idx[i] : -1;
@@ -251,41 +215,546 @@ __global__ __launch_bounds__(kOrderThreads) void order_kernel(const int32_t* __r
       same &= set ? m : ~m;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (in && rank == 0) wave_count[wave][x] = (uint16_t)__popcll(same);
+    if (in && rank == 0) count[wave * E + x] = (uint16_t)__popcll(same);
     __syncthreads();
-    if (t < E) {  // counts -> first rows of the waves
+    for (int x0 = t; x0 < E; x0 += threads) {  // counts -> first rows of the waves within the segment
       int32_t run = 0;
-      for (int w = 0; w < kOrderWaves; w++) {
-        const int32_t n = wave_count[w][t];
-        wave_count[w][t] = (uint16_t)run;
+      for (int w = 0; w < waves; w++) {
+        const int32_t n = count[w * E + x0];
+        count[w * E + x0] = (uint16_t)run;
         run += n;
       }
-      scan[0] = 0;
-      all = run;
+      base[x0] += run;  // the reads below take it off again
+      count[x0] = (uint16_t)run;
     }
     __syncthreads();
     if (in) {
-      const int32_t row = base[x] + wave_count[wave][x] + rank;
+      const int32_t row = base[x] - count[x] + (wave ? count[wave * E + x] : 0) + rank;
       slot[i] = row;
       row_token[row] = (int32_t)(i / K);
     } else if (i < e) {
       slot[i] = -1;
     }
     __syncthreads();
-    if (t < E) base[t] += all;
   }
-  for (int64_t i = total + (int64_t)blockIdx.x * kOrderThreads + t; i < N; i += (int64_t)gridDim.x * kOrderThreads)
+}
+
+__global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
+                                                               int32_t E, uint16_t* __restrict__ counts) {
+  __shared__ int32_t h[MXQ_MAX_GROUPS];
+  for (int x = threadIdx.x; x < E; x += blockDim.x) h[x] = 0;
+  __syncthreads();
+  const int64_t b = blockIdx.x * chunk, e = min(b + chunk, N);
+  for (int64_t i = b + threadIdx.x; i < e; i += blockDim.x) {
+    const int32_t x = idx[i];
+    if (x >= 0 && x < E) atomicAdd(&h[x], 1);  // a count: the order does not matter
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < E; x += blockDim.x) counts[(int64_t)blockIdx.x * E + x] = (uint16_t)h[x];
+}
+
+// Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs.
+__global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
+                                                                int32_t chunks, int32_t per, int32_t E, int32_t K,
+                                                                const uint16_t* __restrict__ counts,
+                                                                int32_t* __restrict__ group_end,
+                                                                int32_t* __restrict__ row_token,
+                                                                int32_t* __restrict__ slot) {
+  extern __shared__ uint16_t lds_count[];
+  __shared__ int32_t base[MXQ_MAX_GROUPS];
+  __shared__ int32_t sums[2][kMaxOrderThreads];
+  __shared__ int32_t part[kMaxOrderWaves];
+  const int t = threadIdx.x;
+  const int32_t first = blockIdx.x * per;
+  // `parts` threads share an expert's column of counts (E <= blockDim.x)
+  const int parts = (int)blockDim.x / E, q = t / E;
+  int32_t all = 0, before = 0;
+  if (q < parts)
+    for (int c = q; c < chunks; c += parts) {
+      const int32_t n = counts[(int64_t)c * E + t - q * E];
+      all += n;
+      before += c < first ? n : 0;
+    }
+  sums[0][t] = all;
+  sums[1][t] = before;
+  __syncthreads();
+  all = before = 0;
+  if (t < E)
+    for (int r = 0; r < parts; r++) {
+      all += sums[0][r * E + t];
+      before += sums[1][r * E + t];
+    }
+  int32_t total;
+  const int32_t start = block_exclusive(t < E ? all : 0, part, total);
+  if (t < E) {
+    base[t] = start + before;
+    if (blockIdx.x == 0) group_end[t] = start + all;
+  }
+  __syncthreads();
+  const int64_t b = first * chunk;
+  order_pairs(idx, b, min(b + per * chunk, N), E, K, base, lds_count, row_token, slot);
+  for (int64_t i = total + (int64_t)blockIdx.x * blockDim.x + t; i < N; i += (int64_t)gridDim.x * blockDim.x)
     row_token[i] = -1;
 }
 
-hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, int32_t* group_end,
-                               int32_t* row_token, int32_t* slot, int32_t* counts, hipStream_t st) {
-  const OrderPlan op = order_plan(N);
-  hist_kernel<<<op.chunks, kOrderThreads, 0, st>>>(idx, N, op.chunk, E, counts);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  order_kernel<<<op.chunks, kOrderThreads, 0, st>>>(idx, N, op.chunk, E, K, counts, group_end, row_token, slot);
+// ------------------------------------------------------------------ fast routing
+// A row is held by LPR lanes (64 / LPR rows to a wave), EPL consecutive experts a
+// lane, each expert group by LPG = LPR / pow2(n_group) lanes.  Keys are ordered
+// 32-bit integers whose lowest bits give way to the expert's place in its lane, so
+// a lane's keys differ and its next largest below a threshold is one subtraction
+// and half a maximum per expert: unsigned(key - threshold) is largest for the
+// nearest key below.  A choice is then a maximum over the lanes.  bf16 logits
+// without a bias leave room for the whole index, and keys are exact.
+struct Shape {
+  int32_t lpg_log2;  // lanes per group
+  int32_t rows;      // of a workgroup, a multiple of its rows per pass
+};
+
+struct OrderOut {
+  int32_t* group_end;
+  int32_t* row_token;
+  int32_t* slot;
+  uint16_t* counts;  // of each workgroup's pairs by expert
+  int32_t mode;      // 0 none, 1 counts, 2 everything (one workgroup)
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// max and sum over the LPR lanes of a row
+template <int LPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = quad_max_u32(v);
+  v = max(v, dpp_half_mirror(v));
+  v = max(v, dpp_mirror(v));
+  if constexpr (LPR > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max((uint32_t)r[0], (uint32_t)r[1]);
+  }
+  if constexpr (LPR > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max((uint32_t)r[0], (uint32_t)r[1]);
+  }
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  auto f = [](uint32_t u) { return __uint_as_float(u); };
+  v += f(dpp_xor1(__float_as_uint(v)));
+  v += f(dpp_xor2(__float_as_uint(v)));
+  v += f(dpp_half_mirror(__float_as_uint(v)));
+  v += f(dpp_mirror(__float_as_uint(v)));
+  if constexpr (LPR > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(r[0]) + f(r[1]);
+  }
+  if constexpr (LPR > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(r[0]) + f(r[1]);
+  }
+  return v;
+}
+
+// order-preserving integers of floats; 0 is below all of them
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t b = __float_as_uint(f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+template <int LPR>
+__device__ __forceinline__ float row_fmax(float v) { return unordered(row_max<LPR>(ordered(v))); }
+
+template <typename LT, int LPR, int EPL>
+__global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__ logits, int64_t T, int64_t ld,
+                                                         const float* __restrict__ bias, const RouteParams p,
+                                                         const Shape sh, int32_t* idx, float* __restrict__ weights,
+                                                         const OrderOut o) {
+  constexpr int RPW = kWave / LPR;                 // rows of a wave
+  constexpr uint32_t LOW = EPL - 1;                // a key's bits for the place in its lane
+  constexpr bool BF16 = sizeof(LT) == 2;
+  constexpr int kSlow = 4;                         // waves that take whole rows to fp64
+  extern __shared__ double lds[];                  // their keys; the ranking's counts
+  __shared__ int32_t hist[MXQ_MAX_GROUPS];
+  __shared__ int32_t slow_rows[16 * RPW], slow_count;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
+  const int sub = lane & (LPR - 1), first_lane = lane - sub;
+  const int per = p.E / p.n_group;
+  const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
+  const int e0 = g * per + part * EPL;             // the lane's experts: e0 .. e0 + n - 1
+  const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
+  const bool grouped = p.n_group > 1;
+  const bool scored = bias || (grouped && p.group_top == 2);   // choices that need scores
+  const bool stats = !p.sigmoid && (scored || !p.renorm);
+  const bool exact_keys = BF16 && !bias;
+  // how far two fp32 keys (group totals) of distinct exact values can swap, beside the
+  // rounding relative to the key: a sigmoid is off by 6 half steps of 1, a softmax by 42
+  const float near_key = p.sigmoid ? 0x1p-20f : 0x1p-17f, near_total = p.sigmoid ? 0x1p-19f : 0x1p-16f;
+  if (o.mode)
+    for (int x = tid; x < p.E; x += blockDim.x) hist[x] = 0;
+  __syncthreads();
+
+  const int64_t row0 = (int64_t)blockIdx.x * sh.rows, row1 = min(row0 + sh.rows, T);
+  for (int64_t r0 = row0; r0 < row1; r0 += waves * RPW) {
+    if (tid == 0) slow_count = 0;
+    __syncthreads();
+    const int64_t t = r0 + wave * RPW + lane / LPR;
+    const bool live = t < row1;
+    const LT* l = logits + (live ? t : row0) * ld;
+
+    // logits; masked and absent ones -inf
+    float x[EPL];
+    if (per % 4 == 0 && EPL % 4 == 0) {
+      Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
+#pragma unroll
+      for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
+#pragma unroll
+      for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
+    }
+    bool odd = false;  // NaN or +inf: the whole row in fp64
+#pragma unroll
+    for (int j = 0; j < EPL; j++) {
+      odd |= j < n && !(x[j] < INFINITY);
+      x[j] = j < n && !(x[j] <= (float)kMasked) ? x[j] : -INFINITY;
+    }
+
+    // scores
+    float top = 0.f, inv_total = 0.f;
+    if (stats) {
+      float m = x[0];
+#pragma unroll
+      for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
+      top = fmaxf(row_fmax<LPR>(m), (float)kMasked);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < EPL; j++) s += exp_f(x[j] - top);
+      s = row_sum<LPR>(s);
+      inv_total = s > 0.f ? 1.f / s : 0.f;
+    }
+    float k[EPL];  // what a choice goes by
+#pragma unroll
+    for (int j = 0; j < EPL; j++) {
+      k[j] = x[j];
+      if (scored) {
+        float s;
+        if (p.sigmoid) {
+          const float e = exp_f(-fabsf(x[j]));
+          s = (x[j] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
+        } else {
+          s = exp_f(x[j] - top) * inv_total;
+        }
+        if (bias) s += bias[j < n ? e0 + j : 0];
+        odd |= x[j] > -INFINITY && !(fabsf(s) < INFINITY);
+        k[j] = x[j] > -INFINITY ? s : -INFINITY;
+      }
+    }
+
+    // groups
+    bool open = false;  // left open by fp32
+    bool kept = true;
+    if (grouped) {
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < EPL; j++) {
+        b = fmaxf(b, fminf(a, k[j]));
+        a = fmaxf(a, k[j]);
+      }
+      for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
+        const float a2 = __shfl_xor(a, m), b2 = __shfl_xor(b, m);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+      }
+      const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
+      int rank = 0;
+      for (int q = 0; q < p.n_group; q++) {
+        const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
+        rank += other > total || (other == total && q < g);
+      }
+      kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
+      if (scored) {  // the least total kept against the largest one not kept
+        const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
+        const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
+        open = most > -INFINITY && least - most <= near_total + fabsf(least) * 0x1p-21f;
+      }
+    }
+
+    // keys
+    uint32_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; j++) {
+      const float f = bias ? k[j] : x[j];
+      const uint32_t u = ordered(f);
+      key[j] = exact_keys ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
+      key[j] = kept && f > -INFINITY ? key[j] : 0u;
+    }
+    uint32_t below = 0, local = 0;  // the lane's largest key below `below`
+    auto next_local = [&] {
+      uint32_t d = 0u - below;  // key 0: none
+#pragma unroll
+      for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
+      local = d + below;
+    };
+    next_local();
+    int chosen = -1;
+    uint32_t chosen_key = 0;
+    auto choose = [&](int r) {
+      const uint32_t m = row_max<LPR>(local);
+      const uint64_t who = __ballot(local == m && m != 0) >> first_lane;
+      const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ((1ull << (LPR & 63)) - 1)))) - 1;
+      int e;
+      if (exact_keys)
+        e = 0xFFFF - (int)(m & 0xFFFFu);
+      else
+        e = (win >> sh.lpg_log2) * per + (win & ((1 << sh.lpg_log2) - 1)) * EPL + (int)(LOW - (m & LOW));
+      if (sub == r) {
+        chosen = m ? e : -1;
+        chosen_key = m;
+      }
+      if (sub == win) below = m;
+      next_local();
+    };
+    for (int r = 0; r < p.K; r++) choose(r);
+
+    // neighbours that fp32 leaves open: the same key but for the place, or scores too close
+    auto close = [&](uint32_t hi, uint32_t lo) {
+      if (lo == 0) return false;
+      if (!bias) return ((hi ^ lo) & ~LOW) == 0;
+      const float a = unordered(hi), b = unordered(lo);
+      return a - b <= near_key + fabsf(a) * 0x1p-18f;
+    };
+    int have = p.K;
+    if (!exact_keys) {
+      uint32_t rest = row_max<LPR>(local);
+      uint32_t after = __shfl_down(chosen_key, 1);
+      if (sub == p.K - 1) after = rest;
+      const bool any_close = sub < p.K && close(chosen_key, after);
+      if (__any(any_close)) {
+        // as many more as may belong among the first K
+        uint32_t last = __shfl(chosen_key, first_lane + have - 1);
+        while (have < LPR && __any(close(last, rest))) {
+          choose(have);
+          have++;
+          last = __shfl(chosen_key, first_lane + have - 1);
+          rest = row_max<LPR>(local);
+        }
+        open |= close(last, rest);
+        // exact keys of the candidates, and their order
+        double dtotal = 1.0;
+        if (bias && !p.sigmoid) {
+          dtotal = 0.0;
+#pragma unroll 1
+          for (int j = 0; j < n; j++) {
+            const float v = load_f(l, e0 + j);
+            if (!(v <= (float)kMasked)) dtotal += exp((double)v - (double)top);
+          }
+          for (int m = 1; m < LPR; m <<= 1) dtotal += __shfl_xor(dtotal, m);
+        }
+        double dk = -INFINITY;
+        int de = 0x7FFFFFFF;
+        if (sub < have && chosen >= 0) {
+          const double v = load_f(l, chosen);
+          dk = bias ? (p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dtotal) + (double)bias[chosen] : v;
+          de = chosen;
+        }
+        int rank = 0;
+        for (int q = 0; q < have; q++) {
+          const double v = __shfl(dk, first_lane + q);
+          const int e = __shfl(de, first_lane + q);
+          rank += v > dk || (v == dk && (e < de || (e == de && q < sub)));
+        }
+        chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
+      }
+    }
+
+    // rows for fp64
+    odd = odd || open;
+    const uint64_t odd_lanes = __ballot(odd && live);
+    const bool slow = (odd_lanes >> first_lane & (LPR == 64 ? ~0ull : (1ull << (LPR & 63)) - 1)) != 0;
+    if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
+
+    // weights of the chosen
+    const bool in = sub < p.K && chosen >= 0;
+    const float v = in ? load_f(l, chosen) : 0.f;
+    float w;
+    if (p.sigmoid) {
+      const float e = exp_f(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e);
+      if (p.renorm) {
+        // over the largest exp of the row, so that no score underflows
+        const float low = fminf(v, 0.f);
+        const float m = row_fmax<LPR>(in ? low : -INFINITY);
+        w = in ? exp_f(low - m) * r : 0.f;
+      } else {
+        w = in ? (v >= 0.f ? 1.f : e) * r : 0.f;
+      }
+    } else {
+      const float m = p.renorm ? row_fmax<LPR>(in ? v : -INFINITY) : top;
+      w = in ? exp_f(v - m) : 0.f;
+      if (!p.renorm) w *= inv_total;
+    }
+    if (p.renorm) {
+      const float s = row_sum<LPR>(w);
+      w = s > 0.f ? w / s : 0.f;
+    }
+    if (live && !slow && sub < p.K) {
+      idx[t * p.K + sub] = chosen;
+      weights[t * p.K + sub] = w * p.scale;
+      if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
+    }
+    __syncthreads();
+    if (wave < kSlow)
+      for (int q = wave; q < slow_count; q += min(kSlow, waves)) {
+        const int64_t s = r0 + slow_rows[q];
+        route_row64(logits + s * ld, bias, p, lds + wave * p.E, idx + s * p.K, weights + s * p.K);
+        if (o.mode && lane < p.K) {
+          const int32_t c = idx[s * p.K + lane];  // written by this lane
+          if (c >= 0) atomicAdd(&hist[c], 1);
+        }
+      }
+    __syncthreads();
+  }
+  if (o.mode == 1) {
+    for (int x = tid; x < p.E; x += blockDim.x) o.counts[(int64_t)blockIdx.x * p.E + x] = (uint16_t)hist[x];
+  } else if (o.mode == 2) {
+    __shared__ int32_t part_sums[kMaxOrderWaves];
+    int32_t total = 0, carry = 0;
+    for (int x0 = 0; x0 < p.E; x0 += blockDim.x) {
+      const int x = x0 + tid;
+      const int32_t c = x < p.E ? hist[x] : 0;
+      const int32_t start = carry + block_exclusive(c, part_sums, total);
+      carry += total;
+      if (x < p.E) {
+        hist[x] = start;
+        o.group_end[x] = start + c;
+      }
+    }
+    __syncthreads();
+    order_pairs(idx, 0, T * p.K, p.E, p.K, hist, (uint16_t*)lds, o.row_token, o.slot);
+    for (int64_t i = carry + tid; i < T * p.K; i += blockDim.x) o.row_token[i] = -1;
+  }
+}
+
+// ------------------------------------------------------------------ launches
+struct OrderPlan {
+  int32_t chunks;
+  int64_t chunk;  // pairs
+};
+
+// Workgroups and threads of order_kernel for these chunks
+hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, OrderPlan op, int32_t* group_end,
+                        int32_t* row_token, int32_t* slot, const uint16_t* counts, hipStream_t st) {
+  // at most 128 workgroups, since each reads all the counts; a thousand pairs at least for each
+  const int64_t most = N / kMaxOrderThreads < 128 ? N / kMaxOrderThreads + 1 : 128;
+  const int32_t per = (int32_t)((op.chunks + most - 1) / most);
+  const int32_t grid = (op.chunks + per - 1) / per;
+  order_kernel<<<grid, kMaxOrderThreads, order_lds(kMaxOrderWaves, E), st>>>(idx, N, op.chunk, op.chunks, per, E, K, counts,
+                                                                            group_end, row_token, slot);
   return hipGetLastError();
+}
+
+OrderPlan order_plan(int64_t N) {
+  int64_t chunk = (N + kMaxChunks - 1) / kMaxChunks;
+  if (chunk < kMaxOrderThreads) chunk = kMaxOrderThreads;
+  if (chunk > kMaxChunkPairs) chunk = kMaxChunkPairs;
+  const int64_t c = (N + chunk - 1) / chunk;
+  return {(int32_t)(c < 1 ? 1 : c), chunk};
+}
+
+hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, int32_t* group_end,
+                               int32_t* row_token, int32_t* slot, uint16_t* counts, hipStream_t st) {
+  const OrderPlan op = order_plan(N);
+  hist_kernel<<<op.chunks, kMaxOrderThreads, 0, st>>>(idx, N, op.chunk, E, counts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_order(idx, N, K, E, op, group_end, row_token, slot, counts, st);
+}
+
+// Largest number of chunks that a call on these sizes cuts its pairs into
+int64_t max_chunks(int64_t T, int32_t K) {
+  const int64_t most = T * K / (kMaxChunkPairs / 2) + 1;
+  return (most > kMaxChunks ? most : T < kMaxChunks ? T : kMaxChunks) + 1;
+}
+
+int ceil_log2(int v) {
+  int l = 0;
+  while (1 << l < v) l++;
+  return l;
+}
+
+// The fast kernel on a shape (LPR lanes of EPL experts) that holds the row:
+// each group in its own lanes, and the chosen in one lane each.
+template <typename LT, int LPR, int EPL>
+bool holds(const RouteParams& p) {
+  const int lanes = LPR >> ceil_log2(p.n_group);
+  return lanes >= 1 && lanes * EPL >= p.E / p.n_group && p.K <= LPR;
+}
+
+constexpr int64_t kManyRows = 4096;
+
+struct RouteArgs {
+  const void* logits;
+  int64_t T, ld;
+  const float* bias;
+  RouteParams p;
+  int32_t* idx;
+  float* weights;
+  OrderOut o;
+  hipStream_t st;
+};
+
+template <typename LT, int LPR, int EPL>
+hipError_t route_fast(RouteArgs a) {
+  constexpr int RPW = kWave / LPR;
+  const bool order = a.o.group_end != nullptr;
+  const int64_t units = (a.T + RPW - 1) / RPW;  // waves' worth of rows
+  // One workgroup does it all where its passes are few and its pairs one segment of the ranking.
+  const bool alone = order && units <= 64 && a.T * a.p.K <= kMaxOrderThreads;
+  // Workgroups of 4 waves, of 16 where the expert order would else have many chunks to add up.
+  int waves = alone ? (int)(units < 1 ? 1 : units < 16 ? units : 16) : order && units > 4 * kMaxChunks ? 16 : 4;
+  const int64_t pass = (int64_t)waves * RPW;
+  int64_t rows = alone ? a.T : pass;
+  if (order && !alone) {
+    while ((a.T + rows - 1) / rows > kMaxChunks && (rows + pass) * a.p.K <= kMaxChunkPairs) rows += pass;
+  }
+  const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
+  a.o.mode = !order ? 0 : alone ? 2 : 1;
+  const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), (int32_t)rows};
+  const size_t lds = (size_t)32 * a.p.E;  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
+  route_fast_kernel<LT, LPR, EPL><<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh,
+                                                                               a.idx, a.weights, a.o);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.o.mode != 1) return e;
+  const OrderPlan op = {(int32_t)grid, rows * a.p.K};
+  return launch_order(a.idx, a.T * a.p.K, a.p.K, a.p.E, op, a.o.group_end, a.o.row_token, a.o.slot, a.o.counts, a.st);
+}
+
+template <typename LT>
+hipError_t route(const RouteArgs& a) {
+  const RouteParams& p = a.p;
+  // Few rows: a wave for each, so that a lane has few experts to go through.  Many: as
+  // few lanes as hold the row, since a choice costs a wave the same for one row or four.
+  if (a.T >= kManyRows) {
+    if (holds<LT, 16, 2>(p)) return route_fast<LT, 16, 2>(a);
+    if (holds<LT, 16, 4>(p)) return route_fast<LT, 16, 4>(a);
+    if (holds<LT, 16, 8>(p)) return route_fast<LT, 16, 8>(a);
+    if (holds<LT, 16, 16>(p)) return route_fast<LT, 16, 16>(a);
+    if (holds<LT, 32, 16>(p)) return route_fast<LT, 32, 16>(a);
+  }
+  if (holds<LT, 64, 4>(p)) return route_fast<LT, 64, 4>(a);
+  if (holds<LT, 64, 16>(p)) return route_fast<LT, 64, 16>(a);
+  // groups that do not fit 64 lanes one by one
+  if (a.T > 0) {
+    const unsigned grid = grid_of((a.T + kRouteWaves - 1) / kRouteWaves);
+    route_kernel64<<<grid, kRouteWaves * kWave, (size_t)kRouteWaves * p.E * sizeof(double), a.st>>>(
+        (const LT*)a.logits, a.T, a.ld, a.bias, p, a.idx, a.weights);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!a.o.group_end) return hipSuccess;
+  return launch_expert_order(a.idx, a.T * p.K, p.K, p.E, a.o.group_end, a.o.row_token, a.o.slot, a.o.counts, a.st);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -431,7 +900,7 @@ extern "C" {
 
 int64_t mxq_expert_order_workspace(int64_t T, int32_t top_k, int32_t E) {
   if (T < 0 || top_k < 1 || top_k > MXQ_MAX_TOPK || E < 1 || E > MXQ_MAX_GROUPS || !pairs_ok(T, top_k)) return 0;
-  return ((int64_t)order_plan(T * top_k).chunks * E * 4 + 15) / 16 * 16;
+  return (max_chunks(T, top_k) * E * (int64_t)sizeof(uint16_t) + 15) / 16 * 16;
 }
 
 mxq_status mxq_expert_order(const int32_t* idx, int64_t T, int32_t top_k, int32_t E, int32_t* group_end,
@@ -447,7 +916,7 @@ mxq_status mxq_expert_order(const int32_t* idx, int64_t T, int32_t top_k, int32_
   const mxq_status s = check_order("mxq_expert_order", T, top_k, E, group_end, row_token, slot, workspace, workspace_bytes);
   if (s != MXQ_OK) return s;
   MXQ_REQUIRE_DEVICE();
-  return launched(launch_expert_order(idx, T * top_k, top_k, E, group_end, row_token, slot, (int32_t*)workspace, st),
+  return launched(launch_expert_order(idx, T * top_k, top_k, E, group_end, row_token, slot, (uint16_t*)workspace, st),
                   "mxq_expert_order");
 }
 
@@ -473,21 +942,9 @@ mxq_status mxq_route(const void* logits, mxq_dtype dt, int64_t T, int32_t E, int
     if (s != MXQ_OK) return s;
   }
   MXQ_REQUIRE_DEVICE();
-  if (T > 0) {
-    const RouteParams p = params(cfg, E);
-    const unsigned grid = grid_of((T + kRouteWaves - 1) / kRouteWaves);
-    const size_t lds = (size_t)kRouteWaves * E * sizeof(double);
-    if (dt == MXQ_DT_F32)
-      route_kernel<<<grid, kRouteWaves * kWave, lds, st>>>((const float*)logits, T, ld, bias, p, idx, weights);
-    else
-      route_kernel<<<grid, kRouteWaves * kWave, lds, st>>>((const uint16_t*)logits, T, ld, bias, p, idx, weights);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return launched(e, "mxq_route");
-  }
-  if (!order) return ok();
-  return launched(launch_expert_order(idx, T * cfg->top_k, cfg->top_k, E, group_end, row_token, slot,
-                                      (int32_t*)workspace, st),
-                  "mxq_route(order)");
+  if (T == 0 && !order) return ok();
+  const RouteArgs a = {logits, T, ld, bias, params(cfg, E), idx, weights, {group_end, row_token, slot, (uint16_t*)workspace, 0}, st};
+  return launched(dt == MXQ_DT_F32 ? route<float>(a) : route<uint16_t>(a), "mxq_route");
 }
 
 mxq_status mxq_route_backward(const void* logits, mxq_dtype dt, int64_t T, int32_t E, int64_t ld,
