@@ -172,6 +172,9 @@ constexpr int kMaxChunks = 512;         // while a chunk then has at most
 constexpr int kMaxChunkPairs = 1 << 15;  // this many pairs: counts are 16-bit
 static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
+// elements of a chunk's row of counts: whole 16-byte loads
+__host__ __device__ constexpr int32_t count_stride(int32_t E) { return (E + 7) / 8 * 8; }
+
 // LDS of the ranking: counts of up to kMaxOrderWaves waves, rows of E
 constexpr size_t order_lds(int waves, int E) { return (size_t)waves * E * sizeof(uint16_t); }
 
@@ -240,7 +243,8 @@ __device__ void order_pairs(const int32_t* idx, int64_t b, int64_t e, int32_t E,
 }
 
 __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                               int32_t E, uint16_t* __restrict__ counts) {
+                                                               int32_t E, int32_t stride,
+                                                               uint16_t* __restrict__ counts) {
   __shared__ int32_t h[MXQ_MAX_GROUPS];
   for (int x = threadIdx.x; x < E; x += blockDim.x) h[x] = 0;
   __syncthreads();
@@ -250,12 +254,14 @@ __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* _
     if (x >= 0 && x < E) atomicAdd(&h[x], 1);  // a count: the order does not matter
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < E; x += blockDim.x) counts[(int64_t)blockIdx.x * E + x] = (uint16_t)h[x];
+  for (int x = threadIdx.x; x < stride; x += blockDim.x)
+    counts[(int64_t)blockIdx.x * stride + x] = x < E ? (uint16_t)h[x] : 0;
 }
 
 // Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs.
 __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                                int32_t chunks, int32_t per, int32_t E, int32_t K,
+                                                                int32_t chunks, int32_t per, int32_t E, int32_t stride,
+                                                                int32_t K,
                                                                 const uint16_t* __restrict__ counts,
                                                                 int32_t* __restrict__ group_end,
                                                                 int32_t* __restrict__ row_token,
@@ -266,24 +272,35 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
   __shared__ int32_t part[kMaxOrderWaves];
   const int t = threadIdx.x;
   const int32_t first = blockIdx.x * per;
-  // `parts` threads share an expert's column of counts (E <= blockDim.x)
-  const int parts = (int)blockDim.x / E, q = t / E;
-  int32_t all = 0, before = 0;
-  if (q < parts)
-    for (int c = q; c < chunks; c += parts) {
-      const int32_t n = counts[(int64_t)c * E + t - q * E];
-      all += n;
-      before += c < first ? n : 0;
-    }
-  sums[0][t] = all;
-  sums[1][t] = before;
+  // Eight experts' counts a load; a row of counts by stride / 8 threads, the chunks dealt to
+  // as many such runs of threads as the workgroup holds.  Whole numbers: the order
+  // of the additions does not matter.
+  const int cols = stride / 8, runs = (int)blockDim.x / cols, run = t / cols, col = t - run * cols;
+  for (int x = t; x < stride; x += blockDim.x) sums[0][x] = sums[1][x] = 0;
   __syncthreads();
-  all = before = 0;
-  if (t < E)
-    for (int r = 0; r < parts; r++) {
-      all += sums[0][r * E + t];
-      before += sums[1][r * E + t];
+  if (run < runs) {
+    int32_t a[8] = {}, f[8] = {};
+    const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
+#pragma unroll 8
+    for (int c = run; c < chunks; c += runs) {
+      const u32x4 v = c4[(int64_t)c * cols];
+      const uint32_t mine = c < first ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        a[2 * j] += v[j] & 0xFFFFu;
+        a[2 * j + 1] += v[j] >> 16;
+        f[2 * j] += v[j] & mine & 0xFFFFu;
+        f[2 * j + 1] += (v[j] & mine) >> 16;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      atomicAdd(&sums[0][8 * col + j], a[j]);
+      atomicAdd(&sums[1][8 * col + j], f[j]);
+    }
+  }
+  __syncthreads();
+  const int32_t all = t < E ? sums[0][t] : 0, before = t < E ? sums[1][t] : 0;
   int32_t total;
   const int32_t start = block_exclusive(t < E ? all : 0, part, total);
   if (t < E) {
@@ -307,7 +324,7 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
 // without a bias leave room for the whole index, and keys are exact.
 struct Shape {
   int32_t lpg_log2;  // lanes per group
-  int32_t rows;      // of a workgroup, a multiple of its rows per pass
+  int32_t stride;    // of the rows of counts
 };
 
 struct OrderOut {
@@ -366,245 +383,272 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 template <int LPR>
 __device__ __forceinline__ float row_fmax(float v) { return unordered(row_max<LPR>(ordered(v))); }
 
-template <typename LT, int LPR, int EPL>
+// What a choice goes by: logits, for groups too (kLogits); logits, and scores for the
+// groups (kScoredGroups); scores and a bias (kBiased).
+enum Keys { kLogits, kScoredGroups, kBiased };
+
+// weights of a row's chosen experts (one a lane, -1: none); lanes of other rows beside
+template <typename LT, int LPR>
+__device__ __forceinline__ float weight_of(const LT* l, int chosen, const RouteParams& p, float top, float inv_total) {
+  const bool in = chosen >= 0;
+  const float v = load_f(l, in ? chosen : 0);
+  float w;
+  if (p.sigmoid) {
+    const float e = exp_f(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e);
+    if (p.renorm) {  // over the largest exp of the row, so that no score underflows
+      const float low = fminf(v, 0.f);
+      const float m = row_fmax<LPR>(in ? low : -INFINITY);
+      w = in ? exp_f(low - m) * r : 0.f;
+    } else {
+      w = in ? (v >= 0.f ? 1.f : e) * r : 0.f;
+    }
+  } else {
+    const float m = p.renorm ? row_fmax<LPR>(in ? v : -INFINITY) : top;
+    w = in ? exp_f(v - m) : 0.f;
+    if (!p.renorm) w *= inv_total;
+  }
+  if (p.renorm) {
+    const float s = row_sum<LPR>(w);
+    w = s > 0.f ? w / s : 0.f;
+  }
+  return w * p.scale;
+}
+
+template <typename LT, int LPR, int EPL, Keys KEYS>
 __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__ logits, int64_t T, int64_t ld,
                                                          const float* __restrict__ bias, const RouteParams p,
                                                          const Shape sh, int32_t* idx, float* __restrict__ weights,
                                                          const OrderOut o) {
   constexpr int RPW = kWave / LPR;                 // rows of a wave
   constexpr uint32_t LOW = EPL - 1;                // a key's bits for the place in its lane
-  constexpr bool BF16 = sizeof(LT) == 2;
+  constexpr bool EXACT = sizeof(LT) == 2 && KEYS != kBiased;
   constexpr int kSlow = 4;                         // waves that take whole rows to fp64
+  constexpr uint64_t ROW = LPR == 64 ? ~0ull : (1ull << (LPR & 63)) - 1;
   extern __shared__ double lds[];                  // their keys; the ranking's counts
   __shared__ int32_t hist[MXQ_MAX_GROUPS];
-  __shared__ int32_t slow_rows[16 * RPW], slow_count;
+  __shared__ int32_t slow_rows[16 * RPW], near_rows[16 * RPW], slow_count, near_count;
+  __shared__ int32_t candidates[16 * RPW][LPR];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
   const int sub = lane & (LPR - 1), first_lane = lane - sub;
   const int per = p.E / p.n_group;
-  const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
-  const int e0 = g * per + part * EPL;             // the lane's experts: e0 .. e0 + n - 1
-  const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
   const bool grouped = p.n_group > 1;
-  const bool scored = bias || (grouped && p.group_top == 2);   // choices that need scores
-  const bool stats = !p.sigmoid && (scored || !p.renorm);
-  const bool exact_keys = BF16 && !bias;
-  // how far two fp32 keys (group totals) of distinct exact values can swap, beside the
-  // rounding relative to the key: a sigmoid is off by 6 half steps of 1, a softmax by 42
-  const float near_key = p.sigmoid ? 0x1p-20f : 0x1p-17f, near_total = p.sigmoid ? 0x1p-19f : 0x1p-16f;
+  const bool stats = !p.sigmoid && (KEYS != kLogits || !p.renorm);
   if (o.mode)
     for (int x = tid; x < p.E; x += blockDim.x) hist[x] = 0;
+
+  auto finish = [&](int64_t t, const LT* l, int chosen, float top, float inv_total, bool write) {
+    const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
+    if (write && sub < p.K) {
+      idx[t * p.K + sub] = chosen;
+      weights[t * p.K + sub] = w;
+      if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
+    }
+  };
+
+  const int64_t r0 = (int64_t)blockIdx.x * (waves * RPW);  // rows r0 .. r0 + waves * RPW - 1
+  if (tid == 0) slow_count = near_count = 0;
   __syncthreads();
+  if (r0 + wave * RPW < T) {
+      const int64_t t = r0 + wave * RPW + lane / LPR;
+      const bool live = t < T;
+      const LT* l = logits + (live ? t : r0) * ld;
+      const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
+      const int e0 = g * per + part * EPL;  // the lane's experts: e0 .. e0 + n - 1
+      const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
 
-  const int64_t row0 = (int64_t)blockIdx.x * sh.rows, row1 = min(row0 + sh.rows, T);
-  for (int64_t r0 = row0; r0 < row1; r0 += waves * RPW) {
-    if (tid == 0) slow_count = 0;
-    __syncthreads();
-    const int64_t t = r0 + wave * RPW + lane / LPR;
-    const bool live = t < row1;
-    const LT* l = logits + (live ? t : row0) * ld;
-
-    // logits; masked and absent ones -inf
-    float x[EPL];
-    if (per % 4 == 0 && EPL % 4 == 0) {
-      Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
+      // logits; masked and absent ones -inf
+      float x[EPL];
+      float k[EPL];  // scores + bias
+      if (EPL % 4 == 0 && per % 4 == 0) {
+        Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
 #pragma unroll
-      for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
+        for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
+        if (KEYS == kBiased)
 #pragma unroll
-      for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
-    } else {
+          for (int q = 0; q < EPL / 4; q++) unpack(load_raw<4, false>(bias + (4 * q < n ? e0 + 4 * q : 0)), &k[4 * q]);
 #pragma unroll
-      for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
-    }
-    bool odd = false;  // NaN or +inf: the whole row in fp64
+        for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
+      } else {
 #pragma unroll
-    for (int j = 0; j < EPL; j++) {
-      odd |= j < n && !(x[j] < INFINITY);
-      x[j] = j < n && !(x[j] <= (float)kMasked) ? x[j] : -INFINITY;
-    }
-
-    // scores
-    float top = 0.f, inv_total = 0.f;
-    if (stats) {
-      float m = x[0];
+        for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
+        if (KEYS == kBiased)
 #pragma unroll
-      for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
-      top = fmaxf(row_fmax<LPR>(m), (float)kMasked);
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < EPL; j++) s += exp_f(x[j] - top);
-      s = row_sum<LPR>(s);
-      inv_total = s > 0.f ? 1.f / s : 0.f;
-    }
-    float k[EPL];  // what a choice goes by
-#pragma unroll
-    for (int j = 0; j < EPL; j++) {
-      k[j] = x[j];
-      if (scored) {
-        float s;
-        if (p.sigmoid) {
-          const float e = exp_f(-fabsf(x[j]));
-          s = (x[j] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
-        } else {
-          s = exp_f(x[j] - top) * inv_total;
-        }
-        if (bias) s += bias[j < n ? e0 + j : 0];
-        odd |= x[j] > -INFINITY && !(fabsf(s) < INFINITY);
-        k[j] = x[j] > -INFINITY ? s : -INFINITY;
+          for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
       }
-    }
-
-    // groups
-    bool open = false;  // left open by fp32
-    bool kept = true;
-    if (grouped) {
-      float a = -INFINITY, b = -INFINITY;
+      bool odd = false;  // NaN or +inf: the whole row in fp64
 #pragma unroll
       for (int j = 0; j < EPL; j++) {
-        b = fmaxf(b, fminf(a, k[j]));
-        a = fmaxf(a, k[j]);
+        x[j] = j < n ? x[j] : -INFINITY;
+        odd |= !(x[j] < INFINITY);
+        x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
       }
-      for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
-        const float a2 = __shfl_xor(a, m), b2 = __shfl_xor(b, m);
-        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-        a = fmaxf(a, a2);
-      }
-      const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
-      int rank = 0;
-      for (int q = 0; q < p.n_group; q++) {
-        const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
-        rank += other > total || (other == total && q < g);
-      }
-      kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
-      if (scored) {  // the least total kept against the largest one not kept
-        const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
-        const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
-        open = most > -INFINITY && least - most <= near_total + fabsf(least) * 0x1p-21f;
-      }
-    }
 
-    // keys
-    uint32_t key[EPL];
+      float top = 0.f, inv_total = 0.f;
+      if (stats) {
+        float m = x[0];
 #pragma unroll
-    for (int j = 0; j < EPL; j++) {
-      const float f = bias ? k[j] : x[j];
-      const uint32_t u = ordered(f);
-      key[j] = exact_keys ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
-      key[j] = kept && f > -INFINITY ? key[j] : 0u;
-    }
-    uint32_t below = 0, local = 0;  // the lane's largest key below `below`
-    auto next_local = [&] {
-      uint32_t d = 0u - below;  // key 0: none
+        for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
+        top = fmaxf(row_fmax<LPR>(m), (float)kMasked);
+        float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
-      local = d + below;
-    };
-    next_local();
-    int chosen = -1;
-    uint32_t chosen_key = 0;
-    auto choose = [&](int r) {
-      const uint32_t m = row_max<LPR>(local);
-      const uint64_t who = __ballot(local == m && m != 0) >> first_lane;
-      const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ((1ull << (LPR & 63)) - 1)))) - 1;
-      int e;
-      if (exact_keys)
-        e = 0xFFFF - (int)(m & 0xFFFFu);
-      else
-        e = (win >> sh.lpg_log2) * per + (win & ((1 << sh.lpg_log2) - 1)) * EPL + (int)(LOW - (m & LOW));
-      if (sub == r) {
-        chosen = m ? e : -1;
-        chosen_key = m;
+        for (int j = 0; j < EPL; j++) s += exp_f(x[j] - top);
+        s = row_sum<LPR>(s);
+        inv_total = s > 0.f ? 1.f / s : 0.f;
       }
-      if (sub == win) below = m;
-      next_local();
-    };
-    for (int r = 0; r < p.K; r++) choose(r);
-
-    // neighbours that fp32 leaves open: the same key but for the place, or scores too close
-    auto close = [&](uint32_t hi, uint32_t lo) {
-      if (lo == 0) return false;
-      if (!bias) return ((hi ^ lo) & ~LOW) == 0;
-      const float a = unordered(hi), b = unordered(lo);
-      return a - b <= near_key + fabsf(a) * 0x1p-18f;
-    };
-    int have = p.K;
-    if (!exact_keys) {
-      uint32_t rest = row_max<LPR>(local);
-      uint32_t after = __shfl_down(chosen_key, 1);
-      if (sub == p.K - 1) after = rest;
-      const bool any_close = sub < p.K && close(chosen_key, after);
-      if (__any(any_close)) {
-        // as many more as may belong among the first K
-        uint32_t last = __shfl(chosen_key, first_lane + have - 1);
-        while (have < LPR && __any(close(last, rest))) {
-          choose(have);
-          have++;
-          last = __shfl(chosen_key, first_lane + have - 1);
-          rest = row_max<LPR>(local);
+      if (KEYS != kLogits) {
+#pragma unroll
+        for (int j = 0; j < EPL; j++) {
+          float s;
+          if (p.sigmoid) {
+            const float e = exp_f(-fabsf(x[j]));
+            s = (x[j] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
+          } else {
+            s = exp_f(x[j] - top) * inv_total;
+          }
+          if (KEYS == kBiased) s += k[j];
+          odd |= x[j] > -INFINITY && !(fabsf(s) < INFINITY);
+          k[j] = x[j] > -INFINITY ? s : -INFINITY;
         }
-        open |= close(last, rest);
-        // exact keys of the candidates, and their order
-        double dtotal = 1.0;
-        if (bias && !p.sigmoid) {
-          dtotal = 0.0;
-#pragma unroll 1
-          for (int j = 0; j < n; j++) {
-            const float v = load_f(l, e0 + j);
+      }
+
+      // groups.  How far two fp32 totals of distinct exact values can swap, beside
+      // their own rounding: a sigmoid is off by 6 half steps of 1, a softmax by 42.
+      bool open = false;  // left open by fp32
+      bool kept = true;
+      if (grouped) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < EPL; j++) {
+          const float f = KEYS == kLogits ? x[j] : k[j];
+          b = fmaxf(b, fminf(a, f));
+          a = fmaxf(a, f);
+        }
+        for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
+          const float a2 = __shfl_xor(a, m), b2 = __shfl_xor(b, m);
+          b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+          a = fmaxf(a, a2);
+        }
+        const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
+        int rank = 0;
+        for (int q = 0; q < p.n_group; q++) {
+          const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
+          rank += other > total || (other == total && q < g);
+        }
+        kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
+        if (KEYS != kLogits) {  // the least total kept against the largest one not kept
+          const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
+          const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
+          open = most > -INFINITY && least - most <= (p.sigmoid ? 0x1p-19f : 0x1p-16f) + fabsf(least) * 0x1p-21f;
+        }
+      }
+
+      uint32_t key[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; j++) {
+        const float f = KEYS == kBiased ? k[j] : x[j];
+        const uint32_t u = ordered(f);
+        key[j] = EXACT ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
+        key[j] = kept && f > -INFINITY ? key[j] : 0u;
+      }
+      uint32_t below = 0, local = 0;  // the lane's largest key below `below`
+      auto next_local = [&] {
+        uint32_t d = 0u - below;  // key 0: none
+#pragma unroll
+        for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
+        local = d + below;
+      };
+      next_local();
+      int chosen = -1;
+      uint32_t chosen_key = 0;
+      auto choose = [&](int r) {
+        const uint32_t m = row_max<LPR>(local);
+        const uint64_t who = __ballot(local == m && m != 0) >> first_lane;
+        const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ROW))) - 1;
+        const int e = EXACT ? 0xFFFF - (int)(m & 0xFFFFu)
+                            : (win >> sh.lpg_log2) * per + (win & ((1 << sh.lpg_log2) - 1)) * EPL + (int)(LOW - (m & LOW));
+        if (sub == r) {
+          chosen = m ? e : -1;
+          chosen_key = m;
+        }
+        if (sub == win) below = m;
+        next_local();
+      };
+      for (int r = 0; r < p.K; r++) choose(r);
+
+      // Neighbours that fp32 leaves open (the same key but for the place, or scores too
+      // close): with as many more as may belong among the first K they are candidates,
+      // ordered by exact keys below.
+      bool near = false;
+      if (!EXACT) {
+        auto close = [&](uint32_t hi, uint32_t lo) {
+          if (lo == 0) return false;
+          if (KEYS != kBiased) return ((hi ^ lo) & ~LOW) == 0;
+          const float a = unordered(hi), b = unordered(lo);
+          return a - b <= (p.sigmoid ? 0x1p-20f : 0x1p-17f) + fabsf(a) * 0x1p-18f;
+        };
+        uint32_t rest = row_max<LPR>(local);
+        uint32_t after = __shfl_down(chosen_key, 1);
+        if (sub == p.K - 1) after = rest;
+        near = sub < p.K && close(chosen_key, after);
+        if (__any(near)) {
+          int have = p.K;
+          uint32_t last = __shfl(chosen_key, first_lane + have - 1);
+          while (have < LPR && __any(close(last, rest))) {
+            choose(have);
+            have++;
+            last = __shfl(chosen_key, first_lane + have - 1);
+            rest = row_max<LPR>(local);
+          }
+          open |= close(last, rest);
+        }
+      }
+
+      const bool slow = live && (__ballot(odd || open) >> first_lane & ROW) != 0;
+      near = live && !slow && (__ballot(near) >> first_lane & ROW) != 0;
+      if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
+      if (near) {
+        int q = 0;
+        if (sub == 0) q = atomicAdd(&near_count, 1);
+        q = __shfl(q, first_lane);
+        near_rows[q] = (int32_t)(t - r0);
+        candidates[q][sub] = chosen;
+      }
+      finish(t, l, chosen, top, inv_total, live && !slow && !near);
+    }
+    __syncthreads();
+    if (!EXACT)
+      for (int q = wave * RPW + lane / LPR; q - lane / LPR < near_count; q += waves * RPW) {
+        const bool live = q < near_count;
+        const int64_t t = r0 + near_rows[live ? q : 0];
+        const LT* l = logits + t * ld;
+        const int c = candidates[live ? q : 0][sub];
+        float top = 0.f, total = 0.f;
+        double dtotal = 0.0;
+        if (!p.sigmoid && (KEYS == kBiased || !p.renorm)) {
+          top = (float)kMasked;
+          for (int e = sub; e < p.E; e += LPR) top = fmaxf(top, load_f(l, e));
+          top = row_fmax<LPR>(top);
+          for (int e = sub; e < p.E; e += LPR) {
+            const float v = load_f(l, e);
             if (!(v <= (float)kMasked)) dtotal += exp((double)v - (double)top);
           }
           for (int m = 1; m < LPR; m <<= 1) dtotal += __shfl_xor(dtotal, m);
+          total = (float)dtotal;
         }
         double dk = -INFINITY;
-        int de = 0x7FFFFFFF;
-        if (sub < have && chosen >= 0) {
-          const double v = load_f(l, chosen);
-          dk = bias ? (p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dtotal) + (double)bias[chosen] : v;
-          de = chosen;
+        if (c >= 0) {
+          const double v = load_f(l, c);
+          dk = KEYS == kBiased ? (p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dtotal) + (double)bias[c] : v;
         }
         int rank = 0;
-        for (int q = 0; q < have; q++) {
-          const double v = __shfl(dk, first_lane + q);
-          const int e = __shfl(de, first_lane + q);
-          rank += v > dk || (v == dk && (e < de || (e == de && q < sub)));
+        for (int r = 0; r < LPR; r++) {
+          const double v = __shfl(dk, first_lane + r);
+          const int e = __shfl(c, first_lane + r);
+          rank += v > dk || (v == dk && (e < c || (e == c && r < sub)));
         }
-        chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
+        const int chosen = __builtin_amdgcn_ds_permute((first_lane + rank) * 4, c);
+        finish(t, l, chosen, top, total > 0.f ? 1.f / total : 0.f, live);
       }
-    }
-
-    // rows for fp64
-    odd = odd || open;
-    const uint64_t odd_lanes = __ballot(odd && live);
-    const bool slow = (odd_lanes >> first_lane & (LPR == 64 ? ~0ull : (1ull << (LPR & 63)) - 1)) != 0;
-    if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
-
-    // weights of the chosen
-    const bool in = sub < p.K && chosen >= 0;
-    const float v = in ? load_f(l, chosen) : 0.f;
-    float w;
-    if (p.sigmoid) {
-      const float e = exp_f(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e);
-      if (p.renorm) {
-        // over the largest exp of the row, so that no score underflows
-        const float low = fminf(v, 0.f);
-        const float m = row_fmax<LPR>(in ? low : -INFINITY);
-        w = in ? exp_f(low - m) * r : 0.f;
-      } else {
-        w = in ? (v >= 0.f ? 1.f : e) * r : 0.f;
-      }
-    } else {
-      const float m = p.renorm ? row_fmax<LPR>(in ? v : -INFINITY) : top;
-      w = in ? exp_f(v - m) : 0.f;
-      if (!p.renorm) w *= inv_total;
-    }
-    if (p.renorm) {
-      const float s = row_sum<LPR>(w);
-      w = s > 0.f ? w / s : 0.f;
-    }
-    if (live && !slow && sub < p.K) {
-      idx[t * p.K + sub] = chosen;
-      weights[t * p.K + sub] = w * p.scale;
-      if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
-    }
-    __syncthreads();
     if (wave < kSlow)
       for (int q = wave; q < slow_count; q += min(kSlow, waves)) {
         const int64_t s = r0 + slow_rows[q];
@@ -615,9 +659,9 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         }
       }
     __syncthreads();
-  }
   if (o.mode == 1) {
-    for (int x = tid; x < p.E; x += blockDim.x) o.counts[(int64_t)blockIdx.x * p.E + x] = (uint16_t)hist[x];
+    for (int x = tid; x < sh.stride; x += blockDim.x)
+      o.counts[(int64_t)blockIdx.x * sh.stride + x] = x < p.E ? (uint16_t)hist[x] : 0;
   } else if (o.mode == 2) {
     __shared__ int32_t part_sums[kMaxOrderWaves];
     int32_t total = 0, carry = 0;
@@ -650,7 +694,7 @@ hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, Ord
   const int64_t most = N / kMaxOrderThreads < 128 ? N / kMaxOrderThreads + 1 : 128;
   const int32_t per = (int32_t)((op.chunks + most - 1) / most);
   const int32_t grid = (op.chunks + per - 1) / per;
-  order_kernel<<<grid, kMaxOrderThreads, order_lds(kMaxOrderWaves, E), st>>>(idx, N, op.chunk, op.chunks, per, E, K, counts,
+  order_kernel<<<grid, kMaxOrderThreads, order_lds(kMaxOrderWaves, E), st>>>(idx, N, op.chunk, op.chunks, per, E, count_stride(E), K, counts,
                                                                             group_end, row_token, slot);
   return hipGetLastError();
 }
@@ -666,16 +710,18 @@ OrderPlan order_plan(int64_t N) {
 hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, int32_t* group_end,
                                int32_t* row_token, int32_t* slot, uint16_t* counts, hipStream_t st) {
   const OrderPlan op = order_plan(N);
-  hist_kernel<<<op.chunks, kMaxOrderThreads, 0, st>>>(idx, N, op.chunk, E, counts);
+  hist_kernel<<<op.chunks, kMaxOrderThreads, 0, st>>>(idx, N, op.chunk, E, count_stride(E), counts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_order(idx, N, K, E, op, group_end, row_token, slot, counts, st);
 }
 
-// Largest number of chunks that a call on these sizes cuts its pairs into
+// Largest number of chunks that a call on these sizes cuts its pairs into: order_plan's,
+// or one for each of route_fast's workgroups.
 int64_t max_chunks(int64_t T, int32_t K) {
-  const int64_t most = T * K / (kMaxChunkPairs / 2) + 1;
-  return (most > kMaxChunks ? most : T < kMaxChunks ? T : kMaxChunks) + 1;
+  const int64_t rows = T <= 4 * 64 * 4 ? T / 4 + 1 : T / 16 + 1;
+  const int64_t plan = order_plan(T * K).chunks;
+  return rows > plan ? rows : plan;
 }
 
 int ceil_log2(int v) {
@@ -691,6 +737,7 @@ bool holds(const RouteParams& p) {
   const int lanes = LPR >> ceil_log2(p.n_group);
   return lanes >= 1 && lanes * EPL >= p.E / p.n_group && p.K <= LPR;
 }
+constexpr int64_t kFastRows = 1 << 25;  // 64 lanes each, in a grid of fewer than 2^32 threads
 
 constexpr int64_t kManyRows = 4096;
 
@@ -710,21 +757,20 @@ hipError_t route_fast(RouteArgs a) {
   constexpr int RPW = kWave / LPR;
   const bool order = a.o.group_end != nullptr;
   const int64_t units = (a.T + RPW - 1) / RPW;  // waves' worth of rows
-  // One workgroup does it all where its passes are few and its pairs one segment of the ranking.
-  const bool alone = order && units <= 64 && a.T * a.p.K <= kMaxOrderThreads;
-  // Workgroups of 4 waves, of 16 where the expert order would else have many chunks to add up.
-  int waves = alone ? (int)(units < 1 ? 1 : units < 16 ? units : 16) : order && units > 4 * kMaxChunks ? 16 : 4;
-  const int64_t pass = (int64_t)waves * RPW;
-  int64_t rows = alone ? a.T : pass;
-  if (order && !alone) {
-    while ((a.T + rows - 1) / rows > kMaxChunks && (rows + pass) * a.p.K <= kMaxChunkPairs) rows += pass;
-  }
+  // One workgroup does it all where it holds the rows and their pairs are one segment of
+  // the ranking.  Else workgroups of 4 waves, of 16 where the expert order would have
+  // many chunks to add up.
+  const bool alone = order && units <= 16 && a.T * a.p.K <= kMaxOrderThreads;
+  const int waves = alone ? (int)(units < 1 ? 1 : units) : order && units > 4 * 64 ? 16 : 4;
+  const int64_t rows = (int64_t)waves * RPW;
   const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
   a.o.mode = !order ? 0 : alone ? 2 : 1;
-  const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), (int32_t)rows};
+  const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E)};
   const size_t lds = (size_t)32 * a.p.E;  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
-  route_fast_kernel<LT, LPR, EPL><<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh,
-                                                                               a.idx, a.weights, a.o);
+  auto f = a.bias                                         ? route_fast_kernel<LT, LPR, EPL, kBiased>
+           : a.p.n_group > 1 && a.p.group_top == 2 ? route_fast_kernel<LT, LPR, EPL, kScoredGroups>
+                                                   : route_fast_kernel<LT, LPR, EPL, kLogits>;
+  f<<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh, a.idx, a.weights, a.o);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.o.mode != 1) return e;
   const OrderPlan op = {(int32_t)grid, rows * a.p.K};
@@ -736,16 +782,17 @@ hipError_t route(const RouteArgs& a) {
   const RouteParams& p = a.p;
   // Few rows: a wave for each, so that a lane has few experts to go through.  Many: as
   // few lanes as hold the row, since a choice costs a wave the same for one row or four.
-  if (a.T >= kManyRows) {
+  if (a.T >= kManyRows && a.T <= kFastRows) {
     if (holds<LT, 16, 2>(p)) return route_fast<LT, 16, 2>(a);
     if (holds<LT, 16, 4>(p)) return route_fast<LT, 16, 4>(a);
-    if (holds<LT, 16, 8>(p)) return route_fast<LT, 16, 8>(a);
     if (holds<LT, 16, 16>(p)) return route_fast<LT, 16, 16>(a);
     if (holds<LT, 32, 16>(p)) return route_fast<LT, 32, 16>(a);
   }
-  if (holds<LT, 64, 4>(p)) return route_fast<LT, 64, 4>(a);
-  if (holds<LT, 64, 16>(p)) return route_fast<LT, 64, 16>(a);
-  // groups that do not fit 64 lanes one by one
+  if (a.T <= kFastRows) {
+    if (holds<LT, 64, 4>(p)) return route_fast<LT, 64, 4>(a);
+    if (holds<LT, 64, 16>(p)) return route_fast<LT, 64, 16>(a);
+  }
+  // groups that do not fit 64 lanes one by one, or very many rows
   if (a.T > 0) {
     const unsigned grid = grid_of((a.T + kRouteWaves - 1) / kRouteWaves);
     route_kernel64<<<grid, kRouteWaves * kWave, (size_t)kRouteWaves * p.E * sizeof(double), a.st>>>(
@@ -900,7 +947,7 @@ extern "C" {
 
 int64_t mxq_expert_order_workspace(int64_t T, int32_t top_k, int32_t E) {
   if (T < 0 || top_k < 1 || top_k > MXQ_MAX_TOPK || E < 1 || E > MXQ_MAX_GROUPS || !pairs_ok(T, top_k)) return 0;
-  return (max_chunks(T, top_k) * E * (int64_t)sizeof(uint16_t) + 15) / 16 * 16;
+  return (max_chunks(T, top_k) * count_stride(E) * (int64_t)sizeof(uint16_t) + 15) / 16 * 16;
 }
 
 mxq_status mxq_expert_order(const int32_t* idx, int64_t T, int32_t top_k, int32_t E, int32_t* group_end,
