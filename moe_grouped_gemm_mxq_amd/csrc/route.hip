@@ -426,8 +426,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
   constexpr uint64_t ROW = LPR == 64 ? ~0ull : (1ull << (LPR & 63)) - 1;
   extern __shared__ double lds[];                  // their keys; the ranking's counts
   __shared__ int32_t hist[MXQ_MAX_GROUPS];
-  __shared__ int32_t slow_rows[16 * RPW], near_rows[16 * RPW], slow_count, near_count;
-  __shared__ int32_t candidates[16 * RPW][LPR];
+  __shared__ int32_t slow_rows[16 * RPW], slow_count;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, waves = blockDim.x / kWave;
   const int sub = lane & (LPR - 1), first_lane = lane - sub;
   const int per = p.E / p.n_group;
@@ -436,17 +435,8 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
   if (o.mode)
     for (int x = tid; x < p.E; x += blockDim.x) hist[x] = 0;
 
-  auto finish = [&](int64_t t, const LT* l, int chosen, float top, float inv_total, bool write) {
-    const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
-    if (write && sub < p.K) {
-      idx[t * p.K + sub] = chosen;
-      weights[t * p.K + sub] = w;
-      if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
-    }
-  };
-
   const int64_t r0 = (int64_t)blockIdx.x * (waves * RPW);  // rows r0 .. r0 + waves * RPW - 1
-  if (tid == 0) slow_count = near_count = 0;
+  if (tid == 0) slow_count = 0;
   __syncthreads();
   if (r0 + wave * RPW < T) {
       const int64_t t = r0 + wave * RPW + lane / LPR;
@@ -511,9 +501,24 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         }
       }
 
-      // groups.  How far two fp32 totals of distinct exact values can swap, beside
-      // their own rounding: a sigmoid is off by 6 half steps of 1, a softmax by 42.
-      bool open = false;  // left open by fp32
+      // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias; without
+      // a bias a softmax's up to its sum, which orders them as well)
+      auto exp_sum = [&] {
+        double s = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < n; j++) {
+          const float v = load_f(l, e0 + j);
+          if (!(v <= (float)kMasked)) s += exp((double)v - (double)top);
+        }
+        for (int m = 1; m < LPR; m <<= 1) s += __shfl_xor(s, m);
+        return s;
+      };
+      auto exact_key = [&](int e, double dsum, bool with_bias) {
+        const double v = load_f(l, e);
+        const double s = p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dsum;
+        return with_bias ? s + (double)bias[e] : s;
+      };
+
       bool kept = true;
       if (grouped) {
         float a = -INFINITY, b = -INFINITY;
@@ -535,10 +540,44 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
           rank += other > total || (other == total && q < g);
         }
         kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
-        if (KEYS != kLogits) {  // the least total kept against the largest one not kept
+        if (KEYS != kLogits) {
+          // Of the least total kept and the largest not kept: fp32 totals of distinct
+          // exact values can swap when they differ by at most twice a total's error, that
+          // of two scores (4 half steps of 1 for a sigmoid, 42 for a softmax) and three
+          // roundings.  Then the totals are taken in fp64, from the experts that can be
+          // among their groups' best two.
           const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
           const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
-          open = most > -INFINITY && least - most <= (p.sigmoid ? 0x1p-19f : 0x1p-16f) + fabsf(least) * 0x1p-21f;
+          const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(least) * 0x1p-22f;
+          const bool open = most > -INFINITY && least - most <= error;
+          if (__any(open)) {
+            const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
+            const float from = (p.group_top == 2 && b > -INFINITY ? b : a) - error;
+            uint32_t which = 0;
+#pragma unroll
+            for (int j = 0; j < EPL; j++) which |= k[j] > -INFINITY && k[j] >= from ? 1u << j : 0u;
+            double da = -INFINITY, db = -INFINITY;
+            while (__any(which)) {
+              if (which) {
+                const double s = exact_key(e0 + __ffs(which) - 1, dsum, KEYS == kBiased);
+                which &= which - 1;
+                db = fmax(db, fmin(da, s));
+                da = fmax(da, s);
+              }
+            }
+            for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
+              const double a2 = __shfl_xor(da, m), b2 = __shfl_xor(db, m);
+              db = fmax(fmin(da, a2), fmax(db, b2));
+              da = fmax(da, a2);
+            }
+            const double dt = p.group_top == 2 && db > -INFINITY ? da + db : da;
+            int r = 0;
+            for (int q = 0; q < p.n_group; q++) {
+              const double other = __shfl(dt, first_lane + (q << sh.lpg_log2));
+              r += other > dt || (other == dt && q < g);
+            }
+            kept = g < p.n_group && r < p.topk_group && dt > -INFINITY;
+          }
         }
       }
 
@@ -576,21 +615,20 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       for (int r = 0; r < p.K; r++) choose(r);
 
       // Neighbours that fp32 leaves open (the same key but for the place, or scores too
-      // close): with as many more as may belong among the first K they are candidates,
-      // ordered by exact keys below.
-      bool near = false;
+      // close): they and as many more as may belong among the first K are put into the
+      // order of their exact keys.
       if (!EXACT) {
         auto close = [&](uint32_t hi, uint32_t lo) {
           if (lo == 0) return false;
           if (KEYS != kBiased) return ((hi ^ lo) & ~LOW) == 0;
-          const float a = unordered(hi), b = unordered(lo);
-          return a - b <= (p.sigmoid ? 0x1p-20f : 0x1p-17f) + fabsf(a) * 0x1p-18f;
+          // twice a score's error (4 or 42 half steps), the sums' roundings, the places' bits
+          const float x = unordered(hi), y = unordered(lo);
+          return x - y <= (p.sigmoid ? 0x1p-21f : 0x1.5p-18f) + fabsf(x) * (EPL * 0x1p-23f + 0x1p-22f);
         };
         uint32_t rest = row_max<LPR>(local);
         uint32_t after = __shfl_down(chosen_key, 1);
         if (sub == p.K - 1) after = rest;
-        near = sub < p.K && close(chosen_key, after);
-        if (__any(near)) {
+        if (__any(sub < p.K && close(chosen_key, after))) {
           int have = p.K;
           uint32_t last = __shfl(chosen_key, first_lane + have - 1);
           while (have < LPR && __any(close(last, rest))) {
@@ -599,56 +637,30 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
             last = __shfl(chosen_key, first_lane + have - 1);
             rest = row_max<LPR>(local);
           }
-          open |= close(last, rest);
+          odd |= close(last, rest);
+          const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
+          double dk = -INFINITY;
+          if (sub < have && chosen >= 0) dk = KEYS == kBiased ? exact_key(chosen, dsum, true) : (double)load_f(l, chosen);
+          int rank = 0;
+          for (int q = 0; q < have; q++) {
+            const double v = __shfl(dk, first_lane + q);
+            const int e = __shfl(chosen, first_lane + q);
+            rank += v > dk || (v == dk && (e < chosen || (e == chosen && q < sub)));
+          }
+          chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
         }
       }
 
-      const bool slow = live && (__ballot(odd || open) >> first_lane & ROW) != 0;
-      near = live && !slow && (__ballot(near) >> first_lane & ROW) != 0;
+      const bool slow = live && (__ballot(odd) >> first_lane & ROW) != 0;
       if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
-      if (near) {
-        int q = 0;
-        if (sub == 0) q = atomicAdd(&near_count, 1);
-        q = __shfl(q, first_lane);
-        near_rows[q] = (int32_t)(t - r0);
-        candidates[q][sub] = chosen;
+      const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
+      if (live && !slow && sub < p.K) {
+        idx[t * p.K + sub] = chosen;
+        weights[t * p.K + sub] = w;
+        if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
       }
-      finish(t, l, chosen, top, inv_total, live && !slow && !near);
     }
     __syncthreads();
-    if (!EXACT)
-      for (int q = wave * RPW + lane / LPR; q - lane / LPR < near_count; q += waves * RPW) {
-        const bool live = q < near_count;
-        const int64_t t = r0 + near_rows[live ? q : 0];
-        const LT* l = logits + t * ld;
-        const int c = candidates[live ? q : 0][sub];
-        float top = 0.f, total = 0.f;
-        double dtotal = 0.0;
-        if (!p.sigmoid && (KEYS == kBiased || !p.renorm)) {
-          top = (float)kMasked;
-          for (int e = sub; e < p.E; e += LPR) top = fmaxf(top, load_f(l, e));
-          top = row_fmax<LPR>(top);
-          for (int e = sub; e < p.E; e += LPR) {
-            const float v = load_f(l, e);
-            if (!(v <= (float)kMasked)) dtotal += exp((double)v - (double)top);
-          }
-          for (int m = 1; m < LPR; m <<= 1) dtotal += __shfl_xor(dtotal, m);
-          total = (float)dtotal;
-        }
-        double dk = -INFINITY;
-        if (c >= 0) {
-          const double v = load_f(l, c);
-          dk = KEYS == kBiased ? (p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dtotal) + (double)bias[c] : v;
-        }
-        int rank = 0;
-        for (int r = 0; r < LPR; r++) {
-          const double v = __shfl(dk, first_lane + r);
-          const int e = __shfl(c, first_lane + r);
-          rank += v > dk || (v == dk && (e < c || (e == c && r < sub)));
-        }
-        const int chosen = __builtin_amdgcn_ds_permute((first_lane + rank) * 4, c);
-        finish(t, l, chosen, top, total > 0.f ? 1.f / total : 0.f, live);
-      }
     if (wave < kSlow)
       for (int q = wave; q < slow_count; q += min(kSlow, waves)) {
         const int64_t s = r0 + slow_rows[q];
@@ -719,7 +731,7 @@ hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t
 // Largest number of chunks that a call on these sizes cuts its pairs into: order_plan's,
 // or one for each of route_fast's workgroups.
 int64_t max_chunks(int64_t T, int32_t K) {
-  const int64_t rows = T <= 4 * 64 * 4 ? T / 4 + 1 : T / 16 + 1;
+  const int64_t rows = T <= 4 * kMaxChunks ? T / 4 + 1 : T / 16 < kMaxChunks ? kMaxChunks + 1 : T / 16 + 1;
   const int64_t plan = order_plan(T * K).chunks;
   return rows > plan ? rows : plan;
 }
@@ -761,7 +773,7 @@ hipError_t route_fast(RouteArgs a) {
   // the ranking.  Else workgroups of 4 waves, of 16 where the expert order would have
   // many chunks to add up.
   const bool alone = order && units <= 16 && a.T * a.p.K <= kMaxOrderThreads;
-  const int waves = alone ? (int)(units < 1 ? 1 : units) : order && units > 4 * 64 ? 16 : 4;
+  const int waves = alone ? (int)(units < 1 ? 1 : units) : order && units > 4 * kMaxChunks ? 16 : 4;
   const int64_t rows = (int64_t)waves * RPW;
   const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
   a.o.mode = !order ? 0 : alone ? 2 : 1;
