@@ -8,6 +8,8 @@
 // alone where that decides, the whole row (route_row64) where it does not.
 #include <math.h>
 
+#include <algorithm>
+
 #include "mxq_device.h"
 #include "mxq_host.h"
 #include "mxq_vec.h"
@@ -172,13 +174,17 @@ constexpr int kMaxChunks = 512;         // while a chunk then has at most
 constexpr int kMaxChunkPairs = 1 << 15;  // this many pairs: counts are 16-bit
 static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
-// elements of a chunk's row of counts: whole 16-byte loads
-__host__ __device__ constexpr int32_t count_stride(int32_t E) { return (E + 7) / 8 * 8; }
+// elements of a chunk's row of counts: a power of two of 16-byte loads
+__host__ __device__ constexpr int32_t count_stride(int32_t E) {
+  int32_t s = 8;
+  while (s < E) s *= 2;
+  return s;
+}
 
 // LDS of the ranking: counts of up to kMaxOrderWaves waves, rows of E
 constexpr size_t order_lds(int waves, int E) { return (size_t)waves * E * sizeof(uint16_t); }
 
-// exclusive sums of one value per thread over the workgroup; total: of all
+// exclusive sums of one value per thread over the workgroup; total: of all.  part: kMaxOrderWaves words
 __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int32_t& total) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
   int32_t incl = v;
@@ -191,55 +197,62 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int
   __syncthreads();
   int32_t off = 0;
   total = 0;
-  for (int w = 0; w < waves; w++) {
-    if (w < wave) off += part[w];
-    total += part[w];
+#pragma unroll
+  for (int w = 0; w < kMaxOrderWaves; w++) {
+    const int32_t n = w < waves ? part[w] : 0;
+    if (w < wave) off += n;
+    total += n;
   }
-  __syncthreads();
   return off + incl - v;
 }
 
-// Ranks pairs [b, e): base[x] is the next row of expert x (moved on), `count` order_lds() bytes.
-__device__ void order_pairs(const int32_t* idx, int64_t b, int64_t e, int32_t E, int32_t K, int32_t* base,
-                            uint16_t* count, int32_t* __restrict__ row_token, int32_t* __restrict__ slot) {
-  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave, threads = blockDim.x, waves = threads / kWave;
-  for (int64_t s = b; s < e; s += threads) {
-    for (int i = t; i < waves * E; i += threads) count[i] = 0;
-    __syncthreads();
-    const int64_t i = s + t;
-    int32_t x = i < e ? idx[i] : -1;
-    const bool in = x >= 0 && x < E;
-    if (!in) x = E;  // a value of its own
-    uint64_t same = ~0ull;
-#pragma unroll
-    for (int bit = 0; bit < 11; bit++) {
-      const bool set = x >> bit & 1;
-      const uint64_t m = __ballot(set);
-      same &= set ? m : ~m;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (in && rank == 0) count[wave * E + x] = (uint16_t)__popcll(same);
-    __syncthreads();
-    for (int x0 = t; x0 < E; x0 += threads) {  // counts -> first rows of the waves within the segment
-      int32_t run = 0;
-      for (int w = 0; w < waves; w++) {
-        const int32_t n = count[w * E + x0];
-        count[w * E + x0] = (uint16_t)run;
-        run += n;
-      }
-      base[x0] += run;  // the reads below take it off again
-      count[x0] = (uint16_t)run;
-    }
-    __syncthreads();
-    if (in) {
-      const int32_t row = base[x] - count[x] + (wave ? count[wave * E + x] : 0) + rank;
-      slot[i] = row;
-      row_token[row] = (int32_t)(i / K);
-    } else if (i < e) {
-      slot[i] = -1;
-    }
-    __syncthreads();
+// A segment is one pair per thread, x its expert (E: none).  rank_in_wave: how many
+// earlier lanes have the same; the wave's count of each expert goes to `count`
+// [waves][E], which is zero before and read after a barrier.
+__device__ __forceinline__ int rank_in_wave(int32_t x, int32_t E, uint16_t* count) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int bits = 32 - __builtin_clz(E);  // of 0 .. E
+  uint64_t same = ~0ull;
+  for (int bit = 0; bit < bits; bit++) {
+    const bool set = x >> bit & 1;
+    const uint64_t m = __ballot(set);
+    same &= set ? m : ~m;
   }
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  if (x < E && rank == 0) count[wave * E + x] = (uint16_t)__popcll(same);
+  return rank;
+}
+// counts of expert x -> pairs in earlier waves; returns the segment's
+__device__ __forceinline__ int32_t waves_exclusive(int x, int32_t E, uint16_t* count) {
+  const int waves = blockDim.x / kWave;
+  int32_t n[kMaxOrderWaves];
+#pragma unroll
+  for (int w = 0; w < kMaxOrderWaves; w++) n[w] = w < waves ? count[w * E + x] : 0;
+  int32_t run = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxOrderWaves; w++) {
+    if (w < waves) count[w * E + x] = (uint16_t)run;
+    run += n[w];
+  }
+  return run;
+}
+__device__ __forceinline__ void clear_counts(int32_t E, uint16_t* count) {
+  for (int i = threadIdx.x; i < (int)(blockDim.x / kWave) * E; i += blockDim.x) count[i] = 0;
+}
+__device__ __forceinline__ int32_t expert_at(const int32_t* idx, int64_t i, int64_t e, int32_t E) {
+  const int32_t x = i < e ? idx[i] : -1;
+  return x >= 0 && x < E ? x : E;
+}
+__device__ __forceinline__ void put_pair(int64_t i, int64_t e, int32_t x, int rank, int32_t E, int32_t K,
+                                         const int32_t* base, const uint16_t* count, int32_t* __restrict__ row_token,
+                                         int32_t* __restrict__ slot) {
+  if (i >= e) return;
+  int32_t row = -1;
+  if (x < E) {
+    row = base[x] + count[threadIdx.x / kWave * E + x] + rank;
+    row_token[row] = (int32_t)((uint32_t)i / (uint32_t)K);  // T * K < 2^31
+  }
+  slot[i] = row;
 }
 
 __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
@@ -266,20 +279,20 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
                                                                 int32_t* __restrict__ group_end,
                                                                 int32_t* __restrict__ row_token,
                                                                 int32_t* __restrict__ slot) {
-  extern __shared__ uint16_t lds_count[];
+  extern __shared__ uint16_t count[];
   __shared__ int32_t base[MXQ_MAX_GROUPS];
-  __shared__ int32_t sums[2][kMaxOrderThreads];
+  __shared__ int32_t sums[2][MXQ_MAX_GROUPS];
   __shared__ int32_t part[kMaxOrderWaves];
   const int t = threadIdx.x;
   const int32_t first = blockIdx.x * per;
+  const int64_t b = first * chunk, e = min(b + per * chunk, N);
+  int32_t x = expert_at(idx, b + t, e, E);
   // Eight experts' counts a load; a row of counts by stride / 8 threads, the chunks dealt to
   // as many such runs of threads as the workgroup holds.  Whole numbers: the order
   // of the additions does not matter.
   const int cols = stride / 8, runs = (int)blockDim.x / cols, run = t / cols, col = t - run * cols;
-  for (int x = t; x < stride; x += blockDim.x) sums[0][x] = sums[1][x] = 0;
-  __syncthreads();
-  if (run < runs) {
-    int32_t a[8] = {}, f[8] = {};
+  int32_t a[8] = {}, f[8] = {};
+  {
     const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
 #pragma unroll 8
     for (int c = run; c < chunks; c += runs) {
@@ -293,23 +306,50 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
         f[2 * j + 1] += (v[j] & mine) >> 16;
       }
     }
+  }
+  for (int i = t; i < stride; i += blockDim.x) sums[0][i] = sums[1][i] = 0;
+  clear_counts(E, count);
+  __syncthreads();
+  int rank = rank_in_wave(x, E, count);
+  // the runs of a wave first: 64 lanes adding to the same few words one by one took 7 us
+  if ((t & ~(kWave - 1)) / cols < chunks) {
+    for (int m = cols; m < kWave; m *= 2)
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      atomicAdd(&sums[0][8 * col + j], a[j]);
-      atomicAdd(&sums[1][8 * col + j], f[j]);
-    }
+      for (int j = 0; j < 8; j++) {
+        a[j] += __shfl_xor(a[j], m);
+        f[j] += __shfl_xor(f[j], m);
+      }
+    if ((t & (kWave - 1)) < cols)
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        atomicAdd(&sums[0][8 * col + j], a[j]);
+        atomicAdd(&sums[1][8 * col + j], f[j]);
+      }
   }
   __syncthreads();
   const int32_t all = t < E ? sums[0][t] : 0, before = t < E ? sums[1][t] : 0;
+  int32_t segment = t < E ? waves_exclusive(t, E, count) : 0;
   int32_t total;
-  const int32_t start = block_exclusive(t < E ? all : 0, part, total);
+  const int32_t start = block_exclusive(all, part, total);
   if (t < E) {
     base[t] = start + before;
     if (blockIdx.x == 0) group_end[t] = start + all;
   }
   __syncthreads();
-  const int64_t b = first * chunk;
-  order_pairs(idx, b, min(b + per * chunk, N), E, K, base, lds_count, row_token, slot);
+  for (int64_t s = b;;) {
+    put_pair(s + t, e, x, rank, E, K, base, count, row_token, slot);
+    s += blockDim.x;
+    if (s >= e) break;
+    __syncthreads();
+    if (t < E) base[t] += segment;
+    clear_counts(E, count);
+    x = expert_at(idx, s + t, e, E);
+    __syncthreads();
+    rank = rank_in_wave(x, E, count);
+    __syncthreads();
+    if (t < E) segment = waves_exclusive(t, E, count);
+    __syncthreads();
+  }
   for (int64_t i = total + (int64_t)blockIdx.x * blockDim.x + t; i < N; i += (int64_t)gridDim.x * blockDim.x)
     row_token[i] = -1;
 }
@@ -675,21 +715,29 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
     for (int x = tid; x < sh.stride; x += blockDim.x)
       o.counts[(int64_t)blockIdx.x * sh.stride + x] = x < p.E ? (uint16_t)hist[x] : 0;
   } else if (o.mode == 2) {
+    // all pairs here, one segment
     __shared__ int32_t part_sums[kMaxOrderWaves];
+    uint16_t* count = (uint16_t*)lds;
+    clear_counts(p.E, count);
+    const int32_t pairs = (int32_t)T * p.K;
+    const int32_t x = expert_at(idx, tid, pairs, p.E);
+    __syncthreads();
+    const int rank = rank_in_wave(x, p.E, count);
     int32_t total = 0, carry = 0;
-    for (int x0 = 0; x0 < p.E; x0 += blockDim.x) {
-      const int x = x0 + tid;
-      const int32_t c = x < p.E ? hist[x] : 0;
+    for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
+      const int e = e0 + tid;
+      const int32_t c = e < p.E ? hist[e] : 0;
       const int32_t start = carry + block_exclusive(c, part_sums, total);
       carry += total;
-      if (x < p.E) {
-        hist[x] = start;
-        o.group_end[x] = start + c;
+      if (e < p.E) {
+        waves_exclusive(e, p.E, count);
+        hist[e] = start;
+        o.group_end[e] = start + c;
       }
+      __syncthreads();
     }
-    __syncthreads();
-    order_pairs(idx, 0, T * p.K, p.E, p.K, hist, (uint16_t*)lds, o.row_token, o.slot);
-    for (int64_t i = carry + tid; i < T * p.K; i += blockDim.x) o.row_token[i] = -1;
+    put_pair(tid, pairs, x, rank, p.E, p.K, hist, count, o.row_token, o.slot);
+    if (tid >= carry && tid < pairs) o.row_token[tid] = -1;
   }
 }
 
@@ -773,7 +821,8 @@ hipError_t route_fast(RouteArgs a) {
   // the ranking.  Else workgroups of 4 waves, of 16 where the expert order would have
   // many chunks to add up.
   const bool alone = order && units <= 16 && a.T * a.p.K <= kMaxOrderThreads;
-  const int waves = alone ? (int)(units < 1 ? 1 : units) : order && units > 4 * kMaxChunks ? 16 : 4;
+  const int64_t pair_waves = (a.T * a.p.K + kWave - 1) / kWave;
+  const int waves = alone ? (int)std::max<int64_t>({units, pair_waves, 1}) : order && units > 4 * kMaxChunks ? 16 : 4;
   const int64_t rows = (int64_t)waves * RPW;
   const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
   a.o.mode = !order ? 0 : alone ? 2 : 1;
