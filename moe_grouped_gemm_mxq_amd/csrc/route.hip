@@ -866,100 +866,146 @@ hipError_t route(const RouteArgs& a) {
 }
 
 // ------------------------------------------------------------------ gradient
-// One token by one wave; its row of gradients is gathered in LDS (`row`, E floats).
-template <typename LT>
-__device__ void route_backward_row(const LT* __restrict__ l, const RouteParams p, const int32_t* __restrict__ idx,
-                                   const float* __restrict__ dweights, float* row, LT* __restrict__ out) {
-  const int lane = threadIdx.x & (kWave - 1);
-  for (int e = lane; e < p.E; e += kWave) row[e] = 0.f;
-  int i = -1;
-  float g = 0.f, x = 0.f;
-  if (lane < p.K) {
-    i = idx[lane];
-    if (i < 0 || i >= p.E) i = -1;
-    if (i >= 0) {
-      g = dweights[lane] * p.scale;
-      x = load_f(l, i);
-      if (x <= (float)kMasked) i = -1;
-    }
-  }
-  const bool in = i >= 0;
-  const bool dense = !p.sigmoid && !p.renorm;
-  float top = -INFINITY;
-  float d = 0.f;
-  if (p.sigmoid) {
-    const float ex = expf(-fabsf(x));
-    const float inv = 1.f / (1.f + ex);
-    const float s = in ? (x >= 0 ? inv : ex * inv) : 0.f, s1 = x >= 0 ? ex * inv : inv;  // s and 1 - s
-    if (p.renorm) {
-      // s of the row over the largest exp, so that no s underflows: s_k / sum s = r_k / sum r
-      const float m = in ? fminf(x, 0.f) : -INFINITY;
-      float mm = m;
-#pragma unroll
-      for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
-      const float r = in ? expf(m - mm) * inv : 0.f;
-      const float sum = wave_sum(r);
-      const float q = in ? r / sum : 0.f;
-      const float mean = wave_sum(q * g);
-      d = q * (g - mean) * s1;
-    } else {
-      d = g * s * s1;
-    }
-  } else if (p.renorm) {
-    float mm = in ? x : -INFINITY;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
-    const float r = in ? expf(x - mm) : 0.f;
-    const float sum = wave_sum(r);
-    const float q = in ? r / sum : 0.f;
-    const float mean = wave_sum(q * g);
-    d = q * (g - mean);
-  } else {
-    d = g;
-  }
-  __threadfence_block();
-  __builtin_amdgcn_wave_barrier();
-  if (in) row[i] = d;
-  __threadfence_block();
-  __builtin_amdgcn_wave_barrier();
-  if (!dense) {
-    for (int e = lane; e < p.E; e += kWave) store_f(out, e, row[e]);
-    return;
-  }
-  for (int e = lane; e < p.E; e += kWave) {
-    const float v = load_f(l, e);
-    if (!(v <= (float)kMasked)) top = fmaxf(top, v);
-  }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  float total = 0.f, dot = 0.f;
-  for (int e = lane; e < p.E; e += kWave) {
-    const float v = load_f(l, e);
-    const float s = v <= (float)kMasked ? 0.f : expf(v - top);
-    total += s;
-    dot += s * row[e];
-  }
-  total = wave_sum(total);
-  dot = wave_sum(dot) / total;
-  for (int e = lane; e < p.E; e += kWave) {
-    const float v = load_f(l, e);
-    const float s = v <= (float)kMasked ? 0.f : expf(v - top) / total;
-    store_f(out, e, v <= (float)kMasked ? 0.f : s * (row[e] - dot));
-  }
-}
-
-template <typename LT>
+// With p = s / sum of the chosen s and c the scale:
+//   sigmoid                dl_k = c g_k s_k (1 - s_k)
+//   sigmoid, renormalised  dl_k = c p_k (g_k - sum_j p_j g_j) (1 - s_k)
+//   softmax, renormalised  dl_k = c p_k (g_k - sum_j p_j g_j)
+// for the chosen k alone, and for a plain softmax (DENSE) over all experts
+//   dl_e = s_e (G_e - sum_j s_j G_j), G_e = c g_e at the chosen, else 0.
+// A row is held by LPR lanes, W consecutive experts a lane and piece; the chosen
+// experts' values are spread over a row of LDS, and rows are written whole.
+template <typename LT, int LPR, int EPL, int W, bool DENSE>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(const LT* __restrict__ logits, int64_t T,
                                                                            int64_t ld, RouteParams p,
                                                                            const int32_t* __restrict__ idx,
                                                                            const float* __restrict__ dweights,
                                                                            LT* __restrict__ dlogits, int64_t ldd) {
-  extern __shared__ float lds_row[];
-  const int wave = threadIdx.x / kWave;
-  float* row = lds_row + wave * p.E;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < T; t += (int64_t)gridDim.x * kRouteWaves)
-    route_backward_row(logits + t * ld, p, idx + t * p.K, dweights + t * p.K, row, dlogits + t * ldd);
+  constexpr int RPW = kWave / LPR, P = EPL / W;
+  __shared__ __attribute__((aligned(16))) float lds_row[kRouteWaves * RPW][LPR * EPL];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int sub = lane & (LPR - 1);
+  float* row = lds_row[wave * RPW + lane / LPR];
+  for (int64_t r0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * RPW; r0 < T; r0 += (int64_t)gridDim.x * kRouteWaves * RPW) {
+    const int64_t t = min(r0 + lane / LPR, T - 1);  // rows past the last repeat it
+    const LT* l = logits + t * ld;
+    int i = -1;
+    float g = 0.f, x = 0.f;
+    if (sub < p.K) {
+      i = idx[t * p.K + sub];
+      g = dweights[t * p.K + sub] * p.scale;
+    }
+    const bool named = i >= 0 && i < p.E;
+    x = load_f(l, named ? i : 0);
+    const bool in = named && !(x <= (float)kMasked);
+    float v[P][W];
+    if (DENSE) {
+      Raw<LT, W> raw[P];
+#pragma unroll
+      for (int q = 0; q < P; q++) {
+        const int e = (q * LPR + sub) * W;
+        raw[q] = load_raw<W, false>(l + (e < p.E ? e : 0));
+      }
+#pragma unroll
+      for (int q = 0; q < P; q++) unpack(raw[q], v[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < P; q++)
+#pragma unroll
+      for (int j = 0; j < W; j++) row[(q * LPR + sub) * W + j] = 0.f;
+    g = in ? g : 0.f;
+
+    float d = g;  // DENSE: G
+    if (p.sigmoid) {
+      const float ex = exp_f(-fabsf(x)), inv = __builtin_amdgcn_rcpf(1.f + ex);
+      const float s = (x >= 0.f ? 1.f : ex) * inv, rest = (x >= 0.f ? ex : 1.f) * inv;  // s and 1 - s
+      if (p.renorm) {  // over the largest exp of the row, so that no score underflows
+        const float low = fminf(x, 0.f);
+        const float m = row_fmax<LPR>(in ? low : -INFINITY);
+        const float r = in ? exp_f(low - m) * inv : 0.f;
+        const float total = row_sum<LPR>(r);  // all lanes take part
+        const float q = in ? r / total : 0.f;
+        d = q * (g - row_sum<LPR>(q * g)) * rest;
+      } else {
+        d = g * s * rest;
+      }
+    } else if (!DENSE) {
+      const float m = row_fmax<LPR>(in ? x : -INFINITY);
+      const float r = in ? exp_f(x - m) : 0.f;
+      const float total = row_sum<LPR>(r);
+      const float q = in ? r / total : 0.f;
+      d = q * (g - row_sum<LPR>(q * g));
+    }
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    if (in) row[i] = d;
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+
+    float top = 0.f, scale = 0.f, dot = 0.f;
+    if (DENSE) {
+      top = (float)kMasked;
+#pragma unroll
+      for (int q = 0; q < P; q++)
+#pragma unroll
+        for (int j = 0; j < W; j++) {
+          const bool there = (q * LPR + sub) * W < p.E && !(v[q][j] <= (float)kMasked);
+          v[q][j] = there ? v[q][j] : -INFINITY;
+          top = fmaxf(top, v[q][j]);
+        }
+      top = row_fmax<LPR>(top);
+      float total = 0.f;
+#pragma unroll
+      for (int q = 0; q < P; q++)
+#pragma unroll
+        for (int j = 0; j < W; j++) {
+          v[q][j] = exp_f(v[q][j] - top);  // 0 where masked
+          total += v[q][j];
+        }
+      total = row_sum<LPR>(total);
+      scale = total == 0.f ? 0.f : 1.f / total;
+      dot = row_sum<LPR>(in ? exp_f(x - top) * g : 0.f) * scale;
+    }
+    LT* out = dlogits + t * ldd;
+#pragma unroll
+    for (int q = 0; q < P; q++) {
+      const int e = (q * LPR + sub) * W;
+      float f[W];
+#pragma unroll
+      for (int j = 0; j < W; j++) {
+        f[j] = row[e + j];
+        if (DENSE) f[j] = v[q][j] * scale * (f[j] - dot);
+      }
+      if (e < p.E && r0 + lane / LPR < T) store_vec<W, false>(out + e, f);
+    }
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+  }
 }
+
+template <typename LT, int LPR, int EPL>
+void launch_backward(const void* logits, int64_t T, int64_t ld, const RouteParams& p, const int32_t* idx,
+                     const float* dweights, void* dlogits, int64_t ldd, hipStream_t st) {
+  constexpr int W = EPL < 4 ? EPL : 4;
+  const bool dense = !p.sigmoid && !p.renorm;
+  auto f = p.E % W == 0 ? (dense ? route_backward_kernel<LT, LPR, EPL, W, true> : route_backward_kernel<LT, LPR, EPL, W, false>)
+                        : (dense ? route_backward_kernel<LT, LPR, EPL, 1, true> : route_backward_kernel<LT, LPR, EPL, 1, false>);
+  const int64_t rows = kRouteWaves * (kWave / LPR);
+  f<<<grid_of((T + rows - 1) / rows), kRouteWaves * kWave, 0, st>>>((const LT*)logits, T, ld, p, idx, dweights, (LT*)dlogits,
+                                                                   ldd);
+}
+
+// As few lanes as hold the row and the chosen; more of them where rows are few.
+template <typename LT>
+hipError_t route_backward(const void* logits, int64_t T, int64_t ld, const RouteParams& p, const int32_t* idx,
+                          const float* dweights, void* dlogits, int64_t ldd, hipStream_t st) {
+  auto f = T >= kManyRows && p.K <= 16 && p.E <= 64    ? launch_backward<LT, 16, 4>
+           : T >= kManyRows && p.K <= 16 && p.E <= 256 ? launch_backward<LT, 16, 16>
+           : p.E <= 256                                ? launch_backward<LT, 64, 4>
+                                                       : launch_backward<LT, 64, 16>;
+  f(logits, T, ld, p, idx, dweights, dlogits, ldd, st);
+  return hipGetLastError();
+}
+
 // ------------------------------------------------------------------ checks
 mxq_status check_config(const char* what, const mxq_route_config* c, int32_t E) {
   MXQ_REQUIRE(c != nullptr, "%s: config is NULL", what);
@@ -1070,15 +1116,9 @@ mxq_status mxq_route_backward(const void* logits, mxq_dtype dt, int64_t T, int32
   MXQ_REQUIRE_DEVICE();
   if (T == 0) return ok();
   const RouteParams p = params(cfg, E);
-  const unsigned grid = grid_of((T + kRouteWaves - 1) / kRouteWaves);
-  const size_t lds = (size_t)kRouteWaves * E * sizeof(float);
-  if (dt == MXQ_DT_F32)
-    route_backward_kernel<<<grid, kRouteWaves * kWave, lds, st>>>((const float*)logits, T, ld, p, idx, dweights,
-                                                                 (float*)dlogits, ldd);
-  else
-    route_backward_kernel<<<grid, kRouteWaves * kWave, lds, st>>>((const uint16_t*)logits, T, ld, p, idx, dweights,
-                                                                 (uint16_t*)dlogits, ldd);
-  return launched(hipGetLastError(), "mxq_route_backward");
+  return launched((dt == MXQ_DT_F32 ? route_backward<float> : route_backward<uint16_t>)(logits, T, ld, p, idx, dweights, dlogits,
+                                                                                       ldd, st),
+                  "mxq_route_backward");
 }
 
 }  // extern "C"
