@@ -24,7 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = 1024;
 constexpr int kPieces = kTile / (4 * kThreads);
 constexpr int kRun = 2 * kTile;
-constexpr int kTensors = 40;   // per launch: the descriptors travel as a kernel argument (< 4 KB)
+constexpr int kTensors = 48;   // per launch: the descriptors travel as a kernel argument, 4 KB at most
 static_assert(kTensors <= 64, "a wave looks its workgroup's tensor up, a tensor per lane");
 constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
 constexpr int64_t kMaxRun = 32 * kRun, kMaxElements = kMaxGrid * kMaxRun;
@@ -38,7 +38,7 @@ struct Tensor {
   uint8_t* vs;
   uint16_t* copy;
   int64_t n;
-  double decay;         // weight decay of this tensor
+  float decay;          // weight decay of this tensor
   uint32_t first_wg;    // of the launch
   uint32_t index;       // in the call
 };
@@ -59,6 +59,7 @@ struct Args {
   double log2_b1, log2_b2;
   const mxq_adamw_control* control;
 };
+static_assert(sizeof(Args) <= 4096, "what a kernel argument holds");
 
 // ------------------------------------------------------------------ random bits
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -428,7 +429,7 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
       const mxq_adamw_tensor& t = tensors[i];
       if (t.n == 0) continue;
       a.t[a.count++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, (uint16_t*)t.copy, t.n,
-                        cfg->weight_decay * t.decay_scale, (uint32_t)wgs, (uint32_t)i};
+                        (float)(cfg->weight_decay * t.decay_scale), (uint32_t)wgs, (uint32_t)i};
       wgs += (t.n + a.chunk - 1) / a.chunk;
     }
     if (a.count == 0) continue;

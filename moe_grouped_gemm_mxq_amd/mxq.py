@@ -421,7 +421,7 @@ def _need_float(t, name, dim=2):
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dims, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dim")
     return dt
 
@@ -509,8 +509,9 @@ def mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream=None):
 
 
 def _need_pairs(slot, weights):
-    _need(slot, torch.int32, "slot", 2)
-    _need_array(slot, "slot", torch.int32, slot.shape)
+    if isinstance(slot, torch.Tensor) and slot.dim() != 2:
+        raise ValueError(f"slot must have 2 dims, got {slot.dim()}")
+    _need_array(slot, "slot", torch.int32, getattr(slot, "shape", None))
     if weights is not None:
         _need_array(weights, "weights", torch.float32, slot.shape)
     return slot.shape
