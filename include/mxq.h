@@ -364,7 +364,8 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1, MXQ_SCORE_MAX_ENUM 
  *    -inf and both types' lowest values) masks its expert: score 0, never
  *    chosen, not counted by a softmax.
  *  - An expert ranks by its key: s + bias[e], or its logit where bias is
- *    NULL.  A NaN key ranks below every number.
+ *    NULL.  A NaN key ranks below every number, and one of -inf (a bias that
+ *    bars its expert) is not chosen.
  *  - n_group > 1 splits the experts into n_group equal runs; a group's total
  *    is the sum of its best `group_top` (1 or 2) s + bias (s without bias)
  *    over unmasked experts; only the topk_group best groups' experts can be
@@ -374,8 +375,8 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1, MXQ_SCORE_MAX_ENUM 
  *    64-bit arithmetic.  A row with fewer available experts than top_k ends
  *    in index -1 with weight 0.
  *  - The weight of a chosen expert is scale * s, or with renormalise
- *    scale * s / (sum of the chosen s) (0 if that sum is 0).  The bias has
- *    no part in it.  NaN and +inf logits follow the arithmetic. */
+ *    scale * s / (sum of the chosen s), taken so that scores which underflow
+ *    still have their ratio.  The bias has no part in it.  NaN and +inf logits follow the arithmetic. */
 typedef struct {
     int32_t score;       /* mxq_score */
     int32_t top_k;       /* 1 .. min(E, MXQ_MAX_TOPK) */

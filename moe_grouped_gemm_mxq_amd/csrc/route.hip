@@ -135,7 +135,13 @@ __device__ void route_row64(const LT* __restrict__ l, const float* __restrict__ 
   }
   double w = chosen >= 0 ? score(load_f(l, chosen)) : 0.0;
   if (p.renorm) {
-    const double sum = wave_sum(lane < p.K ? w : 0.0);
+    double sum = wave_sum(w);
+    if (sum == 0.0) {  // scores that underflow: over the largest of their exps instead
+      const double x = chosen >= 0 ? load_f(l, chosen) : -INFINITY;
+      const double low = p.sigmoid ? fmin(x, 0.0) : x, m = wave_max(low);
+      w = chosen >= 0 ? exp(low - m) / (p.sigmoid ? 1.0 + exp(-fabs(x)) : 1.0) : 0.0;
+      sum = wave_sum(w);
+    }
     w = sum == 0.0 ? 0.0 : w / sum;
   }
   if (lane < p.K) {
@@ -181,18 +187,22 @@ __host__ __device__ constexpr int32_t count_stride(int32_t E) {
   return s;
 }
 
-// LDS of the ranking: counts of up to kMaxOrderWaves waves, rows of E
-constexpr size_t order_lds(int waves, int E) { return (size_t)waves * E * sizeof(uint16_t); }
+// LDS of the ranking: 16-bit counts of up to kMaxOrderWaves waves, rows of E rounded up to 16 bytes
+__host__ __device__ constexpr int count_row(int E) { return (E + 7) / 8 * 8; }
+constexpr size_t order_lds(int waves, int E) { return (size_t)waves * count_row(E) * sizeof(uint16_t); }
 
 // exclusive sums of one value per thread over the workgroup; total: of all.  part: kMaxOrderWaves words
 __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int32_t& total) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+  // inclusive over the wave: lanes 1, 2, 4, 8 below within rows of 16 (0 where there is
+  // none), then the last lane of the row before, and of the 32 lanes before
   int32_t incl = v;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int32_t u = __shfl_up(incl, o);
-    if (lane >= o) incl += u;
-  }
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);
   if (lane == kWave - 1) part[wave] = incl;
   __syncthreads();
   int32_t off = 0;
@@ -208,7 +218,7 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int
 
 // A segment is one pair per thread, x its expert (E: none).  rank_in_wave: how many
 // earlier lanes have the same; the wave's count of each expert goes to `count`
-// [waves][E], which is zero before and read after a barrier.
+// [waves][count_row(E)], which is zero before and read after a barrier.
 __device__ __forceinline__ int rank_in_wave(int32_t x, int32_t E, uint16_t* count) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int bits = 32 - __builtin_clz(E);  // of 0 .. E
@@ -219,25 +229,29 @@ __device__ __forceinline__ int rank_in_wave(int32_t x, int32_t E, uint16_t* coun
     same &= set ? m : ~m;
   }
   const int rank = __popcll(same & ((1ull << lane) - 1));
-  if (x < E && rank == 0) count[wave * E + x] = (uint16_t)__popcll(same);
+  if (x < E && rank == 0) count[wave * count_row(E) + x] = (uint16_t)__popcll(same);
   return rank;
 }
-// counts of expert x -> pairs in earlier waves; returns the segment's
-__device__ __forceinline__ int32_t waves_exclusive(int x, int32_t E, uint16_t* count) {
-  const int waves = blockDim.x / kWave;
-  int32_t n[kMaxOrderWaves];
+// Counts of experts 2 i and 2 i + 1 -> pairs in earlier waves; returns the segment's, packed.
+// (A segment has at most 1024 pairs, so neither half carries into the other.)
+__device__ __forceinline__ uint32_t waves_exclusive(int i, int32_t E, uint16_t* count) {
+  const int waves = blockDim.x / kWave, row = count_row(E) / 2;
+  uint32_t* c = reinterpret_cast<uint32_t*>(count) + i;
+  uint32_t n[kMaxOrderWaves];
 #pragma unroll
-  for (int w = 0; w < kMaxOrderWaves; w++) n[w] = w < waves ? count[w * E + x] : 0;
-  int32_t run = 0;
+  for (int w = 0; w < kMaxOrderWaves; w++) n[w] = w < waves ? c[w * row] : 0;
+  uint32_t run = 0;
 #pragma unroll
   for (int w = 0; w < kMaxOrderWaves; w++) {
-    if (w < waves) count[w * E + x] = (uint16_t)run;
+    if (w < waves) c[w * row] = run;
     run += n[w];
   }
   return run;
 }
 __device__ __forceinline__ void clear_counts(int32_t E, uint16_t* count) {
-  for (int i = threadIdx.x; i < (int)(blockDim.x / kWave) * E; i += blockDim.x) count[i] = 0;
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int i = threadIdx.x; i < (int)(blockDim.x / kWave) * count_row(E) / 8; i += blockDim.x)
+    reinterpret_cast<u32x4*>(count)[i] = zero;
 }
 __device__ __forceinline__ int32_t expert_at(const int32_t* idx, int64_t i, int64_t e, int32_t E) {
   const int32_t x = i < e ? idx[i] : -1;
@@ -249,7 +263,7 @@ __device__ __forceinline__ void put_pair(int64_t i, int64_t e, int32_t x, int ra
   if (i >= e) return;
   int32_t row = -1;
   if (x < E) {
-    row = base[x] + count[threadIdx.x / kWave * E + x] + rank;
+    row = base[x] + count[threadIdx.x / kWave * count_row(E) + x] + rank;
     row_token[row] = (int32_t)((uint32_t)i / (uint32_t)K);  // T * K < 2^31
   }
   slot[i] = row;
@@ -271,9 +285,9 @@ __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* _
     counts[(int64_t)blockIdx.x * stride + x] = x < E ? (uint16_t)h[x] : 0;
 }
 
-// Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs.
+// Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs, at most `most` of them one expert's.
 __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                                int32_t chunks, int32_t per, int32_t E, int32_t stride,
+                                                                int32_t chunks, int32_t per, int32_t E, int32_t most,
                                                                 int32_t K,
                                                                 const uint16_t* __restrict__ counts,
                                                                 int32_t* __restrict__ group_end,
@@ -290,11 +304,29 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
   // Eight experts' counts a load; a row of counts by stride / 8 threads, the chunks dealt to
   // as many such runs of threads as the workgroup holds.  Whole numbers: the order
   // of the additions does not matter.
-  const int cols = stride / 8, runs = (int)blockDim.x / cols, run = t / cols, col = t - run * cols;
+  const int stride = count_stride(E), cols = stride / 8, runs = (int)blockDim.x / cols, run = t / cols, col = t - run * cols;
+  const int visits = (chunks + runs - 1) / runs;
+  // two sums a word where no half can carry, after the wave's runs are added up too
+  const bool packed = (int64_t)most * visits * (cols < kWave ? kWave / cols : 1) <= 0xFFFF;
+  const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  auto add2 = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, a) + __builtin_bit_cast(u16x2, b));
+  };
+  uint32_t a2[4] = {}, f2[4] = {};
   int32_t a[8] = {}, f[8] = {};
-  {
-    const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
+  if (packed) {
 #pragma unroll 8
+    for (int c = run; c < chunks; c += runs) {
+      const u32x4 v = c4[(int64_t)c * cols];
+      const uint32_t mine = c < first ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        a2[j] = add2(a2[j], v[j]);
+        f2[j] = add2(f2[j], v[j] & mine);
+      }
+    }
+  } else {
     for (int c = run; c < chunks; c += runs) {
       const u32x4 v = c4[(int64_t)c * cols];
       const uint32_t mine = c < first ? 0xFFFFFFFFu : 0u;
@@ -313,11 +345,28 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
   int rank = rank_in_wave(x, E, count);
   // the runs of a wave first: 64 lanes adding to the same few words one by one took 7 us
   if ((t & ~(kWave - 1)) / cols < chunks) {
-    for (int m = cols; m < kWave; m *= 2)
+    for (int m = cols; m < kWave; m *= 2) {
+      if (packed) {
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        a[j] += __shfl_xor(a[j], m);
-        f[j] += __shfl_xor(f[j], m);
+        for (int j = 0; j < 4; j++) {
+          a2[j] = add2(a2[j], __shfl_xor(a2[j], m));
+          f2[j] = add2(f2[j], __shfl_xor(f2[j], m));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          a[j] += __shfl_xor(a[j], m);
+          f[j] += __shfl_xor(f[j], m);
+        }
+      }
+    }
+    if (packed)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        a[2 * j] = a2[j] & 0xFFFFu;
+        a[2 * j + 1] = a2[j] >> 16;
+        f[2 * j] = f2[j] & 0xFFFFu;
+        f[2 * j + 1] = f2[j] >> 16;
       }
     if ((t & (kWave - 1)) < cols)
 #pragma unroll
@@ -328,7 +377,8 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
   }
   __syncthreads();
   const int32_t all = t < E ? sums[0][t] : 0, before = t < E ? sums[1][t] : 0;
-  int32_t segment = t < E ? waves_exclusive(t, E, count) : 0;
+  const int pairs = (E + 1) / 2;  // of experts
+  uint32_t segment = t < pairs ? waves_exclusive(t, E, count) : 0;
   int32_t total;
   const int32_t start = block_exclusive(all, part, total);
   if (t < E) {
@@ -341,13 +391,16 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
     s += blockDim.x;
     if (s >= e) break;
     __syncthreads();
-    if (t < E) base[t] += segment;
+    if (t < pairs) {
+      base[2 * t] += segment & 0xFFFFu;
+      base[2 * t + 1] += segment >> 16;
+    }
     clear_counts(E, count);
     x = expert_at(idx, s + t, e, E);
     __syncthreads();
     rank = rank_in_wave(x, E, count);
     __syncthreads();
-    if (t < E) segment = waves_exclusive(t, E, count);
+    if (t < pairs) segment = waves_exclusive(t, E, count);
     __syncthreads();
   }
   for (int64_t i = total + (int64_t)blockIdx.x * blockDim.x + t; i < N; i += (int64_t)gridDim.x * blockDim.x)
@@ -730,7 +783,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       const int32_t start = carry + block_exclusive(c, part_sums, total);
       carry += total;
       if (e < p.E) {
-        waves_exclusive(e, p.E, count);
+        if (e < (p.E + 1) / 2) waves_exclusive(e, p.E, count);
         hist[e] = start;
         o.group_end[e] = start + c;
       }
@@ -745,6 +798,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
 struct OrderPlan {
   int32_t chunks;
   int64_t chunk;  // pairs
+  int32_t most;   // of them with one expert
 };
 
 // Workgroups and threads of order_kernel for these chunks
@@ -754,7 +808,7 @@ hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, Ord
   const int64_t most = N / kMaxOrderThreads < 128 ? N / kMaxOrderThreads + 1 : 128;
   const int32_t per = (int32_t)((op.chunks + most - 1) / most);
   const int32_t grid = (op.chunks + per - 1) / per;
-  order_kernel<<<grid, kMaxOrderThreads, order_lds(kMaxOrderWaves, E), st>>>(idx, N, op.chunk, op.chunks, per, E, count_stride(E), K, counts,
+  order_kernel<<<grid, kMaxOrderThreads, order_lds(kMaxOrderWaves, E), st>>>(idx, N, op.chunk, op.chunks, per, E, op.most, K, counts,
                                                                             group_end, row_token, slot);
   return hipGetLastError();
 }
@@ -764,7 +818,7 @@ OrderPlan order_plan(int64_t N) {
   if (chunk < kMaxOrderThreads) chunk = kMaxOrderThreads;
   if (chunk > kMaxChunkPairs) chunk = kMaxChunkPairs;
   const int64_t c = (N + chunk - 1) / chunk;
-  return {(int32_t)(c < 1 ? 1 : c), chunk};
+  return {(int32_t)(c < 1 ? 1 : c), chunk, (int32_t)chunk};
 }
 
 hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, int32_t* group_end,
@@ -827,14 +881,14 @@ hipError_t route_fast(RouteArgs a) {
   const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
   a.o.mode = !order ? 0 : alone ? 2 : 1;
   const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E)};
-  const size_t lds = (size_t)32 * a.p.E;  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
+  const size_t lds = std::max(order_lds(kMaxOrderWaves, a.p.E), (size_t)32 * a.p.E);  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
   auto f = a.bias                                         ? route_fast_kernel<LT, LPR, EPL, kBiased>
            : a.p.n_group > 1 && a.p.group_top == 2 ? route_fast_kernel<LT, LPR, EPL, kScoredGroups>
                                                    : route_fast_kernel<LT, LPR, EPL, kLogits>;
   f<<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh, a.idx, a.weights, a.o);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.o.mode != 1) return e;
-  const OrderPlan op = {(int32_t)grid, rows * a.p.K};
+  const OrderPlan op = {(int32_t)grid, rows * a.p.K, (int32_t)rows};  // a row names an expert once
   return launch_order(a.idx, a.T * a.p.K, a.p.K, a.p.E, op, a.o.group_end, a.o.row_token, a.o.slot, a.o.counts, a.st);
 }
 

@@ -447,12 +447,14 @@ def _raw(t):
     return None if t is None else t.data_ptr()
 
 
-@functools.lru_cache(maxsize=256)
 def route_config(top_k, score="softmax", n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0):
     """mxq_route_config; score "softmax" or "sigmoid"."""
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}; one of 'softmax', 'sigmoid'")
     return RouteConfig(_SCORES[score], top_k, n_group, topk_group, group_top, int(bool(renormalise)), float(scale))
+
+
+_kept_config = functools.lru_cache(maxsize=256)(route_config)  # the helpers' own, never handed out
 
 
 @functools.lru_cache(maxsize=256)
@@ -693,7 +695,7 @@ def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1,
           order=True, out=None, stream=None):
     """Route tokens: {"idx", "weights"} and, with order, {"group_end", "row_token", "slot"} (the expert order the grouped
     entry points and combine take).  out: a dict of such buffers to write to ("workspace" may be among them)."""
-    cfg = route_config(top_k, score, n_group, topk_group, group_top, renormalise, scale)
+    cfg = _kept_config(top_k, score, n_group, topk_group, group_top, renormalise, scale)
     T, E = logits.shape
     if out is None:
         i32 = functools.partial(torch.empty, dtype=torch.int32, device=logits.device)
@@ -721,7 +723,7 @@ def expert_order(idx, E, stream=None):
 
 def route_backward(logits, idx, dweights, *, score="softmax", renormalise=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
-    cfg = route_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
+    cfg = _kept_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
     dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream)
     return dlogits

@@ -27,12 +27,13 @@ def route(logits, K, score="softmax", bias=None, n_group=1, topk_group=1, group_
             per = E // n_group
             groups = []
             for g in range(n_group):
-                k = np.sort(key[g * per:(g + 1) * per][~off[g * per:(g + 1) * per]])[::-1][:group_top]
+                k = key[g * per:(g + 1) * per][~off[g * per:(g + 1) * per]]
+                k = np.sort(k[k > -np.inf])[::-1][:group_top]
                 groups.append(k.sum() if len(k) else -np.inf)
             kept = [g for g in sorted(range(n_group), key=lambda g: (-groups[g], g))[:topk_group]]
             order = l if bias is None else key
             order = np.where(np.isnan(order), -1e300, order)
-            allowed = [e for e in range(E) if not off[e] and e // per in kept]
+            allowed = [e for e in range(E) if not off[e] and order[e] > -np.inf and e // per in kept and groups[e // per] > -np.inf]
             chosen = sorted(allowed, key=lambda e: (-order[e], e))[:K]
             w = s[chosen]
             if renormalise:

@@ -117,6 +117,34 @@ def test_route_not_finite(score):
         check_route(x, 6, b, score=score, renormalise=True, n_group=5, topk_group=3, group_top=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_bias_not_finite(score):
+    x = logits_of(70, 40, torch.float32, 6, 0.2)
+    for value in (float("nan"), float("inf"), -float("inf"), 3e38):
+        bias = torch.linspace(0.2, -0.2, 40)
+        bias[[3, 17]] = value
+        check_route(x, 5, bias.cuda(), score=score)
+        check_route(x, 5, bias.cuda(), score=score, n_group=4, topk_group=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scores_that_underflow_keep_their_ratio(score):
+    """A bias that forces experts whose scores are below fp32 (and, at -800, below fp64): softmax of the chosen logits."""
+    for far in (-95.0, -800.0):
+        x = torch.zeros(3, 32)
+        x[:, 8:12] = far + torch.tensor([0.0, 1.0, -1.0, 0.5])
+        x[2, 0] = float("inf") if score == "sigmoid" else 0.0  # a row that is taken to fp64
+        bias = torch.zeros(32)
+        bias[8:12] = 5.0
+        got = mxq().route(x.cuda(), 4, score=score, bias=bias.cuda())
+        for t in range(3):
+            i = host(got["idx"])[t].astype(int)
+            assert sorted(i) == [8, 9, 10, 11]
+            want = np.exp(f64(x)[t, i] - far)
+            want /= want.sum()
+            assert np.all(np.abs(f64(got["weights"])[t] - want) <= (4 * 2 * abs(far) + 40) * U * want)
+
+
 def test_route_ties_go_to_the_lowest_index():
     for dtype in (torch.float32, torch.bfloat16):
         x = torch.zeros(5, 96, dtype=dtype, device="cuda")
