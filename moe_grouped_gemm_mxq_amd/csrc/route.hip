@@ -418,6 +418,7 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
 struct Shape {
   int32_t lpg_log2;  // lanes per group
   int32_t stride;    // of the rows of counts
+  int32_t full;      // every lane has EPL experts
 };
 
 struct OrderOut {
@@ -558,16 +559,12 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
 #pragma unroll
           for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
       }
-      bool odd = false;  // NaN or +inf: the whole row in fp64
+      if (!sh.full)
 #pragma unroll
-      for (int j = 0; j < EPL; j++) {
-        x[j] = j < n ? x[j] : -INFINITY;
-        odd |= !(x[j] < INFINITY);
-        x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
-      }
+        for (int j = 0; j < EPL; j++) x[j] = j < n ? x[j] : -INFINITY;
 
       float top = 0.f, inv_total = 0.f;
-      if (stats) {
+      if (stats) {  // masked logits add exp(-inf)
         float m = x[0];
 #pragma unroll
         for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
@@ -578,21 +575,25 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         s = row_sum<LPR>(s);
         inv_total = s > 0.f ? 1.f / s : 0.f;
       }
-      if (KEYS != kLogits) {
+      bool odd = false;  // a NaN or an infinity that is no mask: the whole row in fp64
+      if (KEYS == kLogits) {
+#pragma unroll
+        for (int j = 0; j < EPL; j++) odd |= !(x[j] < INFINITY);
+      } else {
+        float zero = 0.f;  // NaN after any that is not finite
 #pragma unroll
         for (int j = 0; j < EPL; j++) {
-          float s;
-          if (p.sigmoid) {
-            const float e = exp_f(-fabsf(x[j]));
-            s = (x[j] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
-          } else {
-            s = exp_f(x[j] - top) * inv_total;
-          }
+          // 1 / (1 + exp(-x)) for either sign: where exp(-x) is large its relative error is that of the score
+          float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-x[j])) : exp_f(x[j] - top) * inv_total;
           if (KEYS == kBiased) s += k[j];
-          odd |= x[j] > -INFINITY && !(fabsf(s) < INFINITY);
-          k[j] = x[j] > -INFINITY ? s : -INFINITY;
+          zero = __builtin_fmaf(s, 0.f, zero);
+          k[j] = x[j] <= (float)kMasked ? -INFINITY : s;
         }
+        odd = zero != 0.f;
       }
+      if (KEYS != kBiased)
+#pragma unroll
+        for (int j = 0; j < EPL; j++) x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
 
       // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias; without
       // a bias a softmax's up to its sum, which orders them as well)
@@ -618,7 +619,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
 #pragma unroll
         for (int j = 0; j < EPL; j++) {
           const float f = KEYS == kLogits ? x[j] : k[j];
-          b = fmaxf(b, fminf(a, f));
+          b = __builtin_amdgcn_fmed3f(a, b, f);  // a >= b: the second of the three
           a = fmaxf(a, f);
         }
         for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
@@ -680,39 +681,44 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         const float f = KEYS == kBiased ? k[j] : x[j];
         const uint32_t u = ordered(f);
         key[j] = EXACT ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
-        key[j] = kept && f > -INFINITY ? key[j] : 0u;
       }
-      uint32_t below = 0, local = 0;  // the lane's largest key below `below`
+      constexpr uint32_t NONE = 0x007FFFFFu;   // keys of -inf and 0 lie here and below
+      uint32_t below = 0, local = 0;           // the lane's largest key below `below`
       auto next_local = [&] {
-        uint32_t d = 0u - below;  // key 0: none
+        uint32_t d = 0u - below;
 #pragma unroll
         for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
-        local = d + below;
+        local = kept ? d + below : 0u;
       };
       next_local();
-      int chosen = -1;
+      int chosen_lane = 0;
       uint32_t chosen_key = 0;
       auto choose = [&](int r) {
         const uint32_t m = row_max<LPR>(local);
-        const uint64_t who = __ballot(local == m && m != 0) >> first_lane;
+        const uint64_t who = __ballot(local == m) >> first_lane;
         const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ROW))) - 1;
-        const int e = EXACT ? 0xFFFF - (int)(m & 0xFFFFu)
-                            : (win >> sh.lpg_log2) * per + (win & ((1 << sh.lpg_log2) - 1)) * EPL + (int)(LOW - (m & LOW));
         if (sub == r) {
-          chosen = m ? e : -1;
+          chosen_lane = win;
           chosen_key = m;
         }
         if (sub == win) below = m;
         next_local();
       };
       for (int r = 0; r < p.K; r++) choose(r);
+      auto expert = [&] {
+        const int e = EXACT ? 0xFFFF - (int)(chosen_key & 0xFFFFu)
+                            : (chosen_lane >> sh.lpg_log2) * per + (chosen_lane & ((1 << sh.lpg_log2) - 1)) * EPL +
+                                  (int)(LOW - (chosen_key & LOW));
+        return chosen_key > NONE ? e : -1;
+      };
+      int chosen = expert();
 
       // Neighbours that fp32 leaves open (the same key but for the place, or scores too
       // close): they and as many more as may belong among the first K are put into the
       // order of their exact keys.
       if (!EXACT) {
         auto close = [&](uint32_t hi, uint32_t lo) {
-          if (lo == 0) return false;
+          if (lo <= NONE) return false;
           if (KEYS != kBiased) return ((hi ^ lo) & ~LOW) == 0;
           // twice a score's error (4 or 42 half steps), the sums' roundings, the places' bits
           const float x = unordered(hi), y = unordered(lo);
@@ -731,6 +737,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
             rest = row_max<LPR>(local);
           }
           odd |= close(last, rest);
+          chosen = expert();
           const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
           double dk = -INFINITY;
           if (sub < have && chosen >= 0) dk = KEYS == kBiased ? exact_key(chosen, dsum, true) : (double)load_f(l, chosen);
@@ -880,7 +887,8 @@ hipError_t route_fast(RouteArgs a) {
   const int64_t rows = (int64_t)waves * RPW;
   const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
   a.o.mode = !order ? 0 : alone ? 2 : 1;
-  const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E)};
+  const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E),
+                    (EPL * LPR) >> ceil_log2(a.p.n_group) == a.p.E / a.p.n_group && 1 << ceil_log2(a.p.n_group) == a.p.n_group};
   const size_t lds = std::max(order_lds(kMaxOrderWaves, a.p.E), (size_t)32 * a.p.E);  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
   auto f = a.bias                                         ? route_fast_kernel<LT, LPR, EPL, kBiased>
            : a.p.n_group > 1 && a.p.group_top == 2 ? route_fast_kernel<LT, LPR, EPL, kScoredGroups>
