@@ -410,37 +410,45 @@ _DTYPES = {torch.float32: MXQ_DT_F32, torch.bfloat16: MXQ_DT_BF16}
 _SCORES = {"softmax": MXQ_SCORE_SOFTMAX, "sigmoid": MXQ_SCORE_SIGMOID, 0: MXQ_SCORE_SOFTMAX, 1: MXQ_SCORE_SIGMOID}
 
 
-def _need_float(t, name, dim=2):
-    """Type code of a float matrix with unit stride along its last dim."""
+def _need_float(t, name):
+    """Type code of a float matrix on the device with unit stride along its last dim."""
+    try:
+        dt = _DTYPES[t.dtype]
+        if t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
+            return dt
+    except (AttributeError, KeyError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
+    if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dims, got {t.dim()}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have unit stride along its last dim")
-    return dt
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    raise ValueError(f"{name} must have unit stride along its last dim")
 
 
 def _need_array(t, name, dtype, shape):
     """Device tensor of this type and shape, contiguous."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _row_stride(t):
     """Row stride the C entry points take (the stride of a dim of size 1 or 0 says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
 
 
 def _raw(t):
@@ -724,24 +732,24 @@ def expert_order(idx, E, stream=None):
 def route_backward(logits, idx, dweights, *, score="softmax", renormalise=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
     cfg = _kept_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dlogits = logits.new_empty(logits.shape)
     mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream)
     return dlogits
 
 
 def combine(y, slot, weights=None, dtype=torch.bfloat16, stream=None):
     """The experts' rows y [rows][H] back in token order: [T][H] of `dtype`."""
-    out = torch.empty((slot.shape[0], y.shape[1]), dtype=dtype, device=y.device)
+    out = y.new_empty((slot.shape[0], y.shape[1]), dtype=dtype)
     mxq_combine(y, slot, weights, out, stream)
     return out
 
 
 def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=None):
     """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights."""
-    dy = torch.empty((rows, dout.shape[1]), dtype=dtype or dout.dtype, device=dout.device)
+    dy = dout.new_empty((rows, dout.shape[1]), dtype=dtype or dout.dtype)
     dw = None
     if y is not None and weights is not None:
-        dw = torch.empty(slot.shape, dtype=torch.float32, device=dout.device)
+        dw = weights.new_empty(slot.shape)
     mxq_combine_backward(dout, slot, rows, dy, dw, weights, y if dw is not None else None, stream)
     return dy, dw
 
