@@ -176,8 +176,11 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel64(const LT* _
 // of the expert, across waves by their counts.  No atomics order anything, so the
 // result is always the same.
 constexpr int kMaxOrderThreads = 1024, kMaxOrderWaves = kMaxOrderThreads / kWave;
-constexpr int kMaxChunks = 512;         // while a chunk then has at most
-constexpr int kMaxChunkPairs = 1 << 15;  // this many pairs: counts are 16-bit
+constexpr int kMaxChunkPairs = 1 << 15;  // counts are 16-bit
+// Counts of all chunks, read whole by every workgroup of order_kernel: a chunk more costs
+// each of them its row.  16384 x 8 pairs of 1024 experts, counted by 1024-pair chunks of
+// the router (512 KB), took 56 us in all, with 64 chunks counted on their own 39 us.
+constexpr int64_t kCountBytes = 160 << 10;
 static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
 // elements of a chunk's row of counts: a power of two of 16-byte loads
@@ -823,29 +826,30 @@ hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, Ord
   return hipGetLastError();
 }
 
-OrderPlan order_plan(int64_t N) {
-  int64_t chunk = (N + kMaxChunks - 1) / kMaxChunks;
-  if (chunk < kMaxOrderThreads) chunk = kMaxOrderThreads;
-  if (chunk > kMaxChunkPairs) chunk = kMaxChunkPairs;
+int64_t chunks_that_fit(int32_t E) { return kCountBytes / (count_stride(E) * (int64_t)sizeof(uint16_t)); }
+
+OrderPlan order_plan(int64_t N, int32_t E) {
+  const int64_t most = std::min<int64_t>(chunks_that_fit(E), 512);
+  const int64_t chunk = std::min<int64_t>(std::max<int64_t>((N + most - 1) / most, 512), kMaxChunkPairs);
   const int64_t c = (N + chunk - 1) / chunk;
   return {(int32_t)(c < 1 ? 1 : c), chunk, (int32_t)chunk};
 }
 
 hipError_t launch_expert_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, int32_t* group_end,
                                int32_t* row_token, int32_t* slot, uint16_t* counts, hipStream_t st) {
-  const OrderPlan op = order_plan(N);
+  const OrderPlan op = order_plan(N, E);
   hist_kernel<<<op.chunks, kMaxOrderThreads, 0, st>>>(idx, N, op.chunk, E, count_stride(E), counts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_order(idx, N, K, E, op, group_end, row_token, slot, counts, st);
 }
 
+constexpr int64_t kFastRows = 1 << 25;  // of route_fast: 64 lanes each, in a grid of fewer than 2^32 threads
+
 // Largest number of chunks that a call on these sizes cuts its pairs into: order_plan's,
 // or one for each of route_fast's workgroups.
-int64_t max_chunks(int64_t T, int32_t K) {
-  const int64_t rows = T <= 4 * kMaxChunks ? T / 4 + 1 : T / 16 < kMaxChunks ? kMaxChunks + 1 : T / 16 + 1;
-  const int64_t plan = order_plan(T * K).chunks;
-  return rows > plan ? rows : plan;
+int64_t max_chunks(int64_t T, int32_t K, int32_t E) {
+  return std::max<int64_t>(order_plan(T * K, E).chunks, std::min<int64_t>(chunks_that_fit(E), T / 4 + 1));
 }
 
 int ceil_log2(int v) {
@@ -861,7 +865,6 @@ bool holds(const RouteParams& p) {
   const int lanes = LPR >> ceil_log2(p.n_group);
   return lanes >= 1 && lanes * EPL >= p.E / p.n_group && p.K <= LPR;
 }
-constexpr int64_t kFastRows = 1 << 25;  // 64 lanes each, in a grid of fewer than 2^32 threads
 
 constexpr int64_t kManyRows = 4096;
 
@@ -882,14 +885,17 @@ hipError_t route_fast(RouteArgs a) {
   const bool order = a.o.group_end != nullptr;
   const int64_t units = (a.T + RPW - 1) / RPW;  // waves' worth of rows
   // One workgroup does it all where it holds the rows and their pairs are one segment of
-  // the ranking.  Else workgroups of 4 waves, of 16 where the expert order would have
-  // many chunks to add up.
+  // the ranking.  Else workgroups of 4 waves, of 16 where only their counts are few enough
+  // to be added up; where not even theirs are, the order is taken from idx afterwards.
   const bool alone = order && units <= 16 && a.T * a.p.K <= kMaxOrderThreads;
   const int64_t pair_waves = (a.T * a.p.K + kWave - 1) / kWave;
-  const int waves = alone ? (int)std::max<int64_t>({units, pair_waves, 1}) : order && units > 4 * kMaxChunks ? 16 : 4;
+  auto chunks = [&](int64_t waves) { return (units + waves - 1) / waves; };
+  const int waves = alone ? (int)std::max<int64_t>({units, pair_waves, 1})
+                          : order && chunks(4) > chunks_that_fit(a.p.E) && chunks(16) <= chunks_that_fit(a.p.E) ? 16 : 4;
   const int64_t rows = (int64_t)waves * RPW;
-  const int64_t grid = alone ? 1 : (a.T + rows - 1) / rows;
-  a.o.mode = !order ? 0 : alone ? 2 : 1;
+  const int64_t grid = alone ? 1 : chunks(waves);
+  const bool counts = order && !alone && grid <= chunks_that_fit(a.p.E);
+  a.o.mode = alone ? 2 : counts ? 1 : 0;
   const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E),
                     (EPL * LPR) >> ceil_log2(a.p.n_group) == a.p.E / a.p.n_group && 1 << ceil_log2(a.p.n_group) == a.p.n_group};
   const size_t lds = std::max(order_lds(kMaxOrderWaves, a.p.E), (size_t)32 * a.p.E);  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
@@ -898,7 +904,9 @@ hipError_t route_fast(RouteArgs a) {
                                                    : route_fast_kernel<LT, LPR, EPL, kLogits>;
   f<<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh, a.idx, a.weights, a.o);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.o.mode != 1) return e;
+  if (e != hipSuccess || !order || alone) return e;
+  if (!counts)
+    return launch_expert_order(a.idx, a.T * a.p.K, a.p.K, a.p.E, a.o.group_end, a.o.row_token, a.o.slot, a.o.counts, a.st);
   const OrderPlan op = {(int32_t)grid, rows * a.p.K, (int32_t)rows};  // a row names an expert once
   return launch_order(a.idx, a.T * a.p.K, a.p.K, a.p.E, op, a.o.group_end, a.o.row_token, a.o.slot, a.o.counts, a.st);
 }
@@ -1119,7 +1127,7 @@ extern "C" {
 
 int64_t mxq_expert_order_workspace(int64_t T, int32_t top_k, int32_t E) {
   if (T < 0 || top_k < 1 || top_k > MXQ_MAX_TOPK || E < 1 || E > MXQ_MAX_GROUPS || !pairs_ok(T, top_k)) return 0;
-  return (max_chunks(T, top_k) * count_stride(E) * (int64_t)sizeof(uint16_t) + 15) / 16 * 16;
+  return (max_chunks(T, top_k, E) * count_stride(E) * (int64_t)sizeof(uint16_t) + 15) / 16 * 16;
 }
 
 mxq_status mxq_expert_order(const int32_t* idx, int64_t T, int32_t top_k, int32_t E, int32_t* group_end,
