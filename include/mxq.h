@@ -350,10 +350,20 @@ mxq_status mxq_validate_group_end(const int32_t* group_end, int32_t G, int64_t T
  * step of an MoE layer.  T = 0 tokens (and tensors without elements) are
  * valid; pointers of empty arrays may then be NULL. */
 
-/* element type of a float tensor argument */
-typedef enum { MXQ_DT_F32 = 0, MXQ_DT_BF16 = 1, MXQ_DT_MAX_ENUM = 0x7FFFFFFF } mxq_dtype;
+/* element type of a float tensor argument (this and the enums below span every int32) */
+typedef enum {
+    MXQ_DT_F32 = 0,
+    MXQ_DT_BF16 = 1,
+    MXQ_DT_MIN_ENUM = -0x7FFFFFFF - 1,
+    MXQ_DT_MAX_ENUM = 0x7FFFFFFF
+} mxq_dtype;
 
-typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1, MXQ_SCORE_MAX_ENUM = 0x7FFFFFFF } mxq_score;
+typedef enum {
+    MXQ_SCORE_SOFTMAX = 0,
+    MXQ_SCORE_SIGMOID = 1,
+    MXQ_SCORE_MIN_ENUM = -0x7FFFFFFF - 1,
+    MXQ_SCORE_MAX_ENUM = 0x7FFFFFFF
+} mxq_score;
 
 #define MXQ_MAX_TOPK 32          /* largest top_k */
 #define MXQ_MAX_ROUTE_GROUPS 64  /* largest n_group */
@@ -446,7 +456,12 @@ mxq_status mxq_combine_backward(const void* dout, mxq_dtype dt, int64_t ldd, con
 
 /* State format of mxq_adamw: fp32, or MXFP8: E4M3 codes with an E8M0 scale
  * byte for every 32 consecutive elements of the tensor. */
-typedef enum { MXQ_ADAMW_F32 = 0, MXQ_ADAMW_MXFP8 = 1, MXQ_ADAMW_MAX_ENUM = 0x7FFFFFFF } mxq_adamw_format;
+typedef enum {
+    MXQ_ADAMW_F32 = 0,
+    MXQ_ADAMW_MXFP8 = 1,
+    MXQ_ADAMW_MIN_ENUM = -0x7FFFFFFF - 1,
+    MXQ_ADAMW_MAX_ENUM = 0x7FFFFFFF
+} mxq_adamw_format;
 
 /* One tensor of n contiguous elements.  fp32 arrays 4-byte aligned, bf16 2. */
 typedef struct {
