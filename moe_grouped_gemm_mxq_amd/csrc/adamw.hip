@@ -13,21 +13,21 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256;
-// A workgroup passes over its elements a tile at a time, four a thread, so that a
-// wave's loads are unbroken runs.  More pieces per thread and longer runs per
-// workgroup measured slower (940M fp32 weights with MXFP8 states and a copy /
-// 147M bf16 weights with fp32 states): tile and run of 1024 and 2048 2.76 /
-// 0.534 ms, 1024 and 8192 2.84 / 0.559, 2048 and 4096 2.78 / 0.568, 4096 and
-// 65536 2.95 / 0.591 -- neighbouring workgroups run together, and short runs keep
-// what they touch close together.  A run of one tile (3.02 / 0.538) pays a table
-// of scales per tile.  Ordinary instead of non-temporal loads and stores: 2.90 / 0.583.
-constexpr int kTile = 1024;
-constexpr int kPieces = kTile / (4 * kThreads);
-constexpr int kRun = 2 * kTile;
+// A workgroup takes one tile: kPieces pieces of four elements a thread, so that a wave's
+// loads are unbroken runs.  Neighbouring workgroups run together, so short tiles keep
+// what is touched at a time close together, but each pays a table of scales (150
+// instructions a thread).  940M fp32 weights with MXFP8 states and a copy / 147M bf16
+// weights with fp32 states / 200M bf16 weights and gradients with MXFP8 states, on
+// one part: 2048 elements in two pieces 2.93 ms / 554 / 422 us, in two passes of
+// one piece 3.03 / 562 / 423, by 512 threads 2.85 / 550 / 487, 4096 in four pieces
+// 3.01 / 554 / 411; runs of 8192 or more lose 5 to 10%.  Ordinary instead of
+// non-temporal loads and stores lose 5%.
+constexpr int kPieces = 2;
+constexpr int kTile = kPieces * 4 * kThreads;
 constexpr int kTensors = 48;   // per launch: the descriptors travel as a kernel argument, 4 KB at most
 static_assert(kTensors <= 64, "a wave looks its workgroup's tensor up, a tensor per lane");
 constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
-constexpr int64_t kMaxRun = 32 * kRun, kMaxElements = kMaxGrid * kMaxRun;
+constexpr int64_t kMaxRun = 32 * kTile, kMaxElements = kMaxGrid * kMaxRun;
 
 struct Tensor {
   void* p;
@@ -406,17 +406,14 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
   int32_t i = 0;
   while (i < n_tensors) {
     int32_t end = i;  // the launch takes tensors i .. end - 1
-    int64_t tiles = 0, runs = 0;
+    int64_t runs = 0;
     for (int32_t count = 0; end < n_tensors && count < kTensors; end++) {
       const int64_t n = tensors[end].n;
       if (runs + (n + kMaxRun - 1) / kMaxRun > kMaxGrid) break;
       runs += (n + kMaxRun - 1) / kMaxRun;
-      tiles += (n + kTile - 1) / kTile;
       count += n > 0;
     }
-    // one tile per workgroup while that leaves CUs without one, and longer runs than
-    // kRun only where the grid would not hold the workgroups
-    a.chunk = tiles < 1024 ? kTile : kRun;
+    a.chunk = kTile;  // more only where the grid would not hold the workgroups
     auto fits = [&] {
       int64_t w = 0;
       for (int32_t j = i; j < end; j++) w += (tensors[j].n + a.chunk - 1) / a.chunk;
