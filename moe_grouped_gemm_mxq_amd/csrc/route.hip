@@ -536,244 +536,243 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
   if (tid == 0) slow_count = 0;
   __syncthreads();
   if (r0 + wave * RPW < T) {
-      const int64_t t = r0 + wave * RPW + lane / LPR;
-      const bool live = t < T;
-      const LT* l = logits + (live ? t : r0) * ld;
-      const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
-      const int e0 = g * per + part * EPL;  // the lane's experts: e0 .. e0 + n - 1
-      const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
+    const int64_t t = r0 + wave * RPW + lane / LPR;
+    const bool live = t < T;
+    const LT* l = logits + (live ? t : r0) * ld;
+    const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
+    const int e0 = g * per + part * EPL;  // the lane's experts: e0 .. e0 + n - 1
+    const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
 
-      // logits; masked and absent ones -inf
-      float x[EPL];
-      float k[EPL];  // scores + bias
-      if (EPL % 4 == 0 && per % 4 == 0) {
-        Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
+    // logits; masked and absent ones -inf
+    float x[EPL];
+    float k[EPL];  // scores + bias
+    if (EPL % 4 == 0 && per % 4 == 0) {
+      Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
 #pragma unroll
-        for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
-        if (KEYS == kBiased)
+      for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
+      if (KEYS == kBiased)
 #pragma unroll
-          for (int q = 0; q < EPL / 4; q++) unpack(load_raw<4, false>(bias + (4 * q < n ? e0 + 4 * q : 0)), &k[4 * q]);
+        for (int q = 0; q < EPL / 4; q++) unpack(load_raw<4, false>(bias + (4 * q < n ? e0 + 4 * q : 0)), &k[4 * q]);
 #pragma unroll
-        for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
-      } else {
+      for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
-        if (KEYS == kBiased)
+      for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
+      if (KEYS == kBiased)
 #pragma unroll
-          for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
-      }
-      if (!sh.full)
+        for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
+    }
+    if (!sh.full)
 #pragma unroll
-        for (int j = 0; j < EPL; j++) x[j] = j < n ? x[j] : -INFINITY;
+      for (int j = 0; j < EPL; j++) x[j] = j < n ? x[j] : -INFINITY;
 
-      float top = 0.f, inv_total = 0.f;
-      if (stats) {  // masked logits add exp(-inf)
-        float m = x[0];
+    float top = 0.f, inv_total = 0.f;
+    if (stats) {  // masked logits add exp(-inf)
+      float m = x[0];
 #pragma unroll
-        for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
-        top = fmaxf(row_fmax<LPR>(m), (float)kMasked);
-        float s = 0.f;
+      for (int j = 1; j < EPL; j++) m = fmaxf(m, x[j]);
+      top = fmaxf(row_fmax<LPR>(m), (float)kMasked);
+      float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; j++) s += exp_f(x[j] - top);
-        s = row_sum<LPR>(s);
-        inv_total = s > 0.f ? 1.f / s : 0.f;
-      }
-      bool odd = false;  // a NaN or an infinity that is no mask: the whole row in fp64
-      if (KEYS == kLogits) {
+      for (int j = 0; j < EPL; j++) s += exp_f(x[j] - top);
+      s = row_sum<LPR>(s);
+      inv_total = s > 0.f ? 1.f / s : 0.f;
+    }
+    bool odd = false;  // a NaN or an infinity that is no mask: the whole row in fp64
+    if (KEYS == kLogits) {
 #pragma unroll
-        for (int j = 0; j < EPL; j++) odd |= !(x[j] < INFINITY);
-      } else {
-        float zero = 0.f;  // NaN after any that is not finite
-#pragma unroll
-        for (int j = 0; j < EPL; j++) {
-          // 1 / (1 + exp(-x)) for either sign: where exp(-x) is large its relative error is that of the score
-          float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-x[j])) : exp_f(x[j] - top) * inv_total;
-          if (KEYS == kBiased) s += k[j];
-          zero = __builtin_fmaf(s, 0.f, zero);
-          k[j] = x[j] <= (float)kMasked ? -INFINITY : s;
-        }
-        odd = zero != 0.f;
-      }
-      if (KEYS != kBiased)
-#pragma unroll
-        for (int j = 0; j < EPL; j++) x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
-
-      // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias; without
-      // a bias a softmax's up to its sum, which orders them as well)
-      auto exp_sum = [&] {
-        double s = 0.0;
-#pragma unroll 1
-        for (int j = 0; j < n; j++) {
-          const float v = load_f(l, e0 + j);
-          if (!(v <= (float)kMasked)) s += exp((double)v - (double)top);
-        }
-        for (int m = 1; m < LPR; m <<= 1) s += __shfl_xor(s, m);
-        return s;
-      };
-      auto exact_key = [&](int e, double dsum, bool with_bias) {
-        const double v = load_f(l, e);
-        const double s = p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dsum;
-        return with_bias ? s + (double)bias[e] : s;
-      };
-
-      bool kept = true;
-      if (grouped) {
-        float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < EPL; j++) {
-          const float f = KEYS == kLogits ? x[j] : k[j];
-          b = __builtin_amdgcn_fmed3f(a, b, f);  // a >= b: the second of the three
-          a = fmaxf(a, f);
-        }
-        for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
-          const float a2 = __shfl_xor(a, m), b2 = __shfl_xor(b, m);
-          b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-          a = fmaxf(a, a2);
-        }
-        const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
-        int rank = 0;
-        for (int q = 0; q < p.n_group; q++) {
-          const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
-          rank += other > total || (other == total && q < g);
-        }
-        kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
-        if (KEYS != kLogits) {
-          // Of the least total kept and the largest not kept: fp32 totals of distinct
-          // exact values can swap when they differ by at most twice a total's error, that
-          // of two scores (4 half steps of 1 for a sigmoid, 42 for a softmax) and three
-          // roundings.  Then the totals are taken in fp64, from the experts that can be
-          // among their groups' best two.
-          const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
-          const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
-          const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(least) * 0x1p-22f;
-          const bool open = most > -INFINITY && least - most <= error;
-          if (__any(open)) {
-            const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
-            const float from = (p.group_top == 2 && b > -INFINITY ? b : a) - error;
-            uint32_t which = 0;
-#pragma unroll
-            for (int j = 0; j < EPL; j++) which |= k[j] > -INFINITY && k[j] >= from ? 1u << j : 0u;
-            double da = -INFINITY, db = -INFINITY;
-            while (__any(which)) {
-              if (which) {
-                const double s = exact_key(e0 + __ffs(which) - 1, dsum, KEYS == kBiased);
-                which &= which - 1;
-                db = fmax(db, fmin(da, s));
-                da = fmax(da, s);
-              }
-            }
-            for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
-              const double a2 = __shfl_xor(da, m), b2 = __shfl_xor(db, m);
-              db = fmax(fmin(da, a2), fmax(db, b2));
-              da = fmax(da, a2);
-            }
-            const double dt = p.group_top == 2 && db > -INFINITY ? da + db : da;
-            int r = 0;
-            for (int q = 0; q < p.n_group; q++) {
-              const double other = __shfl(dt, first_lane + (q << sh.lpg_log2));
-              r += other > dt || (other == dt && q < g);
-            }
-            kept = g < p.n_group && r < p.topk_group && dt > -INFINITY;
-          }
-        }
-      }
-
-      uint32_t key[EPL];
+      for (int j = 0; j < EPL; j++) odd |= !(x[j] < INFINITY);
+    } else {
+      float zero = 0.f;  // NaN after any that is not finite
 #pragma unroll
       for (int j = 0; j < EPL; j++) {
-        const float f = KEYS == kBiased ? k[j] : x[j];
-        const uint32_t u = ordered(f);
-        key[j] = EXACT ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
+        // 1 / (1 + exp(-x)) for either sign: where exp(-x) is large its relative error is that of the score
+        float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-x[j])) : exp_f(x[j] - top) * inv_total;
+        if (KEYS == kBiased) s += k[j];
+        zero = __builtin_fmaf(s, 0.f, zero);
+        k[j] = x[j] <= (float)kMasked ? -INFINITY : s;
       }
-      constexpr uint32_t NONE = 0x007FFFFFu;   // keys of -inf and 0 lie here and below
-      uint32_t below = 0, local = 0;           // the lane's largest key below `below`
-      auto next_local = [&] {
-        uint32_t d = 0u - below;
+      odd = zero != 0.f;
+    }
+    if (KEYS != kBiased)
 #pragma unroll
-        for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
-        local = kept ? d + below : 0u;
-      };
-      next_local();
-      int chosen_lane = 0;
-      uint32_t chosen_key = 0;
-      auto choose = [&](int r) {
-        const uint32_t m = row_max<LPR>(local);
-        const uint64_t who = __ballot(local == m) >> first_lane;
-        const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ROW))) - 1;
-        if (sub == r) {
-          chosen_lane = win;
-          chosen_key = m;
-        }
-        if (sub == win) below = m;
-        next_local();
-      };
-      for (int r = 0; r < p.K; r++) choose(r);
-      auto expert = [&] {
-        const int e = EXACT ? 0xFFFF - (int)(chosen_key & 0xFFFFu)
-                            : (chosen_lane >> sh.lpg_log2) * per + (chosen_lane & ((1 << sh.lpg_log2) - 1)) * EPL +
-                                  (int)(LOW - (chosen_key & LOW));
-        return chosen_key > NONE ? e : -1;
-      };
-      int chosen = expert();
+      for (int j = 0; j < EPL; j++) x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
 
-      // Neighbours that fp32 leaves open (the same key but for the place, or scores too
-      // close): they and as many more as may belong among the first K are put into the
-      // order of their exact keys.
-      if (!EXACT) {
-        auto close = [&](uint32_t hi, uint32_t lo) {
-          if (lo <= NONE) return false;
-          if (KEYS != kBiased) return ((hi ^ lo) & ~LOW) == 0;
-          // twice a score's error (4 or 42 half steps), the sums' roundings, the places' bits
-          const float x = unordered(hi), y = unordered(lo);
-          return x - y <= (p.sigmoid ? 0x1p-21f : 0x1.5p-18f) + fabsf(x) * (EPL * 0x1p-23f + 0x1p-22f);
-        };
-        uint32_t rest = row_max<LPR>(local);
-        uint32_t after = __shfl_down(chosen_key, 1);
-        if (sub == p.K - 1) after = rest;
-        if (__any(sub < p.K && close(chosen_key, after))) {
-          int have = p.K;
-          uint32_t last = __shfl(chosen_key, first_lane + have - 1);
-          while (have < LPR && __any(close(last, rest))) {
-            choose(have);
-            have++;
-            last = __shfl(chosen_key, first_lane + have - 1);
-            rest = row_max<LPR>(local);
-          }
-          odd |= close(last, rest);
-          chosen = expert();
-          const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
-          double dk = -INFINITY;
-          if (sub < have && chosen >= 0) dk = KEYS == kBiased ? exact_key(chosen, dsum, true) : (double)load_f(l, chosen);
-          int rank = 0;
-          for (int q = 0; q < have; q++) {
-            const double v = __shfl(dk, first_lane + q);
-            const int e = __shfl(chosen, first_lane + q);
-            rank += v > dk || (v == dk && (e < chosen || (e == chosen && q < sub)));
-          }
-          chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
-        }
+    // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias; without
+    // a bias a softmax's up to its sum, which orders them as well)
+    auto exp_sum = [&] {
+      double s = 0.0;
+#pragma unroll 1
+      for (int j = 0; j < n; j++) {
+        const float v = load_f(l, e0 + j);
+        if (!(v <= (float)kMasked)) s += exp((double)v - (double)top);
       }
+      for (int m = 1; m < LPR; m <<= 1) s += __shfl_xor(s, m);
+      return s;
+    };
+    auto exact_key = [&](int e, double dsum, bool with_bias) {
+      const double v = load_f(l, e);
+      const double s = p.sigmoid ? sigmoid64(v) : exp(v - (double)top) / dsum;
+      return with_bias ? s + (double)bias[e] : s;
+    };
 
-      const bool slow = live && (__ballot(odd) >> first_lane & ROW) != 0;
-      if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
-      const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
-      if (live && !slow && sub < p.K) {
-        idx[t * p.K + sub] = chosen;
-        weights[t * p.K + sub] = w;
-        if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
+    bool kept = true;
+    if (grouped) {
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < EPL; j++) {
+        const float f = KEYS == kLogits ? x[j] : k[j];
+        b = __builtin_amdgcn_fmed3f(a, b, f);  // a >= b: the second of the three
+        a = fmaxf(a, f);
+      }
+      for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
+        const float a2 = __shfl_xor(a, m), b2 = __shfl_xor(b, m);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+      }
+      const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
+      int rank = 0;
+      for (int q = 0; q < p.n_group; q++) {
+        const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
+        rank += other > total || (other == total && q < g);
+      }
+      kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
+      if (KEYS != kLogits) {
+        // Of the least total kept and the largest not kept: fp32 totals of distinct
+        // exact values can swap when they differ by at most twice a total's error, that
+        // of two scores (4 half steps of 1 for a sigmoid, 42 for a softmax) and three
+        // roundings.  Then the totals are taken in fp64, from the experts that can be
+        // among their groups' best two.
+        const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
+        const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
+        const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(least) * 0x1p-22f;
+        const bool open = most > -INFINITY && least - most <= error;
+        if (__any(open)) {
+          const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
+          const float from = (p.group_top == 2 && b > -INFINITY ? b : a) - error;
+          uint32_t which = 0;
+#pragma unroll
+          for (int j = 0; j < EPL; j++) which |= k[j] > -INFINITY && k[j] >= from ? 1u << j : 0u;
+          double da = -INFINITY, db = -INFINITY;
+          while (__any(which)) {
+            if (which) {
+              const double s = exact_key(e0 + __ffs(which) - 1, dsum, KEYS == kBiased);
+              which &= which - 1;
+              db = fmax(db, fmin(da, s));
+              da = fmax(da, s);
+            }
+          }
+          for (int m = 1; m < 1 << sh.lpg_log2; m <<= 1) {
+            const double a2 = __shfl_xor(da, m), b2 = __shfl_xor(db, m);
+            db = fmax(fmin(da, a2), fmax(db, b2));
+            da = fmax(da, a2);
+          }
+          const double dt = p.group_top == 2 && db > -INFINITY ? da + db : da;
+          int r = 0;
+          for (int q = 0; q < p.n_group; q++) {
+            const double other = __shfl(dt, first_lane + (q << sh.lpg_log2));
+            r += other > dt || (other == dt && q < g);
+          }
+          kept = g < p.n_group && r < p.topk_group && dt > -INFINITY;
+        }
       }
     }
-    __syncthreads();
-    if (wave < kSlow)
-      for (int q = wave; q < slow_count; q += min(kSlow, waves)) {
-        const int64_t s = r0 + slow_rows[q];
-        route_row64(logits + s * ld, bias, p, lds + wave * p.E, idx + s * p.K, weights + s * p.K);
-        if (o.mode && lane < p.K) {
-          const int32_t c = idx[s * p.K + lane];  // written by this lane
-          if (c >= 0) atomicAdd(&hist[c], 1);
-        }
+
+    uint32_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; j++) {
+      const uint32_t u = ordered(KEYS == kBiased ? k[j] : x[j] + 0.f);  // -0 + 0 is 0: they are equal
+      key[j] = EXACT ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
+    }
+    constexpr uint32_t NONE = 0x007FFFFFu;   // keys of -inf and 0 lie here and below
+    uint32_t below = 0, local = 0;           // the lane's largest key below `below`
+    auto next_local = [&] {
+      uint32_t d = 0u - below;
+#pragma unroll
+      for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
+      local = kept ? d + below : 0u;
+    };
+    next_local();
+    int chosen_lane = 0;
+    uint32_t chosen_key = 0;
+    auto choose = [&](int r) {
+      const uint32_t m = row_max<LPR>(local);
+      const uint64_t who = __ballot(local == m) >> first_lane;
+      const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ROW))) - 1;
+      if (sub == r) {
+        chosen_lane = win;
+        chosen_key = m;
       }
-    __syncthreads();
+      if (sub == win) below = m;
+      next_local();
+    };
+    for (int r = 0; r < p.K; r++) choose(r);
+    auto expert = [&] {
+      const int e = EXACT ? 0xFFFF - (int)(chosen_key & 0xFFFFu)
+                          : (chosen_lane >> sh.lpg_log2) * per + (chosen_lane & ((1 << sh.lpg_log2) - 1)) * EPL +
+                                (int)(LOW - (chosen_key & LOW));
+      return chosen_key > NONE ? e : -1;
+    };
+    int chosen = expert();
+
+    // Neighbours that fp32 leaves open (the same key but for the place, or scores too
+    // close): they and as many more as may belong among the first K are put into the
+    // order of their exact keys.
+    if (!EXACT) {
+      auto close = [&](uint32_t hi, uint32_t lo) {
+        if (lo <= NONE) return false;
+        if (KEYS != kBiased) return ((hi ^ lo) & ~LOW) == 0;
+        // twice a score's error (4 or 42 half steps), the sums' roundings, the places' bits
+        const float x = unordered(hi), y = unordered(lo);
+        return x - y <= (p.sigmoid ? 0x1p-21f : 0x1.5p-18f) + fabsf(x) * (EPL * 0x1p-23f + 0x1p-22f);
+      };
+      uint32_t rest = row_max<LPR>(local);
+      uint32_t after = __shfl_down(chosen_key, 1);
+      if (sub == p.K - 1) after = rest;
+      if (__any(sub < p.K && close(chosen_key, after))) {
+        int have = p.K;
+        uint32_t last = __shfl(chosen_key, first_lane + have - 1);
+        while (have < LPR && __any(close(last, rest))) {
+          choose(have);
+          have++;
+          last = __shfl(chosen_key, first_lane + have - 1);
+          rest = row_max<LPR>(local);
+        }
+        odd |= close(last, rest);
+        chosen = expert();
+        const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
+        double dk = -INFINITY;
+        if (sub < have && chosen >= 0) dk = KEYS == kBiased ? exact_key(chosen, dsum, true) : (double)load_f(l, chosen);
+        int rank = 0;
+        for (int q = 0; q < have; q++) {
+          const double v = __shfl(dk, first_lane + q);
+          const int e = __shfl(chosen, first_lane + q);
+          rank += v > dk || (v == dk && (e < chosen || (e == chosen && q < sub)));
+        }
+        chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
+      }
+    }
+
+    const bool slow = live && (__ballot(odd) >> first_lane & ROW) != 0;
+    if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
+    const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
+    if (live && !slow && sub < p.K) {
+      idx[t * p.K + sub] = chosen;
+      weights[t * p.K + sub] = w;
+      if (o.mode && chosen >= 0) atomicAdd(&hist[chosen], 1);  // a count: the order does not matter
+    }
+  }
+  __syncthreads();
+  if (wave < kSlow)
+    for (int q = wave; q < slow_count; q += min(kSlow, waves)) {
+      const int64_t s = r0 + slow_rows[q];
+      route_row64(logits + s * ld, bias, p, lds + wave * p.E, idx + s * p.K, weights + s * p.K);
+      if (o.mode && lane < p.K) {
+        const int32_t c = idx[s * p.K + lane];  // written by this lane
+        if (c >= 0) atomicAdd(&hist[c], 1);
+      }
+    }
+  __syncthreads();
   if (o.mode == 1) {
     for (int x = tid; x < sh.stride; x += blockDim.x)
       o.counts[(int64_t)blockIdx.x * sh.stride + x] = x < p.E ? (uint16_t)hist[x] : 0;
@@ -898,8 +897,9 @@ hipError_t route_fast(RouteArgs a) {
   a.o.mode = alone ? 2 : counts ? 1 : 0;
   const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E),
                     (EPL * LPR) >> ceil_log2(a.p.n_group) == a.p.E / a.p.n_group && 1 << ceil_log2(a.p.n_group) == a.p.n_group};
-  const size_t lds = std::max(order_lds(kMaxOrderWaves, a.p.E), (size_t)32 * a.p.E);  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
-  auto f = a.bias                                         ? route_fast_kernel<LT, LPR, EPL, kBiased>
+  // 4 waves' fp64 keys, or 16 waves' 16-bit counts
+  const size_t lds = std::max(order_lds(kMaxOrderWaves, a.p.E), (size_t)32 * a.p.E);
+  auto f = a.bias                                  ? route_fast_kernel<LT, LPR, EPL, kBiased>
            : a.p.n_group > 1 && a.p.group_top == 2 ? route_fast_kernel<LT, LPR, EPL, kScoredGroups>
                                                    : route_fast_kernel<LT, LPR, EPL, kLogits>;
   f<<<(unsigned)grid, waves * kWave, lds, a.st>>>((const LT*)a.logits, a.T, a.ld, a.bias, a.p, sh, a.idx, a.weights, a.o);

@@ -159,6 +159,18 @@ def test_route_ties_go_to_the_lowest_index():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_signed_zeros_are_equal(score):
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.full((2, 64), -1.0, dtype=dtype, device="cuda")
+        x[0, [3, 20, 41]] = torch.tensor([-0.0, 0.0, -0.0], dtype=dtype, device="cuda")
+        x[1, ::5] = -0.0
+        x[1, 60] = 0.0
+        for b in (None, torch.zeros(64, device="cuda")):
+            check_route(x, 3, b, score=score)
+            check_route(x, 3, b, score=score, n_group=4, topk_group=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_close_keys(score):
     """Keys that differ by less than fp32 resolves: the bias undoes the scores' differences up to its own rounding."""
     g = torch.Generator().manual_seed(11)
