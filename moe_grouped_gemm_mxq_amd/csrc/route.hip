@@ -703,7 +703,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         chosen_lane = win;
         chosen_key = m;
       }
-      if (sub == win) below = m;
+      if (sub == win && m != 0) below = m;  // 0: no keys are left, and there is nothing below
       next_local();
     };
     for (int r = 0; r < p.K; r++) choose(r);

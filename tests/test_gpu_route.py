@@ -88,6 +88,17 @@ def test_route_groups(E, n_group, topk_group, K, group_top, score):
             check_route(x, K, b, renormalise=True, scale=1.0, **kw)
 
 
+@pytest.mark.parametrize("T", [41, 4100])
+@pytest.mark.parametrize("E,n_group,topk_group,K", [(128, 64, 1, 8), (64, 64, 2, 6), (32, 16, 1, 8), (32, 16, 2, 7), (64, 16, 1, 16)])
+def test_route_groups_smaller_than_top_k(E, n_group, topk_group, K, T):
+    """The kept groups' experts, each once, and -1 after them."""
+    bias = (0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E))).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        x = logits_of(T, E, dtype, E + K)
+        for b in (None, bias):
+            check_route(x, K, b, score="sigmoid", n_group=n_group, topk_group=topk_group, group_top=1, renormalise=True, scale=1.0)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalise", [False, True])
 def test_route_masks(score, renormalise):
