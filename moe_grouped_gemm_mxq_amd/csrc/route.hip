@@ -414,10 +414,14 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
 // A row is held by LPR lanes (64 / LPR rows to a wave), EPL consecutive experts a
 // lane, each expert group by LPG = LPR / pow2(n_group) lanes.  Keys are ordered
 // 32-bit integers whose lowest bits give way to the expert's place in its lane, so
-// a lane's keys differ and its next largest below a threshold is one subtraction
-// and half a maximum per expert: unsigned(key - threshold) is largest for the
-// nearest key below.  A choice is then a maximum over the lanes.  bf16 logits
-// without a bias leave room for the whole index, and keys are exact.
+// a lane's keys differ.  A choice is a maximum over the lanes; each lane keeps its
+// four largest keys in order for it.  bf16 logits without a bias leave room for the
+// whole index, and keys are exact.
+//
+// Bound by the vector units and, up to some 16000 rows, by the latency of one pass
+// (launch, read, choices one after another, write): 16384 x 256 grouped sigmoid rows with a
+// bias take 11 us on the GPU, 65536 take 22 (67 MB, 3.0 TB/s), 65536 x 256 bf16 rows
+// of a softmax 16.7.
 struct Shape {
   int32_t lpg_log2;  // lanes per group
   int32_t stride;    // of the rows of counts
@@ -469,6 +473,10 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t median(uint32_t a, uint32_t b, uint32_t c) {
+  return max(min(a, b), min(max(a, b), c));
+}
+
 // order-preserving integers of floats; 0 is below all of them
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __float_as_uint(f);
@@ -484,11 +492,9 @@ __device__ __forceinline__ float row_fmax(float v) { return unordered(row_max<LP
 // groups (kScoredGroups); scores and a bias (kBiased).
 enum Keys { kLogits, kScoredGroups, kBiased };
 
-// weights of a row's chosen experts (one a lane, -1: none); lanes of other rows beside
-template <typename LT, int LPR>
-__device__ __forceinline__ float weight_of(const LT* l, int chosen, const RouteParams& p, float top, float inv_total) {
-  const bool in = chosen >= 0;
-  const float v = load_f(l, in ? chosen : 0);
+// weights of a row's chosen experts (one a lane, its logit v); lanes of other rows beside
+template <int LPR>
+__device__ __forceinline__ float weight_of(float v, bool in, const RouteParams& p, float top, float inv_total) {
   float w;
   if (p.sigmoid) {
     const float e = exp_f(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + e);
@@ -529,43 +535,42 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
   const int per = p.E / p.n_group;
   const bool grouped = p.n_group > 1;
   const bool stats = !p.sigmoid && (KEYS != kLogits || !p.renorm);
+  const int64_t r0 = (int64_t)blockIdx.x * (waves * RPW);  // rows r0 .. r0 + waves * RPW - 1
+  const int64_t t = r0 + wave * RPW + lane / LPR;
+  const bool live = t < T;
+  const LT* l = logits + (live ? t : r0) * ld;
+  const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
+  const int e0 = g * per + part * EPL;  // the lane's experts: e0 .. e0 + n - 1
+  const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
+
+  // logits and bias, read before the first barrier (by waves without rows too: row r0)
+  float x[EPL];
+  float k[EPL];  // scores + bias
+  if (EPL % 4 == 0 && per % 4 == 0) {
+    Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
+#pragma unroll
+    for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
+    if (KEYS == kBiased)
+#pragma unroll
+      for (int q = 0; q < EPL / 4; q++) unpack(load_raw<4, false>(bias + (4 * q < n ? e0 + 4 * q : 0)), &k[4 * q]);
+#pragma unroll
+    for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
+    if (KEYS == kBiased)
+#pragma unroll
+      for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
+  }
+
   if (o.mode)
     for (int x = tid; x < p.E; x += blockDim.x) hist[x] = 0;
-
-  const int64_t r0 = (int64_t)blockIdx.x * (waves * RPW);  // rows r0 .. r0 + waves * RPW - 1
   if (tid == 0) slow_count = 0;
   __syncthreads();
   if (r0 + wave * RPW < T) {
-    const int64_t t = r0 + wave * RPW + lane / LPR;
-    const bool live = t < T;
-    const LT* l = logits + (live ? t : r0) * ld;
-    const int g = sub >> sh.lpg_log2, part = sub & ((1 << sh.lpg_log2) - 1);
-    const int e0 = g * per + part * EPL;  // the lane's experts: e0 .. e0 + n - 1
-    const int n = g < p.n_group ? min(max(per - part * EPL, 0), EPL) : 0;
-
-    // logits; masked and absent ones -inf
-    float x[EPL];
-    float k[EPL];  // scores + bias
-    if (EPL % 4 == 0 && per % 4 == 0) {
-      Raw<LT, 4> w[EPL >= 4 ? EPL / 4 : 1];
-#pragma unroll
-      for (int q = 0; q < EPL / 4; q++) w[q] = load_raw<4, false>(l + (4 * q < n ? e0 + 4 * q : 0));
-      if (KEYS == kBiased)
-#pragma unroll
-        for (int q = 0; q < EPL / 4; q++) unpack(load_raw<4, false>(bias + (4 * q < n ? e0 + 4 * q : 0)), &k[4 * q]);
-#pragma unroll
-      for (int q = 0; q < EPL / 4; q++) unpack(w[q], &x[4 * q]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPL; j++) x[j] = load_f(l, j < n ? e0 + j : 0);
-      if (KEYS == kBiased)
-#pragma unroll
-        for (int j = 0; j < EPL; j++) k[j] = bias[j < n ? e0 + j : 0];
-    }
-    if (!sh.full)
+    if (!sh.full)  // absent ones
 #pragma unroll
       for (int j = 0; j < EPL; j++) x[j] = j < n ? x[j] : -INFINITY;
-
     float top = 0.f, inv_total = 0.f;
     if (stats) {  // masked logits add exp(-inf)
       float m = x[0];
@@ -583,14 +588,25 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
 #pragma unroll
       for (int j = 0; j < EPL; j++) odd |= !(x[j] < INFINITY);
     } else {
+      // a loop each, or every step of one is a branch
+      if (p.sigmoid) {  // 1 / (1 + exp(-x)) for either sign: where exp(-x) is large its relative error is that of the score
+#pragma unroll
+        for (int j = 0; j < EPL; j++) {
+          const float s = __builtin_amdgcn_rcpf(1.f + exp_f(-x[j]));
+          k[j] = KEYS == kBiased ? s + k[j] : s;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < EPL; j++) {
+          const float s = exp_f(x[j] - top) * inv_total;
+          k[j] = KEYS == kBiased ? s + k[j] : s;
+        }
+      }
       float zero = 0.f;  // NaN after any that is not finite
 #pragma unroll
       for (int j = 0; j < EPL; j++) {
-        // 1 / (1 + exp(-x)) for either sign: where exp(-x) is large its relative error is that of the score
-        float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-x[j])) : exp_f(x[j] - top) * inv_total;
-        if (KEYS == kBiased) s += k[j];
-        zero = __builtin_fmaf(s, 0.f, zero);
-        k[j] = x[j] <= (float)kMasked ? -INFINITY : s;
+        zero = __builtin_fmaf(k[j], 0.f, zero);
+        k[j] = x[j] <= (float)kMasked ? -INFINITY : k[j];
       }
       odd = zero != 0.f;
     }
@@ -685,26 +701,50 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       key[j] = EXACT ? (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + j)) : (u & ~LOW) | (LOW - j);
     }
     constexpr uint32_t NONE = 0x007FFFFFu;   // keys of -inf and 0 lie here and below
-    uint32_t below = 0, local = 0;           // the lane's largest key below `below`
-    auto next_local = [&] {
-      uint32_t d = 0u - below;
+    // The lane's largest keys in order, those that are left: a choice takes the first of
+    // one lane, and a lane that has given all of its list looks through its keys for the
+    // next.  (A look through them for every choice instead of the list: 65536 x 256 bf16
+    // rows, top 8, 19.6 against 17.7 us; for a choice or two the list costs more than it
+    // saves: top 1 of fp32 rows 13.9 against 14.6.)
+    constexpr int LIST = EPL < 4 ? EPL : 4;
+    uint32_t list[LIST] = {};
+    if (EPL <= LIST || p.K > 2) {
 #pragma unroll
-      for (int j = 0; j < EPL; j++) d = max(d, key[j] - below);
-      local = kept ? d + below : 0u;
-    };
-    next_local();
+      for (int j = 0; j < EPL; j++) {
+#pragma unroll
+        for (int i = LIST - 1; i > 0; i--) list[i] = median(list[i - 1], list[i], key[j]);
+        list[0] = max(list[0], key[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; j++) list[0] = max(list[0], key[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < LIST; i++) list[i] = kept ? list[i] : 0u;
     int chosen_lane = 0;
     uint32_t chosen_key = 0;
     auto choose = [&](int r) {
-      const uint32_t m = row_max<LPR>(local);
-      const uint64_t who = __ballot(local == m) >> first_lane;
-      const int win = (LPR == 64 ? __ffsll((unsigned long long)who) : __ffs((uint32_t)(who & ROW))) - 1;
+      const uint32_t m = row_max<LPR>(list[0]);
+      const uint64_t who = __ballot(list[0] == m);
+      int win;
+      if constexpr (LPR == 64)
+        win = __ffsll((unsigned long long)who) - 1;
+      else
+        win = __ffs((lane < 32 ? (uint32_t)who : (uint32_t)(who >> 32)) >> (first_lane & 31)) - 1;
       if (sub == r) {
         chosen_lane = win;
         chosen_key = m;
       }
-      if (sub == win && m != 0) below = m;  // 0: no keys are left, and there is nothing below
-      next_local();
+      const bool mine = sub == win;
+#pragma unroll
+      for (int i = 0; i + 1 < LIST; i++) list[i] = mine ? list[i + 1] : list[i];
+      list[LIST - 1] = mine ? 0u : list[LIST - 1];
+      if (EPL > LIST && __any(mine && list[0] == 0u && m != 0)) {  // largest below m
+        uint32_t d = 0u - m;
+#pragma unroll
+        for (int j = 0; j < EPL; j++) d = max(d, key[j] - m);
+        if (mine && list[0] == 0u && m != 0) list[0] = d + m;
+      }
     };
     for (int r = 0; r < p.K; r++) choose(r);
     auto expert = [&] {
@@ -714,6 +754,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       return chosen_key > NONE ? e : -1;
     };
     int chosen = expert();
+    float logit = load_f(l, max(chosen, 0));
 
     // Neighbours that fp32 leaves open (the same key but for the place, or scores too
     // close): they and as many more as may belong among the first K are put into the
@@ -726,7 +767,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         const float x = unordered(hi), y = unordered(lo);
         return x - y <= (p.sigmoid ? 0x1p-21f : 0x1.5p-18f) + fabsf(x) * (EPL * 0x1p-23f + 0x1p-22f);
       };
-      uint32_t rest = row_max<LPR>(local);
+      uint32_t rest = row_max<LPR>(list[0]);
       uint32_t after = __shfl_down(chosen_key, 1);
       if (sub == p.K - 1) after = rest;
       if (__any(sub < p.K && close(chosen_key, after))) {
@@ -736,7 +777,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
           choose(have);
           have++;
           last = __shfl(chosen_key, first_lane + have - 1);
-          rest = row_max<LPR>(local);
+          rest = row_max<LPR>(list[0]);
         }
         odd |= close(last, rest);
         chosen = expert();
@@ -750,12 +791,13 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
           rank += v > dk || (v == dk && (e < chosen || (e == chosen && q < sub)));
         }
         chosen = __builtin_amdgcn_ds_permute((first_lane + (sub < have ? rank : sub)) * 4, chosen);
+        logit = load_f(l, max(chosen, 0));
       }
     }
 
     const bool slow = live && (__ballot(odd) >> first_lane & ROW) != 0;
     if (slow && sub == 0) slow_rows[atomicAdd(&slow_count, 1)] = (int32_t)(t - r0);
-    const float w = weight_of<LT, LPR>(l, sub < p.K ? chosen : -1, p, top, inv_total);
+    const float w = weight_of<LPR>(logit, sub < p.K && chosen >= 0, p, top, inv_total);
     if (live && !slow && sub < p.K) {
       idx[t * p.K + sub] = chosen;
       weights[t * p.K + sub] = w;
@@ -922,7 +964,7 @@ hipError_t route(const RouteArgs& a) {
     if (holds<LT, 16, 16>(p)) return route_fast<LT, 16, 16>(a);
     if (holds<LT, 32, 16>(p)) return route_fast<LT, 32, 16>(a);
   }
-  if (a.T <= kFastRows) {
+  if (a.T > 0 && a.T <= kFastRows) {  // its waves read a row before they look whether it is there
     if (holds<LT, 64, 4>(p)) return route_fast<LT, 64, 4>(a);
     if (holds<LT, 64, 16>(p)) return route_fast<LT, 64, 16>(a);
   }
