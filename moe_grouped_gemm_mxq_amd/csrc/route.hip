@@ -194,9 +194,11 @@ __host__ __device__ constexpr int32_t count_stride(int32_t E) {
 __host__ __device__ constexpr int count_row(int E) { return (E + 7) / 8 * 8; }
 constexpr size_t order_lds(int waves, int E) { return (size_t)waves * count_row(E) * sizeof(uint16_t); }
 
-// exclusive sums of one value per thread over the workgroup; total: of all.  part: kMaxOrderWaves words
-__device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int32_t& total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+// Exclusive sums of one value per thread over the workgroup's waves (WAVES at most); total: of all.
+// The waves' sums are read without branches between: with one, each read was waited for.
+template <int WAVES>
+__device__ __forceinline__ int32_t block_exclusive(int32_t v, int waves, int32_t (&part)[WAVES], int32_t& total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   // inclusive over the wave: lanes 1, 2, 4, 8 below within rows of 16 (0 where there is
   // none), then the last lane of the row before, and of the 32 lanes before
   int32_t incl = v;
@@ -208,13 +210,14 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part, int
   incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);
   if (lane == kWave - 1) part[wave] = incl;
   __syncthreads();
-  int32_t off = 0;
+  int32_t n[WAVES], off = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; w++) n[w] = part[w];
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kMaxOrderWaves; w++) {
-    const int32_t n = w < waves ? part[w] : 0;
-    if (w < wave) off += n;
-    total += n;
+  for (int w = 0; w < WAVES; w++) {
+    off += w < wave ? n[w] : 0;
+    total += w < waves ? n[w] : 0;
   }
   return off + incl - v;
 }
@@ -237,17 +240,18 @@ __device__ __forceinline__ int rank_in_wave(int32_t x, int32_t E, uint16_t* coun
 }
 // Counts of experts 2 i and 2 i + 1 -> pairs in earlier waves; returns the segment's, packed.
 // (A segment has at most 1024 pairs, so neither half carries into the other.)
-__device__ __forceinline__ uint32_t waves_exclusive(int i, int32_t E, uint16_t* count) {
-  const int waves = blockDim.x / kWave, row = count_row(E) / 2;
+template <int WAVES>
+__device__ __forceinline__ uint32_t waves_exclusive(int i, int32_t E, int waves, uint16_t* count) {
+  const int row = count_row(E) / 2;
   uint32_t* c = reinterpret_cast<uint32_t*>(count) + i;
-  uint32_t n[kMaxOrderWaves];
+  uint32_t n[WAVES];
 #pragma unroll
-  for (int w = 0; w < kMaxOrderWaves; w++) n[w] = w < waves ? c[w * row] : 0;
+  for (int w = 0; w < WAVES; w++) n[w] = c[min(w, waves - 1) * row];
   uint32_t run = 0;
 #pragma unroll
-  for (int w = 0; w < kMaxOrderWaves; w++) {
+  for (int w = 0; w < WAVES; w++) {
     if (w < waves) c[w * row] = run;
-    run += n[w];
+    run += w < waves ? n[w] : 0;
   }
   return run;
 }
@@ -288,102 +292,148 @@ __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* _
     counts[(int64_t)blockIdx.x * stride + x] = x < E ? (uint16_t)h[x] : 0;
 }
 
+// Sum of 16-bit pairs
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, a) + __builtin_bit_cast(u16x2, b));
+}
+
+// Counts of a thread's chunks first, first + runs, ..: of all of them, and of those before
+// chunk `mine`, eight experts each, two a word (PACKED) or one.  LOADS of them at a time, without
+// branches between (past the end the last one is read and not counted).
+template <bool PACKED, int LOADS>
+__device__ __forceinline__ void sum_counts(const u32x4* c4, int cols, int chunks, int first, int runs, int mine,
+                                           uint32_t* all, uint32_t* before) {
+  for (int c0 = first; c0 < chunks; c0 += LOADS * runs) {
+    u32x4 v[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; i++) v[i] = c4[(int64_t)min(c0 + i * runs, chunks - 1) * cols];
+#pragma unroll
+    for (int i = 0; i < LOADS; i++) {
+      const int c = c0 + i * runs;
+      const uint32_t in = c < chunks ? 0xFFFFFFFFu : 0u, earlier = c < mine ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if (PACKED) {
+          all[j] = add2(all[j], v[i][j] & in);
+          before[j] = add2(before[j], v[i][j] & earlier);
+        } else {
+          all[2 * j] += v[i][j] & in & 0xFFFFu;
+          all[2 * j + 1] += (v[i][j] & in) >> 16;
+          before[2 * j] += v[i][j] & earlier & 0xFFFFu;
+          before[2 * j + 1] += (v[i][j] & earlier) >> 16;
+        }
+      }
+    }
+  }
+}
+
+// Sums over the lanes that are a multiple of cols (a power of two) apart, in each of them.
+template <bool PACKED, int N>
+__device__ __forceinline__ void sum_runs(int cols, uint32_t (&v)[N]) {
+  auto add = [](uint32_t a, uint32_t b) { return PACKED ? add2(a, b) : a + b; };
+#define MXQ_ROTATE(n)                                                                             \
+  if (cols <= n)                                                                                  \
+    _Pragma("unroll") for (int j = 0; j < N; j++)                                                 \
+        v[j] = add(v[j], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[j], 0x120 + n, 0xF, 0xF, true));
+  MXQ_ROTATE(8)  // within rows of 16; a sum repeats every 8 lanes from here on
+  MXQ_ROTATE(4)
+  MXQ_ROTATE(2)
+  MXQ_ROTATE(1)
+#undef MXQ_ROTATE
+  if (cols <= 16)
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const auto r = __builtin_amdgcn_permlane16_swap(v[j], v[j], false, false);
+      v[j] = add(r[0], r[1]);
+    }
+  if (cols <= 32)
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const auto r = __builtin_amdgcn_permlane32_swap(v[j], v[j], false, false);
+      v[j] = add(r[0], r[1]);
+    }
+}
+
+constexpr int kParts = 8;  // partial sums of an expert: one of each wave, or of each run of the waves
+
 // Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs, at most `most` of them one expert's.
-__global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
-                                                                int32_t chunks, int32_t per, int32_t E, int32_t most,
-                                                                int32_t K,
-                                                                const uint16_t* __restrict__ counts,
-                                                                int32_t* __restrict__ group_end,
-                                                                int32_t* __restrict__ row_token,
-                                                                int32_t* __restrict__ slot) {
-  extern __shared__ uint16_t count[];
-  __shared__ int32_t base[MXQ_MAX_GROUPS];
-  __shared__ int32_t sums[2][MXQ_MAX_GROUPS];
-  __shared__ int32_t part[kMaxOrderWaves];
+//
+// Bound by latency: 16384 x 8 pairs of 256 experts take @A@ us on the GPU, 5003 x 8 of 32 @B@,
+// a launch that does nothing about 2.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
+                                                            int32_t chunks, int32_t per, int32_t E, int32_t most, int32_t K,
+                                                            const uint16_t* __restrict__ counts,
+                                                            int32_t* __restrict__ group_end,
+                                                            int32_t* __restrict__ row_token,
+                                                            int32_t* __restrict__ slot) {
+  constexpr int THREADS = WAVES * kWave;  // at least E
+  __shared__ __attribute__((aligned(16))) uint16_t count[WAVES * THREADS];
+  __shared__ __attribute__((aligned(16))) int32_t sums[2 * kParts * THREADS];  // of all chunks, of the earlier ones
+  __shared__ int32_t base[THREADS];
+  __shared__ __attribute__((aligned(16))) int32_t part[WAVES];
   const int t = threadIdx.x;
-  const int32_t first = blockIdx.x * per;
-  const int64_t b = first * chunk, e = min(b + per * chunk, N);
-  int32_t x = expert_at(idx, b + t, e, E);
+  const int32_t mine = blockIdx.x * per;
+  const int64_t b = mine * chunk, e = min(b + per * chunk, N);
+  int32_t x = -1;
+  if (N > 0) x = idx[min(b + t, N - 1)];
   // Eight experts' counts a load; a row of counts by stride / 8 threads, the chunks dealt to
   // as many such runs of threads as the workgroup holds.  Whole numbers: the order
   // of the additions does not matter.
-  const int stride = count_stride(E), cols = stride / 8, runs = (int)blockDim.x / cols, run = t / cols, col = t - run * cols;
+  const int stride = count_stride(E), cols = stride / 8, runs = THREADS / cols, run = t / cols, col = t - run * cols;
   const int visits = (chunks + runs - 1) / runs;
   // two sums a word where no half can carry, after the wave's runs are added up too
   const bool packed = (int64_t)most * visits * (cols < kWave ? kWave / cols : 1) <= 0xFFFF;
   const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  auto add2 = [](uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, a) + __builtin_bit_cast(u16x2, b));
-  };
-  uint32_t a2[4] = {}, f2[4] = {};
-  int32_t a[8] = {}, f[8] = {};
+  uint32_t all8[8] = {}, before8[8] = {};
   if (packed) {
-#pragma unroll 8
-    for (int c = run; c < chunks; c += runs) {
-      const u32x4 v = c4[(int64_t)c * cols];
-      const uint32_t mine = c < first ? 0xFFFFFFFFu : 0u;
+    uint32_t a[4] = {}, f[4] = {};
+    if (visits == 1)
+      sum_counts<true, 1>(c4, cols, chunks, run, runs, mine, a, f);
+    else if (visits <= 4)
+      sum_counts<true, 4>(c4, cols, chunks, run, runs, mine, a, f);
+    else
+      sum_counts<true, 8>(c4, cols, chunks, run, runs, mine, a, f);
+    sum_runs<true>(cols, a);
+    sum_runs<true>(cols, f);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        a2[j] = add2(a2[j], v[j]);
-        f2[j] = add2(f2[j], v[j] & mine);
-      }
+    for (int j = 0; j < 4; j++) {
+      all8[2 * j] = a[j] & 0xFFFFu;
+      all8[2 * j + 1] = a[j] >> 16;
+      before8[2 * j] = f[j] & 0xFFFFu;
+      before8[2 * j + 1] = f[j] >> 16;
     }
   } else {
-    for (int c = run; c < chunks; c += runs) {
-      const u32x4 v = c4[(int64_t)c * cols];
-      const uint32_t mine = c < first ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        a[2 * j] += v[j] & 0xFFFFu;
-        a[2 * j + 1] += v[j] >> 16;
-        f[2 * j] += v[j] & mine & 0xFFFFu;
-        f[2 * j + 1] += (v[j] & mine) >> 16;
-      }
-    }
+    sum_counts<false, 8>(c4, cols, chunks, run, runs, mine, all8, before8);
+    sum_runs<false>(cols, all8);
+    sum_runs<false>(cols, before8);
   }
-  for (int i = t; i < stride; i += blockDim.x) sums[0][i] = sums[1][i] = 0;
   clear_counts(E, count);
-  __syncthreads();
-  int rank = rank_in_wave(x, E, count);
-  // the runs of a wave first: 64 lanes adding to the same few words one by one took 7 us
-  if ((t & ~(kWave - 1)) / cols < chunks) {
-    for (int m = cols; m < kWave; m *= 2) {
-      if (packed) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          a2[j] = add2(a2[j], __shfl_xor(a2[j], m));
-          f2[j] = add2(f2[j], __shfl_xor(f2[j], m));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-          a[j] += __shfl_xor(a[j], m);
-          f[j] += __shfl_xor(f[j], m);
-        }
-      }
-    }
-    if (packed)
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        a[2 * j] = a2[j] & 0xFFFFu;
-        a[2 * j + 1] = a2[j] >> 16;
-        f[2 * j] = f2[j] & 0xFFFFu;
-        f[2 * j + 1] = f2[j] >> 16;
-      }
-    if ((t & (kWave - 1)) < cols)
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        atomicAdd(&sums[0][8 * col + j], a[j]);
-        atomicAdd(&sums[1][8 * col + j], f[j]);
-      }
+  // One of the kParts rows of the sums for each wave where a wave holds whole rows, else for each run.
+  if ((t & (kWave - 1)) < cols) {
+    u32x4* s = reinterpret_cast<u32x4*>(sums + (cols < kWave ? t / kWave : run) * stride + 8 * col);
+    s[0] = u32x4{all8[0], all8[1], all8[2], all8[3]};
+    s[1] = u32x4{all8[4], all8[5], all8[6], all8[7]};
+    s += kParts * stride / 4;
+    s[0] = u32x4{before8[0], before8[1], before8[2], before8[3]};
+    s[1] = u32x4{before8[4], before8[5], before8[6], before8[7]};
   }
   __syncthreads();
-  const int32_t all = t < E ? sums[0][t] : 0, before = t < E ? sums[1][t] : 0;
-  const int pairs = (E + 1) / 2;  // of experts
-  uint32_t segment = t < pairs ? waves_exclusive(t, E, count) : 0;
+  x = b + t < e && x >= 0 && x < E ? x : E;
+  int rank = rank_in_wave(x, E, count);
+  int32_t all = 0, before = 0;
+  const int mine_e = min(t, E - 1);
+#pragma unroll
+  for (int i = 0; i < kParts; i++) {
+    all += sums[i * stride + mine_e];
+    before += sums[(kParts + i) * stride + mine_e];
+  }
+  all = t < E ? all : 0;
   int32_t total;
-  const int32_t start = block_exclusive(all, part, total);
+  const int32_t start = block_exclusive<WAVES>(all, WAVES, part, total);  // a barrier: counts of all waves
+  const int pairs = (E + 1) / 2;  // of experts
+  uint32_t segment = t < pairs ? waves_exclusive<WAVES>(t, E, WAVES, count) : 0;
   if (t < E) {
     base[t] = start + before;
     if (blockIdx.x == 0) group_end[t] = start + all;
@@ -391,7 +441,7 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
   __syncthreads();
   for (int64_t s = b;;) {
     put_pair(s + t, e, x, rank, E, K, base, count, row_token, slot);
-    s += blockDim.x;
+    s += THREADS;
     if (s >= e) break;
     __syncthreads();
     if (t < pairs) {
@@ -403,11 +453,10 @@ __global__ __launch_bounds__(kMaxOrderThreads) void order_kernel(const int32_t* 
     __syncthreads();
     rank = rank_in_wave(x, E, count);
     __syncthreads();
-    if (t < pairs) segment = waves_exclusive(t, E, count);
+    if (t < pairs) segment = waves_exclusive<WAVES>(t, E, WAVES, count);
     __syncthreads();
   }
-  for (int64_t i = total + (int64_t)blockIdx.x * blockDim.x + t; i < N; i += (int64_t)gridDim.x * blockDim.x)
-    row_token[i] = -1;
+  for (int64_t i = total + (int64_t)blockIdx.x * THREADS + t; i < N; i += (int64_t)gridDim.x * THREADS) row_token[i] = -1;
 }
 
 // ------------------------------------------------------------------ fast routing
@@ -820,7 +869,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       o.counts[(int64_t)blockIdx.x * sh.stride + x] = x < p.E ? (uint16_t)hist[x] : 0;
   } else if (o.mode == 2) {
     // all pairs here, one segment
-    __shared__ int32_t part_sums[kMaxOrderWaves];
+    __shared__ __attribute__((aligned(16))) int32_t part_sums[kMaxOrderWaves];
     uint16_t* count = (uint16_t*)lds;
     clear_counts(p.E, count);
     const int32_t pairs = (int32_t)T * p.K;
@@ -831,10 +880,10 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
     for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
       const int e = e0 + tid;
       const int32_t c = e < p.E ? hist[e] : 0;
-      const int32_t start = carry + block_exclusive(c, part_sums, total);
+      const int32_t start = carry + block_exclusive<kMaxOrderWaves>(c, waves, part_sums, total);
       carry += total;
       if (e < p.E) {
-        if (e < (p.E + 1) / 2) waves_exclusive(e, p.E, count);
+        if (e < (p.E + 1) / 2) waves_exclusive<kMaxOrderWaves>(e, p.E, waves, count);
         hist[e] = start;
         o.group_end[e] = start + c;
       }
@@ -858,12 +907,12 @@ hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, Ord
   // (1024 threads: 8.0 against 6.7 us for 16384 x 8 pairs of 256 experts, 7.7 against
   // 6.3 for 5003 x 8 of 32; 256 threads: 8.1, 6.5).  A pair per thread, but at most
   // 256 workgroups, since each reads all the counts.
-  const int threads = E > 512 ? kMaxOrderThreads : 512;
-  const int64_t most = N / threads < 256 ? N / threads + 1 : 256;
+  const int waves = E > 512 ? 16 : 8;
+  const int64_t most = N / (waves * kWave) < 256 ? N / (waves * kWave) + 1 : 256;
   const int32_t per = (int32_t)((op.chunks + most - 1) / most);
   const int32_t grid = (op.chunks + per - 1) / per;
-  order_kernel<<<grid, threads, order_lds(threads / kWave, E), st>>>(idx, N, op.chunk, op.chunks, per, E, op.most, K, counts,
-                                                                     group_end, row_token, slot);
+  auto f = waves == 16 ? order_kernel<16> : order_kernel<8>;
+  f<<<grid, waves * kWave, 0, st>>>(idx, N, op.chunk, op.chunks, per, E, op.most, K, counts, group_end, row_token, slot);
   return hipGetLastError();
 }
 
