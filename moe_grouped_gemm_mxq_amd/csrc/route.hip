@@ -184,11 +184,7 @@ constexpr int64_t kCountBytes = 160 << 10;
 static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
 // elements of a chunk's row of counts: a power of two of 16-byte loads
-__host__ __device__ constexpr int32_t count_stride(int32_t E) {
-  int32_t s = 8;
-  while (s < E) s *= 2;
-  return s;
-}
+__host__ __device__ constexpr int32_t count_stride(int32_t E) { return E <= 8 ? 8 : 1 << (32 - __builtin_clz(E - 1)); }
 
 // LDS of the ranking: 16-bit counts of up to kMaxOrderWaves waves, rows of E rounded up to 16 bytes
 __host__ __device__ constexpr int count_row(int E) { return (E + 7) / 8 * 8; }
@@ -226,33 +222,39 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int waves, int32_t
 // earlier lanes have the same; the wave's count of each expert goes to `count`
 // [waves][count_row(E)], which is zero before and read after a barrier.
 __device__ __forceinline__ int rank_in_wave(int32_t x, int32_t E, uint16_t* count) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int wave = threadIdx.x / kWave;
   const int bits = 32 - __builtin_clz(E);  // of 0 .. E
-  uint64_t same = ~0ull;
+  uint32_t lo = ~0u, hi = ~0u;             // lanes with the same
   for (int bit = 0; bit < bits; bit++) {
-    const bool set = x >> bit & 1;
-    const uint64_t m = __ballot(set);
-    same &= set ? m : ~m;
+    const uint32_t set = (uint32_t)((int32_t)((uint32_t)x << (31 - bit)) >> 31);
+    const uint64_t m = __ballot(set != 0);
+    lo &= ~((uint32_t)m ^ set);
+    hi &= ~((uint32_t)(m >> 32) ^ set);
   }
-  const int rank = __popcll(same & ((1ull << lane) - 1));
-  if (x < E && rank == 0) count[wave * count_row(E) + x] = (uint16_t)__popcll(same);
+  const int rank = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
+  if (x < E && rank == 0) count[wave * count_row(E) + x] = (uint16_t)(__popc(lo) + __popc(hi));
   return rank;
 }
-// Counts of experts 2 i and 2 i + 1 -> pairs in earlier waves; returns the segment's, packed.
+// pairs of expert x (E or more: of none) in earlier waves of the segment
+template <int WAVES>
+__device__ __forceinline__ int32_t pairs_before(int32_t x, int32_t E, const uint16_t* count) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint16_t* c = count + min(x, E - 1);
+  int32_t n[WAVES], run = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; w++) n[w] = c[w * count_row(E)];
+#pragma unroll
+  for (int w = 0; w < WAVES; w++) run += w < wave ? n[w] : 0;
+  return run;
+}
+// The segment's counts of experts 2 i and 2 i + 1, packed.
 // (A segment has at most 1024 pairs, so neither half carries into the other.)
 template <int WAVES>
-__device__ __forceinline__ uint32_t waves_exclusive(int i, int32_t E, int waves, uint16_t* count) {
-  const int row = count_row(E) / 2;
-  uint32_t* c = reinterpret_cast<uint32_t*>(count) + i;
-  uint32_t n[WAVES];
-#pragma unroll
-  for (int w = 0; w < WAVES; w++) n[w] = c[min(w, waves - 1) * row];
+__device__ __forceinline__ uint32_t segment_counts(int i, int32_t E, const uint16_t* count) {
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(count) + i;
   uint32_t run = 0;
 #pragma unroll
-  for (int w = 0; w < WAVES; w++) {
-    if (w < waves) c[w * row] = run;
-    run += w < waves ? n[w] : 0;
-  }
+  for (int w = 0; w < WAVES; w++) run += c[w * (count_row(E) / 2)];
   return run;
 }
 __device__ __forceinline__ void clear_counts(int32_t E, uint16_t* count) {
@@ -264,17 +266,19 @@ __device__ __forceinline__ int32_t expert_at(const int32_t* idx, int64_t i, int6
   const int32_t x = i < e ? idx[i] : -1;
   return x >= 0 && x < E ? x : E;
 }
-__device__ __forceinline__ void put_pair(int64_t i, int64_t e, int32_t x, int rank, int32_t E, int32_t K,
-                                         const int32_t* base, const uint16_t* count, int32_t* __restrict__ row_token,
-                                         int32_t* __restrict__ slot) {
+// pair i of token `token` is the rank-th of expert x from row `first` on
+__device__ __forceinline__ void put_pair(int64_t i, int64_t e, int32_t x, int32_t E, int32_t first, int rank,
+                                         int32_t token, int32_t* __restrict__ row_token, int32_t* __restrict__ slot) {
   if (i >= e) return;
   int32_t row = -1;
   if (x < E) {
-    row = base[x] + count[threadIdx.x / kWave * count_row(E) + x] + rank;
-    row_token[row] = (int32_t)((uint32_t)i / (uint32_t)K);  // T * K < 2^31
+    row = first + rank;
+    row_token[row] = token;
   }
   slot[i] = row;
 }
+// token of pair i (T * K < 2^31)
+__device__ __forceinline__ int32_t token_of(int64_t i, int32_t K) { return (int32_t)((uint32_t)i / (uint32_t)K); }
 
 __global__ __launch_bounds__(kMaxOrderThreads) void hist_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
                                                                int32_t E, int32_t stride,
@@ -378,13 +382,15 @@ __global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __re
   const int64_t b = mine * chunk, e = min(b + per * chunk, N);
   int32_t x = -1;
   if (N > 0) x = idx[min(b + t, N - 1)];
+  int32_t token = token_of(b + t, K);
   // Eight experts' counts a load; a row of counts by stride / 8 threads, the chunks dealt to
   // as many such runs of threads as the workgroup holds.  Whole numbers: the order
   // of the additions does not matter.
-  const int stride = count_stride(E), cols = stride / 8, runs = THREADS / cols, run = t / cols, col = t - run * cols;
-  const int visits = (chunks + runs - 1) / runs;
+  const int stride = count_stride(E), shift = __builtin_ctz(stride) - 3;
+  const int cols = 1 << shift, runs = THREADS >> shift, run = t >> shift, col = t & (cols - 1);
+  const int visits = (chunks + runs - 1) >> (__builtin_ctz(THREADS) - shift);
   // two sums a word where no half can carry, after the wave's runs are added up too
-  const bool packed = (int64_t)most * visits * (cols < kWave ? kWave / cols : 1) <= 0xFFFF;
+  const bool packed = (int64_t)most * visits * (cols < kWave ? kWave >> shift : 1) <= 0xFFFF;
   const u32x4* c4 = reinterpret_cast<const u32x4*>(counts) + col;
   uint32_t all8[8] = {}, before8[8] = {};
   if (packed) {
@@ -394,7 +400,7 @@ __global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __re
     else if (visits <= 4)
       sum_counts<true, 4>(c4, cols, chunks, run, runs, mine, a, f);
     else
-      sum_counts<true, 8>(c4, cols, chunks, run, runs, mine, a, f);
+      sum_counts<true, 16>(c4, cols, chunks, run, runs, mine, a, f);
     sum_runs<true>(cols, a);
     sum_runs<true>(cols, f);
 #pragma unroll
@@ -432,29 +438,31 @@ __global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __re
   all = t < E ? all : 0;
   int32_t total;
   const int32_t start = block_exclusive<WAVES>(all, WAVES, part, total);  // a barrier: counts of all waves
-  const int pairs = (E + 1) / 2;  // of experts
-  uint32_t segment = t < pairs ? waves_exclusive<WAVES>(t, E, WAVES, count) : 0;
   if (t < E) {
     base[t] = start + before;
     if (blockIdx.x == 0) group_end[t] = start + all;
   }
+  const int32_t earlier = pairs_before<WAVES>(x, E, count);
   __syncthreads();
+  int32_t row = base[min(x, E - 1)] + earlier;
   for (int64_t s = b;;) {
-    put_pair(s + t, e, x, rank, E, K, base, count, row_token, slot);
+    put_pair(s + t, e, x, E, row, rank, token, row_token, slot);
     s += THREADS;
     if (s >= e) break;
+    const bool two = t < (E + 1) / 2;
+    const uint32_t segment = two ? segment_counts<WAVES>(t, E, count) : 0;
     __syncthreads();
-    if (t < pairs) {
+    if (two) {
       base[2 * t] += segment & 0xFFFFu;
       base[2 * t + 1] += segment >> 16;
     }
     clear_counts(E, count);
     x = expert_at(idx, s + t, e, E);
+    token = token_of(s + t, K);
     __syncthreads();
     rank = rank_in_wave(x, E, count);
     __syncthreads();
-    if (t < pairs) segment = waves_exclusive<WAVES>(t, E, WAVES, count);
-    __syncthreads();
+    row = base[min(x, E - 1)] + pairs_before<WAVES>(x, E, count);
   }
   for (int64_t i = total + (int64_t)blockIdx.x * THREADS + t; i < N; i += (int64_t)gridDim.x * THREADS) row_token[i] = -1;
 }
@@ -883,13 +891,13 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       const int32_t start = carry + block_exclusive<kMaxOrderWaves>(c, waves, part_sums, total);
       carry += total;
       if (e < p.E) {
-        if (e < (p.E + 1) / 2) waves_exclusive<kMaxOrderWaves>(e, p.E, waves, count);
         hist[e] = start;
         o.group_end[e] = start + c;
       }
       __syncthreads();
     }
-    put_pair(tid, pairs, x, rank, p.E, p.K, hist, count, o.row_token, o.slot);
+    const int32_t first = hist[min(x, p.E - 1)] + pairs_before<kMaxOrderWaves>(x, p.E, count);
+    put_pair(tid, pairs, x, p.E, first, rank, token_of(tid, p.K), o.row_token, o.slot);
     if (tid >= carry && tid < pairs) o.row_token[tid] = -1;
   }
 }
