@@ -178,8 +178,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel64(const LT* _
 constexpr int kMaxOrderThreads = 1024, kMaxOrderWaves = kMaxOrderThreads / kWave;
 constexpr int kMaxChunkPairs = 1 << 15;  // counts are 16-bit
 // Counts of all chunks, read whole by every workgroup of order_kernel: a chunk more costs
-// each of them its row.  16384 x 8 pairs of 1024 experts, counted by 1024-pair chunks of
-// the router (512 KB), took 56 us in all, with 64 chunks counted on their own 39 us.
+// each of them its row.  16384 x 8 pairs of 1024 experts in 80 chunks of their own take 33 us with
+// the router, in 160 36; 16384 x 256 in the router's 256 chunks 17.4, in 1024 21.7.
 constexpr int64_t kCountBytes = 160 << 10;
 static_assert(MXQ_MAX_GROUPS <= kMaxOrderThreads, "a thread per expert");
 
@@ -363,8 +363,9 @@ constexpr int kParts = 8;  // partial sums of an expert: one of each wave, or of
 
 // Workgroup b ranks chunks b * per .. (b + 1) * per - 1 of `chunk` pairs, at most `most` of them one expert's.
 //
-// Bound by latency: 16384 x 8 pairs of 256 experts take @A@ us on the GPU, 5003 x 8 of 32 @B@,
-// a launch that does nothing about 2.
+// Bound by latency: a chain of one read of the counts and four barriers.  16384 x 8 pairs of
+// 256 experts take 5 us on the GPU, 5003 x 8 of 32 4, where a launch that does nothing takes 2;
+// 131072 x 8 of 256 with their count 18.5.
 template <int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __restrict__ idx, int64_t N, int64_t chunk,
                                                             int32_t chunks, int32_t per, int32_t E, int32_t most, int32_t K,
@@ -909,14 +910,14 @@ struct OrderPlan {
   int32_t most;   // of them with one expert
 };
 
+// Workgroups of order_kernel at most: each reads all the counts, and there are as many CUs.
+constexpr int64_t kMostOrderGroups = 256;
+
 hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, OrderPlan op, int32_t* group_end,
                         int32_t* row_token, int32_t* slot, const uint16_t* counts, hipStream_t st) {
-  // A thread per expert at least, and no more than 512 for their barriers and sums over waves
-  // (1024 threads: 8.0 against 6.7 us for 16384 x 8 pairs of 256 experts, 7.7 against
-  // 6.3 for 5003 x 8 of 32; 256 threads: 8.1, 6.5).  A pair per thread, but at most
-  // 256 workgroups, since each reads all the counts.
+  // a thread per expert, and few waves to add up
   const int waves = E > 512 ? 16 : 8;
-  const int64_t most = N / (waves * kWave) < 256 ? N / (waves * kWave) + 1 : 256;
+  const int64_t most = std::min<int64_t>(N / (waves * kWave) + 1, kMostOrderGroups);
   const int32_t per = (int32_t)((op.chunks + most - 1) / most);
   const int32_t grid = (op.chunks + per - 1) / per;
   auto f = waves == 16 ? order_kernel<16> : order_kernel<8>;
@@ -926,8 +927,11 @@ hipError_t launch_order(const int32_t* idx, int64_t N, int32_t K, int32_t E, Ord
 
 int64_t chunks_that_fit(int32_t E) { return kCountBytes / (count_stride(E) * (int64_t)sizeof(uint16_t)); }
 
+// Chunks counted on their own: one for each workgroup of order_kernel, not more (320, so two
+// of them for each of 160 workgroups, take 13.0 against 9.8 us for 32768 x 8 pairs of 256 experts
+// and 74 against 50 for 524288 x 8).
 OrderPlan order_plan(int64_t N, int32_t E) {
-  const int64_t most = std::min<int64_t>(chunks_that_fit(E), 512);
+  const int64_t most = std::min<int64_t>(chunks_that_fit(E), kMostOrderGroups);
   const int64_t chunk = std::min<int64_t>(std::max<int64_t>((N + most - 1) / most, 512), kMaxChunkPairs);
   const int64_t c = (N + chunk - 1) / chunk;
   return {(int32_t)(c < 1 ? 1 : c), chunk, (int32_t)chunk};
@@ -947,7 +951,7 @@ constexpr int64_t kFastRows = 1 << 25;  // of route_fast: 64 lanes each, in a gr
 // Largest number of chunks that a call on these sizes cuts its pairs into: order_plan's,
 // or one for each of route_fast's workgroups.
 int64_t max_chunks(int64_t T, int32_t K, int32_t E) {
-  return std::max<int64_t>(order_plan(T * K, E).chunks, std::min<int64_t>(chunks_that_fit(E), T / 4 + 1));
+  return std::max<int64_t>(order_plan(T * K, E).chunks, std::min<int64_t>({chunks_that_fit(E), 2 * kMostOrderGroups, T / 4 + 1}));
 }
 
 int ceil_log2(int v) {
@@ -983,16 +987,21 @@ hipError_t route_fast(RouteArgs a) {
   const bool order = a.o.group_end != nullptr;
   const int64_t units = (a.T + RPW - 1) / RPW;  // waves' worth of rows
   // One workgroup does it all where it holds the rows and their pairs are one segment of
-  // the ranking.  Else workgroups of 4 waves, of 16 where only their counts are few enough
-  // to be added up; where not even theirs are, the order is taken from idx afterwards.
+  // the ranking.  Else workgroups of as few waves, from 4 to 16, as leave a chunk of counts for
+  // each workgroup of order_kernel (8192 x 256: 14.0 us with 8 waves, 15.8 with 16), at
+  // most two chunks with 16 waves.  Where that is not enough, the order is taken from idx
+  // afterwards (65536 x 32: 20.8, in four chunks 21.8; 32768 x 256: 25.5, in two 28.5).
   const bool alone = order && units <= 16 && a.T * a.p.K <= kMaxOrderThreads;
   const int64_t pair_waves = (a.T * a.p.K + kWave - 1) / kWave;
   auto chunks = [&](int64_t waves) { return (units + waves - 1) / waves; };
-  const int waves = alone ? (int)std::max<int64_t>({units, pair_waves, 1})
-                          : order && chunks(4) > chunks_that_fit(a.p.E) && chunks(16) <= chunks_that_fit(a.p.E) ? 16 : 4;
+  auto few = [&](int64_t waves, int64_t most) { return chunks(waves) <= std::min<int64_t>(chunks_that_fit(a.p.E), most); };
+  const bool counts = order && !alone && few(16, 2 * kMostOrderGroups);
+  const int waves = alone                       ? (int)std::max<int64_t>({units, pair_waves, 1})
+                    : !counts || few(4, kMostOrderGroups) ? 4
+                    : few(8, kMostOrderGroups)            ? 8
+                                               : 16;
   const int64_t rows = (int64_t)waves * RPW;
   const int64_t grid = alone ? 1 : chunks(waves);
-  const bool counts = order && !alone && grid <= chunks_that_fit(a.p.E);
   a.o.mode = alone ? 2 : counts ? 1 : 0;
   const Shape sh = {ceil_log2(LPR) - ceil_log2(a.p.n_group), count_stride(a.p.E),
                     (EPL * LPR) >> ceil_log2(a.p.n_group) == a.p.E / a.p.n_group && 1 << ceil_log2(a.p.n_group) == a.p.n_group};
@@ -1013,15 +1022,18 @@ hipError_t route_fast(RouteArgs a) {
 template <typename LT>
 hipError_t route(const RouteArgs& a) {
   const RouteParams& p = a.p;
-  // Few rows: a wave for each, so that a lane has few experts to go through.  Many: as
-  // few lanes as hold the row, since a choice costs a wave the same for one row or four.
-  if (a.T >= kManyRows && a.T <= kFastRows) {
+  // As few lanes as hold the row, since a choice costs a wave the same for one row or four.
+  // But few rows of many experts take a wave each, so that a lane has no 16 experts to go
+  // through: 256 experts, 256 rows 4.5 against 5.2 us, 4096 rows 6.5 against 7.0 (with the
+  // expert order 14.4 against 13.7), 16384 rows 17.9 against 10.2.  (32 experts,
+  // 256 rows: 3.4 by a wave each, 3.0 by 16 lanes.)
+  if (a.T > 0 && a.T <= kFastRows) {  // its waves read a row before they look whether it is there
     if (holds<LT, 16, 2>(p)) return route_fast<LT, 16, 2>(a);
     if (holds<LT, 16, 4>(p)) return route_fast<LT, 16, 4>(a);
-    if (holds<LT, 16, 16>(p)) return route_fast<LT, 16, 16>(a);
-    if (holds<LT, 32, 16>(p)) return route_fast<LT, 32, 16>(a);
-  }
-  if (a.T > 0 && a.T <= kFastRows) {  // its waves read a row before they look whether it is there
+    if (a.T >= kManyRows) {
+      if (holds<LT, 16, 16>(p)) return route_fast<LT, 16, 16>(a);
+      if (holds<LT, 32, 16>(p)) return route_fast<LT, 32, 16>(a);
+    }
     if (holds<LT, 64, 4>(p)) return route_fast<LT, 64, 4>(a);
     if (holds<LT, 64, 16>(p)) return route_fast<LT, 64, 16>(a);
   }
