@@ -410,13 +410,17 @@ _DTYPES = {torch.float32: MXQ_DT_F32, torch.bfloat16: MXQ_DT_BF16}
 _SCORES = {"softmax": MXQ_SCORE_SOFTMAX, "sigmoid": MXQ_SCORE_SIGMOID, 0: MXQ_SCORE_SOFTMAX, 1: MXQ_SCORE_SIGMOID}
 
 
-def _need_float(t, name):
-    """Type code of a float matrix on the device with unit stride along its last dim."""
+def _matrix(t, name):
+    """(type code, rows, columns, row stride) of a float matrix on the device with unit stride along its last dim."""
     try:
         dt = _DTYPES[t.dtype]
-        if t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
-            return dt
-    except (AttributeError, KeyError):
+        rows, cols = t.shape
+        if t.is_cuda:
+            stride, unit = t.stride()
+            if unit == 1 or cols <= 1:
+                # the stride of a dim of size 1 or 0 says nothing
+                return dt, rows, cols, stride if rows > 1 or stride > cols else cols
+    except (AttributeError, KeyError, ValueError):
         pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -445,12 +449,6 @@ def _need_array(t, name, dtype, shape):
     raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _row_stride(t):
-    """Row stride the C entry points take (the stride of a dim of size 1 or 0 says nothing)."""
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
-
-
 def _raw(t):
     return None if t is None else t.data_ptr()
 
@@ -474,15 +472,14 @@ def mxq_route(logits, cfg, idx, weights, bias=None, group_end=None, row_token=No
               stream=None):
     """logits fp32 or bf16 [T][E] (unit column stride) -> idx int32, weights fp32 [T][top_k]; with group_end int32
     [E], row_token int32 [T * top_k], slot int32 [T][top_k] and a uint8 workspace the expert order too."""
-    dt = _need_float(logits, "logits")
-    T, E = logits.shape
+    dt, T, E, ld = _matrix(logits, "logits")
     K = cfg.top_k
     _need_array(idx, "idx", torch.int32, (T, K))
     _need_array(weights, "weights", torch.float32, (T, K))
     if bias is not None:
         _need_array(bias, "bias", torch.float32, (E,))
     nbytes = _need_order(group_end, row_token, slot, workspace, T, K, E) if group_end is not None else 0
-    _check(_lib.mxq_route(logits.data_ptr(), dt, T, E, _row_stride(logits), _raw(bias), ctypes.byref(cfg), idx.data_ptr(),
+    _check(_lib.mxq_route(logits.data_ptr(), dt, T, E, ld, _raw(bias), ctypes.byref(cfg), idx.data_ptr(),
                           weights.data_ptr(), _raw(group_end), _raw(row_token), _raw(slot), _raw(workspace), nbytes,
                           _stream(stream, logits.device)), "mxq_route")
 
@@ -507,60 +504,61 @@ def mxq_expert_order(idx, E, group_end, row_token, slot, workspace, stream=None)
 
 def mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream=None):
     """dweights fp32 [T][top_k] -> dlogits [T][E] of the logits' type, every element written."""
-    dt = _need_float(logits, "logits")
-    T, E = logits.shape
-    if _need_float(dlogits, "dlogits") != dt or dlogits.shape != logits.shape:
+    dt, T, E, ld = _matrix(logits, "logits")
+    ddt, rows, cols, ldd = _matrix(dlogits, "dlogits")
+    if (ddt, rows, cols) != (dt, T, E):
         raise ValueError("dlogits must have the logits' type and shape")
     _need_array(idx, "idx", torch.int32, (T, cfg.top_k))
     _need_array(dweights, "dweights", torch.float32, (T, cfg.top_k))
-    _check(_lib.mxq_route_backward(logits.data_ptr(), dt, T, E, _row_stride(logits), ctypes.byref(cfg), idx.data_ptr(),
-                                   dweights.data_ptr(), dlogits.data_ptr(), _row_stride(dlogits),
+    _check(_lib.mxq_route_backward(logits.data_ptr(), dt, T, E, ld, ctypes.byref(cfg), idx.data_ptr(),
+                                   dweights.data_ptr(), dlogits.data_ptr(), ldd,
                                    _stream(stream, logits.device)), "mxq_route_backward")
 
 
 def _need_pairs(slot, weights):
-    if isinstance(slot, torch.Tensor) and slot.dim() != 2:
-        raise ValueError(f"slot must have 2 dims, got {slot.dim()}")
-    _need_array(slot, "slot", torch.int32, getattr(slot, "shape", None))
+    shape = slot.shape if isinstance(slot, torch.Tensor) else None
+    _need_array(slot, "slot", torch.int32, shape)
+    if len(shape) != 2:
+        raise ValueError(f"slot must have 2 dims, got {len(shape)}")
     if weights is not None:
-        _need_array(weights, "weights", torch.float32, slot.shape)
-    return slot.shape
+        _need_array(weights, "weights", torch.float32, shape)
+    return shape
 
 
 def mxq_combine(y, slot, weights, out, stream=None):
     """out[t] = sum_k weights[t][k] * y[slot[t][k]]; y [rows][H], slot int32 [T][top_k], weights fp32 or None, out
     [T][H]; y and out fp32 or bf16 with unit column stride."""
-    ydt, odt = _need_float(y, "y"), _need_float(out, "out")
+    ydt, rows, H, ldy = _matrix(y, "y")
+    odt, tokens, cols, ldo = _matrix(out, "out")
     T, K = _need_pairs(slot, weights)
-    if out.shape != (T, y.shape[1]):
-        raise ValueError(f"out must have shape {(T, y.shape[1])}, got {tuple(out.shape)}")
-    _check(_lib.mxq_combine(y.data_ptr(), ydt, y.shape[0], _row_stride(y), slot.data_ptr(), _raw(weights), T, K, y.shape[1],
-                            out.data_ptr(), odt, _row_stride(out), _stream(stream, out.device)), "mxq_combine")
+    if tokens != T or cols != H:
+        raise ValueError(f"out must have shape {(T, H)}, got {tuple(out.shape)}")
+    _check(_lib.mxq_combine(y.data_ptr(), ydt, rows, ldy, slot.data_ptr(), _raw(weights), T, K, H, out.data_ptr(), odt, ldo,
+                            _stream(stream, out.device)), "mxq_combine")
 
 
 def mxq_combine_backward(dout, slot, rows, dy=None, dweights=None, weights=None, y=None, stream=None):
     """dy[slot[t][k]] = weights[t][k] * dout[t] ([rows][H]); dweights[t][k] = <dout[t], y[slot[t][k]]> (needs y)."""
-    dt = _need_float(dout, "dout")
+    dt, tokens, H, ldd = _matrix(dout, "dout")
     T, K = _need_pairs(slot, weights)
-    H = dout.shape[1]
-    if dout.shape[0] != T:
-        raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
+    if tokens != T:
+        raise ValueError(f"dout must have {T} rows, got {tokens}")
     ydt = gdt = dt
+    ldy = ldg = 0
     if y is not None:
-        ydt = _need_float(y, "y")
-        if y.shape != (rows, H):
+        ydt, n, cols, ldy = _matrix(y, "y")
+        if n != rows or cols != H:
             raise ValueError(f"y must have shape {(rows, H)}, got {tuple(y.shape)}")
     if dy is not None:
-        gdt = _need_float(dy, "dy")
-        if dy.shape != (rows, H):
+        gdt, n, cols, ldg = _matrix(dy, "dy")
+        if n != rows or cols != H:
             raise ValueError(f"dy must have shape {(rows, H)}, got {tuple(dy.shape)}")
     if dweights is not None:
         _need_array(dweights, "dweights", torch.float32, (T, K))
         if y is None:
             raise ValueError("dweights needs y")
-    _check(_lib.mxq_combine_backward(dout.data_ptr(), dt, _row_stride(dout), _raw(y), ydt, 0 if y is None else _row_stride(y),
-                                     slot.data_ptr(), _raw(weights), T, K, H, rows, _raw(dy), gdt,
-                                     0 if dy is None else _row_stride(dy), _raw(dweights), _stream(stream, dout.device)),
+    _check(_lib.mxq_combine_backward(dout.data_ptr(), dt, ldd, _raw(y), ydt, ldy, slot.data_ptr(), _raw(weights), T, K, H, rows,
+                                     _raw(dy), gdt, ldg, _raw(dweights), _stream(stream, dout.device)),
            "mxq_combine_backward")
 
 
@@ -702,7 +700,8 @@ def _workspace(T, top_k, E, device, stream):
 def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0,
           order=True, out=None, stream=None):
     """Route tokens: {"idx", "weights"} and, with order, {"group_end", "row_token", "slot"} (the expert order the grouped
-    entry points and combine take).  out: a dict of such buffers to write to ("workspace" may be among them)."""
+    entry points and combine take).  out: a dict of such buffers to write to; with order, it may have the "workspace" too,
+    which is put there for the calls after where it is missing."""
     cfg = _kept_config(top_k, score, n_group, topk_group, group_top, renormalise, scale)
     T, E = logits.shape
     if out is None:
@@ -710,14 +709,15 @@ def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1,
         out = {"idx": i32((T, top_k)), "weights": torch.empty((T, top_k), dtype=torch.float32, device=logits.device)}
         if order:
             out.update(group_end=i32((E,)), row_token=i32((T * top_k,)), slot=i32((T, top_k)))
+    idx, weights = out["idx"], out["weights"]
     if not order:
-        mxq_route(logits, cfg, out["idx"], out["weights"], bias, stream=stream)
-        return out
-    ws = out.get("workspace")
+        mxq_route(logits, cfg, idx, weights, bias, stream=stream)
+        return {"idx": idx, "weights": weights}
+    group_end, row_token, slot, ws = out["group_end"], out["row_token"], out["slot"], out.get("workspace")
     if ws is None:
-        ws = _workspace(T, top_k, E, logits.device, stream)
-    mxq_route(logits, cfg, out["idx"], out["weights"], bias, out["group_end"], out["row_token"], out["slot"], ws, stream)
-    return out
+        ws = out["workspace"] = _workspace(T, top_k, E, logits.device, stream)
+    mxq_route(logits, cfg, idx, weights, bias, group_end, row_token, slot, ws, stream)
+    return {"idx": idx, "weights": weights, "group_end": group_end, "row_token": row_token, "slot": slot}
 
 
 def expert_order(idx, E, stream=None):
