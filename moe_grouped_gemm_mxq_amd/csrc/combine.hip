@@ -1,8 +1,10 @@
 // The experts' rows back in token order (weighted combine) and its gradient,
 // which is also the dispatch of tokens into expert order.
 //
-// Both stream: combine reads each row of y once and writes each token once,
-// the gradient reads y and dout and writes dy.  A workgroup takes one token and
+// Both stream and are bound by HBM: combine reads each row of y once and writes
+// each token once (16384 x 8 x 4096 fp32 rows to bf16: 377 to 401 us by part, 6.05 to 5.7
+// TB/s, where copies reach 6.0), the gradient reads y and dout and writes dy
+// (600 to 624 us, 5.6 to 5.4 TB/s, a third of it written).  A workgroup takes one token and
 // a tile of its columns (the gradient's dot products need the whole token, so
 // there it walks the tiles), a thread eight consecutive columns, and the loads
 // of up to kRows rows are issued before the first of them is used.
@@ -18,8 +20,8 @@ constexpr int kWave = 64;
 constexpr int kMaxThreads = 512;
 constexpr int kCols = 8;  // columns of a thread in a tile of kCols * blockDim.x
 // Rows in flight.  A thread's sums are the same few registers however many rows
-// feed them, so combine takes eight; the gradient also writes eight rows then,
-// and measured 5.25 TB/s with eight, 5.35 with four (16384 x 8 x 4096, fp32 y).
+// feed them, so combine takes eight; the gradient also writes eight rows then, and
+// takes 635 us with eight, 624 with four (16384 x 8 x 4096, fp32 y, on one part).
 constexpr int kRows = 8, kRowsBackward = 4;
 
 // workgroups for `units` units of work, one each while a grid can hold them
@@ -203,9 +205,10 @@ mxq_status check_pairs(const char* what, const int32_t* slot, const float* weigh
 }
 
 // Tiles of a row and threads of a workgroup.  As few tiles as up to 512 threads
-// allow (16384 x 8 x 4096 fp32 rows: 372 us with 512, 385 with 256 and two
-// tiles), then as few whole waves as the tiles need, so that most threads have
-// all their columns inside the row.  Few tokens: half as large, to reach more CUs.
+// allow (16384 x 8 x 4096 fp32 rows, 512 threads against 256 and two tiles: the gradient
+// 624 against 649 us, combine 401 against 399), then as few whole waves as the
+// tiles need, so that most threads have all their columns inside the row.  Few
+// tokens: half as large, to reach more CUs.
 struct Shape {
   unsigned threads;
   uint32_t tiles;
@@ -226,8 +229,8 @@ hipError_t combine(const void* y, int64_t rows, int64_t ldy, const int32_t* slot
            : K <= 2 ? combine_kernel<YT, OT, W, 2>
            : K <= 4 ? combine_kernel<YT, OT, W, 4>
                     : combine_kernel<YT, OT, W, kRows>;
-  f<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, (uint32_t)H, (OT*)out, ldo, T,
-                                                s.tiles);
+  f<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, (uint32_t)H, (OT*)out,
+                                                ldo, T, s.tiles);
   return hipGetLastError();
 }
 
