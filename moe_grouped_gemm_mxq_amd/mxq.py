@@ -449,6 +449,12 @@ def _need_array(t, name, dtype, shape):
     raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _type_code(dtype):
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    return _DTYPES[dtype]
+
+
 def _raw(t):
     return None if t is None else t.data_ptr()
 
@@ -508,11 +514,15 @@ def mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream=None):
     ddt, rows, cols, ldd = _matrix(dlogits, "dlogits")
     if (ddt, rows, cols) != (dt, T, E):
         raise ValueError("dlogits must have the logits' type and shape")
-    _need_array(idx, "idx", torch.int32, (T, cfg.top_k))
-    _need_array(dweights, "dweights", torch.float32, (T, cfg.top_k))
-    _check(_lib.mxq_route_backward(logits.data_ptr(), dt, T, E, ld, ctypes.byref(cfg), idx.data_ptr(),
-                                   dweights.data_ptr(), dlogits.data_ptr(), ldd,
-                                   _stream(stream, logits.device)), "mxq_route_backward")
+    _route_backward(logits, dt, T, E, ld, cfg, idx, dweights, dlogits, ldd, stream)
+
+
+def _route_backward(logits, dt, T, E, ld, cfg, idx, dweights, dlogits, ldd, stream):
+    pairs = (T, cfg.top_k)
+    _need_array(idx, "idx", torch.int32, pairs)
+    _need_array(dweights, "dweights", torch.float32, pairs)
+    _check(_lib.mxq_route_backward(logits.data_ptr(), dt, T, E, ld, ctypes.byref(cfg), idx.data_ptr(), dweights.data_ptr(),
+                                   dlogits.data_ptr(), ldd, _stream(stream, logits.device)), "mxq_route_backward")
 
 
 def _need_pairs(slot, weights):
@@ -533,22 +543,18 @@ def mxq_combine(y, slot, weights, out, stream=None):
     T, K = _need_pairs(slot, weights)
     if tokens != T or cols != H:
         raise ValueError(f"out must have shape {(T, H)}, got {tuple(out.shape)}")
+    _combine(y, ydt, rows, ldy, slot, weights, T, K, H, out, odt, ldo, stream)
+
+
+def _combine(y, ydt, rows, ldy, slot, weights, T, K, H, out, odt, ldo, stream):
     _check(_lib.mxq_combine(y.data_ptr(), ydt, rows, ldy, slot.data_ptr(), _raw(weights), T, K, H, out.data_ptr(), odt, ldo,
                             _stream(stream, out.device)), "mxq_combine")
 
 
 def mxq_combine_backward(dout, slot, rows, dy=None, dweights=None, weights=None, y=None, stream=None):
     """dy[slot[t][k]] = weights[t][k] * dout[t] ([rows][H]); dweights[t][k] = <dout[t], y[slot[t][k]]> (needs y)."""
-    dt, tokens, H, ldd = _matrix(dout, "dout")
-    T, K = _need_pairs(slot, weights)
-    if tokens != T:
-        raise ValueError(f"dout must have {T} rows, got {tokens}")
-    ydt = gdt = dt
-    ldy = ldg = 0
-    if y is not None:
-        ydt, n, cols, ldy = _matrix(y, "y")
-        if n != rows or cols != H:
-            raise ValueError(f"y must have shape {(rows, H)}, got {tuple(y.shape)}")
+    dt, T, K, H, ldd, ydt, ldy = _need_gradient(dout, slot, rows, weights, y)
+    gdt, ldg = dt, 0
     if dy is not None:
         gdt, n, cols, ldg = _matrix(dy, "dy")
         if n != rows or cols != H:
@@ -557,6 +563,23 @@ def mxq_combine_backward(dout, slot, rows, dy=None, dweights=None, weights=None,
         _need_array(dweights, "dweights", torch.float32, (T, K))
         if y is None:
             raise ValueError("dweights needs y")
+    _combine_backward(dout, dt, ldd, y, ydt, ldy, slot, weights, T, K, H, rows, dy, gdt, ldg, dweights, stream)
+
+
+def _need_gradient(dout, slot, rows, weights, y):
+    dt, tokens, H, ldd = _matrix(dout, "dout")
+    T, K = _need_pairs(slot, weights)
+    if tokens != T:
+        raise ValueError(f"dout must have {T} rows, got {tokens}")
+    ydt, ldy = dt, 0
+    if y is not None:
+        ydt, n, cols, ldy = _matrix(y, "y")
+        if n != rows or cols != H:
+            raise ValueError(f"y must have shape {(rows, H)}, got {tuple(y.shape)}")
+    return dt, T, K, H, ldd, ydt, ldy
+
+
+def _combine_backward(dout, dt, ldd, y, ydt, ldy, slot, weights, T, K, H, rows, dy, gdt, ldg, dweights, stream):
     _check(_lib.mxq_combine_backward(dout.data_ptr(), dt, ldd, _raw(y), ydt, ldy, slot.data_ptr(), _raw(weights), T, K, H, rows,
                                      _raw(dy), gdt, ldg, _raw(dweights), _stream(stream, dout.device)),
            "mxq_combine_backward")
@@ -732,25 +755,31 @@ def expert_order(idx, E, stream=None):
 def route_backward(logits, idx, dweights, *, score="softmax", renormalise=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
     cfg = _kept_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
-    dlogits = logits.new_empty(logits.shape)
-    mxq_route_backward(logits, cfg, idx, dweights, dlogits, stream)
+    dt, T, E, ld = _matrix(logits, "logits")
+    dlogits = logits.new_empty((T, E))
+    _route_backward(logits, dt, T, E, ld, cfg, idx, dweights, dlogits, E, stream)
     return dlogits
 
 
 def combine(y, slot, weights=None, dtype=torch.bfloat16, stream=None):
     """The experts' rows y [rows][H] back in token order: [T][H] of `dtype`."""
-    out = y.new_empty((slot.shape[0], y.shape[1]), dtype=dtype)
-    mxq_combine(y, slot, weights, out, stream)
+    ydt, rows, H, ldy = _matrix(y, "y")
+    T, K = _need_pairs(slot, weights)
+    odt = _type_code(dtype)
+    out = y.new_empty((T, H), dtype=dtype)
+    _combine(y, ydt, rows, ldy, slot, weights, T, K, H, out, odt, H, stream)
     return out
 
 
 def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=None):
     """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights."""
-    dy = dout.new_empty((rows, dout.shape[1]), dtype=dtype or dout.dtype)
-    dw = None
-    if y is not None and weights is not None:
-        dw = weights.new_empty(slot.shape)
-    mxq_combine_backward(dout, slot, rows, dy, dw, weights, y if dw is not None else None, stream)
+    if weights is None:
+        y = None
+    dt, T, K, H, ldd, ydt, ldy = _need_gradient(dout, slot, rows, weights, y)
+    gdt = dt if dtype is None else _type_code(dtype)
+    dy = dout.new_empty((rows, H), dtype=dtype)
+    dw = None if y is None else torch.empty_like(weights)
+    _combine_backward(dout, dt, ldd, y, ydt, ldy, slot, weights, T, K, H, rows, dy, gdt, H, dw, stream)
     return dy, dw
 
 

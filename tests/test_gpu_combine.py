@@ -209,3 +209,12 @@ def test_on_another_stream():
     st.synchronize()
     assert torch.equal(got, want) and torch.equal(grads[1], g2[1])
     assert torch.equal(grads[0][slot.long()], g2[0][slot.long()])
+
+
+def test_helpers_refuse_other_types():
+    m = mxq()
+    y, slot = torch.zeros(4, 8, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    with pytest.raises(TypeError, match="dtype must be"):
+        m.combine(y, slot, dtype=torch.float16)
+    with pytest.raises(TypeError, match="dtype must be"):
+        m.dispatch(y[:2], slot, 4, dtype=torch.float64)
