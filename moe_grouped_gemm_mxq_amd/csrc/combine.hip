@@ -220,14 +220,26 @@ Shape shape_of(int64_t T, int64_t H) {
   return {(unsigned)waves * kWave, (uint32_t)tiles};
 }
 
+// The K rows in as few passes of at most `most` as hold them, and those of one size: rows that
+// a pass lacks are loads of the last one again.  8192 tokens of 4096 fp32 columns: one row in
+// a pass of one 35 us (the gradient 47), in a pass of two 43 (61); five in the
+// gradient in passes of three 201, of four 224.
+int rows_at_a_time(int32_t K, int most) {
+  const int passes = (K + most - 1) / most;
+  return (K + passes - 1) / passes;
+}
+
 template <typename YT, typename OT>
 hipError_t combine(const void* y, int64_t rows, int64_t ldy, const int32_t* slot, const float* weights, int64_t T,
                    int32_t K, int64_t H, void* out, int64_t ldo, hipStream_t st) {
   const Shape s = shape_of(T, H);
   constexpr int W = width(sizeof(YT), sizeof(OT));
+  const int n = rows_at_a_time(K, kRows);
   auto f = H < W    ? combine_kernel<YT, OT, 1, 2>
-           : K <= 2 ? combine_kernel<YT, OT, W, 2>
-           : K <= 4 ? combine_kernel<YT, OT, W, 4>
+           : n == 1 ? combine_kernel<YT, OT, W, 1>
+           : n == 2 ? combine_kernel<YT, OT, W, 2>
+           : n <= 4 ? combine_kernel<YT, OT, W, 4>
+           : n <= 6 ? combine_kernel<YT, OT, W, 6>
                     : combine_kernel<YT, OT, W, kRows>;
   f<<<grid_of(T * s.tiles), s.threads, 0, st>>>((const YT*)y, (int32_t)rows, ldy, slot, weights, K, (uint32_t)H, (OT*)out,
                                                 ldo, T, s.tiles);
@@ -241,8 +253,11 @@ hipError_t combine_backward(const void* dout, int64_t ldd, const void* y, int64_
   const Shape s = shape_of(T, H);
   // dy's type has no part in W, hence none in the order of the dot products
   constexpr int W = width(sizeof(DT), sizeof(YT));
+  const int n = rows_at_a_time(K, kRowsBackward);
   auto f = dweights ? (H < W    ? combine_backward_kernel<DT, YT, GT, 1, 2, true>
-                       : K <= 2 ? combine_backward_kernel<DT, YT, GT, W, 2, true>
+                       : n == 1 ? combine_backward_kernel<DT, YT, GT, W, 1, true>
+                       : n == 2 ? combine_backward_kernel<DT, YT, GT, W, 2, true>
+                       : n == 3 ? combine_backward_kernel<DT, YT, GT, W, 3, true>
                                 : combine_backward_kernel<DT, YT, GT, W, kRowsBackward, true>)
                     : (H < W ? combine_backward_kernel<DT, YT, GT, 1, kRowsBackward, false>
                              : combine_backward_kernel<DT, YT, GT, W, kRowsBackward, false>);

@@ -84,7 +84,8 @@ def check_backward(d, slot, rows, w, y, gdt):
 
 
 SIZES = [(0, 2, 8), (1, 1, 1), (1, 8, 7), (3, 2, 64), (5, 3, 129), (7, 8, 1000), (2, 32, 1024), (33, 8, 2048), (16, 6, 4095),
-         (9, 4, 4104), (3, 8, 7168), (2, 2, 20000), (70, 1, 256)]
+         (9, 4, 4104), (3, 8, 7168), (2, 2, 20000), (70, 1, 256), (6, 5, 520), (3, 7, 264), (4, 9, 1030), (2, 11, 100),
+         (2, 17, 65)]
 
 
 @pytest.mark.parametrize("ydt", TYPES)
