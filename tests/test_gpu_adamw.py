@@ -244,3 +244,37 @@ def test_on_another_stream():
     st.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(a[0], b[0]))
     assert all(torch.equal(x[0], y[0]) and torch.equal(x[1], y[1]) for s, t in ((a[2], b[2]), (a[3], b[3])) for x, y in zip(s, t))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_places_in_flat_buffers_do_not_matter(bits):
+    """The same tensors at other places give the same bits, and nothing beside them is written."""
+    m = mxq()
+    p, g, mm, vv = tensors(SIZES, torch.float32, torch.float32, bits, 9)
+    flat = lambda x: [x] if torch.is_tensor(x) else list(x)  # noqa: E731
+    groups = [p, g, [flat(x)[0] for x in mm], [flat(x)[0] for x in vv]]
+    for shifts in ((1, 1, 1, 1), (31, 31, 31, 31), (5, 2, 30, 17), (0, 3, 32, 64)):
+        placed, beside = [], []
+        for xs, o in zip(groups, shifts):
+            guard = 77 if xs[0].dtype == torch.uint8 else -7.5
+            buf = torch.full((sum(len(x) + 3 for x in xs) + o + 40,), guard, dtype=xs[0].dtype, device="cuda")
+            free, views = torch.ones(len(buf), dtype=torch.bool, device="cuda"), []
+            for x in xs:
+                buf[o:o + len(x)] = x
+                free[o:o + len(x)] = False
+                views.append(buf[o:o + len(x)])
+                o += len(x) + 3
+            placed.append(views)
+            beside.append((buf, free, guard))
+        scales = lambda s: [x[1].clone() for x in s]  # noqa: E731
+        a = [[x.clone() for x in xs] for xs in groups]
+        am, av, bm, bv = a[2], a[3], placed[2], placed[3]
+        if bits == 8:
+            am, av = list(zip(am, scales(mm))), list(zip(av, scales(vv)))
+            bm, bv = list(zip(bm, scales(mm))), list(zip(bv, scales(vv)))
+        for args in ((a[0], a[1], am, av), (placed[0], placed[1], bm, bv)):
+            m.AdamW(*args).step(step=3, seed=11)
+        for one, other in zip(a, placed):
+            assert all(torch.equal(x, y) for x, y in zip(one, other)), shifts
+        for buf, free, guard in beside:
+            assert torch.all(buf[free] == guard), shifts
