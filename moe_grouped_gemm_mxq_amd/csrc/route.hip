@@ -478,7 +478,7 @@ __global__ __launch_bounds__(WAVES* kWave) void order_kernel(const int32_t* __re
 //
 // Bound by the vector units and, up to some 16000 rows, by the latency of one pass
 // (launch, read, choices one after another, write): 16384 x 256 sigmoid rows with a bias in 8
-// groups take 10.2 us, 65536 in one group 20.5 (67 MB, 3.3 TB/s), 65536 x 256 bf16
+// groups take 9.6 us, 65536 in one group 20.5 (67 MB, 3.3 TB/s), 65536 x 256 bf16
 // rows of a softmax 16.8.
 struct Shape {
   int32_t lpg_log2;  // lanes per group
@@ -705,22 +705,37 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         a = fmaxf(a, a2);
       }
       const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
-      int rank = 0;
-      for (int q = 0; q < p.n_group; q++) {
-        const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
-        rank += other > total || (other == total && q < g);
-      }
-      kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
-      if (KEYS != kLogits) {
+      if (KEYS == kLogits) {  // exact
+        int rank = 0;
+        for (int q = 0; q < p.n_group; q++) {
+          const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
+          rank += other > total || (other == total && q < g);
+        }
+        kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
+      } else {
+        // The largest total topk_group times over; groups of one total go together, and
+        // too many of them are told apart below.  (16384 x 256 rows in 8 groups 9.6 us, by
+        // comparing each group with each 10.0; 1024 experts in 64 groups 33.6 and 45.5.)
+        uint32_t left = g < p.n_group && total > -INFINITY ? ordered(total) : 0u, least = 0;
+        kept = false;
+        for (int r = 0; r < p.topk_group; r++) {
+          const uint32_t m = row_max<LPR>(left);
+          least = m != 0 ? m : least;  // 0: no group is left
+          if (left == m && m != 0) {
+            kept = true;
+            left = 0;
+          }
+        }
         // Of the least total kept and the largest not kept: fp32 totals of distinct
         // exact values can swap when they differ by at most twice a total's error, that
         // of two scores (4 half steps of 1 for a sigmoid, 42 for a softmax) and three
         // roundings.  Then the totals are taken in fp64, from the experts that can be
         // among their groups' best two.
-        const float least = -row_fmax<LPR>(kept ? -total : -INFINITY);
-        const float most = row_fmax<LPR>(!kept && g < p.n_group ? total : -INFINITY);
-        const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(least) * 0x1p-22f;
-        const bool open = most > -INFINITY && least - most <= error;
+        const uint32_t most = row_max<LPR>(left);
+        const float low = unordered(least);
+        const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(low) * 0x1p-22f;
+        const bool many = __popcll(__ballot(kept) >> first_lane & ROW) > p.topk_group << sh.lpg_log2;
+        const bool open = many || (most != 0 && low - unordered(most) <= error);
         if (__any(open)) {
           const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
           const float from = (p.group_top == 2 && b > -INFINITY ? b : a) - error;

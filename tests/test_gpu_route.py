@@ -88,6 +88,25 @@ def test_route_groups(E, n_group, topk_group, K, group_top, score):
             check_route(x, K, b, renormalise=True, scale=1.0, **kw)
 
 
+@pytest.mark.parametrize("T", [9, 4100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,K", [(64, 8, 3, 6), (256, 8, 4, 8), (96, 3, 2, 4), (512, 64, 20, 8)])
+def test_route_groups_of_equal_totals(E, n_group, topk_group, K, score, T):
+    """Rows of few distinct logits: groups tie for the last place, for the first, and all of them; some are masked."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.randint(0, 2, (T, E), generator=g).float()
+    x[0], x[1, E // 2:] = 0.25, 1.0
+    x[2, : E // n_group * (n_group - topk_group + 1)] = -float("inf")
+    x[3] = torch.arange(E) // (E // n_group) % 2
+    zero = torch.zeros(E, device="cuda")
+    few = T < 100  # the reference takes its time
+    for dtype in (torch.float32, torch.bfloat16) if few else (torch.float32,):
+        for b in (None, zero) if few else (zero,):
+            for top in (1, 2) if few else (2,):
+                check_route(x.to(dtype).cuda(), K, b, score=score, n_group=n_group, topk_group=topk_group, group_top=top,
+                            renormalise=True, scale=1.0)
+
+
 @pytest.mark.parametrize("T", [41, 4100])
 @pytest.mark.parametrize("E,n_group,topk_group,K", [(128, 64, 1, 8), (64, 64, 2, 6), (32, 16, 1, 8), (32, 16, 2, 7), (64, 16, 1, 16)])
 def test_route_groups_smaller_than_top_k(E, n_group, topk_group, K, T):
