@@ -182,26 +182,43 @@ struct Step {
         }
       }
     } else {
+      // one by one, elements that are not there from the nearest that is, without branches between
+      uint32_t m1[kPieces][4], v1[kPieces][4];
 #pragma unroll
       for (int j = 0; j < kPieces; j++) {
-        mc[j] = vc[j] = mb[j] = vb[j] = 0;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-          const int64_t i = at[j] + k;
-          const bool in = (uint64_t)i < (uint64_t)n;
-          gr[j][k] = in ? load_f(g, i) : 0.f;
-          pr[j][k] = in ? load_f(p, i) : 0.f;
+          const int64_t i = min(max(at[j] + k, (int64_t)0), n - 1);
+          gr[j][k] = load_f(g, i);
+          pr[j][k] = load_f(p, i);
           if constexpr (MX) {
-            mc[j] |= in ? (uint32_t)((const uint8_t*)m)[i] << (8 * k) : 0;
-            vc[j] |= in ? (uint32_t)((const uint8_t*)v)[i] << (8 * k) : 0;
+            m1[j][k] = ((const uint8_t*)m)[i];
+            v1[j][k] = ((const uint8_t*)v)[i];
           } else {
-            mr[j][k] = in ? ((const float*)m)[i] : 0.f;
-            vr[j][k] = in ? ((const float*)v)[i] : 0.f;
+            mr[j][k] = ((const float*)m)[i];
+            vr[j][k] = ((const float*)v)[i];
           }
         }
-        if (MX && at[j] < n) {
-          mb[j] = ms[at[j] >> 5];
-          vb[j] = vs[at[j] >> 5];
+        if constexpr (MX) {
+          mb[j] = ms[min(at[j], n - 1) >> 5];
+          vb[j] = vs[min(at[j], n - 1) >> 5];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; j++) {
+        mc[j] = vc[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const bool in = (uint64_t)(at[j] + k) < (uint64_t)n;
+          gr[j][k] = in ? gr[j][k] : 0.f;
+          pr[j][k] = in ? pr[j][k] : 0.f;
+          if constexpr (MX) {
+            mc[j] |= in ? m1[j][k] << (8 * k) : 0u;
+            vc[j] |= in ? v1[j][k] << (8 * k) : 0u;
+          } else {
+            mr[j][k] = in ? mr[j][k] : 0.f;
+            vr[j][k] = in ? vr[j][k] : 0.f;
+          }
         }
       }
     }
