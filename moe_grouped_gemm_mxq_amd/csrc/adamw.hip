@@ -1,5 +1,10 @@
 // AdamW step of many tensors in one launch per kTensors of them, with the
 // states in fp32 or in MXFP8 blocks.
+//
+// One pass, bound by HBM: 940M fp32 weights with MXFP8 states and a bf16 copy take 2.90 ms
+// (5.9 TB/s), 147M bf16 weights with fp32 states 558 us (5.8).  With MXFP8 states and
+// both weights and gradients in bf16 the vector units bind it (200M: 414 us, 4.9 TB/s), and small
+// tensors the chain of reads: 48 of them with 120000 elements take 5.6 us.
 #include <math.h>
 
 #include <type_traits>
@@ -18,7 +23,7 @@ constexpr int kThreads = 256;
 // what is touched at a time close together, but each pays a table of scales (150
 // instructions a thread).  940M fp32 weights with MXFP8 states and a copy / 147M bf16
 // weights with fp32 states / 200M bf16 weights and gradients with MXFP8 states, on
-// one part: 2048 elements in two pieces 2.93 ms / 554 / 422 us, in two passes of
+// one part (before the last steps): 2048 elements in two pieces 2.93 ms / 554 / 422 us, in two passes of
 // one piece 3.03 / 562 / 423, by 512 threads 2.85 / 550 / 487, 4096 in four pieces
 // 3.01 / 554 / 411; runs of 8192 or more lose 5 to 10%.  Ordinary instead of
 // non-temporal stores lose 13% (200M fp32 weights, MXFP8 states: 609 against 689 us).
