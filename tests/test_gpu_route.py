@@ -371,3 +371,20 @@ def test_route_backward_against_differences(score, renormalise):
     got = check_backward(x, idx, dw, score, renormalise)[0]
     total = float(dw.abs().sum())
     assert np.all(np.abs(diff - got) <= total * (h * h + (4 * 10 + 40) * U / h + 1e-5))
+
+
+@pytest.mark.parametrize("T,E,K", [(5, 64, 4), (700, 96, 6)])
+def test_route_into_the_callers_buffers(T, E, K):
+    """The same buffers call after call, with a workspace that the first call puts there or the caller's own."""
+    m = mxq()
+    x = [logits_of(T, E, torch.float32, s) for s in (1, 2)]
+    fresh = [m.route(v, K) for v in x]
+    out = {k: torch.full_like(v, -9) for k, v in fresh[0].items()}
+    own = dict(out, workspace=torch.full((m.mxq_expert_order_workspace(T, K, E),), 255, dtype=torch.uint8, device="cuda"))
+    for buffers in (out, own):
+        for v, want in zip(x, fresh):
+            got = m.route(v, K, out=buffers)
+            assert set(got) == set(want)
+            for k in want:
+                assert got[k] is buffers[k] and torch.equal(got[k], want[k]), k
+        assert buffers["workspace"].numel() >= m.mxq_expert_order_workspace(T, K, E)
