@@ -704,7 +704,8 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         b = fmaxf(fminf(a, a2), fmaxf(b, b2));
         a = fmaxf(a, a2);
       }
-      const float total = p.group_top == 2 && b > -INFINITY ? a + b : a;
+      const bool two = p.group_top == 2 && b > -INFINITY;
+      const float total = two ? a + b : a;
       if (KEYS == kLogits) {  // exact
         int rank = 0;
         for (int q = 0; q < p.n_group; q++) {
@@ -716,29 +717,31 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         // The largest total topk_group times over; groups of one total go together, and
         // too many of them are told apart below.  (16384 x 256 rows in 8 groups 9.6 us, by
         // comparing each group with each 10.0; 1024 experts in 64 groups 33.6 and 45.5.)
-        uint32_t left = g < p.n_group && total > -INFINITY ? ordered(total) : 0u, least = 0;
+        uint32_t left = g < p.n_group && total > -INFINITY ? ordered(total) : 0u;
         kept = false;
         for (int r = 0; r < p.topk_group; r++) {
           const uint32_t m = row_max<LPR>(left);
-          least = m != 0 ? m : least;  // 0: no group is left
-          if (left == m && m != 0) {
+          if (left == m && m != 0) {  // 0: no group is left
             kept = true;
             left = 0;
           }
         }
-        // Of the least total kept and the largest not kept: fp32 totals of distinct
-        // exact values can swap when they differ by at most twice a total's error, that
-        // of two scores (4 half steps of 1 for a sigmoid, 42 for a softmax) and three
-        // roundings.  Then the totals are taken in fp64, from the experts that can be
-        // among their groups' best two.
-        const uint32_t most = row_max<LPR>(left);
-        const float low = unordered(least);
-        const float error = (p.sigmoid ? 0x1p-20f : 0x1.5p-17f) + fabsf(low) * 0x1p-22f;
+        // A total is off by the errors of its two scores (4 half steps of 1 for a sigmoid, 42
+        // for a softmax), and by the roundings of the two keys and their sum: at most two
+        // half steps of |a| + |b|, which is far more than of the total where the keys have
+        // opposite signs.  `error` is twice the former for two totals, `slack` twice the latter
+        // for one, which leaves room for its own roundings.  Where the least total kept, lowered,
+        // does not clear the largest not kept, raised, the totals are taken in fp64, from the
+        // experts that can be among their groups' best two.
+        const float error = p.sigmoid ? 0x1p-20f : 0x1.5p-17f;
+        const float slack = fabsf(a) * 0x1p-22f + (two ? fabsf(b) * 0x1p-22f : 0.f);
+        const uint32_t most = row_max<LPR>(left != 0 ? ordered(total + slack) : 0u);
+        const float least = unordered(~row_max<LPR>(kept ? ~ordered(total - slack) : 0u));
         const bool many = __popcll(__ballot(kept) >> first_lane & ROW) > p.topk_group << sh.lpg_log2;
-        const bool open = many || (most != 0 && low - unordered(most) <= error);
+        const bool open = many || (most != 0 && !(least - unordered(most) > error));
         if (__any(open)) {
           const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
-          const float from = (p.group_top == 2 && b > -INFINITY ? b : a) - error;
+          const float last = two ? b : a, from = last - (error + fabsf(last) * 0x1p-22f);
           uint32_t which = 0;
 #pragma unroll
           for (int j = 0; j < EPL; j++) which |= k[j] > -INFINITY && k[j] >= from ? 1u << j : 0u;
@@ -756,7 +759,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
             db = fmax(fmin(da, a2), fmax(db, b2));
             da = fmax(da, a2);
           }
-          const double dt = p.group_top == 2 && db > -INFINITY ? da + db : da;
+          const double dt = two ? da + db : da;
           int r = 0;
           for (int q = 0; q < p.n_group; q++) {
             const double other = __shfl(dt, first_lane + (q << sh.lpg_log2));

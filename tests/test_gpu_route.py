@@ -388,3 +388,32 @@ def test_route_into_the_callers_buffers(T, E, K):
             for k in want:
                 assert got[k] is buffers[k] and torch.equal(got[k], want[k]), k
         assert buffers["workspace"].numel() >= m.mxq_expert_order_workspace(T, K, E)
+
+
+def group_totals(x, bias, score, n_group, group_top):
+    """fp64 [T][n_group]: sums of each group's best keys (masked experts left out)."""
+    off = x <= ref.LOWEST
+    s = 1 / (1 + np.exp(-x)) if score == "sigmoid" else np.exp(x - np.where(off, -np.inf, x).max(1, keepdims=True))
+    s = np.where(off, 0, s)
+    s = s if score == "sigmoid" else s / s.sum(1, keepdims=True)
+    k = np.sort(np.where(off, -np.inf, s + bias).reshape(len(x), n_group, -1), axis=2)[:, :, -group_top:]
+    return np.where(np.isinf(k), 0, k).sum(2)
+
+
+@pytest.mark.parametrize("magnitude", [16.0, 128.0, 1e3, 1e4])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,K,masked", [(64, 32, 7, 8, 0), (128, 64, 20, 6, 0), (16, 8, 3, 4, 0), (64, 8, 3, 4, 6),
+                                                          (256, 16, 5, 8, 14)])
+def test_route_groups_with_biases_of_both_signs(E, n_group, topk_group, K, masked, score, magnitude):
+    """A group's best two keys are +magnitude and -magnitude: its total is small, but the keys are rounded at the
+    magnitude.  Logits are drawn so close that the totals differ by about those roundings, and stay apart in 64 bits."""
+    g = torch.Generator().manual_seed(E + int(magnitude))
+    T, per = 200, E // n_group
+    x = magnitude * 2.0 ** -20 * torch.randn(T, E, generator=g)
+    bias = torch.where(torch.arange(per) % 2 == 0, magnitude, -magnitude).repeat(n_group)
+    if masked:  # all but the last two of a group
+        x.view(T, n_group, per)[:, :, :masked] = -float("inf")
+    total = np.sort(group_totals(f64(x), f64(bias), score, n_group, 2), axis=1)[:, ::-1]
+    gap = total[:, topk_group - 1] - total[:, topk_group]
+    assert gap.min() > 16 * magnitude * 2.0 ** -53 and np.median(gap) < magnitude * 2.0 ** -22
+    check_route(x.cuda(), K, bias.cuda(), score=score, n_group=n_group, topk_group=topk_group, group_top=2, renormalise=True, scale=1.0)
