@@ -379,7 +379,9 @@ typedef enum {
  *  - n_group > 1 splits the experts into n_group equal runs; a group's total
  *    is the sum of its best `group_top` (1 or 2) s + bias (s without bias)
  *    over unmasked experts; only the topk_group best groups' experts can be
- *    chosen.  E must be a multiple of n_group.
+ *    chosen.  E must be a multiple of n_group.  (Totals are of scores also where
+ *    experts rank by logits: groups whose scores are one number in 64 bits, as
+ *    sigmoids of 40 and 45 are, tie.)
  *  - The top_k largest keys are chosen, largest first; ties go to the lowest
  *    index (experts and groups).  Order is that of the keys and totals in
  *    64-bit arithmetic.  A row with fewer available experts than top_k ends

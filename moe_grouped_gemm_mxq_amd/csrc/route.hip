@@ -672,8 +672,7 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
 #pragma unroll
       for (int j = 0; j < EPL; j++) x[j] = x[j] <= (float)kMasked ? -INFINITY : x[j];
 
-    // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias; without
-    // a bias a softmax's up to its sum, which orders them as well)
+    // fp64 pieces for what fp32 leaves open: the sum of a softmax, a score (+ bias)
     auto exp_sum = [&] {
       double s = 0.0;
 #pragma unroll 1
@@ -706,13 +705,22 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
       }
       const bool two = p.group_top == 2 && b > -INFINITY;
       const float total = two ? a + b : a;
-      if (KEYS == kLogits) {  // exact
+      if (KEYS == kLogits) {
+        // A group's total is the score of its largest logit and grows with that, so logits order
+        // the groups; but where the scores of the least kept and the largest not kept may be
+        // one number in 64 bits, the lower group goes first, and the row is taken to fp64:
+        // scores that underflow, and those apart by 2^-47 of the score or less (the
+        // logits' difference times 1 - s for a sigmoid, at least min(exp(-l), 1) / 2).
         int rank = 0;
         for (int q = 0; q < p.n_group; q++) {
           const float other = __shfl(total, first_lane + (q << sh.lpg_log2));
           rank += other > total || (other == total && q < g);
         }
         kept = g < p.n_group && rank < p.topk_group && total > -INFINITY;
+        const uint32_t most = row_max<LPR>(!kept && g < p.n_group && total > -INFINITY ? ordered(total) : 0u);
+        const float least = unordered(~row_max<LPR>(kept ? ~ordered(total) : 0u));
+        const float apart = least - unordered(most), low = p.sigmoid ? least : least - row_fmax<LPR>(total);
+        odd |= most != 0 && apart != 0.f && (!(apart * (p.sigmoid ? fminf(exp_f(-least), 1.f) : 1.f) > 0x1p-46f) || low < -600.f);
       } else {
         // The largest total topk_group times over; groups of one total go together, and
         // too many of them are told apart below.  (16384 x 256 rows in 8 groups 9.6 us, by
@@ -740,7 +748,9 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         const bool many = __popcll(__ballot(kept) >> first_lane & ROW) > p.topk_group << sh.lpg_log2;
         const bool open = many || (most != 0 && !(least - unordered(most) > error));
         if (__any(open)) {
-          const double dsum = KEYS == kBiased && !p.sigmoid ? exp_sum() : 1.0;
+          // without a bias the sum divides all totals of the row, which matters where they underflow
+          const bool divide = !p.sigmoid && (KEYS == kBiased || __any(open && least < 0x1p-100f));
+          const double dsum = divide ? exp_sum() : 1.0;
           const float last = two ? b : a, from = last - (error + fabsf(last) * 0x1p-22f);
           uint32_t which = 0;
 #pragma unroll

@@ -417,3 +417,40 @@ def test_route_groups_with_biases_of_both_signs(E, n_group, topk_group, K, maske
     gap = total[:, topk_group - 1] - total[:, topk_group]
     assert gap.min() > 16 * magnitude * 2.0 ** -53 and np.median(gap) < magnitude * 2.0 ** -22
     check_route(x.cuda(), K, bias.cuda(), score=score, n_group=n_group, topk_group=topk_group, group_top=2, renormalise=True, scale=1.0)
+
+
+@pytest.mark.parametrize("T,E,n_group", [(6, 8, 2), (6, 64, 8), (6, 96, 3), (6, 256, 8), (4100, 64, 8)])
+def test_route_groups_go_by_scores_where_logits_differ(T, E, n_group):
+    """Without a bias, logits whose scores are one number in 64 bits: a sigmoid of 1, a softmax that underflows.  Groups of
+    one total go by their index, the experts of the kept ones by their logits."""
+    per = E // n_group
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn(T, E, generator=g)
+    x[1::2, 0], x[1::2, per] = 40.0, 45.0  # scores 1 and 1: the first group
+    x[0, 0], x[0, per] = 30.0, 45.0        # apart in 64 bits
+    x[2, 2], x[2, per] = 1e-3, 1e-3 + 2.0 ** -30
+    for dtype in (torch.float32, torch.bfloat16) if T < 100 else (torch.float32,):
+        for top in (1, 2):
+            check_route(x.to(dtype).cuda(), 2, score="sigmoid", n_group=n_group, topk_group=1, group_top=top)
+            check_route(x.to(dtype).cuda(), 5, score="sigmoid", n_group=n_group, topk_group=n_group - 1, group_top=top)
+    x[1::2] *= 0.125
+    x[1::2, :per] -= 900.0            # score 0
+    x[1::2, per:2 * per] -= 800.0     # score 0
+    x[3, :per] += 300.0               # not 0 in 64 bits, 0 in 32
+    x[5, 1] = float("nan")
+    for topk_group in (1, n_group - 1):
+        for top in (1, 2):
+            check_route(x.cuda(), 2, score="softmax", n_group=n_group, topk_group=topk_group, group_top=top, renormalise=True)
+    for far in (5.0, 40.0, 400.0):  # scores from ordinary ones to those of 0 and 1
+        for score in ("softmax", "sigmoid"):
+            check_route((far * torch.randn(T, E, generator=g)).cuda(), 4, score=score, n_group=n_group, topk_group=n_group - 1, renormalise=True)
+    close = 1.0 + 2.0 ** -23 * torch.randint(0, 3, (T, E), generator=g) * torch.tensor([1.0, 2.0 ** -10, 2.0 ** -20, 0.0]).repeat(E // 4)
+    for score in ("softmax", "sigmoid"):
+        check_route(close.cuda(), 4, score=score, n_group=n_group, topk_group=n_group - 1)
+        check_route((close - 1.0).cuda(), 4, score=score, n_group=n_group, topk_group=n_group - 1)
+    if n_group > 2:  # exp(-744.9) is the least number of 64 bits, and 0 after the division by the sum
+        x = torch.full((T, E), -900.0)
+        x[:, 0], x[:, per], x[:, 2 * per:3 * per] = -746.5, -744.9, 0.0
+        for top in (1, 2):
+            check_route(x.cuda(), 3, score="softmax", n_group=n_group, topk_group=2, group_top=top)
+            check_route(x.cuda(), min(per + 2, 32), score="softmax", n_group=n_group, topk_group=2, group_top=top)
