@@ -6,6 +6,7 @@
 // evaluated.  The fast kernel chooses in fp32, knows how far its keys can be
 // off, and takes what that leaves open to fp64: the order of the candidates
 // alone where that decides, the whole row (route_row64) where it does not.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -704,7 +705,8 @@ __global__ __launch_bounds__(1024) void route_fast_kernel(const LT* __restrict__
         a = fmaxf(a, a2);
       }
       const bool two = p.group_top == 2 && b > -INFINITY;
-      const float total = two ? a + b : a;
+      // finite keys: a sum past fp32 is still a group's total, not a masked group's -inf
+      const float total = two ? fmaxf(a + b, -FLT_MAX) : a;
       if (KEYS == kLogits) {
         // A group's total is the score of its largest logit and grows with that, so logits order
         // the groups; but where the scores of the least kept and the largest not kept may be

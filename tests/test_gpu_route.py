@@ -454,3 +454,14 @@ def test_route_groups_go_by_scores_where_logits_differ(T, E, n_group):
         for top in (1, 2):
             check_route(x.cuda(), 3, score="softmax", n_group=n_group, topk_group=2, group_top=top)
             check_route(x.cuda(), min(per + 2, 32), score="softmax", n_group=n_group, topk_group=2, group_top=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_of_keys_that_overflow_when_added(score):
+    """Best two keys of 3e38 of one sign: their total is past fp32, and finite in 64 bits."""
+    x = logits_of(50, 16, torch.float32, 21)
+    bias = torch.tensor([-3e38, -3e38, 0, 0, 3e38, 3e38, -3.4e38, -3e38, 3e38, 2.5e38, -3e38, 1, 0, 0, -3e38, -3e38])
+    for topk_group in range(1, 9):
+        for top in (1, 2):
+            for b in (bias, -bias):
+                check_route(x, 16, b.cuda(), score=score, n_group=8, topk_group=topk_group, group_top=top)
