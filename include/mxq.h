@@ -479,7 +479,7 @@ typedef struct {
 } mxq_adamw_tensor;
 
 typedef struct {
-    double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps > 0 */
+    double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps >= 2^-126 (normal in fp32) */
     double grad_scale;                          /* multiplies every gradient */
     int64_t step;                               /* of this update, 1 for the first */
     uint32_t seed;                              /* of the stochastic rounding */

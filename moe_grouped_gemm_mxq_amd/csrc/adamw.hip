@@ -5,6 +5,7 @@
 // (5.9 TB/s), 147M bf16 weights with fp32 states 558 us (5.8).  With MXFP8 states and
 // both weights and gradients in bf16 the vector units bind it (200M: 414 us, 4.9 TB/s), and small
 // tensors the chain of reads: 48 of them with 120000 elements take 5.6 us.
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -402,7 +403,8 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
   MXQ_REQUIRE(grad_dt == MXQ_DT_F32 || grad_dt == MXQ_DT_BF16, "mxq_adamw: unknown gradient type %d", (int)grad_dt);
   MXQ_REQUIRE(format == MXQ_ADAMW_F32 || format == MXQ_ADAMW_MXFP8, "mxq_adamw: unknown state format %d", (int)format);
   MXQ_REQUIRE(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1, "mxq_adamw: betas must be in [0, 1)");
-  MXQ_REQUIRE(cfg->eps > 0 && isfinite(cfg->eps), "mxq_adamw: eps must be positive");
+  // in fp32: an eps that is 0 or subnormal there makes 0 / (0 + eps) a NaN
+  MXQ_REQUIRE((float)cfg->eps >= FLT_MIN && isfinite(cfg->eps), "mxq_adamw: eps must be finite and at least 2^-126");
   MXQ_REQUIRE(isfinite(cfg->lr) && isfinite(cfg->weight_decay), "mxq_adamw: lr and weight_decay must be finite");
   MXQ_REQUIRE(control != nullptr || cfg->step >= 1, "mxq_adamw: step must be >= 1");
   MXQ_REQUIRE(aligned_to(control, 16), "mxq_adamw: control must be 16-byte aligned");

@@ -278,3 +278,14 @@ def test_places_in_flat_buffers_do_not_matter(bits):
             assert all(torch.equal(x, y) for x, y in zip(one, other)), shifts
         for buf, free, guard in beside:
             assert torch.all(buf[free] == guard), shifts
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_least_eps_leaves_untouched_elements(bits):
+    """Elements without gradient or state stay where they are under the smallest eps that is accepted."""
+    lib = mxq()
+    fmt = lib.MXQ_ADAMW_F32 if bits == 32 else lib.MXQ_ADAMW_MXFP8
+    p = torch.linspace(-1, 1, 300, device="cuda")
+    want, m, v = p.clone(), lib.adamw_state(p, fmt), lib.adamw_state(p, fmt)
+    lib.AdamW([p], [torch.zeros_like(p)], [m], [v]).step(lr=0.1, eps=2.0 ** -126, weight_decay=0.0)
+    assert torch.equal(p, want)

@@ -190,3 +190,10 @@ def test_struct_sizes_match_the_header(tmp_path):
     got = re.findall(r"mxq_\w+ (\d+) (\d+)", subprocess.run([exe], capture_output=True, text=True, check=True).stdout)
     want = [(str(ctypes.sizeof(c)), str(getattr(c, f[0]).offset)) for _, c in pairs for f in c._fields_]
     assert got == want
+
+
+@pytest.mark.parametrize("eps", [1e-300, 1e-46, 2.0 ** -149, 1e-39, 2.0 ** -127, -1e-8, float("inf")])
+def test_adamw_eps_has_to_be_normal_in_fp32(eps):
+    """An eps that fp32 has as 0 or as a subnormal would turn elements without gradient or state into NaN."""
+    assert adamw(config=dict(eps=eps)) == INVALID and "eps" in last()
+    assert adamw(config=dict(eps=2.0 ** -126), tensor=dict(param=None)) == INVALID and "NULL" in last()  # accepted: the next check ends it
