@@ -487,7 +487,8 @@ typedef struct {
 
 /* What changes from step to step, in device memory (16 bytes, 16-byte aligned), so that a
  * captured step can be replayed with new values: where given to mxq_adamw, it
- * replaces the config's lr, grad_scale, step and seed. */
+ * replaces the config's lr, grad_scale, step and seed.  An lr or a grad_scale
+ * that is not finite, or a step below 1, skips the step: nothing changes. */
 typedef struct {
     float lr;
     float grad_scale;

@@ -347,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
   Hyper h = a.h;
   if (a.control) {
     const mxq_adamw_control c = *a.control;
-    if (c.step < 1) return;
+    if (c.step < 1 || !isfinite(c.lr)) return;  // as the host refuses them in the config
     h.lr = c.lr;
     h.grad_scale = c.grad_scale;
     h.key = c.seed + 0x9E3779B9u * (uint32_t)c.step;

@@ -289,3 +289,15 @@ def test_the_least_eps_leaves_untouched_elements(bits):
     want, m, v = p.clone(), lib.adamw_state(p, fmt), lib.adamw_state(p, fmt)
     lib.AdamW([p], [torch.zeros_like(p)], [m], [v]).step(lr=0.1, eps=2.0 ** -126, weight_decay=0.0)
     assert torch.equal(p, want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr", [float("nan"), float("inf")])
+def test_a_control_rate_that_is_not_finite_skips_the_step(bits, lr):
+    """As the config's own rate is refused."""
+    lib = mxq()
+    p, g, m, v = tensors([500, 3], torch.float32, torch.float32, bits, 8)
+    flat = lambda: [x.clone() for s in (p, m, v) for t in s for x in (t if isinstance(t, tuple) else (t,))]  # noqa: E731
+    before = flat()
+    lib.AdamW(p, g, m, v).step(**HYPER, control=lib.adamw_control(lr, 7, 1, 1.0))
+    assert all(torch.equal(a, b) for a, b in zip(before, flat()))
