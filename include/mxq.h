@@ -500,7 +500,9 @@ typedef struct {
  * returns), all of one parameter, gradient and state type:
  *   g' = grad_scale g;  m' = beta1 m + (1 - beta1) g';  v' = beta2 v + (1 - beta2) g'^2
  *   p' = p (1 - lr wd) - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
- * in fp32, the products and sums in this order without contraction; p'
+ * in fp32.  The products and sums of the moments are rounded one by one in this
+ * order, without contraction; those of p' may be contracted and its quotient is
+ * m' times a reciprocal (the update is within 2^-20 of itself).  p' is
  * rounded to nearest for bf16.  A grad_scale that is not finite (a gradient
  * norm or loss scale that overflowed) skips the step: nothing changes.
  * MXFP8 states hold m and r = sqrt(v); the block's scale is the smallest
@@ -509,7 +511,9 @@ typedef struct {
  * stochastically, y -> step * floor(y / step + u) with u in (0, 1) from a
  * counter hash of (seed, step, index of the tensor in the call, element), so
  * that moments whose change in one step is below half an E4M3 step still
- * move; a positive r stays positive; a moment that is not finite becomes NaN.  Zero codes
+ * move.  y is the element times 2^(127-byte), off by at most 2^-18 of a step
+ * (u comes in steps of 2^-16, and a y that E4M3 holds stays what it is).  A positive
+ * r stays positive; a moment that is not finite becomes NaN.  Zero codes
  * and scales are the state before the first step. */
 mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dtype param_dt, mxq_dtype grad_dt,
                      mxq_adamw_format format, const mxq_adamw_config* cfg, const mxq_adamw_control* control,

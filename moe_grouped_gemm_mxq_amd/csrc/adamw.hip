@@ -355,10 +355,15 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args a) {
     h.alpha = (float)(h.lr / (1.0 - exp2(c.step * a.log2_b1)));
   }
   if (!isfinite(h.grad_scale)) return;
-  // 2^(127 - byte) by powf, which on this GPU is off by one step for some
+  // 2^(127 - byte) by powf, which on this GPU is off by one step of fp32 for some
   // exponents.  torch.ldexp and torch.pow take it the same way, so the states are
-  // bit for bit those of these formulas in torch operations; one step of the scaled
-  // value changes a probability of rounding up by at most 2^-20.
+  // bit for bit those of these formulas in torch operations.  A scaled value is then off by at
+  // most three steps of fp32 (this one, doubled where the value's mantissa is near 2, and the
+  // product's), 3 * 2^-20 of an E4M3 step: it rounds the other way where u lies
+  // within that of the border, for some of the exponents 1 element in 10^6, and a value that
+  // E4M3 holds stays (u is 2^-17 or more from 0 and 1).  The exact power is a shift of
+  // the exponent and needs no table: 200M bf16 weights and gradients 391 against 434 us, but
+  // other bits in the states.
   if constexpr (MX) {
     static_assert(kThreads == 256, "one entry per thread");
     inverse[threadIdx.x] = powf(2.0f, 127.0f - (float)threadIdx.x);

@@ -301,3 +301,39 @@ def test_a_control_rate_that_is_not_finite_skips_the_step(bits, lr):
     before = flat()
     lib.AdamW(p, g, m, v).step(**HYPER, control=lib.adamw_control(lr, 7, 1, 1.0))
     assert all(torch.equal(a, b) for a, b in zip(before, flat()))
+
+
+def near_the_border(u, e, rng):
+    """E4M3 values + (1 - u +- 2^-18) of their step, times 2^e, each an fp32 number from 2^-6 to below 448 before the 2^e:
+    rounded up with the plus and down with the minus."""
+    k = rng.integers(8, 126, len(u))  # normal codes with a successor
+    up = rng.integers(0, 2, len(u)).astype(bool)
+    y = ref.E4M3[k] + (1 - u + np.where(up, 2.0 ** -18, -(2.0 ** -18))) * (ref.E4M3[k + 1] - ref.E4M3[k])
+    x = y * 2.0 ** e
+    assert np.array_equal(x.astype(np.float32).astype(np.float64), x)
+    return x, np.where(up, k + 1, k)
+
+
+@pytest.mark.parametrize("values", ["near the border", "of E4M3"])
+@pytest.mark.parametrize("moment", ["m", "r"])
+def test_rounding_is_decided_within_2_to_the_minus_18_of_a_step(moment, values):
+    """Under every scale; values that E4M3 holds keep their codes.  With betas of 0, m' is the gradient and r its
+    magnitude, both exactly."""
+    lib = mxq()
+    rng = np.random.default_rng(5)
+    lo, hi = (-110, 110) if moment == "m" else (-50, 55)  # squares stay normal
+    exps = np.repeat(np.arange(lo, hi), 32)
+    n = 32 * len(exps)
+    um, ur = ref.uniforms(77, 3, 0, n)
+    if values == "of E4M3":
+        code = rng.integers(1, 127, n)
+        x = ref.E4M3[code] * 2.0 ** exps.repeat(32)
+    else:
+        x, code = near_the_border(um if moment == "m" else ur, exps.repeat(32).astype(np.float64), rng)
+    x[::32], code[::32] = 448.0 * 2.0 ** exps, 126  # fixes the block's scale
+    p, g = torch.zeros(n, device="cuda"), torch.from_numpy(x.astype(np.float32)).cuda()
+    m, v = lib.adamw_state(p), lib.adamw_state(p)
+    lib.AdamW([p], [g], [m], [v]).step(lr=0.0, betas=(0.0, 0.0), weight_decay=0.0, step=3, seed=77)
+    codes, scales = m if moment == "m" else v
+    assert np.array_equal(host(scales), (exps + 127).astype(np.uint8))
+    assert np.array_equal(host(codes), code.astype(np.uint8))
