@@ -708,23 +708,29 @@ def grouped_gemm(mode, A, sA, B, sB, group_end, stream=None, fmt=MXQ_FMT_E4M3):
     return C
 
 
-def _on(stream):
-    """Context in which temporaries belong to the stream that the call runs on."""
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+def _on(stream, device):
+    """Context in which `stream` is the current one, so that what is allocated belongs to it.  A helper that is given a
+    stream runs as a call within it: outputs of another stream's memory could still be in use there, or be handed
+    out again there before the call has ended."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    return torch.cuda.stream(stream)
 
 
-def _workspace(T, top_k, E, device, stream):
-    if stream is None:
-        return torch.empty(mxq_expert_order_workspace(T, top_k, E), dtype=torch.uint8, device=device)
-    with _on(stream):
-        return torch.empty(mxq_expert_order_workspace(T, top_k, E), dtype=torch.uint8, device=device)
+def _workspace(T, top_k, E, device):
+    return torch.empty(mxq_expert_order_workspace(T, top_k, E), dtype=torch.uint8, device=device)
 
 
 def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0,
           order=True, out=None, stream=None):
     """Route tokens: {"idx", "weights"} and, with order, {"group_end", "row_token", "slot"} (the expert order the grouped
     entry points and combine take).  out: a dict of such buffers to write to; with order, it may have the "workspace" too,
-    which is put there for the calls after where it is missing."""
+    which is put there for the calls after where it is missing.  stream: as a call within torch.cuda.stream(stream), whose
+    memory the outputs then are; so for the helpers below."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return route(logits, top_k, score=score, bias=bias, n_group=n_group, topk_group=topk_group, group_top=group_top,
+                         renormalise=renormalise, scale=scale, order=order, out=out)
     cfg = _kept_config(top_k, score, n_group, topk_group, group_top, renormalise, scale)
     T, E = logits.shape
     if out is None:
@@ -734,52 +740,64 @@ def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1,
             out.update(group_end=i32((E,)), row_token=i32((T * top_k,)), slot=i32((T, top_k)))
     idx, weights = out["idx"], out["weights"]
     if not order:
-        mxq_route(logits, cfg, idx, weights, bias, stream=stream)
+        mxq_route(logits, cfg, idx, weights, bias)
         return {"idx": idx, "weights": weights}
     group_end, row_token, slot, ws = out["group_end"], out["row_token"], out["slot"], out.get("workspace")
     if ws is None:
-        ws = out["workspace"] = _workspace(T, top_k, E, logits.device, stream)
-    mxq_route(logits, cfg, idx, weights, bias, group_end, row_token, slot, ws, stream)
+        ws = out["workspace"] = _workspace(T, top_k, E, logits.device)
+    mxq_route(logits, cfg, idx, weights, bias, group_end, row_token, slot, ws)
     return {"idx": idx, "weights": weights, "group_end": group_end, "row_token": row_token, "slot": slot}
 
 
 def expert_order(idx, E, stream=None):
     """Expert order of chosen experts idx int32 [T][top_k]: {"group_end", "row_token", "slot"}."""
+    if stream is not None:
+        with _on(stream, idx.device):
+            return expert_order(idx, E)
     T, K = idx.shape
     i32 = functools.partial(torch.empty, dtype=torch.int32, device=idx.device)
     out = {"group_end": i32((E,)), "row_token": i32((T * K,)), "slot": i32((T, K))}
-    mxq_expert_order(idx, E, out["group_end"], out["row_token"], out["slot"], _workspace(T, K, E, idx.device, stream), stream)
+    mxq_expert_order(idx, E, out["group_end"], out["row_token"], out["slot"], _workspace(T, K, E, idx.device))
     return out
 
 
 def route_backward(logits, idx, dweights, *, score="softmax", renormalise=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return route_backward(logits, idx, dweights, score=score, renormalise=renormalise, scale=scale)
     cfg = _kept_config(idx.shape[1], score, 1, 1, 1, renormalise, scale)
     dt, T, E, ld = _matrix(logits, "logits")
     dlogits = logits.new_empty((T, E))
-    _route_backward(logits, dt, T, E, ld, cfg, idx, dweights, dlogits, E, stream)
+    _route_backward(logits, dt, T, E, ld, cfg, idx, dweights, dlogits, E, None)
     return dlogits
 
 
 def combine(y, slot, weights=None, dtype=torch.bfloat16, stream=None):
     """The experts' rows y [rows][H] back in token order: [T][H] of `dtype`."""
+    if stream is not None:
+        with _on(stream, y.device):
+            return combine(y, slot, weights, dtype)
     ydt, rows, H, ldy = _matrix(y, "y")
     T, K = _need_pairs(slot, weights)
     odt = _type_code(dtype)
     out = y.new_empty((T, H), dtype=dtype)
-    _combine(y, ydt, rows, ldy, slot, weights, T, K, H, out, odt, H, stream)
+    _combine(y, ydt, rows, ldy, slot, weights, T, K, H, out, odt, H, None)
     return out
 
 
 def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=None):
     """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights."""
+    if stream is not None:
+        with _on(stream, dout.device):
+            return combine_backward(dout, slot, rows, weights, y, dtype)
     if weights is None:
         y = None
     dt, T, K, H, ldd, ydt, ldy = _need_gradient(dout, slot, rows, weights, y)
     gdt = dt if dtype is None else _type_code(dtype)
     dy = dout.new_empty((rows, H), dtype=dtype)
     dw = None if y is None else torch.empty_like(weights)
-    _combine_backward(dout, dt, ldd, y, ydt, ldy, slot, weights, T, K, H, rows, dy, gdt, H, dw, stream)
+    _combine_backward(dout, dt, ldd, y, ydt, ldy, slot, weights, T, K, H, rows, dy, gdt, H, dw, None)
     return dy, dw
 
 
