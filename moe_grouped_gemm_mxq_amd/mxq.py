@@ -7,7 +7,8 @@ is no fallback.
 
 Functions named like the C entry points take every buffer from the caller;
 the lower-case helpers (``quantize``, ``gemm`` ...) allocate the outputs with
-``torch.empty`` and call them.
+``torch.empty`` and call them.  A helper given a stream does both as a call within
+``torch.cuda.stream(stream)`` would.
 
 GEMM operand scale arrays are uint8 tensors of shape ``scale_shape(rows,
 nblk)`` = ``(ceil128(rows) // 128, nblk, 32, 4)``: element
@@ -592,12 +593,24 @@ def mxq_adamw(tensors, n_tensors, param_dt, grad_dt, fmt, cfg, control=None, str
 
 
 # ------------------------------------------------------------------ allocate-and-call helpers
+def _on(stream, device):
+    """Context in which `stream` is the current one, so that what is allocated belongs to it.  A helper that is given a
+    stream runs as a call within it: outputs of another stream's memory could still be in use there, or be handed
+    out again there before the call has ended."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    return torch.cuda.stream(stream)
+
+
 def _u8(shape, device):
     return torch.empty(shape, dtype=torch.uint8, device=device)
 
 
 def quantize(x, axis_mask=MXQ_AXIS_ROW | MXQ_AXIS_COLT, stream=None):
     """Returns a dict with 'q_row', 's_row' and/or 'q_colT', 's_colT'."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize(x, axis_mask)
     R, C = x.shape
     out = {}
     if axis_mask & MXQ_AXIS_ROW:
@@ -607,12 +620,15 @@ def quantize(x, axis_mask=MXQ_AXIS_ROW | MXQ_AXIS_COLT, stream=None):
         out["q_colT"] = _u8((C, ceil32(R)), x.device)
         out["s_colT"] = _u8(scale_shape(C, ceil32(R) // BLOCK), x.device)
     mxq_quantize(x, axis_mask, out.get("q_row"), out.get("s_row"), out.get("q_colT"),
-                 out.get("s_colT"), stream)
+                 out.get("s_colT"))
     return out
 
 
 def quantize_batched(x, axis_mask=MXQ_AXIS_ROW | MXQ_AXIS_COLT, stream=None):
     """x bf16 [batch][R][C] -> dict of batched outputs (see mxq_quantize_batched)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize_batched(x, axis_mask)
     nb, R, C = x.shape
     out = {}
     if axis_mask & MXQ_AXIS_ROW:
@@ -621,12 +637,14 @@ def quantize_batched(x, axis_mask=MXQ_AXIS_ROW | MXQ_AXIS_COLT, stream=None):
     if axis_mask & MXQ_AXIS_COLT:
         out["q_colT"] = _u8((nb, C, ceil32(R)), x.device)
         out["s_colT"] = _u8((nb,) + scale_shape(C, ceil32(R) // BLOCK), x.device)
-    mxq_quantize_batched(x, axis_mask, out.get("q_row"), out.get("s_row"), out.get("q_colT"), out.get("s_colT"),
-                         stream)
+    mxq_quantize_batched(x, axis_mask, out.get("q_row"), out.get("s_row"), out.get("q_colT"), out.get("s_colT"))
     return out
 
 
 def quantize_grouped(x, group_end, axis_mask=MXQ_AXIS_COLT, ldq=None, stream=None):
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize_grouped(x, group_end, axis_mask, ldq)
     T, C = x.shape
     if ldq is None:
         ldq = mxq_grouped_cols_max(T, group_end.numel())
@@ -638,11 +656,14 @@ def quantize_grouped(x, group_end, axis_mask=MXQ_AXIS_COLT, ldq=None, stream=Non
         out["q_colT"] = _u8((C, ldq), x.device)
         out["s_colT"] = _u8(scale_shape(C, ldq // BLOCK), x.device)
     mxq_quantize_grouped(x, group_end, ldq, axis_mask, out.get("q_row"), out.get("s_row"),
-                         out.get("q_colT"), out.get("s_colT"), stream)
+                         out.get("q_colT"), out.get("s_colT"))
     return out
 
 
 def qdq_fp4(x, want_codes=False, stream=None):
+    if stream is not None:
+        with _on(stream, x.device):
+            return qdq_fp4(x, want_codes)
     y = torch.empty_like(x)
     codes = scales = None
     if want_codes:
@@ -650,32 +671,41 @@ def qdq_fp4(x, want_codes=False, stream=None):
         rows = x.numel() // L
         codes = _u8((rows, ceil32(L) // 2), x.device)
         scales = _u8((rows, ceil32(L) // BLOCK), x.device)
-    mxq_qdq_fp4(x, y, codes, scales, stream)
+    mxq_qdq_fp4(x, y, codes, scales)
     return (y, codes, scales) if want_codes else y
 
 
 def quantize_fp4(x, scale_factor=6.0, stream=None):
     """MXFP4 GEMM operand of a 2-D fp32 tensor: (codes, scales in the operand layout)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize_fp4(x, scale_factor)
     rows, L = x.shape
     codes = _u8((rows, ceil32(L) // 2), x.device)
     scales = _u8(scale_shape(rows, ceil32(L) // BLOCK), x.device)
-    mxq_quantize_fp4(x, codes, scales, scale_factor, stream)
+    mxq_quantize_fp4(x, codes, scales, scale_factor)
     return codes, scales
 
 
 def quantize_fp4_grouped(x, group_end, ldq=None, scale_factor=6.0, stream=None):
     """Grouped token-axis MXFP4 operand of x fp32 [T][C]: {"ldq", "codes", "scales"}."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize_fp4_grouped(x, group_end, ldq, scale_factor)
     T, C = x.shape
     if ldq is None:
         ldq = mxq_grouped_cols_max(T, group_end.numel())
     out = {"ldq": ldq, "codes": _u8((C, ldq // 2), x.device), "scales": _u8(scale_shape(C, ldq // BLOCK), x.device)}
-    mxq_quantize_fp4_grouped(x, group_end, ldq, out["codes"], out["scales"], scale_factor, stream)
+    mxq_quantize_fp4_grouped(x, group_end, ldq, out["codes"], out["scales"], scale_factor)
     return out
 
 
 def qdq_fp4_ste(x, scale_factor=6.0, want_codes=False, stream=None):
     """Forward of the clipped-STE fake quantiser: returns (y, sat_mask) or,
     with want_codes, (y, sat_mask, codes, scales)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return qdq_fp4_ste(x, scale_factor, want_codes)
     rows, L = _rows_L(x)
     y = torch.empty_like(x)
     mask = _u8((rows, ceil32(L) // 8), x.device)
@@ -683,38 +713,38 @@ def qdq_fp4_ste(x, scale_factor=6.0, want_codes=False, stream=None):
     if want_codes:
         codes = _u8((rows, ceil32(L) // 2), x.device)
         scales = _u8((rows, ceil32(L) // BLOCK), x.device)
-    mxq_qdq_fp4_ex(x, y, scale_factor, codes, scales, mask, stream)
+    mxq_qdq_fp4_ex(x, y, scale_factor, codes, scales, mask)
     return (y, mask, codes, scales) if want_codes else (y, mask)
 
 
 def ste_backward_fp4(grad_y, sat_mask, stream=None):
+    if stream is not None:
+        with _on(stream, grad_y.device):
+            return ste_backward_fp4(grad_y, sat_mask)
     grad_x = torch.empty_like(grad_y)
-    mxq_ste_backward_fp4(grad_y, sat_mask, grad_x, stream)
+    mxq_ste_backward_fp4(grad_y, sat_mask, grad_x)
     return grad_x
 
 
 def gemm(A, sA, B, sB, stream=None, fmt=MXQ_FMT_E4M3):
+    if stream is not None:
+        with _on(stream, A.device):
+            return gemm(A, sA, B, sB, fmt=fmt)
     C = torch.empty((A.shape[0], B.shape[0]), dtype=torch.float32, device=A.device)
-    mxq_gemm(A, sA, B, sB, C, stream, fmt)
+    mxq_gemm(A, sA, B, sB, C, fmt=fmt)
     return C
 
 
 def grouped_gemm(mode, A, sA, B, sB, group_end, stream=None, fmt=MXQ_FMT_E4M3):
+    if stream is not None:
+        with _on(stream, A.device):
+            return grouped_gemm(mode, A, sA, B, sB, group_end, fmt=fmt)
     if mode == MXQ_GG_RAGGED_M:
         C = torch.empty((A.shape[0], B.shape[1]), dtype=torch.float32, device=A.device)
     else:
         C = torch.empty((group_end.numel(), A.shape[0], B.shape[0]), dtype=torch.float32, device=A.device)
-    mxq_grouped_gemm(mode, A, sA, B, sB, C, group_end, stream, fmt)
+    mxq_grouped_gemm(mode, A, sA, B, sB, C, group_end, fmt=fmt)
     return C
-
-
-def _on(stream, device):
-    """Context in which `stream` is the current one, so that what is allocated belongs to it.  A helper that is given a
-    stream runs as a call within it: outputs of another stream's memory could still be in use there, or be handed
-    out again there before the call has ended."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
-    return torch.cuda.stream(stream)
 
 
 def _workspace(T, top_k, E, device):
@@ -726,7 +756,7 @@ def route(logits, top_k, *, score="softmax", bias=None, n_group=1, topk_group=1,
     """Route tokens: {"idx", "weights"} and, with order, {"group_end", "row_token", "slot"} (the expert order the grouped
     entry points and combine take).  out: a dict of such buffers to write to; with order, it may have the "workspace" too,
     which is put there for the calls after where it is missing.  stream: as a call within torch.cuda.stream(stream), whose
-    memory the outputs then are; so for the helpers below."""
+    memory the outputs then are."""
     if stream is not None:
         with _on(stream, logits.device):
             return route(logits, top_k, score=score, bias=bias, n_group=n_group, topk_group=topk_group, group_top=group_top,

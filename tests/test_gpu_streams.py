@@ -49,3 +49,31 @@ def test_routing_and_combine():
     check(lambda st: m.combine(y, r["slot"], r["weights"], stream=st))
     check(lambda st: m.combine_backward(x, r["slot"], T * K, r["weights"], y, stream=st))
     check(lambda st: m.dispatch(x, r["slot"], T * K, stream=st))
+
+
+def test_quantisers_and_gemms():
+    m = mxq()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x32 = torch.randn(256, 256, generator=g, device="cuda")
+    x = x32.to(torch.bfloat16)
+    ends = torch.tensor([100, 256], dtype=torch.int32, device="cuda")
+    q, w, k = m.quantize(x), m.quantize_batched(x.view(2, 128, 256)), m.quantize_grouped(x, ends)
+    y, mask = m.qdq_fp4_ste(x32)
+    check(lambda st: m.quantize(x, stream=st))
+    check(lambda st: m.quantize_batched(x.view(2, 128, 256), stream=st))
+    check(lambda st: m.quantize_grouped(x, ends, m.MXQ_AXIS_ROW, stream=st))
+    check(lambda st: m.qdq_fp4(x32, True, stream=st))
+    check(lambda st: m.quantize_fp4(x32, stream=st))
+    check(lambda st: m.qdq_fp4_ste(x32, want_codes=True, stream=st))
+    check(lambda st: m.ste_backward_fp4(x32, mask, stream=st))
+    check(lambda st: m.gemm(q["q_row"], q["s_row"], q["q_row"], q["s_row"], stream=st))
+    check(lambda st: m.grouped_gemm(m.MXQ_GG_RAGGED_M, q["q_row"], q["s_row"], w["q_row"], w["s_row"], ends, stream=st))
+    check(lambda st: m.grouped_gemm(m.MXQ_GG_RAGGED_K, k["q_colT"], k["s_colT"], k["q_colT"], k["s_colT"], ends, stream=st))
+    # columns between the groups of a grouped operand need not be written: compared by what a product reads
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    a, b = m.quantize_grouped(x, ends, stream=st), m.quantize_fp4_grouped(x32, ends, stream=st)
+    assert all(stream_of(t) == st.cuda_stream for d in (a, b) for t in tensors(d))
+    torch.cuda.current_stream().wait_stream(st)
+    product = lambda d: m.grouped_gemm(m.MXQ_GG_RAGGED_K, d["q_colT"], d["s_colT"], d["q_colT"], d["s_colT"], ends)  # noqa: E731
+    assert torch.equal(product(a), product(k))

@@ -52,6 +52,32 @@ HELPERS = {
 }
 
 
+G, R = 2, 64
+END = dev(G, dtype=torch.int32)
+
+
+def u8(*shape):
+    return dev(*shape, dtype=torch.uint8)
+
+
+def operand(rows, k=64):
+    return u8(rows, k), u8(*mxq.scale_shape(rows, k // 32))
+
+
+HELPERS |= {
+    "quantize": lambda st: mxq.quantize(dev(R, R, dtype=torch.bfloat16), stream=st),
+    "quantize_batched": lambda st: mxq.quantize_batched(dev(2, R, R, dtype=torch.bfloat16), stream=st),
+    "quantize_grouped": lambda st: mxq.quantize_grouped(dev(R, R, dtype=torch.bfloat16), END, 3, 256, stream=st),
+    "qdq_fp4": lambda st: mxq.qdq_fp4(dev(R, R), True, stream=st),
+    "quantize_fp4": lambda st: mxq.quantize_fp4(dev(R, R), stream=st),
+    "quantize_fp4_grouped": lambda st: mxq.quantize_fp4_grouped(dev(R, R), END, 256, stream=st),
+    "qdq_fp4_ste": lambda st: mxq.qdq_fp4_ste(dev(R, R), want_codes=True, stream=st),
+    "ste_backward_fp4": lambda st: mxq.ste_backward_fp4(dev(R, R), u8(R, R // 8), stream=st),
+    "gemm": lambda st: mxq.gemm(*operand(R), *operand(R), stream=st),
+    "grouped_gemm": lambda st: mxq.grouped_gemm(mxq.MXQ_GG_RAGGED_K, *operand(R, 256), *operand(R, 256), END, stream=st),
+}
+
+
 @pytest.fixture
 def events(monkeypatch):
     empty = torch.empty
