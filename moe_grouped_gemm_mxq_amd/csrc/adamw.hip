@@ -30,8 +30,11 @@ constexpr int kThreads = 256;
 // non-temporal stores lose 13% (200M fp32 weights, MXFP8 states: 609 against 689 us).
 constexpr int kPieces = 2;
 constexpr int kTile = kPieces * 4 * kThreads;
-constexpr int kTensors = 48;   // per launch: the descriptors travel as a kernel argument, 4 KB at most
-static_assert(kTensors <= 64, "a wave looks its workgroup's tensor up, a tensor per lane");
+// Tensors of a launch: as many descriptors as fit the 4 KB of a kernel's arguments, in which they
+// travel.  (At most 64: a wave looks its workgroup's tensor up, a tensor per lane.)  50 small
+// tensors take 3.2 us on the GPU in a graph, 51 in two launches 5.9.
+constexpr int kTensors = 50;
+constexpr size_t kArgumentBytes = 4096;
 constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
 constexpr int kLine = 32;  // fp32 states in a cache line
 constexpr int64_t kMaxRun = 32 * kTile, kMaxElements = kMaxGrid * kMaxRun - kLine;
@@ -75,7 +78,8 @@ struct Args {
   double log2_b1, log2_b2;
   const mxq_adamw_control* control;
 };
-static_assert(sizeof(Args) <= 4096, "what a kernel argument holds");
+static_assert(kTensors <= 64 && sizeof(Args) <= kArgumentBytes && sizeof(Args) + sizeof(Tensor) > kArgumentBytes,
+              "as many tensors as fit");
 
 // ------------------------------------------------------------------ random bits
 __device__ __forceinline__ uint32_t mix(uint32_t x) {

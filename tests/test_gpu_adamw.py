@@ -337,3 +337,10 @@ def test_rounding_is_decided_within_2_to_the_minus_18_of_a_step(moment, values):
     codes, scales = m if moment == "m" else v
     assert np.array_equal(host(scales), (exps + 127).astype(np.uint8))
     assert np.array_equal(host(codes), code.astype(np.uint8))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [47, 50, 51, 64, 101])
+def test_as_many_tensors_as_a_launch_holds_and_more(bits, count):
+    p, g, m, v = tensors([1 + 37 * i % 90 for i in range(count)], torch.bfloat16, torch.float32, bits, count)
+    check_step(p, g, m, v)
