@@ -42,6 +42,33 @@ def route(logits, K, score="softmax", bias=None, n_group=1, topk_group=1, group_
     return idx, weights
 
 
+def route_rows(logits, K, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalise=True, scale=1.0):
+    """route of many rows at once; logits and keys finite or masked."""
+    T, E = logits.shape
+    off = logits <= LOWEST
+    with np.errstate(all="ignore"):
+        if score == "sigmoid":
+            e = np.exp(-np.abs(logits))
+            s = np.where(logits >= 0, 1.0, e) / (1.0 + e)
+        else:
+            e = np.where(off, 0.0, np.exp(logits - np.where(off, -np.inf, logits).max(1, keepdims=True)))
+            s = e / e.sum(1, keepdims=True)
+        s = np.where(off, 0.0, s)
+        key = np.where(off, -np.inf, s if bias is None else s + bias)
+        order = np.where(off, -np.inf, logits) if bias is None else key
+        if n_group > 1:
+            best = np.sort(key.reshape(T, n_group, -1), axis=2)[:, :, ::-1][:, :, :group_top]
+            total = np.where(best[:, :, 0] > -np.inf, np.where(best > -np.inf, best, 0.0).sum(2), -np.inf)
+            rank = np.argsort(np.argsort(-total, axis=1, kind="stable"), axis=1, kind="stable")
+            order = np.where((rank < topk_group).repeat(E // n_group, axis=1), order, -np.inf)
+        chosen = np.argsort(-order, axis=1, kind="stable")[:, :K]
+        there = np.take_along_axis(order, chosen, 1) > -np.inf
+        w = np.where(there, np.take_along_axis(s, chosen, 1), 0.0)
+        if renormalise:
+            w = np.where(there, w / np.where(w.sum(1, keepdims=True) != 0, w.sum(1, keepdims=True), 1.0), 0.0)
+    return np.where(there, chosen, -1).astype(np.int32), w * scale
+
+
 def expert_order(idx, E):
     T, K = idx.shape
     flat = idx.reshape(-1)
@@ -82,6 +109,36 @@ def route_backward(logits, idx, dweights, score="softmax", renormalise=True, sca
             dw_ds = np.eye(len(sel))
         out[t] = (g @ dw_ds) @ ds_dl[sel]
     return out
+
+
+def route_backward_rows(logits, idx, dweights, score="softmax", renormalise=True, scale=1.0):
+    """route_backward of many rows at once, by the closed forms."""
+    T, E = logits.shape
+    off = logits <= LOWEST
+    there = (idx >= 0) & (idx < E)
+    at = np.where(there, idx, 0)
+    there &= ~np.take_along_axis(off, at, 1)
+    g = np.where(there, dweights * scale, 0.0)
+    out = np.zeros((T, E + 1))
+    put = np.where(there, at, E)  # no gradient: the column past the last
+    l = np.where(off, -np.inf, logits)
+    x = np.where(there, np.take_along_axis(l, at, 1), -np.inf)
+    sig = 1.0 / (1.0 + np.exp(-np.where(there, x, 0.0)))
+    if score == "sigmoid" and not renormalise:
+        np.put_along_axis(out, put, g * sig * (1.0 - sig), 1)
+    elif renormalise:
+        some = there.any(1, keepdims=True)
+        p = np.where(there, sig if score == "sigmoid" else np.exp(x - np.where(some, x.max(1, keepdims=True), 0.0)), 0.0)
+        p = p / np.where(some, p.sum(1, keepdims=True), 1.0)
+        d = p * (g - (p * g).sum(1, keepdims=True))
+        np.put_along_axis(out, put, d * (1.0 - sig) if score == "sigmoid" else d, 1)
+    else:
+        top = l.max(1, keepdims=True)
+        e = np.where(off, 0.0, np.exp(l - np.where(top > -np.inf, top, 0.0)))
+        s = e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+        np.put_along_axis(out, put, g, 1)
+        out[:, :E] = s * (out[:, :E] - (s * out[:, :E]).sum(1, keepdims=True))
+    return out[:, :E]
 
 
 def mix(x):

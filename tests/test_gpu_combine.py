@@ -219,3 +219,16 @@ def test_helpers_refuse_other_types():
         m.combine(y, slot, dtype=torch.float16)
     with pytest.raises(TypeError, match="dtype must be"):
         m.dispatch(y[:2], slot, 4, dtype=torch.float64)
+
+
+@pytest.mark.parametrize("ydt", TYPES)
+@pytest.mark.parametrize("odt", TYPES)
+@pytest.mark.parametrize("T,K,H", [(257, 3, 2056), (257, 8, 4096), (257, 2, 4104), (300, 5, 7168)])
+def test_workgroups_of_more_than_four_waves(T, K, H, ydt, odt):
+    """From 256 tokens on, rows of more than 2048 columns take 5 to 8 waves a workgroup."""
+    rows, slot, y, w, d = case(T, K, H, ydt, odt, T + H, 0.2)
+    check_combine(y, slot, w, odt)
+    check_combine(y, slot, None, odt)
+    for gdt in TYPES:
+        check_backward(d, slot, rows, w, y, gdt)
+    check_backward(d, slot, rows, None, None, odt)

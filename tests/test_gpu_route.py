@@ -465,3 +465,88 @@ def test_route_groups_of_keys_that_overflow_when_added(score):
         for top in (1, 2):
             for b in (bias, -bias):
                 check_route(x, 16, b.cuda(), score=score, n_group=8, topk_group=topk_group, group_top=top)
+
+
+# ------------------------------------------------------------------ many rows: other shapes of the kernels
+def row_spread(l):
+    """spread of rows, vectorised: range of the unmasked logits and their largest magnitude."""
+    off = l <= ref.LOWEST
+    some = ~off.all(1)
+    hi, lo = (np.where(some, f(np.where(off, o, l), axis=1), 0.0) for f, o in ((np.max, -np.inf), (np.min, np.inf)))
+    return (hi - lo + np.maximum(np.abs(hi), np.abs(lo)))[:, None]
+
+
+def check_route_rows(x, K, bias=None, **kw):
+    E = x.shape[1]
+    got = mxq().route(x, K, bias=bias, **kw)
+    idx, w = ref.route_rows(f64(x), K, bias=None if bias is None else f64(bias), **kw)
+    assert np.array_equal(host(got["idx"]), idx)
+    assert np.all(np.abs(f64(got["weights"]) - w) <= (4 * row_spread(f64(x)) + 40) * U * np.abs(w) + 2.0 ** -126)
+    for name, want in zip(("group_end", "row_token", "slot"), ref.expert_order(idx, E)):
+        assert np.array_equal(host(got[name]), want), name
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,K,n_group", [(4099, 40, 20, 1), (4099, 100, 6, 1), (4099, 256, 8, 1), (4099, 256, 8, 8), (4099, 200, 20, 1),
+                                           (4099, 300, 8, 1), (4099, 512, 8, 1), (4099, 512, 8, 8), (4099, 1000, 8, 1), (2000, 1024, 8, 1),
+                                           (65536, 32, 8, 1), (33000, 256, 2, 1), (5003, 32, 8, 4)])
+def test_route_many_rows(T, E, K, n_group, score):
+    """Rows held by 16, 32 and 64 lanes with up to 16 experts each, and the expert order by either way."""
+    bias = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))).cuda()
+    for dtype, b, masked in ((torch.float32, bias, 0.0), (torch.float32, None, 0.1), (torch.bfloat16, bias, 0.1), (torch.bfloat16, None, 0.0)):
+        kw = dict(n_group=n_group, topk_group=max(1, n_group // 2), group_top=2) if n_group > 1 else {}
+        check_route_rows(logits_of(T, E, dtype, T + E + K, masked), K, b, score=score, renormalise=b is not None, scale=2.5, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("T,E,K", [(4099, 40, 5), (4099, 100, 6), (4099, 256, 8), (4099, 255, 16), (4099, 256, 20), (4099, 300, 8),
+                                   (4099, 512, 8), (16390, 256, 8)])
+def test_route_backward_many_rows(T, E, K, score, renormalise):
+    """The bounds of check_backward, on all rows at once."""
+    for dtype, masked in ((torch.float32, 0.0), (torch.bfloat16, 0.2)):
+        x = logits_of(T, E, dtype, T + E, masked)
+        idx = mxq().route(x, K, score=score, order=False)["idx"]
+        dw = torch.randn(T, K, generator=torch.Generator().manual_seed(E)).cuda()
+        got = f64(mxq().route_backward(x, idx, dw, score=score, renormalise=renormalise, scale=2.5))
+        l, i, g = f64(x), host(idx), f64(dw)
+        want = ref.route_backward_rows(l, i, g, score, renormalise, 2.5)
+        off, there = l <= ref.LOWEST, i >= 0
+        with np.errstate(all="ignore"):
+            s = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - np.where(off, -np.inf, l).max(1, keepdims=True))
+        s = np.where(off, 0, s)
+        if score == "softmax":
+            s = s / np.maximum(s.sum(1, keepdims=True), 1e-300)
+        G, named = np.zeros((T, E + 1)), np.zeros((T, E + 1), bool)
+        np.put_along_axis(G, np.where(there, i, E), np.abs(g) * 2.5, 1)
+        np.put_along_axis(named, np.where(there, i, E), True, 1)
+        G, named = G[:, :E], named[:, :E]
+        if renormalise:
+            p = np.where(named, s, 0)
+            p = p / np.maximum(p.sum(1, keepdims=True), 1e-300)
+            size = p * (G + (p * G).sum(1, keepdims=True))
+        elif score == "sigmoid":
+            size = s * G
+        else:
+            size = s * (G + (s * G).sum(1, keepdims=True))
+        tol = (6 * row_spread(l) + 64) * U * size + 2.0 ** -126 + (ref.UBF16 * np.abs(want) if dtype == torch.bfloat16 else 0)
+        assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_route_random(seed):
+    """Twelve routings of random sizes, groups, types, masks and biases from none to a thousand."""
+    rng = np.random.default_rng(seed)
+    for _ in range(12):
+        n_group = int(rng.choice([1, 1, 2, 3, 4, 8, 16, 64]))
+        per = int(np.exp(rng.uniform(0, np.log(1024 / n_group))))
+        E = n_group * per
+        T, K = int(np.exp(rng.uniform(0, np.log(6000)))), int(rng.integers(1, min(E, 32) + 1))
+        dtype = (torch.float32, torch.bfloat16)[rng.integers(2)]
+        size = float(rng.choice([0.0, 0.0, 0.1, 1.0, 30.0, 1000.0]))
+        bias = torch.from_numpy(size * rng.standard_normal(E)).float().cuda() if size else None
+        kw = dict(score=("softmax", "sigmoid")[rng.integers(2)], n_group=n_group, topk_group=int(rng.integers(1, n_group + 1)),
+                  group_top=int(rng.integers(1, 3)), renormalise=bool(rng.integers(2)))
+        x = logits_of(T, E, dtype, int(rng.integers(1 << 30)), float(rng.choice([0.0, 0.0, 0.3, 0.8])), float(rng.choice([0.3, 1.5, 5.0])))
+        print(T, E, K, dtype, size, kw, flush=True)
+        check_route_rows(x, K, bias, **kw)

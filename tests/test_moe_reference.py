@@ -109,3 +109,24 @@ def test_adamw_is_torchs():
         opt.step()
         x, m, v, _, _, _ = ref.adamw(x, gr.numpy() * t, m, v, 0.01, (0.8, 0.95), 1e-6, 0.1, t, 1.0)
         assert np.allclose(x, q.detach().numpy(), rtol=1e-12)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_references_of_many_rows(score, renormalise):
+    """The vectorised references are those of one row at a time."""
+    rng = np.random.default_rng(3)
+    l = rng.standard_normal((40, 24))
+    l[rng.random(l.shape) < 0.3] = -np.inf
+    l[7] = -np.inf
+    l[8] = np.round(l[8])
+    for bias in (None, rng.standard_normal(24) * 0.2):
+        for groups in ({}, dict(n_group=4, topk_group=2, group_top=2), dict(n_group=6, topk_group=1, group_top=1)):
+            kw = dict(score=score, bias=bias, renormalise=renormalise, scale=1.5, **groups)
+            (i, w), (ri, rw) = ref.route(l, 5, **kw), ref.route_rows(l, 5, **kw)
+            assert np.array_equal(i, ri) and np.allclose(w, rw, rtol=1e-14, atol=0)
+    idx = ref.route(l, 5, score)[0]
+    idx[3, 2], idx[4, 0] = 24, -(2 ** 31)
+    dw = rng.standard_normal(idx.shape)
+    a, b = (f(l, idx, dw, score, renormalise, 2.5) for f in (ref.route_backward, ref.route_backward_rows))
+    assert np.allclose(a, b, rtol=1e-11, atol=1e-15)
