@@ -375,7 +375,9 @@ typedef enum {
  *    chosen, not counted by a softmax.
  *  - An expert ranks by its key: s + bias[e], or its logit where bias is
  *    NULL.  A NaN key ranks below every number, and one of -inf (a bias that
- *    bars its expert) is not chosen.
+ *    bars its expert) is not chosen.  (Rows with keys that are not finite take
+ *    several times as long as others, so a bias of -inf costs all rows; masked
+ *    logits cost nothing.)
  *  - n_group > 1 splits the experts into n_group equal runs; a group's total
  *    is the sum of its best `group_top` (1 or 2) s + bias (s without bias)
  *    over unmasked experts; only the topk_group best groups' experts can be

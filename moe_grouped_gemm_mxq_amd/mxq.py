@@ -817,7 +817,8 @@ def combine(y, slot, weights=None, dtype=torch.bfloat16, stream=None):
 
 
 def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=None):
-    """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights."""
+    """(dy [rows][H] of `dtype` (dout's), dweights [T][top_k]); dweights is None without y or weights.  Rows of dy that no
+    slot names are not written (mxq_combine_backward takes a dy that the caller has filled)."""
     if stream is not None:
         with _on(stream, dout.device):
             return combine_backward(dout, slot, rows, weights, y, dtype)
@@ -832,7 +833,8 @@ def combine_backward(dout, slot, rows, weights=None, y=None, dtype=None, stream=
 
 
 def dispatch(x, slot, rows, dtype=None, stream=None):
-    """Tokens x [T][H] in expert order: row slot[t][k] of the result is x[t].  Its gradient is combine without weights."""
+    """Tokens x [T][H] in expert order: row slot[t][k] of the result is x[t], and rows that no slot names (those past
+    the last group end) are not written.  Its gradient is combine without weights."""
     return combine_backward(x, slot, rows, dtype=dtype, stream=stream)[0]
 
 
