@@ -210,7 +210,7 @@ def run(s):
 
 def _codes(out):
     """The copies, 8-bit codes as the values they stand for."""
-    return {k: v.view(torch.float8_e4m3fn) if v.dtype == torch.uint8 else v for k, v in out.items()}
+    return {k: v.view(torch.float8_e4m3fn) if v.dtype == torch.uint8 else v for k, v in out.items() if isinstance(v, torch.Tensor)}
 
 
 def _run_own(s):
