@@ -1,0 +1,412 @@
+// Products of FP8 (E4M3) operands with one fp32 scale for every block of 128
+// along the reduction axis:
+//   C[m][n] = sum over blocks b of sA[b][m] sB[b][n] P_b[m][n],
+//   P_b[m][n] = sum over the block's k of A[m][k] B[n][k],
+// A's blocks 1 x 128, B's 1 x 128 or 128 x 128 (weights).  Dense, ragged M (rows
+// split into expert groups, group g times B[g]) and ragged K (one product per
+// group over its padded columns).
+//
+// The scales are fp32, so the matrix instruction cannot apply them: each block's
+// partial product starts from zero and is added to the tile's sums with one
+// multiply-add an element (two where B's blocks are 1 x 128), which the vector
+// units do while the matrix units work on the next block.
+//
+// Rounded to bf16, the partial products come from the FP8 matrix instruction,
+// whose sums of eight products keep about 13 bits below the largest, far below
+// the output's 8 bits.  An fp32 output takes the codes as bf16 numbers (exact) through the
+// bf16 instruction at half the rate: its products and sums are fp32's.
+#include <type_traits>
+
+#include "mxq_device.h"
+#include "mxq_groups.h"
+#include "mxq_host.h"
+#include "mxq_internal.h"
+#include "mxq_tile.h"
+#include "mxq_vec.h"
+
+namespace mxq {
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr int kB = 128;  // block, and the bytes of a tile row in a stage
+
+enum Mode { kDense = 0, kRaggedM = 1, kRaggedK = 2 };
+
+// Output tile of a workgroup: BM rows of A by BN rows of B, WAVES_M x WAVES_N waves.
+template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M;
+  static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;  // wave tile
+  static constexpr int TM = WM / 16, TN = WN / 16;            // 16 x 16 blocks of a wave
+  static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;  // 1 KB loads of a wave and stage
+  static constexpr int kCodesA = BM * kB, kCodesB = BN * kB;
+  static constexpr int kStage = kCodesA + kCodesB + (BM + BN) * 4;  // codes, then the block's scales of every row
+  static_assert(BM / 64 + BN / 64 <= kWaves, "each wave loads the scales of at most 64 rows");
+  static_assert(kLoadsA % 2 == 0 && kLoadsB % 2 == 0, "a load's parity is its place's");
+};
+
+struct Problem {
+  const uint8_t* A;
+  const float* sA;
+  const uint8_t* B;
+  const float* sB;
+  void* C;
+  int64_t M, N, K, ldc;
+  const int32_t* group_end;
+  int G;
+  int tiles_m, tiles_n;
+};
+
+// What a workgroup computes; uniform.
+struct Tile {
+  int64_t m0, n0;
+  int rows, cols;           // valid ones of the tile
+  int64_t kb0;              // first block of the reduction
+  int nkb;                  // its blocks; 0: zeros
+  const uint8_t* B;         // codes and scales of the tile's expert
+  const float* sB;
+  int64_t c0;               // first element of its matrix in C
+};
+
+// Groups of a ragged-K product, largest first where one wave can rank them.
+__device__ __forceinline__ void ragged_k_group(const int32_t* group_end, int G, int64_t K, int rank, int& g, int64_t& before,
+                                               int& blocks) {
+  const int lane = threadIdx.x & 63;
+  if (G <= 64) {
+    int32_t start = 0, size = -1;
+    if (lane < G) group_span(group_end, lane, K, start, size);
+    int place = 0;
+    for (int h = 0; h < G; h++) {
+      const int32_t other = __builtin_amdgcn_readlane(size, h);
+      place += other > size || (other == size && h < lane);
+    }
+    const int32_t units = lane < G ? (int32_t)(((uint32_t)size + (kB - 1)) / kB) : 0;
+    int32_t upto = units;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int32_t v = __shfl_up(upto, off);
+      if (lane >= off) upto += v;
+    }
+    g = __builtin_ctzll(__ballot(lane < G && place == rank));
+    blocks = __builtin_amdgcn_readlane(units, g);
+    before = __builtin_amdgcn_readlane(upto - units, g);
+    return;
+  }
+  g = rank;
+  int64_t sum = 0;
+  for (int g0 = 0; g0 < g; g0 += 64) {
+    int32_t start = 0, size = 0;
+    if (g0 + lane < g) group_span(group_end, g0 + lane, K, start, size);
+    int32_t units = (int32_t)(((uint32_t)size + (kB - 1)) / kB);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) units += __shfl_xor(units, off);
+    sum += units;
+  }
+  int32_t start, size;
+  group_span(group_end, g, K, start, size);
+  before = sum;
+  blocks = __builtin_amdgcn_readfirstlane((int32_t)(((uint32_t)size + (kB - 1)) / kB));
+}
+
+// The tile of workgroup `bid`; false where there is none.
+template <int MODE, class S, bool TILE128>
+__device__ __forceinline__ bool find_tile(const Problem& p, int bid, Tile& t) {
+  const int64_t Kb = p.K / kB;
+  const int64_t scales_n = TILE128 ? (p.N + kB - 1) / kB : p.N;
+  t.kb0 = 0;
+  t.nkb = (int)Kb;
+  t.B = p.B;
+  t.sB = p.sB;
+  t.c0 = 0;
+  int mt, nt;
+  int64_t rows;
+  if constexpr (MODE == kDense) {
+    raster(xcd_remap(bid, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, mt, nt);
+    t.m0 = (int64_t)mt * S::BM;
+    rows = p.M - t.m0;
+  } else if constexpr (MODE == kRaggedM) {
+    raster(xcd_remap(bid, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, mt, nt);
+    GroupUnit u;
+    if (!find_group_unit<S::BM>(p.group_end, p.G, p.M, mt, u)) return false;
+    t.m0 = u.start + (int64_t)u.local * S::BM;
+    rows = u.size - (int64_t)u.local * S::BM;
+    t.B = p.B + (int64_t)u.g * p.N * p.K;
+    t.sB = p.sB + (int64_t)u.g * Kb * scales_n;
+  } else {
+    const int per = p.tiles_m * p.tiles_n;
+    const int rank = bid / per;
+    int g, blocks;
+    int64_t before;
+    ragged_k_group(p.group_end, p.G, p.K, rank, g, before, blocks);
+    t.kb0 = min(before, Kb);
+    t.nkb = (int)min((int64_t)blocks, Kb - t.kb0);
+    t.c0 = (int64_t)g * p.M * p.N;
+    raster(xcd_remap(bid - rank * per, per), p.tiles_m, p.tiles_n, mt, nt);
+    t.m0 = (int64_t)mt * S::BM;
+    rows = p.M - t.m0;
+  }
+  t.n0 = (int64_t)nt * S::BN;
+  t.rows = (int)min<int64_t>(rows, S::BM);
+  t.cols = (int)min<int64_t>(p.N - t.n0, S::BN);
+  return true;
+}
+
+// 32 code bytes of a lane: of tile row r0 + lane % 16, the block's bytes 32g ..
+// 32g + 31 (g = lane / 16).  Both operands map bytes to the instruction's k alike,
+// which is all that a sum over the block asks for.
+__device__ __forceinline__ v8i load_frag(const uint8_t* codes, int r0, int lane) {
+  const int r = r0 + (lane & 15), c = 2 * (lane >> 4);
+  const uint4 lo = *reinterpret_cast<const uint4*>(codes + swz(r, c));
+  const uint4 hi = *reinterpret_cast<const uint4*>(codes + swz(r, c + 1));
+  v8i f;
+  f[0] = (int)lo.x; f[1] = (int)lo.y; f[2] = (int)lo.z; f[3] = (int)lo.w;
+  f[4] = (int)hi.x; f[5] = (int)hi.y; f[6] = (int)hi.z; f[7] = (int)hi.w;
+  return f;
+}
+
+struct Wide {
+  v8bf f[4];
+};
+// the same 32 codes as bf16 numbers (exact), eight for each of four instructions
+__device__ __forceinline__ Wide widen(const v8i& c) {
+  Wide w;
+#pragma unroll
+  for (int s = 0; s < 4; s++) {
+    const v2bf16 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * s], 1.f, false);
+    const v2bf16 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * s], 1.f, true);
+    const v2bf16 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * s + 1], 1.f, false);
+    const v2bf16 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * s + 1], 1.f, true);
+    w.f[s] = v8bf{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+  }
+  return w;
+}
+
+template <bool F32>
+struct FragOf {
+  typedef v8i type;
+  static __device__ __forceinline__ v8i of(const v8i& c) { return c; }
+};
+template <>
+struct FragOf<true> {
+  typedef Wide type;
+  static __device__ __forceinline__ Wide of(const v8i& c) { return widen(c); }
+};
+
+// partial product of a block: rows of n by columns (lanes) of m
+__device__ __forceinline__ v4f block_product(const v8i& n, const v8i& m) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ v4f block_product(const Wide& n, const Wide& m) {
+  v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; s++) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.f[s], m.f[s], d, 0, 0, 0);
+  return d;
+}
+
+__device__ __forceinline__ void store4(float* p, const v4f& v, int n) {
+  if (n >= 4) {
+    *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, v);
+  } else {
+    for (int e = 0; e < n; e++) p[e] = v[e];
+  }
+}
+__device__ __forceinline__ void store4(uint16_t* p, const v4f& v, int n) {
+  if (n >= 4) {
+    u32x2 w;
+    w[0] = bf16x2_of(v[0], v[1]);
+    w[1] = bf16x2_of(v[2], v[3]);
+    *reinterpret_cast<u32x2_any*>(p) = w;
+  } else {
+    for (int e = 0; e < n; e++) p[e] = bf16_of(v[e]);
+  }
+}
+
+// One stage is one block of 128 along K: codes and scales of the tile's rows,
+// loaded straight into LDS one stage ahead.  The two stages are separate arrays
+// so that the compiler can tell the one being read from the one being filled.
+template <int MODE, bool F32, bool TILE128, class S>
+__global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
+  typedef std::conditional_t<F32, float, uint16_t> Out;
+  constexpr int TM = S::TM, TN = S::TN;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStage];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % S::kWavesM, wn = wave / S::kWavesM;
+  Tile t;
+  if (!find_tile<MODE, S, TILE128>(p, blockIdx.x, t)) return;
+
+  // per-lane offsets of this wave's loads: rows past the tile read its last row
+  uint32_t offA[S::kLoadsA], offB[S::kLoadsB];
+#pragma unroll
+  for (int j = 0; j < S::kLoadsA; j++)
+    offA[j] = (uint32_t)min((wave * S::kLoadsA + j) * 8 + (lane >> 3), t.rows - 1) * (uint32_t)p.K + dma_chunk(j, lane) * 16;
+#pragma unroll
+  for (int j = 0; j < S::kLoadsB; j++)
+    offB[j] = (uint32_t)min((wave * S::kLoadsB + j) * 8 + (lane >> 3), t.cols - 1) * (uint32_t)p.K + dma_chunk(j, lane) * 16;
+  const uint8_t* const baseA = p.A + t.m0 * p.K + t.kb0 * kB;
+  const uint8_t* const baseB = t.B + t.n0 * p.K + t.kb0 * kB;
+  // scales: wave w those of the 64 tile rows from 64 w on, A's rows before B's
+  const bool of_a = wave < S::BM / 64;
+  const int srow = (of_a ? wave : wave - S::BM / 64) * 64 + lane;
+  const int64_t scales_n = TILE128 ? (p.N + kB - 1) / kB : p.N;
+  const int64_t spitch = of_a ? p.M : scales_n;
+  const float* sp = of_a ? p.sA + t.m0 + min(srow, t.rows - 1)
+                         : t.sB + (TILE128 ? (t.n0 + min(srow, t.cols - 1)) / kB : t.n0 + min(srow, t.cols - 1));
+  sp += t.kb0 * spitch;
+
+  auto issue = [&](uint8_t* st, int s) {
+    const uint8_t* a = baseA + (int64_t)s * kB;
+    const uint8_t* b = baseB + (int64_t)s * kB;
+#pragma unroll
+    for (int j = 0; j < S::kLoadsA; j++)
+      load_lds16(a + offA[j], st + (wave * S::kLoadsA + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < S::kLoadsB; j++)
+      load_lds16(b + offB[j], st + S::kCodesA + (wave * S::kLoadsB + j) * 1024);
+    if (wave < S::BM / 64 + S::BN / 64)
+      load_lds4(sp + s * spitch, st + S::kCodesA + S::kCodesB + wave * 256);
+  };
+
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; i++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  typedef FragOf<F32> Frag;
+  auto compute = [&](const uint8_t* st) {
+    const float* sa_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + wm * S::WM;
+    const float* sb_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + S::BM + wn * S::WN;
+    typename Frag::type fm[TM];
+    float f[TM];
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+      fm[j] = Frag::of(load_frag(st, wm * S::WM + j * 16, lane));
+      f[j] = sa_of[j * 16 + (lane & 15)];
+      if constexpr (TILE128) f[j] *= sb_of[0];
+    }
+#pragma unroll
+    for (int i = 0; i < TN; i++) {
+      const typename Frag::type fn = Frag::of(load_frag(st + S::kCodesA, wn * S::WN + i * 16, lane));
+      v4f sb;
+      if constexpr (!TILE128) sb = *reinterpret_cast<const v4f*>(sb_of + i * 16 + 4 * (lane >> 4));
+#pragma unroll
+      for (int j = 0; j < TM; j++) {
+        v4f d = block_product(fn, fm[j]);
+        if constexpr (!TILE128) d *= sb;
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(d[e], f[j], acc[i][j][e]);
+      }
+    }
+  };
+  auto step = [&](uint8_t* cur, uint8_t* next, int s) {
+    if (s + 1 < t.nkb) issue(next, s + 1);
+    compute(cur);
+    wait_vmcnt<0>();  // the next stage has landed
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (t.nkb > 0) {
+    issue(stage0, 0);
+    wait_vmcnt<0>();
+    __builtin_amdgcn_s_barrier();
+    for (int s = 0; s < t.nkb; s += 2) {
+      step(stage0, stage1, s);
+      if (s + 1 < t.nkb) step(stage1, stage0, s + 1);
+    }
+  }
+
+  // lane l holds C[m = l % 16][n = 4 (l / 16) .. + 3] of each 16 x 16 block
+  Out* C = static_cast<Out*>(p.C) + t.c0 + t.m0 * p.ldc + t.n0;
+#pragma unroll
+  for (int j = 0; j < TM; j++) {
+    const int m = wm * S::WM + j * 16 + (lane & 15);
+    if (m >= t.rows) continue;
+    Out* row = C + (int64_t)m * p.ldc;
+#pragma unroll
+    for (int i = 0; i < TN; i++) {
+      const int n = wn * S::WN + i * 16 + 4 * (lane >> 4);
+      store4(row + n, acc[i][j], t.cols - n);
+    }
+  }
+}
+
+typedef Shape<128, 128, 2, 2> Small;
+
+template <int MODE, bool F32, bool TILE128, class S>
+hipError_t launch_shape(Problem p, hipStream_t st) {
+  p.tiles_n = (int)((p.N + S::BN - 1) / S::BN);
+  const int64_t tm = (p.M + S::BM - 1) / S::BM + (MODE == kRaggedM ? p.G : 0);
+  const int64_t total = tm * p.tiles_n * (MODE == kRaggedK ? p.G : 1);
+  if (total > INT32_MAX) return hipErrorInvalidValue;
+  p.tiles_m = (int)tm;
+  gemm128_kernel<MODE, F32, TILE128, S><<<(unsigned)total, S::kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <int MODE, bool TILE128>
+hipError_t launch_gemm128(const Problem& p, bool f32, hipStream_t st) {
+  if (f32) return launch_shape<MODE, true, TILE128, Small>(p, st);
+  return launch_shape<MODE, false, TILE128, Small>(p, st);
+}
+
+mxq_status check(const char* who, const Problem& p, mxq_dtype cdt) {
+  MXQ_REQUIRE(cdt == MXQ_DT_F32 || cdt == MXQ_DT_BF16, "%s: unknown output type %d", who, (int)cdt);
+  MXQ_REQUIRE(p.M >= 0 && p.M <= INT32_MAX && p.N >= 1 && p.N <= INT32_MAX, "%s: M must be in [0, 2^31), N in [1, 2^31)", who);
+  MXQ_REQUIRE(p.K >= kB && p.K % kB == 0, "%s: K must be a positive multiple of 128 (got %lld)", who, (long long)p.K);
+  MXQ_REQUIRE(p.K < MXQ_GEMM_MAX_ROW_BYTES, "%s: K = %lld gives code rows of MXQ_GEMM_MAX_ROW_BYTES or more", who, (long long)p.K);
+  MXQ_REQUIRE(p.ldc >= p.N, "%s: ldc < N", who);
+  if (p.M == 0) return MXQ_OK;
+  MXQ_REQUIRE(p.A && p.sA && p.B && p.sB && p.C, "%s: NULL operand", who);
+  MXQ_REQUIRE(aligned_to(p.A, 16) && aligned_to(p.B, 16), "%s: A, B must be 16-byte aligned", who);
+  MXQ_REQUIRE(aligned_to(p.sA, 4) && aligned_to(p.sB, 4), "%s: sA, sB must be 4-byte aligned", who);
+  MXQ_REQUIRE(aligned_to(p.C, cdt == MXQ_DT_F32 ? 4 : 2), "%s: C must be aligned to its elements", who);
+  return MXQ_OK;
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" {
+
+mxq_status mxq_gemm128(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, int b_tile, void* C,
+                       mxq_dtype cdt, int64_t M, int64_t N, int64_t K, int64_t ldc, hipStream_t st) {
+  const Problem p{A, sA, B, sB, C, M, N, K, ldc, nullptr, 1, 0, 0};
+  MXQ_REQUIRE(b_tile == 1 || b_tile == 128, "mxq_gemm128: b_tile must be 1 or 128 (got %d)", b_tile);
+  const mxq_status s = check("mxq_gemm128", p, cdt);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE_DEVICE();
+  if (M == 0) return ok();
+  const bool f32 = cdt == MXQ_DT_F32;
+  return launched(b_tile == 128 ? launch_gemm128<kDense, true>(p, f32, st) : launch_gemm128<kDense, false>(p, f32, st),
+                  "mxq_gemm128");
+}
+
+mxq_status mxq_grouped_gemm128(mxq_gg_mode mode, const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                               void* C, mxq_dtype cdt, int64_t M, int64_t N, int64_t K, const int32_t* group_end,
+                               int32_t G, hipStream_t st) {
+  const Problem p{A, sA, B, sB, C, M, N, K, N, group_end, G, 0, 0};
+  MXQ_REQUIRE(mode == MXQ_GG_RAGGED_M || mode == MXQ_GG_RAGGED_K, "mxq_grouped_gemm128: bad mode");
+  MXQ_REQUIRE(G >= 1 && G <= MXQ_MAX_GROUPS, "mxq_grouped_gemm128: G must be in [1, %d] (got %d)", MXQ_MAX_GROUPS, G);
+  const mxq_status s = check("mxq_grouped_gemm128", p, cdt);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE(group_end != nullptr && aligned_to(group_end, 4), "mxq_grouped_gemm128: group_end must be 4-byte aligned, not NULL");
+  MXQ_REQUIRE_DEVICE();
+  if (M == 0) return ok();
+  const bool f32 = cdt == MXQ_DT_F32;
+  return launched(mode == MXQ_GG_RAGGED_M ? launch_gemm128<kRaggedM, true>(p, f32, st)
+                                          : launch_gemm128<kRaggedK, false>(p, f32, st),
+                  "mxq_grouped_gemm128");
+}
+
+}  // extern "C"

@@ -51,6 +51,7 @@
 #include "mxq_device.h"
 #include "mxq_groups.h"
 #include "mxq_internal.h"
+#include "mxq_tile.h"
 
 namespace mxq {
 
@@ -58,7 +59,6 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int kThreads = 512;
 constexpr int BM = 256, BN = 256, BK = 64;   // BK: codes (bytes) per MFMA step
@@ -88,9 +88,7 @@ struct Fmt {
   static constexpr int kLanesPerRow = kRowBytes / 16;                    // lanes of one load on one row
   static constexpr int kScaleLoads = kScaleRegion / 256 / 4;             // dword loads per wave (4 waves an operand)
 };
-constexpr int kXcds = 8;                      // XCDs per MI355X; workgroups are dealt round robin
 constexpr int kIlvSteps = 16;                 // interleaved steps per E4M3 stage (8 K values each)
-constexpr int kGroupM = 8;                    // m-tiles per raster group
 
 enum Mode { kDense = 0, kRaggedM = 1, kRaggedK = 2 };
 
@@ -100,16 +98,6 @@ template <int KIND, int I, int J>
 __device__ __forceinline__ v16f mfma_scaled(const v8i& a, const v8i& b, const v16f& c, int sa, int sb) {
   constexpr int f = KIND == kE4M3 ? 0 : 4;
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, f, f, I, sa, J, sb);
-}
-
-// LDS position of 16-byte chunk c of tile row r (8 chunks, 128 bytes per
-// row).  A fragment read has its lanes on consecutive rows at one chunk; the
-// XOR swizzle f(r) = (r & 7) ^ ((r >> 3) & 1) makes any 8 aligned consecutive
-// rows land on 8 distinct 16-byte bank groups of a 128-byte bank row (32
-// banks) and any 16 on 16 distinct groups of a 256-byte one (64 banks), so
-// the read is conflict-free.
-__device__ __forceinline__ int swz(int r, int c) {
-  return r * 128 + ((c ^ ((r & 7) ^ ((r >> 3) & 1))) << 4);
 }
 
 // One operand of one workgroup tile: tile rows [0, rows_valid), which are rows
@@ -156,12 +144,6 @@ struct OperandAddr {
   uint32_t sgroup;       // scale bytes per 128-row group (128 * blocks per row)
   int halves;            // 128-row halves of the tile with a valid row (1 or 2)
 };
-
-// Load j of wave w covers tile rows 8q .. 8q+7 (q = 4w + j), 8 lanes a row.
-// Lane l fills slot l % 8 of its row, which holds chunk slot ^ f(row).
-__device__ __forceinline__ int dma_chunk(int j, int lane) {
-  return (lane & 7) ^ (lane >> 3) ^ (j & 1);
-}
 
 // per-lane code row offsets and the tile's scale base of one operand
 template <int KIND>
@@ -339,36 +321,6 @@ __device__ __forceinline__ void mfma_step(v16f (&acc)[TM][TN], const Frags& f) {
   acc[3][0] = mfma_scaled<KIND, 3, 0>(f.a[3], f.b[0], acc[3][0], sa, sb);
   acc[3][1] = mfma_scaled<KIND, 3, 1>(f.a[3], f.b[1], acc[3][1], sa, sb);
   if constexpr (PRIO) __builtin_amdgcn_s_setprio(0);
-}
-
-// s_waitcnt with vmcnt(n) only (expcnt / lgkmcnt left at their maximum), gfx9 encoding
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-__device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt((15) | (3 << 14) | (0x7 << 4)); }
-
-// Logical tile order: workgroups are dealt to the XCDs round robin, so remap
-// blockIdx so that each XCD walks a contiguous run of the logical order (tiles
-// that share operand panels then share that XCD's L2).
-// (Used where every tile carries the same work; bid < n.)
-__device__ __forceinline__ int xcd_remap(int bid, int n) {
-  const int per = n / kXcds;
-  const int x = bid % kXcds, i = bid / kXcds;
-  if (i >= per) return bid;  // the last partial round stays in place
-  return x * per + i;
-}
-
-// grouped raster: kGroupM m-tiles at a time, m fastest
-__device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int& mt, int& nt) {
-  const int span = kGroupM * tiles_n;
-  const int grp = t / span;
-  const int first = grp * kGroupM;
-  const int gm = min(kGroupM, tiles_m - first);
-  const int r = t - grp * span;
-  mt = first + r % gm;
-  nt = r / gm;
 }
 
 // group bookkeeping of the grouped modes, placed in stage 1 (used only

@@ -111,4 +111,48 @@ __device__ __forceinline__ int find_group(const GroupTable& gt, int G, int32_t u
   return lo;
 }
 
+// Where unit u of the ragged groups lies, when each group is cut into units of
+// UNIT rows from its first one on.
+struct GroupUnit {
+  int g;                // its group
+  int32_t start, size;  // the group's first row and rows (clamped as in group_span)
+  int32_t local;        // the unit within the group
+  int64_t before;       // units of the earlier groups
+};
+// All lanes of a wave call this with one u (no LDS, no barrier; a few hundred
+// cycles for up to 64 groups).  False where u is past the last unit, with
+// out.before all units.  A chunk of 64 groups holds fewer than 2^31 units for UNIT >= 64.
+template <int UNIT>
+__device__ __forceinline__ bool find_group_unit(const int32_t* __restrict__ group_end, int G, int64_t R, int64_t u,
+                                                GroupUnit& out) {
+  static_assert(UNIT >= 64, "the sum of a chunk's units must fit int32");
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    int32_t start = 0, size = 0;
+    if (g0 + lane < G) group_span(group_end, g0 + lane, R, start, size);
+    const int32_t units = (int32_t)(((uint32_t)size + (UNIT - 1)) / UNIT);
+    int32_t upto = units;  // units of the chunk's groups up to this lane's
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int32_t v = __shfl_up(upto, off);
+      if (lane >= off) upto += v;
+    }
+    const uint64_t has = __ballot(u < before + upto);
+    if (has) {
+      const int at = __builtin_ctzll(has);
+      out.g = g0 + at;
+      out.start = __builtin_amdgcn_readlane(start, at);
+      out.size = __builtin_amdgcn_readlane(size, at);
+      const int32_t earlier = __builtin_amdgcn_readlane(upto - units, at);
+      out.before = before + earlier;
+      out.local = (int32_t)(u - out.before);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  out.before = before;
+  return false;
+}
+
 }  // namespace mxq

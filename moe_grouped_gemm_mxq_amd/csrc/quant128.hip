@@ -1,0 +1,393 @@
+// FP8 (E4M3) quantisation with one fp32 scale for every block of 128: blocks of
+// 1 x 128 along the reduction axis (activations, gradients) or of 128 x 128
+// (weights), of a matrix, of its transpose, or of both from one read; the
+// transposed copy may restart its blocks with each group of rows.
+//
+// With amax the largest magnitude of the block (no less than 2^-100, so that
+// scales and their reciprocals stay normal):  scale = amax / 448,
+// code = e4m3(448 x / amax) to nearest even.  The quotient is (7/8 x) / (amax / 512):
+// a bf16 x times 7/8 and amax / 512 are exact, y0 = 7/8 x * r with r the rounded
+// 512 / amax is off by a few units of the last place, and one step
+// y = y0 + (7/8 x - y0 amax / 512) * r gives the correctly rounded quotient, which
+// for bf16 x has the exact quotient's E4M3 rounding (a quotient of an 11-bit and
+// an 8-bit number that is not half way between two codes is at least 2^-14 away).
+// The division would cost about ten instructions an element where this takes four.
+//
+// Both kernels stream and are bound by HBM.
+#include "mxq_device.h"
+#include "mxq_groups.h"
+#include "mxq_host.h"
+#include "mxq_vec.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kB = 128;          // block
+constexpr int kThreads = 256;
+constexpr int kLanes = 16;       // lanes of a row's block, eight elements each
+constexpr float kMaxCode = 448.f;
+constexpr uint32_t kAmaxFloor = 0x0D800000u;  // 2^-100
+constexpr uint32_t kInf = 0x7F800000u;
+
+// Eight consecutive elements as fp32, zero from the n-th on.
+__device__ __forceinline__ void load8(const float* p, int n, float* v) {
+  if (n >= 8) {
+    unpack(load_raw<4, false>(p), v);
+    unpack(load_raw<4, false>(p + 4), v + 4);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < n ? p[j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
+  if (n >= 8) {
+    unpack(load_raw<8, false>(p), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < n ? load_f(p, j) : 0.f;
+  }
+}
+
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// largest of 16 lanes of a DPP row
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, dpp_xor1(v));
+  v = max(v, dpp_xor2(v));
+  v = max(v, dpp_half_mirror(v));
+  return max(v, dpp_mirror(v));
+}
+
+// amax as fp32 bits: magnitudes compare as integers, with NaN above infinity
+__device__ __forceinline__ float amax_of(uint32_t m) { return __uint_as_float(max(m, kAmaxFloor)); }
+
+// one code's quotient: d = amax / 512, r = 1 / d (both rounded to nearest)
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float xs = x * 0.875f;
+  const float y0 = xs * r;
+  const float y = __builtin_fmaf(__builtin_fmaf(-y0, d, xs), r, y0);
+  return __builtin_copysignf(y, x);  // (the step loses a zero's sign)
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+// eight codes of one block's elements; a block with an infinity or a NaN divides
+__device__ __forceinline__ uint2 encode8(const float* x, float amax) {
+  const float d = amax * 0x1p-9f;
+  float y[8];
+  if (__builtin_expect(__float_as_uint(amax) >= kInf, 0)) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = x[j] * 0.875f / d;
+  } else {
+    const float r = 1.f / d;
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = quotient(x[j], d, r);
+  }
+  return make_uint2(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
+}
+
+// Row copy with 1 x 128 blocks.  16 lanes take a block; the workgroup's 16
+// groups take 16 rows, so that their scales, which lie next to each other
+// (scales[block][row]), are written together.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rows_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ldx,
+                                                        int64_t x_stride, uint8_t* __restrict__ q,
+                                                        float* __restrict__ s, int64_t chunks, int per_chunk) {
+  const int64_t Cb = (C + kB - 1) / kB, Cp = Cb * kB;
+  const int64_t rt = blockIdx.x / chunks, chunk = blockIdx.x - rt * chunks;
+  const int64_t row = rt * 16 + threadIdx.x / kLanes;
+  if (row >= R) return;
+  const int c = (threadIdx.x % kLanes) * 8;
+  const T* xr = x + blockIdx.y * x_stride + row * ldx;
+  uint8_t* qr = q + ((int64_t)blockIdx.y * R + row) * Cp;
+  float* sr = s + (int64_t)blockIdx.y * Cb * R + row;
+  const int64_t last = min((chunk + 1) * per_chunk, Cb);
+  for (int64_t b = chunk * per_chunk; b < last; b++) {
+    const int64_t col = b * kB + c;
+    float v[8];
+    load8(xr + col, (int)min<int64_t>(C - col, 8), v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) m = max(m, mag(v[j]));
+    const float amax = amax_of(max16(m));
+    *reinterpret_cast<uint2*>(qr + col) = encode8(v, amax);
+    if (c == 0) sr[b * R] = amax / kMaxCode;
+  }
+}
+
+// One 128 x 128 tile of x: any of the copies from one read.  Thread (i, c) holds
+// rows 8i .. 8i+7 and columns 8c .. 8c+7 of the tile, so a row's block is 16
+// lanes, and a column's codes come in runs of eight, which go through LDS
+// ([column][16 runs], run i of column 8c + j at i ^ c: sixteen lanes with one i
+// write to all banks) into whole 128-byte lines of the transpose.
+template <typename T, bool TILE128, bool ROW, bool COLT, bool GROUPED>
+__global__ __launch_bounds__(kThreads) void tile_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ldx,
+                                                        int64_t x_stride, const int32_t* __restrict__ group_end,
+                                                        int G, int64_t ldq, uint8_t* __restrict__ q_row,
+                                                        float* __restrict__ s_row, uint8_t* __restrict__ q_colT,
+                                                        float* __restrict__ s_colT, int64_t tiles_c) {
+  __shared__ uint2 turned[COLT ? kB * 16 : 1];
+  __shared__ uint32_t part[4][kB];
+  const int t = threadIdx.x, wave = t >> 6;
+  const int c = t & 15, i = t >> 4;
+  const int64_t rt = blockIdx.x / tiles_c, ct = blockIdx.x - rt * tiles_c;
+  const int64_t Cb = tiles_c, Cp = Cb * kB;
+  const int64_t Rb = (R + kB - 1) / kB;
+  int64_t row0 = rt * kB, out0 = rt * kB;  // first row, and its place along the transpose's rows
+  int64_t rows = R - row0;
+  bool turn = COLT;
+  if constexpr (GROUPED) {
+    GroupUnit u;
+    if (find_group_unit<kB>(group_end, G, R, rt, u)) {
+      row0 = u.start + (int64_t)u.local * kB;
+      rows = u.size - (int64_t)u.local * kB;
+      out0 = (u.before + u.local) * kB;
+      turn = out0 + kB <= ldq;
+    } else {  // rows past the last group: in the row copy alone
+      if constexpr (!ROW) return;
+      turn = false;
+      row0 = min(max((int64_t)group_end[G - 1], (int64_t)0), R) + (rt - u.before) * kB;
+      rows = R - row0;
+      if (rows <= 0) return;
+    }
+  }
+  const int nrows = (int)min<int64_t>(rows, kB);
+  const int64_t col0 = ct * kB;
+  const int ncols = (int)min<int64_t>(C - col0, kB);
+  x += (int64_t)blockIdx.y * x_stride;
+
+  float v[8][8];
+  const int n = min(max(ncols - 8 * c, 0), 8);
+  const T* xp = x + row0 * ldx + col0 + 8 * c;
+#pragma unroll
+  for (int p = 0; p < 8; p++) load8(xp + (int64_t)(8 * i + p) * ldx, 8 * i + p < nrows ? n : 0, v[p]);
+
+  uint32_t cm[8];  // columns' magnitudes
+#pragma unroll
+  for (int j = 0; j < 8; j++) cm[j] = 0;
+  uint32_t rm[8];
+#pragma unroll
+  for (int p = 0; p < 8; p++) {
+    rm[p] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      rm[p] = max(rm[p], mag(v[p][j]));
+      cm[j] = max(cm[j], mag(v[p][j]));
+    }
+  }
+  float tile_amax = 0.f;
+  if constexpr (TILE128) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < 8; p++) m = max(m, rm[p]);
+    m = max16(m);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if ((t & 63) == 0) part[wave][0] = m;
+    __syncthreads();
+    tile_amax = amax_of(max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0])));
+    if (t == 0) {
+      if constexpr (ROW) s_row[((int64_t)blockIdx.y * Cb + ct) * Rb + rt] = tile_amax / kMaxCode;
+      if constexpr (COLT) s_colT[((int64_t)blockIdx.y * Rb + rt) * Cb + ct] = tile_amax / kMaxCode;
+    }
+  } else if constexpr (COLT) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 16));
+      cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32));
+    }
+    if ((t & 63) < 16) {
+      *reinterpret_cast<uint4*>(&part[wave][8 * c]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+      *reinterpret_cast<uint4*>(&part[wave][8 * c + 4]) = make_uint4(cm[4], cm[5], cm[6], cm[7]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      cm[j] = max(max(part[0][8 * c + j], part[1][8 * c + j]), max(part[2][8 * c + j], part[3][8 * c + j]));
+  }
+
+  if constexpr (ROW) {
+    uint8_t* qp = q_row + ((int64_t)blockIdx.y * R + row0) * Cp + col0 + 8 * c;
+#pragma unroll
+    for (int p = 0; p < 8; p++) {
+      const int r = 8 * i + p;
+      const float amax = TILE128 ? tile_amax : amax_of(max16(rm[p]));
+      const uint2 code = encode8(v[p], amax);
+      if constexpr (TILE128 && COLT) {  // the same codes both ways
+        *reinterpret_cast<uint2*>(&v[p][0]) = code;
+      }
+      if (r < nrows) {
+        *reinterpret_cast<uint2*>(qp + (int64_t)r * Cp) = code;
+        if (!TILE128 && c == 0) s_row[((int64_t)blockIdx.y * Cb + ct) * R + row0 + r] = amax / kMaxCode;
+      }
+    }
+  }
+  if constexpr (COLT) {
+    const int64_t Rp = GROUPED ? ldq : Rb * kB;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      uint2 code;
+      if constexpr (TILE128 && ROW) {  // byte j of the rows' codes
+        uint32_t w[8];
+#pragma unroll
+        for (int p = 0; p < 8; p++) w[p] = __float_as_uint(v[p][j >> 2]);
+        const uint32_t sel = (uint32_t)(j & 3);
+        auto four = [&](uint32_t a, uint32_t b, uint32_t e, uint32_t f) {
+          const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0000u | sel | ((4u + sel) << 8));
+          const uint32_t hi = __builtin_amdgcn_perm(f, e, 0x0c0c0000u | sel | ((4u + sel) << 8));
+          return lo | (hi << 16);
+        };
+        code = make_uint2(four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7]));
+      } else {
+        float col[8];
+#pragma unroll
+        for (int p = 0; p < 8; p++) col[p] = v[p][j];
+        code = encode8(col, TILE128 ? tile_amax : amax_of(cm[j]));
+      }
+      turned[(8 * c + j) * 16 + (i ^ c)] = code;
+    }
+    __syncthreads();
+    if (!turn) return;
+    uint8_t* qp = q_colT + (int64_t)blockIdx.y * C * Rp + out0;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int col = 32 * k + (t >> 3), pair = t & 7;
+      const int cc = col >> 3;
+      const uint2 a = turned[col * 16 + ((2 * pair) ^ cc)], b = turned[col * 16 + ((2 * pair + 1) ^ cc)];
+      if (col < ncols)
+        *reinterpret_cast<uint4*>(qp + (col0 + col) * Rp + 16 * pair) = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    if constexpr (!TILE128) {
+      if (t < ncols) {
+        const uint32_t m = max(max(part[0][t], part[1][t]), max(part[2][t], part[3][t]));
+        s_colT[((int64_t)blockIdx.y * (Rp / kB) + out0 / kB) * C + col0 + t] = amax_of(m) / kMaxCode;
+      }
+    }
+  }
+}
+
+struct Args {
+  int64_t batch, R, C, ldx, x_stride;
+  const int32_t* group_end;
+  int G;
+  int64_t ldq;
+  uint8_t* q_row;
+  float* s_row;
+  uint8_t* q_colT;
+  float* s_colT;
+};
+
+template <typename T, bool TILE128, bool ROW, bool COLT>
+void launch_tile(const T* x, const Args& a, dim3 grid, int64_t tiles_c, hipStream_t st) {
+  if constexpr (!TILE128 && COLT) {
+    if (a.group_end) {
+      tile_kernel<T, TILE128, ROW, COLT, true><<<grid, kThreads, 0, st>>>(x, a.R, a.C, a.ldx, a.x_stride, a.group_end, a.G,
+                                                                          a.ldq, a.q_row, a.s_row, a.q_colT, a.s_colT, tiles_c);
+      return;
+    }
+  }
+  tile_kernel<T, TILE128, ROW, COLT, false><<<grid, kThreads, 0, st>>>(x, a.R, a.C, a.ldx, a.x_stride, nullptr, 0, 0,
+                                                                       a.q_row, a.s_row, a.q_colT, a.s_colT, tiles_c);
+}
+
+template <typename T>
+hipError_t launch(const T* x, int tile, bool row, bool col, const Args& a, hipStream_t st) {
+  const int64_t Cb = (a.C + kB - 1) / kB;
+  if (tile == 1 && !col) {
+    const int64_t tiles_r = (a.R + 15) / 16;
+    int per_chunk = 4;
+    const int64_t chunks = (Cb + per_chunk - 1) / per_chunk;
+    if (tiles_r * chunks > INT32_MAX) return hipErrorInvalidValue;
+    rows_kernel<T><<<dim3((unsigned)(tiles_r * chunks), (unsigned)a.batch), kThreads, 0, st>>>(
+        x, a.R, a.C, a.ldx, a.x_stride, a.q_row, a.s_row, chunks, per_chunk);
+    return hipGetLastError();
+  }
+  const int64_t tiles = ((a.R + kB - 1) / kB + (a.group_end ? a.G + 1 : 0)) * Cb;
+  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)tiles, (unsigned)a.batch);
+  if (tile == 1) {
+    if (row)
+      launch_tile<T, false, true, true>(x, a, grid, Cb, st);
+    else
+      launch_tile<T, false, false, true>(x, a, grid, Cb, st);
+  } else if (row && col) {
+    launch_tile<T, true, true, true>(x, a, grid, Cb, st);
+  } else if (row) {
+    launch_tile<T, true, true, false>(x, a, grid, Cb, st);
+  } else {
+    launch_tile<T, true, false, true>(x, a, grid, Cb, st);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_any(const void* x, mxq_dtype dt, int tile, bool row, bool col, const Args& a, hipStream_t st) {
+  if (a.R == 0) return hipSuccess;
+  if (dt == MXQ_DT_F32) return launch(static_cast<const float*>(x), tile, row, col, a, st);
+  return launch(static_cast<const uint16_t*>(x), tile, row, col, a, st);
+}
+
+mxq_status check(const char* who, const void* x, mxq_dtype dt, int64_t R, int64_t C, int64_t ldx, int axis_mask,
+                 const Args& a) {
+  MXQ_REQUIRE(dt == MXQ_DT_F32 || dt == MXQ_DT_BF16, "%s: unknown type %d", who, (int)dt);
+  MXQ_REQUIRE(R >= 0 && R <= INT32_MAX, "%s: the rows must be in [0, 2^31) (got %lld)", who, (long long)R);
+  MXQ_REQUIRE(C >= 1 && C <= INT32_MAX - kB, "%s: the columns must be in [1, 2^31 - 128) (got %lld)", who, (long long)C);
+  MXQ_REQUIRE(ldx >= C, "%s: ldx (%lld) < C (%lld)", who, (long long)ldx, (long long)C);
+  MXQ_REQUIRE(axis_mask >= 1 && axis_mask <= 3, "%s: axis_mask must be ROW, COLT or ROW|COLT", who);
+  if (R == 0 || a.batch == 0) return MXQ_OK;
+  const bool row = axis_mask & MXQ_AXIS_ROW, col = axis_mask & MXQ_AXIS_COLT;
+  MXQ_REQUIRE(x != nullptr, "%s: x is NULL", who);
+  MXQ_REQUIRE(!row || (a.q_row && a.s_row), "%s: row outputs are NULL", who);
+  MXQ_REQUIRE(!col || (a.q_colT && a.s_colT), "%s: colT outputs are NULL", who);
+  MXQ_REQUIRE(aligned_to(x, dt == MXQ_DT_F32 ? 4 : 2), "%s: x must be aligned to its elements", who);
+  MXQ_REQUIRE((!row || aligned_to(a.q_row, 16)) && (!col || aligned_to(a.q_colT, 16)),
+              "%s: code outputs must be 16-byte aligned", who);
+  MXQ_REQUIRE((!row || aligned_to(a.s_row, 4)) && (!col || aligned_to(a.s_colT, 4)),
+              "%s: scale outputs must be 4-byte aligned", who);
+  return MXQ_OK;
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" {
+
+int64_t mxq_grouped128_cols_max(int64_t T, int32_t G) {
+  if (T < 0 || G < 0 || T > INT32_MAX) return 0;
+  return ((T + 127 * (int64_t)G + kB - 1) / kB | 1) * kB;
+}
+
+mxq_status mxq_quantize128(const void* x, mxq_dtype dt, int64_t batch, int64_t R, int64_t C, int64_t ldx,
+                           int64_t x_stride, int tile, int axis_mask, uint8_t* q_row, float* s_row, uint8_t* q_colT,
+                           float* s_colT, hipStream_t st) {
+  const Args a{batch, R, C, ldx, x_stride, nullptr, 0, 0, q_row, s_row, q_colT, s_colT};
+  MXQ_REQUIRE(tile == 1 || tile == 128, "mxq_quantize128: tile must be 1 or 128 (got %d)", tile);
+  MXQ_REQUIRE(batch >= 0 && batch <= 65535, "mxq_quantize128: batch must be in [0, 65535] (got %lld)", (long long)batch);
+  const mxq_status s = check("mxq_quantize128", x, dt, R, C, ldx, axis_mask, a);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE(batch <= 1 || R == 0 || x_stride >= (R - 1) * ldx + C,
+              "mxq_quantize128: x_stride (%lld) smaller than one matrix", (long long)x_stride);
+  MXQ_REQUIRE_DEVICE();
+  if (batch == 0) return ok();
+  return launched(launch_any(x, dt, tile, axis_mask & MXQ_AXIS_ROW, axis_mask & MXQ_AXIS_COLT, a, st), "mxq_quantize128");
+}
+
+mxq_status mxq_quantize128_grouped(const void* x, mxq_dtype dt, int64_t T, int64_t C, int64_t ldx,
+                                   const int32_t* group_end, int32_t G, int64_t ldq, int axis_mask, uint8_t* q_row,
+                                   float* s_row, uint8_t* q_colT, float* s_colT, hipStream_t st) {
+  const bool col = axis_mask & MXQ_AXIS_COLT;
+  const Args a{1, T, C, ldx, 0, col ? group_end : nullptr, G, ldq, q_row, s_row, q_colT, s_colT};
+  const mxq_status s = check("mxq_quantize128_grouped", x, dt, T, C, ldx, axis_mask, a);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE(group_end != nullptr && aligned_to(group_end, 4), "mxq_quantize128_grouped: group_end must be 4-byte aligned, not NULL");
+  MXQ_REQUIRE(G >= 1 && G <= MXQ_MAX_GROUPS, "mxq_quantize128_grouped: G must be in [1, %d] (got %d)", MXQ_MAX_GROUPS, G);
+  MXQ_REQUIRE(!col || (ldq >= kB && ldq % kB == 0), "mxq_quantize128_grouped: ldq must be a positive multiple of 128");
+  MXQ_REQUIRE_DEVICE();
+  return launched(launch_any(x, dt, 1, axis_mask & MXQ_AXIS_ROW, col, a, st), "mxq_quantize128_grouped");
+}
+
+}  // extern "C"

@@ -49,6 +49,7 @@ MXQ_SCORE_SIGMOID = 1
 MXQ_ADAMW_F32 = 0
 MXQ_ADAMW_MXFP8 = 1
 BLOCK = 32
+BLOCK128 = 128  # elements per block of the operands with fp32 scales
 MAX_GROUPS = 1024
 MAX_TOPK = 32  # MXQ_MAX_TOPK
 MAX_ROW_BYTES = 1 << 23  # MXQ_GEMM_MAX_ROW_BYTES: GEMM code rows (K, or K/2 for E2M1) stay below this
@@ -59,6 +60,7 @@ EXPORTED = [
     "mxq_ste_backward_fp4", "mxq_fp4_scale_threshold", "mxq_quantize_fp4", "mxq_gemm", "mxq_grouped_gemm",
     "mxq_validate_group_end", "mxq_quantize_fp4_grouped", "mxq_expert_order_workspace", "mxq_route",
     "mxq_expert_order", "mxq_route_backward", "mxq_combine", "mxq_combine_backward", "mxq_adamw",
+    "mxq_grouped128_cols_max", "mxq_quantize128", "mxq_quantize128_grouped", "mxq_gemm128", "mxq_grouped_gemm128",
 ]
 
 
@@ -115,6 +117,11 @@ def _load(path: str = LIB_PATH):
         "mxq_combine": ([P, I, I64, I64, P, P, I64, I32, I64, P, I, I64, P], I),
         "mxq_combine_backward": ([P, I, I64, P, I, I64, P, P, I64, I32, I64, I64, P, I, I64, P, P], I),
         "mxq_adamw": ([P, I32, I, I, I, P, P, P], I),
+        "mxq_grouped128_cols_max": ([I64, I32], I64),
+        "mxq_quantize128": ([P, I, I64, I64, I64, I64, I64, I, I, P, P, P, P, P], I),
+        "mxq_quantize128_grouped": ([P, I, I64, I64, I64, P, I32, I64, I, P, P, P, P, P], I),
+        "mxq_gemm128": ([P, P, P, P, I, P, I, I64, I64, I64, I64, P], I),
+        "mxq_grouped_gemm128": ([I, P, P, P, P, P, I, I64, I64, I64, P, I32, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -123,7 +130,7 @@ def _load(path: str = LIB_PATH):
     return lib
 
 
-ABI_VERSION = 8  # MXQ_ABI_VERSION of include/mxq.h this binding is written against
+ABI_VERSION = 9  # MXQ_ABI_VERSION of include/mxq.h this binding is written against
 
 _lib = _load()
 if _lib.mxq_abi_version() != ABI_VERSION:
@@ -592,6 +599,113 @@ def mxq_adamw(tensors, n_tensors, param_dt, grad_dt, fmt, cfg, control=None, str
                           _stream(stream, device)), "mxq_adamw")
 
 
+# ---- FP8 with an fp32 scale for each block of 128
+def ceil128(v: int) -> int:
+    return (v + BLOCK128 - 1) // BLOCK128 * BLOCK128
+
+
+def _here(t, name):
+    """The entry points work on the current device's memory and streams."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _copy128_shapes(R, C, tile, lead=(), ldq=None):
+    """Shapes of the row copy's and the colT copy's codes and scales."""
+    Rp = ceil128(R) if ldq is None else ldq
+    return {"q_row": (*lead, R, ceil128(C)), "s_row": (*lead, ceil128(C) // BLOCK128, -(-R // tile)),
+            "q_colT": (*lead, C, Rp), "s_colT": (*lead, Rp // BLOCK128, -(-C // tile))}
+
+
+def _need_copies128(axis_mask, shapes, copies):
+    for bit, names in ((MXQ_AXIS_ROW, ("q_row", "s_row")), (MXQ_AXIS_COLT, ("q_colT", "s_colT"))):
+        for name in names:
+            if axis_mask & bit:
+                _need_array(copies[name], name, torch.uint8 if name[0] == "q" else torch.float32, shapes[name])
+
+
+def mxq_grouped128_cols_max(T: int, G: int) -> int:
+    return _lib.mxq_grouped128_cols_max(T, G)
+
+
+def mxq_quantize128(x, tile, axis_mask, q_row=None, s_row=None, q_colT=None, s_colT=None, stream=None):
+    """x fp32 or bf16 [R][C] or [batch][R][C] (unit column stride) in blocks of tile x 128: q_row uint8 [R][ceil128(C)],
+    s_row fp32 [C / 128][R / tile], q_colT [C][ceil128(R)], s_colT [R / 128][C / tile], each under [batch] for three dims."""
+    if isinstance(x, torch.Tensor) and x.dim() == 3:
+        nb, R, C = x.shape
+        batch_stride = x.stride(0)
+        # (the rows of one matrix where there is none)
+        dt, _, _, ldx = _matrix(x[0] if nb else x.new_empty((R, C)), "x")
+        lead = (nb,)
+    else:
+        dt, R, C, ldx = _matrix(x, "x")
+        nb, batch_stride, lead = 1, 0, ()
+    if tile not in (1, 128):
+        raise ValueError(f"tile must be 1 or 128, got {tile}")
+    _here(x, "x")
+    _need_copies128(axis_mask, _copy128_shapes(R, C, tile, lead),
+                    {"q_row": q_row, "s_row": s_row, "q_colT": q_colT, "s_colT": s_colT})
+    _check(_lib.mxq_quantize128(x.data_ptr(), dt, nb, R, C, ldx, batch_stride, tile, axis_mask, _raw(q_row), _raw(s_row),
+                                _raw(q_colT), _raw(s_colT), _stream(stream, x.device)), "mxq_quantize128")
+
+
+def mxq_quantize128_grouped(x, group_end, ldq, axis_mask, q_row=None, s_row=None, q_colT=None, s_colT=None, stream=None):
+    """x fp32 or bf16 [T][C], rows in groups: q_colT uint8 [C][ldq], s_colT fp32 [ldq / 128][C], the blocks restarting with
+    each group; q_row, s_row as mxq_quantize128's of all rows."""
+    dt, T, C, ldx = _matrix(x, "x")
+    _need(group_end, torch.int32, "group_end", 1)
+    _need_array(group_end, "group_end", torch.int32, (group_end.numel(),))
+    _here(x, "x")
+    _need_copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq),
+                    {"q_row": q_row, "s_row": s_row, "q_colT": q_colT, "s_colT": s_colT})
+    _check(_lib.mxq_quantize128_grouped(x.data_ptr(), dt, T, C, ldx, group_end.data_ptr(), group_end.numel(), ldq or 0, axis_mask,
+                                        _raw(q_row), _raw(s_row), _raw(q_colT), _raw(s_colT), _stream(stream, x.device)),
+           "mxq_quantize128_grouped")
+
+
+def _need_operand128(codes, scales, name, lead=(), tiles=(1,)):
+    """(rows, K, tile) of an operand's codes [lead.., rows, K] and scales [lead.., K / 128, rows / tile], tile one of `tiles`."""
+    _need(codes, torch.uint8, name)
+    if codes.dim() != 2 + len(lead) or tuple(codes.shape[:-2]) != lead or not codes.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {(*lead, 'rows', 'K')}, got {tuple(codes.shape)}")
+    rows, K = codes.shape[-2:]
+    _need(scales, torch.float32, "s" + name)
+    for tile in tiles:
+        if scales.is_contiguous() and tuple(scales.shape) == (*lead, K // BLOCK128, -(-rows // tile)):
+            return rows, K, tile
+    want = " or ".join(str((*lead, K // BLOCK128, -(-rows // tile))) for tile in tiles)
+    raise ValueError(f"s{name} must be a contiguous tensor of shape {want}, got {tuple(scales.shape)}")
+
+
+def mxq_gemm128(A, sA, B, sB, C, stream=None):
+    """A uint8 [M][K], sA fp32 [K / 128][M]; B [N][K], sB [K / 128][N] or [K / 128][ceil(N / 128)] -> C fp32 or bf16 [M][N]."""
+    M, K, _ = _need_operand128(A, sA, "A")
+    N, KB, tile = _need_operand128(B, sB, "B", tiles=(128, 1))
+    cdt, rows, cols, ldc = _matrix(C, "C")
+    if KB != K or (rows, cols) != (M, N):
+        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    _here(A, "A")
+    _check(_lib.mxq_gemm128(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), tile, C.data_ptr(), cdt, M, N, K, ldc,
+                            _stream(stream, A.device)), "mxq_gemm128")
+
+
+def mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end, stream=None):
+    """RAGGED_M: A [M][K], B [G][N][K] in 128 x 128 blocks, C [M][N].  RAGGED_K: A [M][K], B [N][K], C [G][M][N].  C fp32 or
+    bf16."""
+    _need(group_end, torch.int32, "group_end", 1)
+    G = group_end.numel()
+    _need_array(group_end, "group_end", torch.int32, (G,))
+    M, K, _ = _need_operand128(A, sA, "A")
+    ragged_m = mode == MXQ_GG_RAGGED_M
+    N, KB, _ = _need_operand128(B, sB, "B", (G,), (128,)) if ragged_m else _need_operand128(B, sB, "B")
+    _need(C, C.dtype if C.dtype in _DTYPES else torch.float32, "C")
+    if KB != K or tuple(C.shape) != ((M, N) if ragged_m else (G, M, N)) or not C.is_contiguous():
+        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    _here(A, "A")
+    _check(_lib.mxq_grouped_gemm128(mode, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), _DTYPES[C.dtype],
+                                    M, N, K, group_end.data_ptr(), G, _stream(stream, A.device)), "mxq_grouped_gemm128")
+
+
 # ------------------------------------------------------------------ allocate-and-call helpers
 def _on(stream, device):
     """Context in which `stream` is the current one, so that what is allocated belongs to it.  A helper that is given a
@@ -836,6 +950,63 @@ def dispatch(x, slot, rows, dtype=None, stream=None):
     """Tokens x [T][H] in expert order: row slot[t][k] of the result is x[t], and rows that no slot names (those past
     the last group end) are not written.  Its gradient is combine without weights."""
     return combine_backward(x, slot, rows, dtype=dtype, stream=stream)[0]
+
+
+def _copies128(axis_mask, shapes, device, out):
+    """The requested copies, from `out` where it has them."""
+    names = (("q_row", "s_row") if axis_mask & MXQ_AXIS_ROW else ()) + (("q_colT", "s_colT") if axis_mask & MXQ_AXIS_COLT else ())
+    if out is not None:
+        return {n: out[n] for n in names}
+    return {n: torch.empty(shapes[n], dtype=torch.uint8 if n[0] == "q" else torch.float32, device=device) for n in names}
+
+
+def quantize128(x, axis_mask=MXQ_AXIS_ROW, tile=1, out=None, stream=None):
+    """Blocks of tile x 128 (tile 1: activations and gradients, 128: weights) of x [R][C] or [batch][R][C], fp32 or bf16: a dict
+    with 'q_row', 's_row' and/or 'q_colT', 's_colT' (see mxq_quantize128).  out: a dict of such buffers to write to."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize128(x, axis_mask, tile, out)
+    *lead, R, C = x.shape
+    got = _copies128(axis_mask, _copy128_shapes(R, C, tile, tuple(lead)) if out is None else None, x.device, out)
+    mxq_quantize128(x, tile, axis_mask, **got)
+    return got
+
+
+def quantize128_grouped(x, group_end, axis_mask=MXQ_AXIS_COLT, ldq=None, out=None, stream=None):
+    """Blocks of 1 x 128 of x [T][C] whose rows are in groups (see mxq_quantize128_grouped): a dict with the copies, as
+    quantize128's, and "ldq"."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize128_grouped(x, group_end, axis_mask, ldq, out)
+    T, C = x.shape
+    if ldq is None:
+        ldq = out["q_colT"].shape[1] if out is not None and "q_colT" in out else mxq_grouped128_cols_max(T, group_end.numel())
+    got = _copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq) if out is None else None, x.device, out)
+    mxq_quantize128_grouped(x, group_end, ldq, axis_mask, **got)
+    return {**got, "ldq": ldq}
+
+
+def gemm128(A, sA, B, sB, dtype=torch.bfloat16, stream=None):
+    """A B^T of operands with fp32 scales for blocks of 128 (see mxq_gemm128): [M][N] of `dtype`."""
+    if stream is not None:
+        with _on(stream, A.device):
+            return gemm128(A, sA, B, sB, dtype)
+    _type_code(dtype)
+    C = torch.empty((A.shape[0], B.shape[0]), dtype=dtype, device=A.device)
+    mxq_gemm128(A, sA, B, sB, C)
+    return C
+
+
+def grouped_gemm128(mode, A, sA, B, sB, group_end, dtype=torch.bfloat16, stream=None):
+    """Grouped products (see mxq_grouped_gemm128): [M][N] or [G][M][N] of `dtype`."""
+    if stream is not None:
+        with _on(stream, A.device):
+            return grouped_gemm128(mode, A, sA, B, sB, group_end, dtype)
+    _type_code(dtype)
+    shape = (A.shape[0], B.shape[1]) if mode == MXQ_GG_RAGGED_M else (group_end.numel(), A.shape[0], B.shape[0])
+    C = torch.empty(shape, dtype=dtype, device=A.device)
+    mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end)
+    return C
 
 
 def adamw_state(param, fmt=MXQ_ADAMW_MXFP8):
