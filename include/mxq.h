@@ -590,6 +590,54 @@ mxq_status mxq_grouped_gemm128(mxq_gg_mode mode, const uint8_t* A, const float* 
                                void* C, mxq_dtype cdt, int64_t M, int64_t N, int64_t K, const int32_t* group_end,
                                int32_t G, hipStream_t st);
 
+/* ------------------------------------------------------------------ orthogonalised updates (Muon)
+ * Newton-Schulz iterations on matrices u [R][C]:
+ *   X = u / (|u|_F + eps), then `steps` times X = a X + (b A + c A^2) X, A = X X^T
+ * (the same for u and its transpose).  a s + b s^3 + c s^5 must stay within 1.25
+ * in magnitude for s in [0, 1.25]; 3.4445, -4.7750, 2.0315 and 5 steps bring singular
+ * values from 1/500 of the norm up to between 0.68 and 1.21.
+ * The products are taken on fp16 operands with fp32 sums, X being kept in 22 bits:
+ * a bf16 result is within about 2^-9 of itself (2-norm) before it is rounded; for
+ * an fp32 one every product is taken in three (about 2^-16 with the default
+ * coefficients).  A norm far below eps loses bits (u/eps is then small in fp16).
+ * A matrix with a NaN or an infinity becomes NaN. */
+#define MXQ_MAX_NS_STEPS 32
+typedef struct {
+    double a, b, c; /* each at most 64 in magnitude */
+    double eps;     /* >= 0 */
+    int32_t steps;  /* 1 .. MXQ_MAX_NS_STEPS */
+} mxq_newton_schulz;
+
+/* Workspace bytes of mxq_orthogonalize with a result, or mxq_muon with parameters,
+ * of type odt.  Pure host arithmetic; 0 for arguments those would refuse.  It needs
+ * no initialisation and holds nothing between calls. */
+int64_t mxq_orthogonalize_workspace(int64_t batch, int64_t R, int64_t C, mxq_dtype odt);
+
+/* x [batch][R][C] of type dt, contiguous -> out [batch][R][C] of type odt, each
+ * matrix by itself.  0 <= batch <= 65535; 1 <= R, C <= 2^20.  workspace 256-byte
+ * aligned. */
+mxq_status mxq_orthogonalize(const void* x, mxq_dtype dt, int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz* cfg,
+                             void* out, mxq_dtype odt, void* workspace, int64_t workspace_bytes, hipStream_t st);
+
+typedef struct {
+    mxq_newton_schulz ns;
+    double lr, momentum, weight_decay; /* 0 <= momentum < 1 */
+    double scale;                      /* times the orthogonalised update */
+    double grad_scale;                 /* multiplies every gradient */
+    int32_t nesterov;                  /* 0 or 1 */
+} mxq_muon_config;
+
+/* One Muon step of `batch` matrices [R][C], contiguous:
+ *   g' = grad_scale g;  m' = momentum m + (1 - momentum) g'
+ *   u = (1 - momentum) g' + momentum m' (nesterov), or m'
+ *   p' = p (1 - lr wd) - lr scale orthogonalised(u)
+ * param fp32 or bf16 (rounded to nearest), grad fp32 or bf16, m fp32; copy: bf16,
+ * gets p' too, or NULL.  control: as for mxq_adamw, its lr and grad_scale replace
+ * the config's; where one of the two is not finite, nothing changes. */
+mxq_status mxq_muon(void* param, mxq_dtype param_dt, const void* grad, mxq_dtype grad_dt, float* m, uint16_t* copy,
+                    int64_t batch, int64_t R, int64_t C, const mxq_muon_config* cfg, const mxq_adamw_control* control,
+                    void* workspace, int64_t workspace_bytes, hipStream_t st);
+
 #ifdef __cplusplus
 }
 #endif

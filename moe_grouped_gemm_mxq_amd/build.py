@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxq.so")
 SOURCES = ["mxq_api.hip", "quant_mxfp8.hip", "qdq_mxfp4.hip", "gemm_mxfp8.hip", "route.hip", "combine.hip",
-           "adamw.hip", "quant128.hip", "gemm128.hip"]
+           "adamw.hip", "quant128.hip", "gemm128.hip", "muon.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,628 @@
+// Orthogonalised updates of weight matrices: Newton-Schulz iterations
+//   X <- u / (|u|_F + eps),   X <- a X + (b A + c A^2) X  with  A = X X^T,
+// and the Muon step around them (momentum, decayed weights).
+//
+// X is the matrix or its transpose, so that A is the smaller of the two Gram
+// matrices: lo x lo, X lo x hi.  An iteration is three products on fp16
+// operands with fp32 sums:
+//   gram    A = X X^T, and square  B = b A + c A^2 + (a - e) I: symmetric, so only
+//           the tiles on and above the diagonal are computed and each is stored
+//           twice;
+//   update  X' = e X + B X, from rows of B and of X's transpose, stored both ways
+//           (each product reads both operands along their rows).
+// Splitting a into e and a - e changes nothing but the rounding: e = a while the
+// iteration grows X, and less in the last two, where B is near its diagonal.
+//
+// Precision.  The iteration multiplies small singular values by up to a = 3.4
+// each time, and rounding errors in their directions with them, so X itself is
+// kept in two fp16 numbers (22 bits).  The operands of the products are fp16: its
+// 11 bits put the result within about 1e-3 of itself (2-norm), under bf16's own
+// rounding, where bf16 operands would be off by 1e-2 to 2e-1 (gradients of low
+// rank).  Results kept in fp32 take each product three times, high x high, high
+// x low and low x high, within 1e-5.
+// fp16's range is kept by powers of two: X is stored times S = 2^s, about the
+// root of lo x hi (its norm is at most 1 at the start and its singular values at
+// most 1.25 throughout), A times 2^14, B times a power that its coefficients allow.
+#include <cmath>
+
+#include "mxq_device.h"
+#include "mxq_host.h"
+#include "mxq_internal.h"
+#include "mxq_tile.h"
+#include "mxq_vec.h"
+
+namespace mxq {
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+
+constexpr int kStageK = 64;     // fp16 elements of a tile row in a stage (128 bytes)
+constexpr float kScaleA = 16384.f;
+constexpr int kMaxSide = 1 << 20;
+constexpr int kThreads = 256;
+constexpr int kMaxParts = 256;  // partial sums of squares of a matrix
+
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// Where a matrix's operands lie.  lo arrays hold what fp16 leaves of hi ones.
+struct Space {
+  int64_t lo, hi, Lp, Hp;  // sides, and rounded up to 64 (zeros there)
+  _Float16 *x, *xl;        // [batch][Lp][Hp]
+  _Float16 *t, *tl;        // [batch][Hp][Lp], this iteration's
+  _Float16 *t2, *tl2;      // and the next one's
+  _Float16 *a, *al, *b, *bl;  // [batch][Lp][Lp]
+  double* parts;           // [batch][kMaxParts]
+};
+
+// total bytes; fills sp where base is given
+int64_t lay_out(Space* sp, uint8_t* base, int64_t batch, int64_t R, int64_t C, bool split) {
+  const int64_t lo = R < C ? R : C, hi = R < C ? C : R;
+  const int64_t Lp = up64(lo), Hp = up64(hi);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return base ? base + here : nullptr;
+  };
+  auto half = [&](int64_t n, bool used) { return used ? reinterpret_cast<_Float16*>(take(batch * n * 2)) : nullptr; };
+  Space s;
+  s.lo = lo, s.hi = hi, s.Lp = Lp, s.Hp = Hp;
+  s.x = half(Lp * Hp, true), s.xl = half(Lp * Hp, true);
+  s.t = half(Lp * Hp, true), s.tl = half(Lp * Hp, split);
+  s.t2 = half(Lp * Hp, true), s.tl2 = half(Lp * Hp, split);
+  s.a = half(Lp * Lp, true), s.al = half(Lp * Lp, split);
+  s.b = half(Lp * Lp, true), s.bl = half(Lp * Lp, split);
+  s.parts = reinterpret_cast<double*>(take(batch * kMaxParts * 8));
+  if (sp) *sp = s;
+  return at;
+}
+
+// What an update's matrix is made of: the momentum's combination with the
+// gradient, or the matrix given.
+struct Source {
+  const void* grad;
+  float* m;          // fp32 [batch][n] or null: the update is the gradient itself
+  int64_t n;         // elements of a matrix
+  float beta, keep;  // m' = beta m + keep g
+  float grad_scale;
+  int nesterov;
+  const mxq_adamw_control* control;
+};
+
+// learning rate and gradient scale of this step; false: skip it
+__device__ __forceinline__ bool step_of(const mxq_adamw_control* control, float& lr, float& grad_scale) {
+  if (control) {
+    lr = control->lr;
+    grad_scale = control->grad_scale;
+  }
+  return fabsf(lr) < __builtin_inff() && fabsf(grad_scale) < __builtin_inff();
+}
+
+// W elements of the momentum's update and of u, from W gradients; m advances where FIRST
+template <typename G, bool MOMENTUM, bool FIRST, int W>
+__device__ __forceinline__ void update_of(const G* grad, float* m, const Source& s, float scale, float* u) {
+  Raw<G, W> g = load_raw<W, false>(grad);
+  float gf[W];
+  unpack(g, gf);
+  if constexpr (!MOMENTUM) {
+#pragma unroll
+    for (int j = 0; j < W; j++) u[j] = gf[j];
+    return;
+  }
+  float mf[W];
+  unpack(load_raw<W, false>(m), mf);
+#pragma unroll
+  for (int j = 0; j < W; j++) {
+    const float gj = gf[j] * scale;
+    if constexpr (FIRST) mf[j] = __builtin_fmaf(s.beta, mf[j], s.keep * gj);
+    u[j] = s.nesterov ? __builtin_fmaf(s.beta, mf[j], s.keep * gj) : mf[j];
+  }
+  if constexpr (FIRST) store_vec<W, false>(m, mf);
+}
+
+// Momentum, and the sums of squares of u: one partial sum a workgroup, in 64 bits
+// (fp32 squares of gradients below 2^-63 or above 2^63 would leave its range).
+template <typename G, bool MOMENTUM>
+__global__ __launch_bounds__(kThreads) void momentum_kernel(Source s, double* __restrict__ parts) {
+  float lr = 0.f, scale = s.grad_scale;
+  if (!step_of(s.control, lr, scale)) return;
+  const int64_t base = blockIdx.y * s.n;
+  const G* g = static_cast<const G*>(s.grad) + base;
+  float* m = MOMENTUM ? s.m + base : nullptr;
+  double sum = 0.0;
+  const int64_t quads = s.n / 4, stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < quads; i += stride) {
+    float u[4];
+    update_of<G, MOMENTUM, true, 4>(g + 4 * i, MOMENTUM ? m + 4 * i : nullptr, s, scale, u);
+#pragma unroll
+    for (int j = 0; j < 4; j++) sum = __builtin_fma((double)u[j], (double)u[j], sum);
+  }
+  if (blockIdx.x == 0 && (int64_t)threadIdx.x < s.n - 4 * quads) {
+    const int64_t i = 4 * quads + threadIdx.x;
+    float u[1];
+    update_of<G, MOMENTUM, true, 1>(g + i, MOMENTUM ? m + i : nullptr, s, scale, u);
+    sum = __builtin_fma((double)u[0], (double)u[0], sum);
+  }
+  __shared__ double waves[kThreads / 64];
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) parts[blockIdx.y * (int64_t)kMaxParts + blockIdx.x] = (waves[0] + waves[1]) + (waves[2] + waves[3]);
+}
+
+__device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) {
+  hi = (_Float16)v;
+  lo = (_Float16)(v - (float)hi);
+}
+
+// u / (|u| + eps) times S in fp16, both ways round: 64 x 64 of [R][C], its high
+// and low halves along the rows (`same`) and turned through LDS (`turn`).
+template <typename G, bool MOMENTUM>
+__global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, int64_t C, int64_t Rp, int64_t Cp, int nparts,
+                                                         float eps, float S, const double* __restrict__ parts,
+                                                         _Float16* __restrict__ same, _Float16* __restrict__ same_l,
+                                                         _Float16* __restrict__ turn, _Float16* __restrict__ turn_l) {
+  __shared__ float tile[64][65];
+  __shared__ double waves[kThreads / 64];
+  float lr = 0.f, scale = s.grad_scale;
+  const bool run = step_of(s.control, lr, scale);
+  const int t = threadIdx.x;
+  double sum = run && t < nparts ? parts[blockIdx.y * (int64_t)kMaxParts + t] : 0.0;
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((t & 63) == 0) waves[t >> 6] = sum;
+  __syncthreads();
+  const float inv = (float)((double)S / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + (double)eps));
+  const int64_t tiles_c = Cp / 64;
+  const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
+  const int64_t base = blockIdx.y * s.n, out = blockIdx.y * Rp * Cp;
+  const int c = t & 63;
+#pragma unroll 4
+  for (int k = 0; k < 16; k++) {
+    const int64_t r = r0 + 4 * k + (t >> 6);
+    float u[1] = {0.f};
+    if (run && r < R && c0 + c < C) {
+      const int64_t i = base + r * C + c0 + c;
+      update_of<G, MOMENTUM, false, 1>(static_cast<const G*>(s.grad) + i, MOMENTUM ? s.m + i : nullptr, s, scale, u);
+    }
+    const float v = u[0] * inv;
+    tile[4 * k + (t >> 6)][c] = v;
+    _Float16 hi, lo;
+    split_half(v, hi, lo);
+    same[out + r * Cp + c0 + c] = hi;
+    if (same_l) same_l[out + r * Cp + c0 + c] = lo;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int k = 0; k < 16; k++) {
+    const int cc = 4 * k + (t >> 6);
+    _Float16 hi, lo;
+    split_half(tile[c][cc], hi, lo);
+    turn[out + (c0 + cc) * Rp + r0 + c] = hi;
+    if (turn_l) turn_l[out + (c0 + cc) * Rp + r0 + c] = lo;
+  }
+}
+
+enum Product { kGram, kSquare, kUpdate, kLast };
+
+// D[p][q] = sum_k P[p][k] Q[q][k]; rows, columns and K of one matrix, in elements.
+struct Args {
+  const _Float16 *P, *Pl, *Q, *Ql;  // operands and their low halves
+  int64_t rows_p, rows_q, K;
+  int tiles_p, tiles_q;
+  // gram, square: A (read by square) and the result
+  const _Float16 *a, *al;
+  float of_sum, of_a, on_diag;  // result = of_sum * sum + of_a * A + on_diag on the diagonal
+  _Float16 *out, *out_l;
+  // update: X (read and written), its transpose
+  float e;
+  _Float16 *x, *xl, *t, *tl;
+  int64_t ldx, ldt, x_stride, t_stride;
+  // last: the result's matrix
+  void* param;
+  uint16_t* copy;
+  int64_t n, lo, hi;  // elements of a matrix, its sides
+  int tall;           // it is [hi][lo]
+  float from_x;       // result = from_x * X'
+  float lr, decay, scale, grad_scale;
+  const mxq_adamw_control* control;
+};
+
+template <int BP, int BQ, int WAVES_P, int WAVES_Q>
+struct Shape {
+  static constexpr int kP = BP, kQ = BQ, kWavesP = WAVES_P;
+  static constexpr int kWaves = WAVES_P * WAVES_Q, kThreads = 64 * kWaves;
+  static constexpr int WP = BP / WAVES_P, WQ = BQ / WAVES_Q;
+  static constexpr int TP = WP / 32, TQ = WQ / 32;  // 32 x 32 blocks of a wave
+  static constexpr int kLoadsP = BP / 8 / kWaves, kLoadsQ = BQ / 8 / kWaves;
+  static constexpr int kBytesP = BP * 128, kBytesQ = BQ * 128, kStage = kBytesP + kBytesQ;
+  static_assert(kLoadsP % 2 == 0 && kLoadsQ % 2 == 0, "a load's parity is its place's");
+};
+
+__device__ __forceinline__ v8h load_half8(const uint8_t* st, int r0, int s, int lane) {
+  return *reinterpret_cast<const v8h*>(st + swz(r0 + (lane & 31), 2 * s + (lane >> 5)));
+}
+
+// SPLIT: the reduction runs three times, over high x high, high x low, low x high.
+// T: the last product's parameter (float or bf16's bits); STEP: it is updated
+// rather than overwritten.
+template <int WHAT, bool SPLIT, class S, typename T = float, bool STEP = false>
+__global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
+  constexpr int TP = S::TP, TQ = S::TQ;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStage];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave % S::kWavesP, wq = wave / S::kWavesP;
+  const int64_t b = blockIdx.y;
+  int pt, qt;
+  if constexpr (WHAT == kGram || WHAT == kSquare) {  // row pt of the upper triangle has tiles_p - pt tiles
+    int at = blockIdx.x;
+    pt = 0;
+    while (at >= p.tiles_p - pt) at -= p.tiles_p - pt++;
+    qt = pt + at;
+  } else {
+    raster(xcd_remap(blockIdx.x, p.tiles_p * p.tiles_q), p.tiles_p, p.tiles_q, pt, qt);
+  }
+  const int64_t p0 = (int64_t)pt * S::kP, q0 = (int64_t)qt * S::kQ;
+  const int np = (int)min<int64_t>(S::kP, p.rows_p - p0), nq = (int)min<int64_t>(S::kQ, p.rows_q - q0);
+
+  const uint32_t ld = (uint32_t)p.K * 2;
+  uint32_t offP[S::kLoadsP], offQ[S::kLoadsQ];
+#pragma unroll
+  for (int j = 0; j < S::kLoadsP; j++)
+    offP[j] = (uint32_t)min((wave * S::kLoadsP + j) * 8 + (lane >> 3), np - 1) * ld + dma_chunk(j, lane) * 16;
+#pragma unroll
+  for (int j = 0; j < S::kLoadsQ; j++)
+    offQ[j] = (uint32_t)min((wave * S::kLoadsQ + j) * 8 + (lane >> 3), nq - 1) * ld + dma_chunk(j, lane) * 16;
+  const int64_t at_p = (b * p.rows_p + p0) * p.K, at_q = (b * p.rows_q + q0) * p.K;
+  const int nk = (int)(p.K / kStageK), ns = SPLIT ? 3 * nk : nk;
+  auto issue = [&](uint8_t* st, int s) {
+    int k = s;
+    const _Float16 *P = p.P, *Q = p.Q;
+    if constexpr (SPLIT) {
+      if (s >= 2 * nk) {
+        k -= 2 * nk;
+        P = p.Pl;
+      } else if (s >= nk) {
+        k -= nk;
+        Q = p.Ql;
+      }
+    }
+    const uint8_t* a = reinterpret_cast<const uint8_t*>(P + at_p + (int64_t)k * kStageK);
+    const uint8_t* c = reinterpret_cast<const uint8_t*>(Q + at_q + (int64_t)k * kStageK);
+#pragma unroll
+    for (int j = 0; j < S::kLoadsP; j++) load_lds16(a + offP[j], st + (wave * S::kLoadsP + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < S::kLoadsQ; j++) load_lds16(c + offQ[j], st + S::kBytesP + (wave * S::kLoadsQ + j) * 1024);
+  };
+  v16f acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; i++)
+#pragma unroll
+    for (int j = 0; j < TQ; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
+  auto compute = [&](const uint8_t* st) {
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      v8h fp[TP], fq[TQ];
+#pragma unroll
+      for (int i = 0; i < TP; i++) fp[i] = load_half8(st, wp * S::WP + 32 * i, s, lane);
+#pragma unroll
+      for (int j = 0; j < TQ; j++) fq[j] = load_half8(st + S::kBytesP, wq * S::WQ + 32 * j, s, lane);
+#pragma unroll
+      for (int i = 0; i < TP; i++)
+#pragma unroll
+        for (int j = 0; j < TQ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  auto step = [&](uint8_t* cur, uint8_t* next, int s) {
+    if (s + 1 < ns) issue(next, s + 1);
+    compute(cur);
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  issue(stage0, 0);
+  wait_vmcnt<0>();
+  __builtin_amdgcn_s_barrier();
+  for (int s = 0; s < ns; s += 2) {
+    step(stage0, stage1, s);
+    if (s + 1 < ns) step(stage1, stage0, s + 1);
+  }
+
+  float lr = 0.f, rate = 0.f, decay = 0.f;
+  if constexpr (WHAT == kLast && STEP) {
+    lr = p.lr;
+    float unused = p.grad_scale;
+    if (!step_of(p.control, lr, unused)) return;
+    rate = lr * p.scale;
+    decay = 1.f - lr * p.decay;
+  }
+  // lane l holds D[8 (e / 4) + 4 (l / 32) + e % 4][l % 32] of each 32 x 32 block
+#pragma unroll
+  for (int j = 0; j < TQ; j++) {
+    const int qq = wq * S::WQ + 32 * j + (lane & 31);
+    if (qq >= nq) continue;
+    const int64_t q = q0 + qq;
+#pragma unroll
+    for (int i = 0; i < TP; i++) {
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int pp = wp * S::WP + 32 * i + 8 * r + 4 * (lane >> 5);
+        if (pp >= np) continue;  // (rows come in multiples of 64)
+        const int64_t row = p0 + pp;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = acc[i][j][4 * r + e];
+        if constexpr (WHAT == kGram || WHAT == kSquare) {
+          const int64_t at = (b * p.rows_p + q) * p.rows_p + row;
+          if constexpr (WHAT == kSquare) {
+            const v4h a = *reinterpret_cast<const v4h*>(p.a + at);
+            v4h al = {0, 0, 0, 0};
+            if constexpr (SPLIT) al = *reinterpret_cast<const v4h*>(p.al + at);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              v[e] = __builtin_fmaf(p.of_a, (float)a[e] + (float)al[e], p.of_sum * v[e]) + (row + e == q ? p.on_diag : 0.f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] *= p.of_sum;
+          }
+          v4h h, l;
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            _Float16 hi, lo;
+            split_half(v[e], hi, lo);
+            h[e] = hi;
+            l[e] = lo;
+          }
+          *reinterpret_cast<v4h*>(p.out + at) = h;
+          if constexpr (SPLIT) *reinterpret_cast<v4h*>(p.out_l + at) = l;
+          if (pt != qt) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const int64_t mirror = (b * p.rows_p + row + e) * p.rows_p + q;
+              p.out[mirror] = h[e];
+              if constexpr (SPLIT) p.out_l[mirror] = l[e];
+            }
+          }
+        } else {
+          const int64_t at = b * p.x_stride + q * p.ldx + row;
+          const v4h xh = *reinterpret_cast<const v4h*>(p.x + at), xl = *reinterpret_cast<const v4h*>(p.xl + at);
+#pragma unroll
+          for (int e = 0; e < 4; e++) v[e] = __builtin_fmaf(p.e, (float)xh[e] + (float)xl[e], p.of_sum * v[e]);
+          if constexpr (WHAT == kUpdate) {
+            v4h h, l;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              _Float16 hi, lo;
+              split_half(v[e], hi, lo);
+              h[e] = hi;
+              l[e] = lo;
+            }
+            *reinterpret_cast<v4h*>(p.x + at) = h;
+            *reinterpret_cast<v4h*>(p.xl + at) = l;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const int64_t turned = b * p.t_stride + (row + e) * p.ldt + q;
+              p.t[turned] = h[e];
+              if constexpr (SPLIT) p.tl[turned] = l[e];
+            }
+          } else {
+            if (q >= p.lo) continue;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              if (row + e >= p.hi) continue;
+              const int64_t o = b * p.n + (p.tall ? (row + e) * p.lo + q : q * p.hi + row + e);
+              T* param = static_cast<T*>(p.param);
+              float y = v[e] * p.from_x;
+              if constexpr (STEP) y = __builtin_fmaf(load_f(param, o), decay, -rate * y);
+              store_f(param, o, y);
+              if constexpr (STEP)
+                if (p.copy) store_f(p.copy, o, y);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+typedef Shape<128, 128, 2, 2> Tile;
+
+// what the host has checked
+struct Plan {
+  int64_t batch, R, C;
+  int steps;
+  double a, b, c;
+  float eps;
+};
+
+template <int WHAT, bool SPLIT, typename T = float, bool STEP = false>
+hipError_t launch_product(Args& p, int64_t batch, hipStream_t st) {
+  p.tiles_p = (int)((p.rows_p + Tile::kP - 1) / Tile::kP);
+  p.tiles_q = (int)((p.rows_q + Tile::kQ - 1) / Tile::kQ);
+  const int64_t tiles = WHAT == kGram || WHAT == kSquare ? (int64_t)p.tiles_p * (p.tiles_p + 1) / 2 : (int64_t)p.tiles_p * p.tiles_q;
+  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  product_kernel<WHAT, SPLIT, Tile, T, STEP><<<dim3((unsigned)tiles, (unsigned)batch), Tile::kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <typename G, bool MOMENTUM>
+void launch_start(const Source& s, const Plan& pl, Space& sp, bool split, float S, hipStream_t st) {
+  const int64_t per = 4 * kThreads;
+  int64_t parts = (s.n + per - 1) / per;
+  if (parts > kMaxParts) parts = kMaxParts;
+  momentum_kernel<G, MOMENTUM><<<dim3((unsigned)parts, (unsigned)pl.batch), kThreads, 0, st>>>(s, sp.parts);
+  const int64_t Rp = up64(pl.R), Cp = up64(pl.C);
+  const bool tall = pl.R > pl.C;
+  // (without the low halves of the transpose where only X's are read)
+  _Float16 *same = tall ? sp.t : sp.x, *turn = tall ? sp.x : sp.t;
+  _Float16 *same_l = tall ? (split ? sp.tl : nullptr) : sp.xl, *turn_l = tall ? sp.xl : (split ? sp.tl : nullptr);
+  start_kernel<G, MOMENTUM><<<dim3((unsigned)(Rp / 64 * (Cp / 64)), (unsigned)pl.batch), kThreads, 0, st>>>(
+      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, same, same_l, turn, turn_l);
+}
+
+template <bool SPLIT, typename T, bool STEP>
+hipError_t iterate(const Plan& pl, Space& sp, float S, Args last, hipStream_t st) {
+  // B = b A + c A^2 + (a - e) I with A's eigenvalues in [0, 1.25^2]
+  const double reach = std::fabs(pl.b) * 1.5625 + std::fabs(pl.c) * 1.5625 * 1.5625 + std::fabs(pl.a);
+  const float scale_b = std::ldexp(1.f, 15 - (int)std::ceil(std::log2(reach > 1.0 ? reach : 1.0)));
+  for (int i = 0; i < pl.steps; i++) {
+    const int left = pl.steps - 1 - i;
+    const float e = (float)(pl.a * (left == 0 ? 0.4375 : left == 1 ? 0.71875 : 1.0));
+    Args g{};
+    g.P = g.Q = sp.x, g.Pl = g.Ql = sp.xl, g.rows_p = g.rows_q = sp.Lp, g.K = sp.Hp;
+    g.of_sum = kScaleA / (S * S), g.out = sp.a, g.out_l = sp.al;
+    hipError_t err = launch_product<kGram, SPLIT>(g, pl.batch, st);
+    if (err != hipSuccess) return err;
+    Args q{};
+    q.P = q.Q = sp.a, q.Pl = q.Ql = sp.al, q.rows_p = q.rows_q = q.K = sp.Lp, q.a = sp.a, q.al = sp.al;
+    q.of_sum = (float)(pl.c * scale_b / ((double)kScaleA * kScaleA)), q.of_a = (float)(pl.b * scale_b / kScaleA);
+    q.on_diag = (float)((pl.a - e) * scale_b), q.out = sp.b, q.out_l = sp.bl;
+    err = launch_product<kSquare, SPLIT>(q, pl.batch, st);
+    if (err != hipSuccess) return err;
+    Args u = last;
+    u.P = sp.t, u.Pl = sp.tl, u.Q = sp.b, u.Ql = sp.bl, u.rows_p = sp.Hp, u.rows_q = u.K = sp.Lp;
+    u.of_sum = 1.f / scale_b, u.e = e;
+    u.x = sp.x, u.xl = sp.xl, u.t = sp.t2, u.tl = sp.tl2, u.ldx = sp.Hp, u.ldt = sp.Lp;
+    u.x_stride = u.t_stride = sp.Lp * sp.Hp;
+    if (left) {
+      err = launch_product<kUpdate, SPLIT>(u, pl.batch, st);
+      _Float16* v = sp.t;
+      sp.t = sp.t2, sp.t2 = v;
+      v = sp.tl;
+      sp.tl = sp.tl2, sp.tl2 = v;
+    } else {
+      err = launch_product<kLast, SPLIT, T, STEP>(u, pl.batch, st);
+    }
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+// u from s, orthogonalised into last.param
+template <bool STEP>
+hipError_t run(const Plan& pl, const Source& s, mxq_dtype gdt, mxq_dtype odt, Args last, uint8_t* workspace, hipStream_t st) {
+  const bool split = odt == MXQ_DT_F32;
+  Space sp;
+  lay_out(&sp, workspace, pl.batch, pl.R, pl.C, split);
+  int log = (int)std::floor(0.5 * std::log2((double)sp.lo * (double)sp.hi));
+  const float S = std::ldexp(1.f, log < 15 ? log : 15);
+  if (gdt == MXQ_DT_F32) {
+    if (STEP) launch_start<float, true>(s, pl, sp, split, S, st);
+    else launch_start<float, false>(s, pl, sp, split, S, st);
+  } else {
+    if (STEP) launch_start<uint16_t, true>(s, pl, sp, split, S, st);
+    else launch_start<uint16_t, false>(s, pl, sp, split, S, st);
+  }
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  last.n = pl.R * pl.C, last.lo = sp.lo, last.hi = sp.hi, last.tall = pl.R > pl.C, last.from_x = 1.f / S;
+  if (split) return iterate<true, float, STEP>(pl, sp, S, last, st);
+  return iterate<false, uint16_t, STEP>(pl, sp, S, last, st);
+}
+
+// largest |a s + b s^3 + c s^5| for s in [0, 1.25]
+double reach_of(double a, double b, double c) {
+  auto at = [&](double s) { return std::fabs(((c * s * s + b) * s * s + a) * s); };
+  double most = at(1.25);
+  const double d = 9 * b * b - 20 * a * c;  // 5 c s^4 + 3 b s^2 + a = 0
+  if (c == 0) {
+    if (b != 0 && -a / (3 * b) > 0) most = std::fmax(most, at(std::fmin(1.25, std::sqrt(-a / (3 * b)))));
+  } else if (d >= 0) {
+    for (double sign : {-1.0, 1.0}) {
+      const double s2 = (-3 * b + sign * std::sqrt(d)) / (10 * c);
+      if (s2 > 0) most = std::fmax(most, at(std::fmin(1.25, std::sqrt(s2))));
+    }
+  }
+  return most;
+}
+
+mxq_status check(const char* who, int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz* ns, mxq_dtype gdt, mxq_dtype odt,
+                 const void* workspace, int64_t bytes) {
+  MXQ_REQUIRE(gdt == MXQ_DT_F32 || gdt == MXQ_DT_BF16, "%s: unknown type %d", who, (int)gdt);
+  MXQ_REQUIRE(odt == MXQ_DT_F32 || odt == MXQ_DT_BF16, "%s: unknown type %d", who, (int)odt);
+  MXQ_REQUIRE(batch >= 0 && batch <= 65535, "%s: batch must be in [0, 65535] (got %lld)", who, (long long)batch);
+  MXQ_REQUIRE(R >= 1 && R <= kMaxSide && C >= 1 && C <= kMaxSide, "%s: R and C must be in [1, %d]", who, kMaxSide);
+  MXQ_REQUIRE(ns != nullptr, "%s: config is NULL", who);
+  MXQ_REQUIRE(ns->steps >= 1 && ns->steps <= MXQ_MAX_NS_STEPS, "%s: steps must be in [1, %d] (got %d)", who, MXQ_MAX_NS_STEPS, ns->steps);
+  MXQ_REQUIRE(std::isfinite(ns->a) && std::isfinite(ns->b) && std::isfinite(ns->c), "%s: coefficients must be finite", who);
+  MXQ_REQUIRE(std::fabs(ns->a) <= 64 && std::fabs(ns->b) <= 64 && std::fabs(ns->c) <= 64 && reach_of(ns->a, ns->b, ns->c) <= 1.25,
+              "%s: coefficients must keep singular values in [0, 1.25] there", who);
+  MXQ_REQUIRE(std::isfinite(ns->eps) && ns->eps >= 0, "%s: eps must be finite and not negative", who);
+  if (batch == 0) return MXQ_OK;
+  MXQ_REQUIRE(workspace != nullptr && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned, not NULL", who);
+  MXQ_REQUIRE(bytes >= mxq_orthogonalize_workspace(batch, R, C, odt), "%s: workspace is too small (%lld bytes)", who, (long long)bytes);
+  return MXQ_OK;
+}
+
+Plan plan_of(int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz& ns) {
+  return Plan{batch, R, C, ns.steps, ns.a, ns.b, ns.c, (float)ns.eps};
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" {
+
+int64_t mxq_orthogonalize_workspace(int64_t batch, int64_t R, int64_t C, mxq_dtype odt) {
+  if (batch < 0 || batch > 65535 || R < 1 || R > kMaxSide || C < 1 || C > kMaxSide) return 0;
+  if (odt != MXQ_DT_F32 && odt != MXQ_DT_BF16) return 0;
+  const int64_t one = lay_out(nullptr, nullptr, 1, R, C, odt == MXQ_DT_F32);
+  if (batch > INT64_MAX / one) return 0;
+  return lay_out(nullptr, nullptr, batch, R, C, odt == MXQ_DT_F32);
+}
+
+mxq_status mxq_orthogonalize(const void* x, mxq_dtype dt, int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz* cfg,
+                             void* out, mxq_dtype odt, void* workspace, int64_t workspace_bytes, hipStream_t st) {
+  const mxq_status s = check("mxq_orthogonalize", batch, R, C, cfg, dt, odt, workspace, workspace_bytes);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE(batch == 0 || (x && out), "mxq_orthogonalize: NULL matrix");
+  MXQ_REQUIRE(aligned_to(x, dt == MXQ_DT_F32 ? 4 : 2) && aligned_to(out, odt == MXQ_DT_F32 ? 4 : 2),
+              "mxq_orthogonalize: x and out must be aligned to their elements");
+  MXQ_REQUIRE_DEVICE();
+  if (batch == 0) return ok();
+  const Source src{x, nullptr, R * C, 0.f, 0.f, 1.f, 0, nullptr};
+  Args last{};
+  last.param = out;
+  return launched(run<false>(plan_of(batch, R, C, *cfg), src, dt, odt, last, static_cast<uint8_t*>(workspace), st),
+                  "mxq_orthogonalize");
+}
+
+mxq_status mxq_muon(void* param, mxq_dtype param_dt, const void* grad, mxq_dtype grad_dt, float* m, uint16_t* copy,
+                    int64_t batch, int64_t R, int64_t C, const mxq_muon_config* cfg, const mxq_adamw_control* control,
+                    void* workspace, int64_t workspace_bytes, hipStream_t st) {
+  MXQ_REQUIRE(cfg != nullptr, "mxq_muon: config is NULL");
+  const mxq_status s = check("mxq_muon", batch, R, C, &cfg->ns, grad_dt, param_dt, workspace, workspace_bytes);
+  if (s != MXQ_OK) return s;
+  MXQ_REQUIRE(batch == 0 || (param && grad && m), "mxq_muon: NULL tensor");
+  MXQ_REQUIRE(aligned_to(param, param_dt == MXQ_DT_F32 ? 4 : 2) && aligned_to(grad, grad_dt == MXQ_DT_F32 ? 4 : 2) &&
+                  aligned_to(m, 4) && aligned_to(copy, 2),
+              "mxq_muon: tensors must be aligned to their elements");
+  MXQ_REQUIRE(cfg->momentum >= 0 && cfg->momentum < 1, "mxq_muon: momentum must be in [0, 1)");
+  MXQ_REQUIRE(cfg->nesterov == 0 || cfg->nesterov == 1, "mxq_muon: nesterov must be 0 or 1");
+  MXQ_REQUIRE(std::isfinite(cfg->weight_decay) && std::isfinite(cfg->scale), "mxq_muon: weight_decay and scale must be finite");
+  MXQ_REQUIRE(aligned_to(control, 16), "mxq_muon: control must be 16-byte aligned");
+  MXQ_REQUIRE_DEVICE();
+  if (batch == 0) return ok();
+  const Source src{grad, m, R * C, (float)cfg->momentum, (float)(1 - cfg->momentum), (float)cfg->grad_scale, cfg->nesterov, control};
+  Args last{};
+  last.param = param, last.copy = copy;
+  last.lr = (float)cfg->lr, last.decay = (float)cfg->weight_decay, last.scale = (float)cfg->scale;
+  last.grad_scale = (float)cfg->grad_scale, last.control = control;
+  if (!control && !(std::isfinite(last.lr) && std::isfinite(last.grad_scale))) return ok();  // (a step to skip)
+  return launched(run<true>(plan_of(batch, R, C, cfg->ns), src, grad_dt, param_dt, last, static_cast<uint8_t*>(workspace), st),
+                  "mxq_muon");
+}
+
+}  // extern "C"

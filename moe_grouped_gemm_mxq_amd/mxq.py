@@ -61,6 +61,7 @@ EXPORTED = [
     "mxq_validate_group_end", "mxq_quantize_fp4_grouped", "mxq_expert_order_workspace", "mxq_route",
     "mxq_expert_order", "mxq_route_backward", "mxq_combine", "mxq_combine_backward", "mxq_adamw",
     "mxq_grouped128_cols_max", "mxq_quantize128", "mxq_quantize128_grouped", "mxq_gemm128", "mxq_grouped_gemm128",
+    "mxq_orthogonalize_workspace", "mxq_orthogonalize", "mxq_muon",
 ]
 
 
@@ -83,6 +84,18 @@ class AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint32)]
+
+
+class NewtonSchulz(ctypes.Structure):
+    """mxq_newton_schulz."""
+    _fields_ = [("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double), ("eps", ctypes.c_double),
+                ("steps", ctypes.c_int32)]
+
+
+class MuonConfig(ctypes.Structure):
+    """mxq_muon_config."""
+    _fields_ = [("ns", NewtonSchulz), ("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("grad_scale", ctypes.c_double), ("nesterov", ctypes.c_int32)]
 
 
 def _load(path: str = LIB_PATH):
@@ -117,6 +130,9 @@ def _load(path: str = LIB_PATH):
         "mxq_combine": ([P, I, I64, I64, P, P, I64, I32, I64, P, I, I64, P], I),
         "mxq_combine_backward": ([P, I, I64, P, I, I64, P, P, I64, I32, I64, I64, P, I, I64, P, P], I),
         "mxq_adamw": ([P, I32, I, I, I, P, P, P], I),
+        "mxq_orthogonalize_workspace": ([I64, I64, I64, I], I64),
+        "mxq_orthogonalize": ([P, I, I64, I64, I64, P, P, I, P, I64, P], I),
+        "mxq_muon": ([P, I, P, I, P, P, I64, I64, I64, P, P, P, I64, P], I),
         "mxq_grouped128_cols_max": ([I64, I32], I64),
         "mxq_quantize128": ([P, I, I64, I64, I64, I64, I64, I, I, P, P, P, P, P], I),
         "mxq_quantize128_grouped": ([P, I, I64, I64, I64, P, I32, I64, I, P, P, P, P, P], I),
@@ -706,6 +722,62 @@ def mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end, stream=None):
                                     M, N, K, group_end.data_ptr(), G, _stream(stream, A.device)), "mxq_grouped_gemm128")
 
 
+# ---- orthogonalised updates
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7):
+    """mxq_newton_schulz."""
+    return NewtonSchulz(*coefficients, eps, steps)
+
+
+@functools.lru_cache(maxsize=256)
+def mxq_orthogonalize_workspace(batch: int, R: int, C: int, odt: int) -> int:
+    return _lib.mxq_orthogonalize_workspace(batch, R, C, odt)
+
+
+def _matrices(t, name):
+    """(type code, batch, R, C) of contiguous float matrices [R][C] or [batch][R][C] on the device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() not in (2, 3) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with 2 or 3 dims, got shape {tuple(t.shape)}")
+    return (_DTYPES[t.dtype], 1, *t.shape) if t.dim() == 2 else (_DTYPES[t.dtype], *t.shape)
+
+
+def mxq_orthogonalize(x, cfg, out, workspace, stream=None):
+    """x fp32 or bf16 [R][C] or [batch][R][C], contiguous -> out of its shape, fp32 or bf16; workspace uint8."""
+    dt, nb, R, C = _matrices(x, "x")
+    odt = _matrices(out, "out")[0]
+    if out.shape != x.shape:
+        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    _need(workspace, torch.uint8, "workspace", 1)
+    _here(x, "x")
+    _check(_lib.mxq_orthogonalize(x.data_ptr(), dt, nb, R, C, ctypes.byref(cfg), out.data_ptr(), odt, workspace.data_ptr(),
+                                  workspace.numel(), _stream(stream, x.device)), "mxq_orthogonalize")
+
+
+def mxq_muon(param, grad, m, cfg, workspace, copy=None, control=None, stream=None):
+    """One Muon step of param [R][C] or [batch][R][C] (see the Muon class)."""
+    pdt, nb, R, C = _matrices(param, "param")
+    gdt = _matrices(grad, "grad")[0]
+    _need_array(m, "m", torch.float32, param.shape)
+    if grad.shape != param.shape:
+        raise ValueError(f"grad must have shape {tuple(param.shape)}, got {tuple(grad.shape)}")
+    if copy is not None:
+        _need_array(copy, "copy", torch.bfloat16, param.shape)
+    if control is not None:
+        _need_array(control, "control", torch.int32, (4,))
+    _need(workspace, torch.uint8, "workspace", 1)
+    _here(param, "param")
+    _check(_lib.mxq_muon(param.data_ptr(), pdt, grad.data_ptr(), gdt, m.data_ptr(), _raw(copy), nb, R, C, ctypes.byref(cfg),
+                         _raw(control), workspace.data_ptr(), workspace.numel(), _stream(stream, param.device)), "mxq_muon")
+
+
 # ------------------------------------------------------------------ allocate-and-call helpers
 def _on(stream, device):
     """Context in which `stream` is the current one, so that what is allocated belongs to it.  A helper that is given a
@@ -1086,3 +1158,71 @@ class AdamW:
             return
         cfg = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, seed & 0xFFFFFFFF)
         mxq_adamw(self.tensors, self.n, self.param_dt, self.grad_dt, self.fmt, cfg, control, stream, self.device)
+
+
+def _orthogonalize_workspace(batch, R, C, odt, device):
+    return torch.empty(mxq_orthogonalize_workspace(batch, R, C, odt), dtype=torch.uint8, device=device)
+
+
+def orthogonalize(x, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, dtype=torch.bfloat16, stream=None):
+    """Newton-Schulz iterations on each matrix of x [R][C] or [batch][R][C] (see mxq_orthogonalize): a result of `dtype`, fp32
+    with three times the products of bf16."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return orthogonalize(x, steps, coefficients, eps, dtype)
+    odt = _type_code(dtype)
+    _, nb, R, C = _matrices(x, "x")
+    out = torch.empty_like(x, dtype=dtype)
+    mxq_orthogonalize(x, newton_schulz(steps, coefficients, eps), out, _orthogonalize_workspace(nb, R, C, odt, x.device))
+    return out
+
+
+def muon_scale(shape, rule="match_rms"):
+    """What an orthogonalised update of a weight [.., R][C] is multiplied by: 0.2 sqrt(max(R, C)), with which its elements are
+    about the size of an AdamW update's ("match_rms"), or sqrt(max(1, R / C)) ("original")."""
+    R, C = shape[-2:]
+    if rule == "match_rms":
+        return 0.2 * max(R, C) ** 0.5
+    if rule == "original":
+        return max(1.0, R / C) ** 0.5
+    raise ValueError(f"unknown rule {rule!r}; one of 'match_rms', 'original'")
+
+
+class Muon:
+    """Muon steps of a list of weights (mxq_muon), each [R][C] or a stack [batch][R][C] of such (experts).
+
+    params fp32 or bf16, grads fp32 or bf16, m the momenta (fp32, zeros before the first step), copies: bf16 tensors that get
+    the new parameters too, or None.  The tensors stay the caller's: they are read and written where they are, so a gradient
+    that moves to other storage needs a new Muon.  The workspace is shared by the tensors, which are updated one after the
+    other on the step's stream."""
+
+    def __init__(self, params, grads, m, copies=None):
+        n = len(params)
+        if not (len(grads) == len(m) == n) or (copies is not None and len(copies) != n):
+            raise ValueError("params, grads, m and copies must be of one length")
+        copies = [None] * n if copies is None else list(copies)
+        need = 1
+        for i, p in enumerate(params):
+            name = f"tensor {i}: "
+            pdt, nb, R, C = _matrices(p, name + "param")
+            _matrices(grads[i], name + "grad")
+            _need_array(m[i], name + "m", torch.float32, p.shape)
+            if copies[i] is not None:
+                _need_array(copies[i], name + "copy", torch.bfloat16, p.shape)
+            if grads[i].shape != p.shape:
+                raise ValueError(f"{name}grad must have shape {tuple(p.shape)}, got {tuple(grads[i].shape)}")
+            if any(t is not None and t.device != params[0].device for t in (p, grads[i], m[i], copies[i])):
+                raise ValueError(f"{name}all tensors must be on one device")
+            need = max(need, mxq_orthogonalize_workspace(nb, R, C, pdt))
+        self.tensors = list(zip(params, grads, m, copies))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=params[0].device) if n else None
+
+    def step(self, *, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.1, scale="match_rms", grad_scale=1.0, steps=5,
+             coefficients=NS_COEFFICIENTS, eps=1e-7, control=None, stream=None):
+        """One step.  scale: a rule of muon_scale or a number.  control: an adamw_control tensor whose lr and grad_scale replace
+        these (for graphs)."""
+        for param, grad, m, copy in self.tensors:
+            factor = muon_scale(param.shape, scale) if isinstance(scale, str) else scale
+            cfg = MuonConfig(newton_schulz(steps, coefficients, eps), lr, momentum, weight_decay, factor, grad_scale,
+                             int(bool(nesterov)))
+            mxq_muon(param, grad, m, cfg, self.workspace, copy, control, stream)
