@@ -36,17 +36,20 @@ constexpr int kB = 128;  // block, and the bytes of a tile row in a stage
 
 enum Mode { kDense = 0, kRaggedM = 1, kRaggedK = 2 };
 
-// Output tile of a workgroup: BM rows of A by BN rows of B, WAVES_M x WAVES_N waves.
-template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+// Output tile of a workgroup: BM rows of A by BN rows of B, WAVES_M x WAVES_N
+// waves, with STAGES stages in LDS.
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int STAGES>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M;
+  static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M, kStages = STAGES;
   static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;  // wave tile
   static constexpr int TM = WM / 16, TN = WN / 16;            // 16 x 16 blocks of a wave
   static constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;  // 1 KB loads of a wave and stage
+  static constexpr int kLoads = kLoadsA + kLoadsB + 1;                        // with the scales'
   static constexpr int kCodesA = BM * kB, kCodesB = BN * kB;
-  static constexpr int kStage = kCodesA + kCodesB + (BM + BN) * 4;  // codes, then the block's scales of every row
+  static constexpr int kStage = kCodesA + kCodesB + kWaves * 256;  // codes, then the block's scales of 64 rows a wave
   static_assert(BM / 64 + BN / 64 <= kWaves, "each wave loads the scales of at most 64 rows");
+  static_assert(STAGES >= 2 && STAGES <= 4, "the stages are spelled out");
   static_assert(kLoadsA % 2 == 0 && kLoadsB % 2 == 0, "a load's parity is its place's");
 };
 
@@ -169,12 +172,12 @@ __device__ __forceinline__ v8i load_frag(const uint8_t* codes, int r0, int lane)
   return f;
 }
 
-struct Wide {
+struct AsBf16 {
   v8bf f[4];
 };
 // the same 32 codes as bf16 numbers (exact), eight for each of four instructions
-__device__ __forceinline__ Wide widen(const v8i& c) {
-  Wide w;
+__device__ __forceinline__ AsBf16 widen(const v8i& c) {
+  AsBf16 w;
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     const v2bf16 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * s], 1.f, false);
@@ -193,19 +196,35 @@ struct FragOf {
 };
 template <>
 struct FragOf<true> {
-  typedef Wide type;
-  static __device__ __forceinline__ Wide of(const v8i& c) { return widen(c); }
+  typedef AsBf16 type;
+  static __device__ __forceinline__ AsBf16 of(const v8i& c) { return widen(c); }
 };
 
 // partial product of a block: rows of n by columns (lanes) of m
 __device__ __forceinline__ v4f block_product(const v8i& n, const v8i& m) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ v4f block_product(const Wide& n, const Wide& m) {
+__device__ __forceinline__ v4f block_product(const AsBf16& n, const AsBf16& m) {
   v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < 4; s++) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.f[s], m.f[s], d, 0, 0, 0);
   return d;
+}
+
+// of TM blocks of m
+template <int TM>
+__device__ __forceinline__ void block_products(const v8i& n, const v8i (&m)[TM], v4f (&d)[TM]) {
+#pragma unroll
+  for (int j = 0; j < TM; j++) d[j] = block_product(n, m[j]);
+}
+template <int TM>
+__device__ __forceinline__ void block_products(const AsBf16& n, const AsBf16 (&m)[TM], v4f (&d)[TM]) {
+#pragma unroll
+  for (int j = 0; j < TM; j++) d[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; s++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.f[s], m[j].f[s], d[j], 0, 0, 0);
 }
 
 __device__ __forceinline__ void store4(float* p, const v4f& v, int n) {
@@ -227,14 +246,15 @@ __device__ __forceinline__ void store4(uint16_t* p, const v4f& v, int n) {
 }
 
 // One stage is one block of 128 along K: codes and scales of the tile's rows,
-// loaded straight into LDS one stage ahead.  The two stages are separate arrays
-// so that the compiler can tell the one being read from the one being filled.
+// loaded straight into LDS kStages - 1 stages ahead.  The stages are separate
+// arrays so that the compiler can tell the one being read from those being filled.
 template <int MODE, bool F32, bool TILE128, class S>
 __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
   typedef std::conditional_t<F32, float, uint16_t> Out;
-  constexpr int TM = S::TM, TN = S::TN;
-  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStage];
+  constexpr int TM = S::TM, TN = S::TN, NS = S::kStages;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage], stage1[S::kStage], stage2[NS > 2 ? S::kStage : 16],
+      stage3[NS > 3 ? S::kStage : 16];
+  uint8_t* const stages[4] = {stage0, stage1, stage2, stage3};
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % S::kWavesM, wn = wave / S::kWavesM;
@@ -251,26 +271,38 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
     offB[j] = (uint32_t)min((wave * S::kLoadsB + j) * 8 + (lane >> 3), t.cols - 1) * (uint32_t)p.K + dma_chunk(j, lane) * 16;
   const uint8_t* const baseA = p.A + t.m0 * p.K + t.kb0 * kB;
   const uint8_t* const baseB = t.B + t.n0 * p.K + t.kb0 * kB;
-  // scales: wave w those of the 64 tile rows from 64 w on, A's rows before B's
+  // scales: wave w those of the 64 tile rows from 64 w on, A's rows before B's (past the last: of B's last row)
   const bool of_a = wave < S::BM / 64;
   const int srow = (of_a ? wave : wave - S::BM / 64) * 64 + lane;
   const int64_t scales_n = TILE128 ? (p.N + kB - 1) / kB : p.N;
   const int64_t spitch = of_a ? p.M : scales_n;
-  const float* sp = of_a ? p.sA + t.m0 + min(srow, t.rows - 1)
-                         : t.sB + (TILE128 ? (t.n0 + min(srow, t.cols - 1)) / kB : t.n0 + min(srow, t.cols - 1));
-  sp += t.kb0 * spitch;
+  const int64_t sn = t.n0 + min(srow, t.cols - 1);
+  const float* sp = (of_a ? p.sA + t.m0 + min(srow, t.rows - 1) : t.sB + (TILE128 ? sn / kB : sn)) + t.kb0 * spitch;
 
-  auto issue = [&](uint8_t* st, int s) {
-    const uint8_t* a = baseA + (int64_t)s * kB;
-    const uint8_t* b = baseB + (int64_t)s * kB;
-#pragma unroll
-    for (int j = 0; j < S::kLoadsA; j++)
-      load_lds16(a + offA[j], st + (wave * S::kLoadsA + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < S::kLoadsB; j++)
-      load_lds16(b + offB[j], st + S::kCodesA + (wave * S::kLoadsB + j) * 1024);
-    if (wave < S::BM / 64 + S::BN / 64)
+  // load n of a stage: A's codes, B's, and the scales (every wave has as many in flight)
+  auto load = [&](uint8_t* st, int s, int n) {
+    if (n < S::kLoadsA) {
+      load_lds16(baseA + (int64_t)s * kB + offA[n], st + (wave * S::kLoadsA + n) * 1024);
+    } else if (n < S::kLoadsA + S::kLoadsB) {
+      load_lds16(baseB + (int64_t)s * kB + offB[n - S::kLoadsA], st + S::kCodesA + (wave * S::kLoadsB + n - S::kLoadsA) * 1024);
+    } else {
       load_lds4(sp + s * spitch, st + S::kCodesA + S::kCodesB + wave * 256);
+    }
+  };
+  auto load_stage = [&](uint8_t* st, int s) {
+#pragma unroll
+    for (int n = 0; n < S::kLoads; n++) load(st, s, n);
+  };
+  // The stage after s has landed; the loads of those after it may be in flight.
+  auto next_landed = [&](int s) {
+    if (NS > 2 && s + NS - 1 < t.nkb)
+      wait_vmcnt<(NS - 2) * S::kLoads>();
+    else
+      wait_vmcnt<0>();
+  };
+  auto meet = [&]() {
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   v4f acc[TN][TM];
@@ -280,7 +312,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
     for (int j = 0; j < TM; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
   typedef FragOf<F32> Frag;
-  auto compute = [&](const uint8_t* st) {
+  // loads of each of the wave's TN row blocks of B, so that all are out by about half of the stage
+  constexpr int kPer = (S::kLoads + TN / 2) / TN + 1;
+  // stage s, which is in st; meanwhile stage s + NS - 1 is loaded to next
+  auto stage = [&](const uint8_t* st, uint8_t* next, int s) {
+    const bool more = s + NS - 1 < t.nkb;
     const float* sa_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + wm * S::WM;
     const float* sb_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + S::BM + wn * S::WN;
     typename Frag::type fm[TM];
@@ -291,35 +327,61 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
       f[j] = sa_of[j * 16 + (lane & 15)];
       if constexpr (TILE128) f[j] *= sb_of[0];
     }
-#pragma unroll
-    for (int i = 0; i < TN; i++) {
-      const typename Frag::type fn = Frag::of(load_frag(st + S::kCodesA, wn * S::WN + i * 16, lane));
-      v4f sb;
-      if constexpr (!TILE128) sb = *reinterpret_cast<const v4f*>(sb_of + i * 16 + 4 * (lane >> 4));
+    // While block i's matrix instructions run, the sums of block i - 1 are taken and
+    // the codes of block i + 1 widened, whose reads went out a block earlier.
+    v4f d[2][TM], sb[2];
+    typename Frag::type fn = Frag::of(load_frag(st + S::kCodesA, wn * S::WN, lane));
+    v8i ahead = load_frag(st + S::kCodesA, wn * S::WN + (TN > 1 ? 16 : 0), lane);
+    auto add = [&](int i) {
 #pragma unroll
       for (int j = 0; j < TM; j++) {
-        v4f d = block_product(fn, fm[j]);
-        if constexpr (!TILE128) d *= sb;
+        v4f v = d[i & 1][j];
+        if constexpr (!TILE128) v *= sb[i & 1];
 #pragma unroll
-        for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(d[e], f[j], acc[i][j][e]);
+        for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(v[e], f[j], acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));  // here, not after the stage's last instruction
       }
-    }
-  };
-  auto step = [&](uint8_t* cur, uint8_t* next, int s) {
-    if (s + 1 < t.nkb) issue(next, s + 1);
-    compute(cur);
-    wait_vmcnt<0>();  // the next stage has landed
-    wait_lgkmcnt0();
-    __builtin_amdgcn_s_barrier();
+    };
     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < TN; i++) {
+      if constexpr (!TILE128) sb[i & 1] = *reinterpret_cast<const v4f*>(sb_of + i * 16 + 4 * (lane >> 4));
+      const v8i raw = ahead;
+      if (i + 2 < TN) ahead = load_frag(st + S::kCodesA, wn * S::WN + (i + 2) * 16, lane);
+      block_products(fn, fm, d[i & 1]);
+      // the loads a few at a time: a wave that issues all of them at once waits for
+      // the queue, and its matrix instructions with it
+      if (more) {
+#pragma unroll
+        for (int n = i * kPer; n < (i + 1) * kPer && n < S::kLoads; n++) load(next, s + NS - 1, n);
+      }
+      if (i > 0) add(i - 1);
+      if (i + 1 < TN) fn = Frag::of(raw);
+      // one matrix instruction, then its share of the others: two waves that meet in
+      // the same phase would otherwise wait for one another in both
+      constexpr int kMfma = TM * (F32 ? 4 : 1), kValu = (TM * (TILE128 ? 4 : 8) + (F32 ? 16 : 0) + kMfma - 1) / kMfma;
+#pragma unroll
+      for (int n = 0; n < kMfma; n++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(TN - 1);
+    next_landed(s);
+    wait_lgkmcnt0();
+    meet();
   };
   if (t.nkb > 0) {
-    issue(stage0, 0);
-    wait_vmcnt<0>();
-    __builtin_amdgcn_s_barrier();
-    for (int s = 0; s < t.nkb; s += 2) {
-      step(stage0, stage1, s);
-      if (s + 1 < t.nkb) step(stage1, stage0, s + 1);
+#pragma unroll
+    for (int s = 0; s < NS - 1; s++)
+      if (s < t.nkb) load_stage(stages[s], s);
+    next_landed(-1);
+    meet();
+    for (int s0 = 0; s0 < t.nkb; s0 += NS) {
+#pragma unroll
+      for (int u = 0; u < NS; u++)
+        if (s0 + u < t.nkb) stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
     }
   }
 
@@ -338,7 +400,132 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
   }
 }
 
-typedef Shape<128, 128, 2, 2> Small;
+// Few rows of A (decoding): B is read once, straight into the lanes' registers,
+// and the waves of a workgroup take different blocks of K of the same 16 NB rows
+// of B by 16 MB rows of A; their sums are added through LDS in the order of
+// the waves.  A comes from L2.  Bound by B's bytes: many waves with a block each in
+// flight read them faster than few with several (measured 33 us against 38 for
+// 132 MB, where reading alone takes 25), so registers are kept few.  Of the
+// scales, lane (row, part) loads those of its row and of the part-th of the next
+// kU blocks, and the lanes of the other parts get them from it.
+constexpr int kU = 4;
+
+// a lane's 32 bytes of a block: 16 of either half, so that a load covers 64 bytes of each row
+__device__ __forceinline__ v8i load_lane32(const uint8_t* p) {
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(p), hi = *reinterpret_cast<const u32x4*>(p + 64);
+  return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+template <int MODE, bool F32, bool TILE128, int MB, int NB, int W, int OCC>
+__global__ __launch_bounds__(64 * W, OCC) void few_rows_kernel(Problem p) {
+  typedef std::conditional_t<F32, float, uint16_t> Out;
+  __shared__ float sums[W][NB * MB][256];
+  const int lane = threadIdx.x & 63, in = lane & 15, part = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int Kb = (int)(p.K / kB);
+  const int64_t scales_n = TILE128 ? (p.N + kB - 1) / kB : p.N;
+  int64_t m_first = 0, m_rows = p.M;
+  const uint8_t* B = p.B;
+  const float* sB = p.sB;
+  int nt = blockIdx.x;
+  if constexpr (MODE == kRaggedM) {
+    const int g = blockIdx.x / p.tiles_n;
+    nt = blockIdx.x - g * p.tiles_n;
+    int32_t start, size;
+    group_span(p.group_end, g, p.M, start, size);
+    m_first = start;
+    m_rows = size;
+    B += (int64_t)g * p.N * p.K;
+    sB += (int64_t)g * Kb * scales_n;
+  }
+  const int64_t n0 = (int64_t)nt * (16 * NB);
+  const uint8_t* b_row[NB];
+  const float* sb_row[NB];
+#pragma unroll
+  for (int i = 0; i < NB; i++) {
+    b_row[i] = B + min(n0 + 16 * i + in, p.N - 1) * p.K + 16 * part;
+    sb_row[i] = sB + (TILE128 ? min(n0 + 16 * i, p.N - 1) / kB : min(n0 + 16 * i + in, p.N - 1));
+  }
+
+  for (int64_t m0 = 0; m0 < m_rows; m0 += 16 * MB) {
+    const uint8_t* a_row[MB];
+    const float* sa_row[MB];
+#pragma unroll
+    for (int j = 0; j < MB; j++) {
+      const int64_t m = m_first + min(m0 + 16 * j + in, m_rows - 1);
+      a_row[j] = p.A + m * p.K + 16 * part;
+      sa_row[j] = p.sA + m;
+    }
+    v4f acc[NB][MB];
+#pragma unroll
+    for (int i = 0; i < NB; i++)
+#pragma unroll
+      for (int j = 0; j < MB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wave; k0 < Kb; k0 += W * kU) {
+      const int64_t ks = min(k0 + part * W, Kb - 1);
+      float sa[MB], sb[NB];
+#pragma unroll
+      for (int j = 0; j < MB; j++) sa[j] = sa_row[j][ks * p.M];
+#pragma unroll
+      for (int i = 0; i < NB; i++) sb[i] = sb_row[i][ks * scales_n];
+#pragma unroll
+      for (int u = 0; u < kU; u++) {
+        const int64_t k = k0 + u * W;
+        if (k >= Kb) break;
+        v8i b[NB], a[MB];
+#pragma unroll
+        for (int i = 0; i < NB; i++) b[i] = load_lane32(b_row[i] + k * kB);
+#pragma unroll
+        for (int j = 0; j < MB; j++) a[j] = load_lane32(a_row[j] + k * kB);
+        typename FragOf<F32>::type fm[MB];
+#pragma unroll
+        for (int j = 0; j < MB; j++) fm[j] = FragOf<F32>::of(a[j]);
+#pragma unroll
+        for (int i = 0; i < NB; i++) {
+          const typename FragOf<F32>::type fn = FragOf<F32>::of(b[i]);
+          v4f sbn;  // of the lane's four rows of B
+          if constexpr (!TILE128) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) sbn[e] = __shfl(sb[i], 16 * u + 4 * part + e);
+          }
+#pragma unroll
+          for (int j = 0; j < MB; j++) {
+            v4f d = block_product(fn, fm[j]);
+            float f;
+            if constexpr (TILE128) {
+              f = __shfl(sa[j] * sb[i], 16 * u + in);
+            } else {
+              f = __shfl(sa[j], 16 * u + in);
+              d *= sbn;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(d[e], f, acc[i][j][e]);
+          }
+        }
+      }
+    }
+    // [m][n] of each 16 x 16 block
+#pragma unroll
+    for (int i = 0; i < NB; i++)
+#pragma unroll
+      for (int j = 0; j < MB; j++) *reinterpret_cast<v4f*>(&sums[wave][i * MB + j][in * 16 + 4 * part]) = acc[i][j];
+    __syncthreads();
+    for (int at = threadIdx.x; at < NB * MB * 256; at += 64 * W) {
+      const int ij = at >> 8, r = at & 255;
+      float v = sums[0][ij][r];
+#pragma unroll
+      for (int w = 1; w < W; w++) v += sums[w][ij][r];
+      const int64_t m = m0 + 16 * (ij % MB) + (r >> 4), n = n0 + 16 * (ij / MB) + (r & 15);
+      if (m < m_rows && n < p.N) store_f(static_cast<Out*>(p.C), (m_first + m) * p.ldc + n, v);
+    }
+    if (m0 + 16 * MB < m_rows) __syncthreads();
+  }
+}
+
+typedef Shape<256, 256, 4, 2, 2> Large;
+typedef Shape<128, 128, 2, 2, 2> Medium;
+typedef Shape<128, 128, 2, 4, 4> Deep;
+typedef Shape<64, 64, 2, 2, 4> Small;
 
 template <int MODE, bool F32, bool TILE128, class S>
 hipError_t launch_shape(Problem p, hipStream_t st) {
@@ -351,10 +538,56 @@ hipError_t launch_shape(Problem p, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int MODE, bool F32, bool TILE128, int MB, int NB, int W, int OCC>
+hipError_t launch_few(Problem p, hipStream_t st) {
+  const int64_t tiles = (p.N + 16 * NB - 1) / (16 * NB), total = tiles * (MODE == kRaggedM ? p.G : 1);
+  if (total > INT32_MAX) return hipErrorInvalidValue;
+  p.tiles_n = (int)tiles;
+  few_rows_kernel<MODE, F32, TILE128, MB, NB, W, OCC><<<(unsigned)total, 64 * W, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+// Waves a workgroup, and rows of B in it, from what they measured (us; bf16 C, N x K = 4096 x 7168 / 18432 x 7168 / 32
+// experts of 4096 x 7168 with 64 rows): 16 rows of B by 16 waves 8.2 / 33.4 / 102, 32 by 8 waves 11.4 / 35.2 / 97.
+template <int MODE, bool F32, bool TILE128>
+hipError_t launch_few_of(const Problem& p, int64_t rows, hipStream_t st) {
+  const bool many = (p.N + 31) / 32 * (MODE == kRaggedM ? p.G : 1) >= 4 * (int64_t)device_cu_count();
+  if (rows <= 16) {
+    if (many) return launch_few<MODE, F32, TILE128, 1, 2, 8, 4>(p, st);
+    return launch_few<MODE, F32, TILE128, 1, 1, 16, 8>(p, st);
+  }
+  if (rows <= 32) {
+    if (many) return launch_few<MODE, F32, TILE128, 2, 2, 8, 4>(p, st);
+    return launch_few<MODE, F32, TILE128, 2, 1, 8, 4>(p, st);
+  }
+  return launch_few<MODE, F32, TILE128, 4, 1, 8, 4>(p, st);
+}
+
+// tiles of side `side`
+int64_t tiles_of(const Problem& p, int mode, int64_t side) {
+  return (p.M + side - 1) / side * ((p.N + side - 1) / side) * (mode == kRaggedK ? p.G : 1);
+}
+
+template <int MODE, bool F32, bool TILE128>
+hipError_t launch_tiles(const Problem& p, hipStream_t st) {
+  const int64_t cus = device_cu_count();
+  if (tiles_of(p, MODE, 64) <= cus) return launch_shape<MODE, F32, TILE128, Small>(p, st);
+  if (tiles_of(p, MODE, 128) <= cus) return launch_shape<MODE, F32, TILE128, Deep>(p, st);
+  if constexpr (!F32 && TILE128)
+    if (4 * tiles_of(p, MODE, 256) >= 3 * cus) return launch_shape<MODE, F32, TILE128, Large>(p, st);
+  return launch_shape<MODE, F32, TILE128, Medium>(p, st);
+}
+
 template <int MODE, bool TILE128>
 hipError_t launch_gemm128(const Problem& p, bool f32, hipStream_t st) {
-  if (f32) return launch_shape<MODE, true, TILE128, Small>(p, st);
-  return launch_shape<MODE, false, TILE128, Small>(p, st);
+  if constexpr (MODE != kRaggedK) {
+    // Rows of A, or of a larger group.  B is read again for every 64 (or 16, 32) rows; with
+    // more, and with more than 16 where N alone fills the card, tiles are faster (N = 18432,
+    // 64 rows: 44 us against 84; N = 4096: 26 against 20).
+    const int64_t rows = MODE == kRaggedM ? 4 * p.M / p.G : p.M;
+    if (rows <= 16 || (rows <= 64 && p.N <= 32 * (int64_t)device_cu_count())) return f32 ? launch_few_of<MODE, true, TILE128>(p, rows, st) : launch_few_of<MODE, false, TILE128>(p, rows, st);
+  }
+  return f32 ? launch_tiles<MODE, true, TILE128>(p, st) : launch_tiles<MODE, false, TILE128>(p, st);
 }
 
 mxq_status check(const char* who, const Problem& p, mxq_dtype cdt) {

@@ -30,26 +30,94 @@ constexpr float kMaxCode = 448.f;
 constexpr uint32_t kAmaxFloor = 0x0D800000u;  // 2^-100
 constexpr uint32_t kInf = 0x7F800000u;
 
-// Eight consecutive elements as fp32, zero from the n-th on.
-__device__ __forceinline__ void load8(const float* p, int n, float* v) {
+// Eight consecutive elements as they lie in memory, zero from the n-th on.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ float at(int j) const { return __uint_as_float((j & 1) ? a[j >> 1] & 0xFFFF0000u : a[j >> 1] << 16); }
+};
+template <>
+struct Eight<float> {
+  u32x4 a, b;
+  __device__ __forceinline__ float at(int j) const { return __uint_as_float(j < 4 ? a[j & 3] : b[j & 3]); }
+};
+__device__ __forceinline__ Eight<float> load8(const float* p, int n) {
+  Eight<float> v;
   if (n >= 8) {
-    unpack(load_raw<4, false>(p), v);
-    unpack(load_raw<4, false>(p + 4), v + 4);
+    v.a = load_raw<4, false>(p).a;
+    v.b = load_raw<4, false>(p + 4).a;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = j < n ? p[j] : 0.f;
+    for (int j = 0; j < 4; j++) {
+      v.a[j] = j < n ? __float_as_uint(p[j]) : 0u;
+      v.b[j] = j + 4 < n ? __float_as_uint(p[j + 4]) : 0u;
+    }
   }
+  return v;
 }
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
+__device__ __forceinline__ Eight<uint16_t> load8(const uint16_t* p, int n) {
+  Eight<uint16_t> v;
   if (n >= 8) {
-    unpack(load_raw<8, false>(p), v);
+    v.a = load_raw<8, false>(p).a;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = j < n ? load_f(p, j) : 0.f;
+    for (int j = 0; j < 4; j++)
+      v.a[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
   }
+  return v;
 }
 
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// Magnitudes as integers, which order them with NaN above infinity.  Of eight
+// columns: their largest so far, two to a register for bf16.
+template <typename T>
+struct Largest;
+template <>
+struct Largest<float> {
+  uint32_t m[8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; j++) m[j] = 0;
+  }
+  __device__ __forceinline__ void take(const Eight<float>& v) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) m[j] = max(m[j], __float_as_uint(v.at(j)) & 0x7FFFFFFFu);
+  }
+  __device__ __forceinline__ void fold(int lanes) {  // with those of the lane `lanes` away
+#pragma unroll
+    for (int j = 0; j < 8; j++) m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], lanes));
+  }
+  __device__ __forceinline__ uint32_t of(int j) const { return m[j]; }
+  __device__ __forceinline__ uint32_t all() const {
+    return max(max(max(m[0], m[1]), max(m[2], m[3])), max(max(m[4], m[5]), max(m[6], m[7])));
+  }
+};
+template <>
+struct Largest<uint16_t> {
+  uint32_t m[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 4; j++) m[j] = 0;
+  }
+  __device__ __forceinline__ void take(const Eight<uint16_t>& v) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) m[j] = pkmax_u16(m[j], v.a[j] & 0x7FFF7FFFu);
+  }
+  __device__ __forceinline__ void fold(int lanes) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) m[j] = pkmax_u16(m[j], (uint32_t)__shfl_xor((int)m[j], lanes));
+  }
+  __device__ __forceinline__ uint32_t of(int j) const { return (j & 1) ? m[j >> 1] & 0xFFFF0000u : m[j >> 1] << 16; }
+  __device__ __forceinline__ uint32_t all() const { return hmax_u16x2(pkmax_u16(pkmax_u16(m[0], m[1]), pkmax_u16(m[2], m[3]))) << 16; }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t largest_of(const Eight<T>& v) {
+  Largest<T> l;
+  l.clear();
+  l.take(v);
+  return l.all();
+}
 
 // largest of 16 lanes of a DPP row
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
@@ -59,34 +127,32 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, dpp_mirror(v));
 }
 
-// amax as fp32 bits: magnitudes compare as integers, with NaN above infinity
-__device__ __forceinline__ float amax_of(uint32_t m) { return __uint_as_float(max(m, kAmaxFloor)); }
-
-// one code's quotient: d = amax / 512, r = 1 / d (both rounded to nearest)
-__device__ __forceinline__ float quotient(float x, float d, float r) {
-  const float xs = x * 0.875f;
-  const float y0 = xs * r;
-  const float y = __builtin_fmaf(__builtin_fmaf(-y0, d, xs), r, y0);
-  return __builtin_copysignf(y, x);  // (the step loses a zero's sign)
-}
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
-}
-// eight codes of one block's elements; a block with an infinity or a NaN divides
-__device__ __forceinline__ uint2 encode8(const float* x, float amax) {
-  const float d = amax * 0x1p-9f;
-  float y[8];
-  if (__builtin_expect(__float_as_uint(amax) >= kInf, 0)) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = x[j] * 0.875f / d;
-  } else {
-    const float r = 1.f / d;
-#pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = quotient(x[j], d, r);
+// What a block's elements are divided by: d = amax / 512 and its reciprocal, both
+// rounded to nearest.  With an infinite amax (r = 0) the step must not see d: the
+// finite elements' quotients are 0 then, and the infinities' 0 x inf, a NaN.
+struct Divisor {
+  float amax, d, r;
+  __device__ __forceinline__ explicit Divisor(uint32_t m) {
+    amax = __uint_as_float(max(m, kAmaxFloor));
+    const float whole = amax * 0x1p-9f;
+    r = 1.f / whole;
+    d = m >= kInf ? 0.f : whole;
   }
-  return make_uint2(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
-}
+  __device__ __forceinline__ float of(float x) const {
+    const float xs = x * 0.875f;
+    const float y0 = xs * r;
+    const float y = __builtin_fmaf(__builtin_fmaf(-y0, d, xs), r, y0);
+    return __builtin_copysignf(y, x);  // (the step loses a zero's sign)
+  }
+  __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float e) const {
+    const int v = __builtin_amdgcn_cvt_pk_fp8_f32(of(a), of(b), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(of(c), of(e), v, true);
+  }
+  template <typename T>
+  __device__ __forceinline__ uint2 codes8(const Eight<T>& v) const {
+    return make_uint2(codes4(v.at(0), v.at(1), v.at(2), v.at(3)), codes4(v.at(4), v.at(5), v.at(6), v.at(7)));
+  }
+};
 
 // Row copy with 1 x 128 blocks.  16 lanes take a block; the workgroup's 16
 // groups take 16 rows, so that their scales, which lie next to each other
@@ -106,14 +172,10 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T* __restrict__ x,
   const int64_t last = min((chunk + 1) * per_chunk, Cb);
   for (int64_t b = chunk * per_chunk; b < last; b++) {
     const int64_t col = b * kB + c;
-    float v[8];
-    load8(xr + col, (int)min<int64_t>(C - col, 8), v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; j++) m = max(m, mag(v[j]));
-    const float amax = amax_of(max16(m));
-    *reinterpret_cast<uint2*>(qr + col) = encode8(v, amax);
-    if (c == 0) sr[b * R] = amax / kMaxCode;
+    const Eight<T> v = load8(xr + col, (int)min<int64_t>(C - col, 8));
+    const Divisor by(max16(largest_of(v)));
+    *reinterpret_cast<uint2*>(qr + col) = by.codes8(v);
+    if (c == 0) sr[b * R] = by.amax / kMaxCode;
   }
 }
 
@@ -158,95 +220,74 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(const T* __restrict__ x,
   const int ncols = (int)min<int64_t>(C - col0, kB);
   x += (int64_t)blockIdx.y * x_stride;
 
-  float v[8][8];
+  Eight<T> v[8];
   const int n = min(max(ncols - 8 * c, 0), 8);
   const T* xp = x + row0 * ldx + col0 + 8 * c;
 #pragma unroll
-  for (int p = 0; p < 8; p++) load8(xp + (int64_t)(8 * i + p) * ldx, 8 * i + p < nrows ? n : 0, v[p]);
+  for (int p = 0; p < 8; p++) v[p] = load8(xp + (int64_t)(8 * i + p) * ldx, 8 * i + p < nrows ? n : 0);
 
-  uint32_t cm[8];  // columns' magnitudes
+  Largest<T> cm;  // of the thread's columns
+  cm.clear();
 #pragma unroll
-  for (int j = 0; j < 8; j++) cm[j] = 0;
-  uint32_t rm[8];
-#pragma unroll
-  for (int p = 0; p < 8; p++) {
-    rm[p] = 0;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      rm[p] = max(rm[p], mag(v[p][j]));
-      cm[j] = max(cm[j], mag(v[p][j]));
-    }
-  }
-  float tile_amax = 0.f;
+  for (int p = 0; p < 8; p++) cm.take(v[p]);
+  uint32_t tile_max = 0;
   if constexpr (TILE128) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int p = 0; p < 8; p++) m = max(m, rm[p]);
-    m = max16(m);
+    uint32_t m = max16(cm.all());
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     if ((t & 63) == 0) part[wave][0] = m;
     __syncthreads();
-    tile_amax = amax_of(max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0])));
+    tile_max = max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0]));
     if (t == 0) {
-      if constexpr (ROW) s_row[((int64_t)blockIdx.y * Cb + ct) * Rb + rt] = tile_amax / kMaxCode;
-      if constexpr (COLT) s_colT[((int64_t)blockIdx.y * Rb + rt) * Cb + ct] = tile_amax / kMaxCode;
+      const float scale = __uint_as_float(max(tile_max, kAmaxFloor)) / kMaxCode;
+      if constexpr (ROW) s_row[((int64_t)blockIdx.y * Cb + ct) * Rb + rt] = scale;
+      if constexpr (COLT) s_colT[((int64_t)blockIdx.y * Rb + rt) * Cb + ct] = scale;
     }
   } else if constexpr (COLT) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 16));
-      cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32));
-    }
+    cm.fold(16);
+    cm.fold(32);
     if ((t & 63) < 16) {
-      *reinterpret_cast<uint4*>(&part[wave][8 * c]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
-      *reinterpret_cast<uint4*>(&part[wave][8 * c + 4]) = make_uint4(cm[4], cm[5], cm[6], cm[7]);
-    }
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      cm[j] = max(max(part[0][8 * c + j], part[1][8 * c + j]), max(part[2][8 * c + j], part[3][8 * c + j]));
+      for (int j = 0; j < 8; j++) part[wave][8 * c + j] = cm.of(j);
+    }
   }
 
-  if constexpr (ROW) {
+  uint2 code[TILE128 ? 8 : 1];
+  if constexpr (ROW || TILE128) {
+    const Divisor tile_by(tile_max);
     uint8_t* qp = q_row + ((int64_t)blockIdx.y * R + row0) * Cp + col0 + 8 * c;
 #pragma unroll
     for (int p = 0; p < 8; p++) {
       const int r = 8 * i + p;
-      const float amax = TILE128 ? tile_amax : amax_of(max16(rm[p]));
-      const uint2 code = encode8(v[p], amax);
-      if constexpr (TILE128 && COLT) {  // the same codes both ways
-        *reinterpret_cast<uint2*>(&v[p][0]) = code;
-      }
-      if (r < nrows) {
-        *reinterpret_cast<uint2*>(qp + (int64_t)r * Cp) = code;
-        if (!TILE128 && c == 0) s_row[((int64_t)blockIdx.y * Cb + ct) * R + row0 + r] = amax / kMaxCode;
+      const Divisor by = TILE128 ? tile_by : Divisor(max16(largest_of(v[p])));
+      const uint2 w = by.codes8(v[p]);
+      if constexpr (TILE128) code[p] = w;  // the same codes both ways
+      if (ROW && r < nrows) {
+        *reinterpret_cast<uint2*>(qp + (int64_t)r * Cp) = w;
+        if (!TILE128 && c == 0) s_row[((int64_t)blockIdx.y * Cb + ct) * R + row0 + r] = by.amax / kMaxCode;
       }
     }
   }
   if constexpr (COLT) {
     const int64_t Rp = GROUPED ? ldq : Rb * kB;
+    if constexpr (!TILE128) __syncthreads();  // the waves' columns are in
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      uint2 code;
-      if constexpr (TILE128 && ROW) {  // byte j of the rows' codes
-        uint32_t w[8];
-#pragma unroll
-        for (int p = 0; p < 8; p++) w[p] = __float_as_uint(v[p][j >> 2]);
+      uint2 w;
+      if constexpr (TILE128) {  // byte j of the rows' codes
         const uint32_t sel = (uint32_t)(j & 3);
-        auto four = [&](uint32_t a, uint32_t b, uint32_t e, uint32_t f) {
-          const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0000u | sel | ((4u + sel) << 8));
-          const uint32_t hi = __builtin_amdgcn_perm(f, e, 0x0c0c0000u | sel | ((4u + sel) << 8));
-          return lo | (hi << 16);
+        auto two = [&](int p) {
+          const uint32_t a = j < 4 ? code[p].x : code[p].y, b = j < 4 ? code[p + 1].x : code[p + 1].y;
+          return __builtin_amdgcn_perm(b, a, 0x0c0c0000u | sel | ((4u + sel) << 8));
         };
-        code = make_uint2(four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7]));
+        w = make_uint2(two(0) | (two(2) << 16), two(4) | (two(6) << 16));
       } else {
-        float col[8];
-#pragma unroll
-        for (int p = 0; p < 8; p++) col[p] = v[p][j];
-        code = encode8(col, TILE128 ? tile_amax : amax_of(cm[j]));
+        const int k = 8 * c + j;
+        const Divisor by(max(max(part[0][k], part[1][k]), max(part[2][k], part[3][k])));
+        w = make_uint2(by.codes4(v[0].at(j), v[1].at(j), v[2].at(j), v[3].at(j)),
+                       by.codes4(v[4].at(j), v[5].at(j), v[6].at(j), v[7].at(j)));
       }
-      turned[(8 * c + j) * 16 + (i ^ c)] = code;
+      turned[(8 * c + j) * 16 + (i ^ c)] = w;
     }
     __syncthreads();
     if (!turn) return;
@@ -262,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(const T* __restrict__ x,
     if constexpr (!TILE128) {
       if (t < ncols) {
         const uint32_t m = max(max(part[0][t], part[1][t]), max(part[2][t], part[3][t]));
-        s_colT[((int64_t)blockIdx.y * (Rp / kB) + out0 / kB) * C + col0 + t] = amax_of(m) / kMaxCode;
+        s_colT[((int64_t)blockIdx.y * (Rp / kB) + out0 / kB) * C + col0 + t] = __uint_as_float(max(m, kAmaxFloor)) / kMaxCode;
       }
     }
   }
