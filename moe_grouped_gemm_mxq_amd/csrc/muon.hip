@@ -36,10 +36,9 @@ namespace mxq {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 
-constexpr int kStageK = 64;     // fp16 elements of a tile row in a stage (128 bytes)
 constexpr float kScaleA = 16384.f;
 constexpr int kMaxSide = 1 << 20;
 constexpr int kThreads = 256;
@@ -47,34 +46,43 @@ constexpr int kMaxParts = 256;  // partial sums of squares of a matrix
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// Where a matrix's operands lie.  lo arrays hold what fp16 leaves of hi ones.
+// An operand's row of K numbers in fp16.  Where products are taken three times
+// (SPLIT), the high and the low halves of 32 numbers lie side by side in a
+// 128-byte line, so that a stage's line feeds all three; else it is the high halves.
+template <bool SPLIT>
+struct Row {
+  static constexpr int kWide = SPLIT ? 2 : 1;  // fp16 numbers an element takes
+  static __host__ __device__ __forceinline__ int64_t at(int64_t k) { return SPLIT ? (k >> 5) * 64 + (k & 31) : k; }
+  static constexpr int kLow = 32;  // from a high half to its low one
+};
+
+// Where a matrix's operands lie.
 struct Space {
   int64_t lo, hi, Lp, Hp;  // sides, and rounded up to 64 (zeros there)
-  _Float16 *x, *xl;        // [batch][Lp][Hp]
-  _Float16 *t, *tl;        // [batch][Hp][Lp], this iteration's
-  _Float16 *t2, *tl2;      // and the next one's
-  _Float16 *a, *al, *b, *bl;  // [batch][Lp][Lp]
+  _Float16* x;             // [batch][Lp] rows of Hp
+  _Float16* xl;            // what fp16 leaves of them, [batch][Lp][Hp], where the rows do not hold it
+  _Float16 *t, *t2;        // [batch][Hp] rows of Lp: the transpose, this iteration's and the next one's
+  _Float16 *a, *b;         // [batch][Lp] rows of Lp
   double* parts;           // [batch][kMaxParts]
 };
 
 // total bytes; fills sp where base is given
 int64_t lay_out(Space* sp, uint8_t* base, int64_t batch, int64_t R, int64_t C, bool split) {
   const int64_t lo = R < C ? R : C, hi = R < C ? C : R;
-  const int64_t Lp = up64(lo), Hp = up64(hi);
+  const int64_t Lp = up64(lo), Hp = up64(hi), wide = split ? 2 : 1;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += (bytes + 255) / 256 * 256;
     return base ? base + here : nullptr;
   };
-  auto half = [&](int64_t n, bool used) { return used ? reinterpret_cast<_Float16*>(take(batch * n * 2)) : nullptr; };
+  auto half = [&](int64_t n) { return reinterpret_cast<_Float16*>(take(batch * n * 2)); };
   Space s;
   s.lo = lo, s.hi = hi, s.Lp = Lp, s.Hp = Hp;
-  s.x = half(Lp * Hp, true), s.xl = half(Lp * Hp, true);
-  s.t = half(Lp * Hp, true), s.tl = half(Lp * Hp, split);
-  s.t2 = half(Lp * Hp, true), s.tl2 = half(Lp * Hp, split);
-  s.a = half(Lp * Lp, true), s.al = half(Lp * Lp, split);
-  s.b = half(Lp * Lp, true), s.bl = half(Lp * Lp, split);
+  s.x = half(Lp * Hp * wide);
+  s.xl = split ? nullptr : half(Lp * Hp);
+  s.t = half(Lp * Hp * wide), s.t2 = half(Lp * Hp * wide);
+  s.a = half(Lp * Lp * wide), s.b = half(Lp * Lp * wide);
   s.parts = reinterpret_cast<double*>(take(batch * kMaxParts * 8));
   if (sp) *sp = s;
   return at;
@@ -159,13 +167,15 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
   lo = (_Float16)(v - (float)hi);
 }
 
-// u / (|u| + eps) times S in fp16, both ways round: 64 x 64 of [R][C], its high
-// and low halves along the rows (`same`) and turned through LDS (`turn`).
-template <typename G, bool MOMENTUM>
+// u / (|u| + eps) times S, both ways round: 64 x 64 of [R][C], along its rows
+// (`same`) and turned through LDS (`turn`); low: where the low halves of X go that
+// its rows do not hold.
+template <typename G, bool MOMENTUM, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, int64_t C, int64_t Rp, int64_t Cp, int nparts,
                                                          float eps, float S, const double* __restrict__ parts,
-                                                         _Float16* __restrict__ same, _Float16* __restrict__ same_l,
-                                                         _Float16* __restrict__ turn, _Float16* __restrict__ turn_l) {
+                                                         _Float16* __restrict__ same, _Float16* __restrict__ same_low,
+                                                         _Float16* __restrict__ turn, _Float16* __restrict__ turn_low) {
+  typedef Row<SPLIT> L;
   __shared__ float tile[64][65];
   __shared__ double waves[kThreads / 64];
   float lr = 0.f, scale = s.grad_scale;
@@ -181,6 +191,13 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
   const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
   const int64_t base = blockIdx.y * s.n, out = blockIdx.y * Rp * Cp;
   const int c = t & 63;
+  auto put = [&](_Float16* rows, _Float16* low, int64_t row, int64_t width, int64_t k, float v) {
+    _Float16 hi, lo;
+    split_half(v, hi, lo);
+    rows[(out + row * width) * L::kWide + L::at(k)] = hi;
+    if constexpr (SPLIT) rows[(out + row * width) * L::kWide + L::at(k) + L::kLow] = lo;
+    else if (low) low[out + row * width + k] = lo;
+  };
 #pragma unroll 4
   for (int k = 0; k < 16; k++) {
     const int64_t r = r0 + 4 * k + (t >> 6);
@@ -191,19 +208,13 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
     }
     const float v = u[0] * inv;
     tile[4 * k + (t >> 6)][c] = v;
-    _Float16 hi, lo;
-    split_half(v, hi, lo);
-    same[out + r * Cp + c0 + c] = hi;
-    if (same_l) same_l[out + r * Cp + c0 + c] = lo;
+    put(same, same_low, r, Cp, c0 + c, v);
   }
   __syncthreads();
 #pragma unroll 4
   for (int k = 0; k < 16; k++) {
     const int cc = 4 * k + (t >> 6);
-    _Float16 hi, lo;
-    split_half(tile[c][cc], hi, lo);
-    turn[out + (c0 + cc) * Rp + r0 + c] = hi;
-    if (turn_l) turn_l[out + (c0 + cc) * Rp + r0 + c] = lo;
+    put(turn, turn_low, c0 + cc, Rp, r0 + c, tile[c][cc]);
   }
 }
 
@@ -211,17 +222,17 @@ enum Product { kGram, kSquare, kUpdate, kLast };
 
 // D[p][q] = sum_k P[p][k] Q[q][k]; rows, columns and K of one matrix, in elements.
 struct Args {
-  const _Float16 *P, *Pl, *Q, *Ql;  // operands and their low halves
+  const _Float16 *P, *Q;  // operands
   int64_t rows_p, rows_q, K;
   int tiles_p, tiles_q;
   // gram, square: A (read by square) and the result
-  const _Float16 *a, *al;
+  const _Float16* a;
   float of_sum, of_a, on_diag;  // result = of_sum * sum + of_a * A + on_diag on the diagonal
-  _Float16 *out, *out_l;
+  _Float16* out;
   // update: X (read and written), its transpose
   float e;
-  _Float16 *x, *xl, *t, *tl;
-  int64_t ldx, ldt, x_stride, t_stride;
+  _Float16 *x, *xl, *t;
+  int64_t ldx, ldt;
   // last: the result's matrix
   void* param;
   uint16_t* copy;
@@ -232,29 +243,35 @@ struct Args {
   const mxq_adamw_control* control;
 };
 
-template <int BP, int BQ, int WAVES_P, int WAVES_Q>
+// Output tile of a workgroup: BP rows of P by BQ rows of Q, WAVES_P x WAVES_Q waves,
+// STAGES stages in LDS.
+template <int BP, int BQ, int WAVES_P, int WAVES_Q, int STAGES>
 struct Shape {
-  static constexpr int kP = BP, kQ = BQ, kWavesP = WAVES_P;
+  static constexpr int kP = BP, kQ = BQ, kWavesP = WAVES_P, kStages = STAGES;
   static constexpr int kWaves = WAVES_P * WAVES_Q, kThreads = 64 * kWaves;
   static constexpr int WP = BP / WAVES_P, WQ = BQ / WAVES_Q;
   static constexpr int TP = WP / 32, TQ = WQ / 32;  // 32 x 32 blocks of a wave
-  static constexpr int kLoadsP = BP / 8 / kWaves, kLoadsQ = BQ / 8 / kWaves;
+  static constexpr int kLoadsP = BP / 8 / kWaves, kLoadsQ = BQ / 8 / kWaves, kLoads = kLoadsP + kLoadsQ;
   static constexpr int kBytesP = BP * 128, kBytesQ = BQ * 128, kStage = kBytesP + kBytesQ;
+  static_assert(STAGES >= 2 && STAGES <= 4, "the stages are spelled out");
   static_assert(kLoadsP % 2 == 0 && kLoadsQ % 2 == 0, "a load's parity is its place's");
 };
 
-__device__ __forceinline__ v8h load_half8(const uint8_t* st, int r0, int s, int lane) {
-  return *reinterpret_cast<const v8h*>(st + swz(r0 + (lane & 31), 2 * s + (lane >> 5)));
+// eight numbers of a lane for a 32 x 32 x 16 instruction: row r0 + lane % 32, 16-byte chunk c + lane / 32
+__device__ __forceinline__ v8h load_half8(const uint8_t* st, int r0, int c, int lane) {
+  return *reinterpret_cast<const v8h*>(st + swz(r0 + (lane & 31), c + (lane >> 5)));
 }
 
-// SPLIT: the reduction runs three times, over high x high, high x low, low x high.
 // T: the last product's parameter (float or bf16's bits); STEP: it is updated
-// rather than overwritten.
+// rather than overwritten.  A stage is a 128-byte line of every row of the tile:
+// 64 numbers, or the halves of 32.
 template <int WHAT, bool SPLIT, class S, typename T = float, bool STEP = false>
 __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
-  constexpr int TP = S::TP, TQ = S::TQ;
-  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStage];
+  typedef Row<SPLIT> L;
+  constexpr int TP = S::TP, TQ = S::TQ, NS = S::kStages;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage], stage1[S::kStage], stage2[NS > 2 ? S::kStage : 16],
+      stage3[NS > 3 ? S::kStage : 16];
+  uint8_t* const stages[4] = {stage0, stage1, stage2, stage3};
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave % S::kWavesP, wq = wave / S::kWavesP;
@@ -271,7 +288,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
   const int64_t p0 = (int64_t)pt * S::kP, q0 = (int64_t)qt * S::kQ;
   const int np = (int)min<int64_t>(S::kP, p.rows_p - p0), nq = (int)min<int64_t>(S::kQ, p.rows_q - q0);
 
-  const uint32_t ld = (uint32_t)p.K * 2;
+  const uint32_t ld = (uint32_t)p.K * 2 * L::kWide;
   uint32_t offP[S::kLoadsP], offQ[S::kLoadsQ];
 #pragma unroll
   for (int j = 0; j < S::kLoadsP; j++)
@@ -279,26 +296,18 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
 #pragma unroll
   for (int j = 0; j < S::kLoadsQ; j++)
     offQ[j] = (uint32_t)min((wave * S::kLoadsQ + j) * 8 + (lane >> 3), nq - 1) * ld + dma_chunk(j, lane) * 16;
-  const int64_t at_p = (b * p.rows_p + p0) * p.K, at_q = (b * p.rows_q + q0) * p.K;
-  const int nk = (int)(p.K / kStageK), ns = SPLIT ? 3 * nk : nk;
-  auto issue = [&](uint8_t* st, int s) {
-    int k = s;
-    const _Float16 *P = p.P, *Q = p.Q;
-    if constexpr (SPLIT) {
-      if (s >= 2 * nk) {
-        k -= 2 * nk;
-        P = p.Pl;
-      } else if (s >= nk) {
-        k -= nk;
-        Q = p.Ql;
-      }
-    }
-    const uint8_t* a = reinterpret_cast<const uint8_t*>(P + at_p + (int64_t)k * kStageK);
-    const uint8_t* c = reinterpret_cast<const uint8_t*>(Q + at_q + (int64_t)k * kStageK);
-#pragma unroll
-    for (int j = 0; j < S::kLoadsP; j++) load_lds16(a + offP[j], st + (wave * S::kLoadsP + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < S::kLoadsQ; j++) load_lds16(c + offQ[j], st + S::kBytesP + (wave * S::kLoadsQ + j) * 1024);
+  const uint8_t* const baseP = reinterpret_cast<const uint8_t*>(p.P) + (b * p.rows_p + p0) * ld;
+  const uint8_t* const baseQ = reinterpret_cast<const uint8_t*>(p.Q) + (b * p.rows_q + q0) * ld;
+  const int ns = (int)(ld / 128);
+  auto load = [&](uint8_t* st, int s, int n) {
+    if (n < S::kLoadsP)
+      load_lds16(baseP + (int64_t)s * 128 + offP[n], st + (wave * S::kLoadsP + n) * 1024);
+    else
+      load_lds16(baseQ + (int64_t)s * 128 + offQ[n - S::kLoadsP], st + S::kBytesP + (wave * S::kLoadsQ + n - S::kLoadsP) * 1024);
+  };
+  auto meet = [&]() {
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
   v16f acc[TP][TQ];
 #pragma unroll
@@ -307,134 +316,254 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
     for (int j = 0; j < TQ; j++)
 #pragma unroll
       for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
-  auto compute = [&](const uint8_t* st) {
-#pragma unroll
-    for (int s = 0; s < 4; s++) {
-      v8h fp[TP], fq[TQ];
-#pragma unroll
-      for (int i = 0; i < TP; i++) fp[i] = load_half8(st, wp * S::WP + 32 * i, s, lane);
-#pragma unroll
-      for (int j = 0; j < TQ; j++) fq[j] = load_half8(st + S::kBytesP, wq * S::WQ + 32 * j, s, lane);
-#pragma unroll
-      for (int i = 0; i < TP; i++)
-#pragma unroll
-        for (int j = 0; j < TQ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
-    }
-  };
-  auto step = [&](uint8_t* cur, uint8_t* next, int s) {
-    if (s + 1 < ns) issue(next, s + 1);
-    compute(cur);
-    wait_vmcnt<0>();
-    wait_lgkmcnt0();
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  issue(stage0, 0);
-  wait_vmcnt<0>();
-  __builtin_amdgcn_s_barrier();
-  for (int s = 0; s < ns; s += 2) {
-    step(stage0, stage1, s);
-    if (s + 1 < ns) step(stage1, stage0, s + 1);
-  }
 
-  float lr = 0.f, rate = 0.f, decay = 0.f;
+  auto read = [&](const uint8_t* st, int chunk, v8h (&fp)[TP], v8h (&fq)[TQ]) {
+#pragma unroll
+    for (int i = 0; i < TP; i++) fp[i] = load_half8(st, wp * S::WP + 32 * i, chunk, lane);
+#pragma unroll
+    for (int j = 0; j < TQ; j++) fq[j] = load_half8(st + S::kBytesP, wq * S::WQ + 32 * j, chunk, lane);
+  };
+  auto multiply = [&](const v8h (&fp)[TP], const v8h (&fq)[TQ]) {
+#pragma unroll
+    for (int i = 0; i < TP; i++)
+#pragma unroll
+      for (int j = 0; j < TQ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+  };
+  // Stage s, which is in st, while stage s + NS - 1 is loaded to next (past the last
+  // one, the last again: every stage has the same loads in flight, and no branch
+  // parts them from the matrix instructions).  Each part's numbers are read while the
+  // part before it multiplies.
+  constexpr int kM = TP * TQ, kD = TP + TQ, kG = (S::kLoads + 1) / 2;
+  auto stage = [&](const uint8_t* st, uint8_t* next, int s) {
+    const int ahead = min(s + NS - 1, ns - 1);
+    auto load_half_of = [&](int which) {
+#pragma unroll
+      for (int n = which * kG; n < (which + 1) * kG && n < S::kLoads; n++) load(next, ahead, n);
+    };
+    if constexpr (SPLIT) {
+      v8h hp[2][TP], hq[2][TQ], lp[TP], lq[TQ];
+      read(st, 0, hp[0], hq[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      read(st, 4, lp, lq);
+      multiply(hp[0], hq[0]);
+      load_half_of(0);
+      interleave<kM, 0, kD, kG>();
+      __builtin_amdgcn_sched_barrier(0);
+      read(st, 2, hp[1], hq[1]);
+      multiply(hp[0], lq);
+      multiply(lp, hq[0]);
+      load_half_of(1);
+      interleave<2 * kM, 0, kD, S::kLoads - kG>();
+      __builtin_amdgcn_sched_barrier(0);
+      read(st, 6, lp, lq);
+      multiply(hp[1], hq[1]);
+      interleave<kM, 0, kD, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(hp[1], lq);
+      multiply(lp, hq[1]);
+    } else {
+      v8h fp[2][TP], fq[2][TQ];
+      read(st, 0, fp[0], fq[0]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        if (k < 3) read(st, 2 * k + 2, fp[(k + 1) & 1], fq[(k + 1) & 1]);
+        multiply(fp[k & 1], fq[k & 1]);
+        if (k == 0) {
+          load_half_of(0);
+          interleave<kM, 0, kD, kG>();
+        } else if (k == 1) {
+          load_half_of(1);
+          interleave<kM, 0, kD, S::kLoads - kG>();
+        } else if (k == 2) {
+          interleave<kM, 0, kD, 0>();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_vmcnt<(NS - 2) * S::kLoads>();  // the next stage has landed
+    wait_lgkmcnt0();
+    meet();
+  };
+#pragma unroll
+  for (int s = 0; s < NS - 1; s++)
+#pragma unroll
+    for (int n = 0; n < S::kLoads; n++) load(stages[s], min(s, ns - 1), n);
+  wait_vmcnt<(NS - 2) * S::kLoads>();
+  meet();
+  for (int s0 = 0; s0 < ns; s0 += NS) {
+#pragma unroll
+    for (int u = 0; u < NS; u++)
+      if (s0 + u < ns) stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
+  }
+  wait_vmcnt<0>();  // the LDS is used again below
+  meet();
+
+  // The sums go through LDS (every wave by itself, kP2 x 32 TQ numbers at a time) so
+  // that what they are combined with, and where they go, is read and written in whole
+  // lines both ways round.
+  float rate = 0.f, decay = 0.f;
   if constexpr (WHAT == kLast && STEP) {
-    lr = p.lr;
-    float unused = p.grad_scale;
+    float lr = p.lr, unused = p.grad_scale;
     if (!step_of(p.control, lr, unused)) return;
     rate = lr * p.scale;
     decay = 1.f - lr * p.decay;
   }
-  // lane l holds D[8 (e / 4) + 4 (l / 32) + e % 4][l % 32] of each 32 x 32 block
+  constexpr int kI = TP < 2 ? 1 : 2, kPw = 32 * kI, kQw = 32 * TQ;
+  constexpr int kPerStage = S::kStage / (kPw * kQw * 4);
+  static_assert(2 * kPerStage >= S::kWaves, "two stages hold every wave's numbers");
+  float* const mine = reinterpret_cast<float*>((wave < kPerStage ? stage0 : stage1) + wave % kPerStage * (kPw * kQw * 4));
+  // element (row, col) of rows of `width`: 16-byte chunks by the row's last bits
+  auto spot = [&](int row, int col, int width) { return row * width + (((col >> 2) ^ (row & (width / 4 - 1) & 15)) << 2) + (col & 3); };
+  // rows of `width`, eight numbers of one a lane
+  auto each_row = [&](int rows, int width, auto&& body) {
+    const int per = width / 8, step = 64 / per;
 #pragma unroll
-  for (int j = 0; j < TQ; j++) {
-    const int qq = wq * S::WQ + 32 * j + (lane & 31);
-    if (qq >= nq) continue;
-    const int64_t q = q0 + qq;
+    for (int r = 0; r < rows; r += step) body(r + lane / per, lane % per * 8);
+  };
+  auto get8 = [&](int row, int col, int width, float* v) {
+    const v4f a = *reinterpret_cast<const v4f*>(mine + spot(row, col, width)), c = *reinterpret_cast<const v4f*>(mine + spot(row, col + 4, width));
 #pragma unroll
-    for (int i = 0; i < TP; i++) {
+    for (int e = 0; e < 4; e++) v[e] = a[e], v[e + 4] = c[e];
+  };
+  auto between = [&]() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+  // eight halves of a row of an operand, from element k on
+  auto store_halves = [&](_Float16* row, _Float16* low, int64_t k, const float* v) {
+    v8h h, l;
 #pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int pp = wp * S::WP + 32 * i + 8 * r + 4 * (lane >> 5);
-        if (pp >= np) continue;  // (rows come in multiples of 64)
-        const int64_t row = p0 + pp;
-        float v[4];
+    for (int e = 0; e < 8; e++) {
+      _Float16 hi, lo;
+      split_half(v[e], hi, lo);
+      h[e] = hi;
+      l[e] = lo;
+    }
+    *reinterpret_cast<v8h*>(row + L::at(k)) = h;
+    if constexpr (SPLIT) *reinterpret_cast<v8h*>(row + L::at(k) + L::kLow) = l;
+    else if (low) *reinterpret_cast<v8h*>(low + k) = l;
+  };
+  auto load_halves = [&](const _Float16* row, const _Float16* low, int64_t k, float* v) {
+    const v8h h = *reinterpret_cast<const v8h*>(row + L::at(k));
+    v8h l = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (SPLIT) l = *reinterpret_cast<const v8h*>(row + L::at(k) + L::kLow);
+    else if (low) l = *reinterpret_cast<const v8h*>(low + k);
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = acc[i][j][4 * r + e];
-        if constexpr (WHAT == kGram || WHAT == kSquare) {
-          const int64_t at = (b * p.rows_p + q) * p.rows_p + row;
-          if constexpr (WHAT == kSquare) {
-            const v4h a = *reinterpret_cast<const v4h*>(p.a + at);
-            v4h al = {0, 0, 0, 0};
-            if constexpr (SPLIT) al = *reinterpret_cast<const v4h*>(p.al + at);
+    for (int e = 0; e < 8; e++) v[e] = (float)h[e] + (float)l[e];
+  };
+  // eight results of one row of the parameter, from column k on
+  auto finish = [&](int64_t row, int64_t k, int64_t rows, int64_t width, const float* x) {
+    if (row >= rows || k >= width) return;
+    T* param = static_cast<T*>(p.param) + b * p.n + row * width + k;
+    uint16_t* copy = STEP && p.copy ? p.copy + b * p.n + row * width + k : nullptr;
+    float y[8];
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-              v[e] = __builtin_fmaf(p.of_a, (float)a[e] + (float)al[e], p.of_sum * v[e]) + (row + e == q ? p.on_diag : 0.f);
-          } else {
+    for (int e = 0; e < 8; e++) y[e] = x[e] * p.from_x;
+    if (k + 8 <= width) {
+      if constexpr (STEP) {
+        float old[8];
+        constexpr int W = sizeof(T) == 4 ? 4 : 8;
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] *= p.of_sum;
-          }
-          v4h h, l;
+        for (int e = 0; e < 8; e += W) unpack(load_raw<W, false>(param + e), old + e);
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            _Float16 hi, lo;
-            split_half(v[e], hi, lo);
-            h[e] = hi;
-            l[e] = lo;
-          }
-          *reinterpret_cast<v4h*>(p.out + at) = h;
-          if constexpr (SPLIT) *reinterpret_cast<v4h*>(p.out_l + at) = l;
-          if (pt != qt) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const int64_t mirror = (b * p.rows_p + row + e) * p.rows_p + q;
-              p.out[mirror] = h[e];
-              if constexpr (SPLIT) p.out_l[mirror] = l[e];
-            }
-          }
-        } else {
-          const int64_t at = b * p.x_stride + q * p.ldx + row;
-          const v4h xh = *reinterpret_cast<const v4h*>(p.x + at), xl = *reinterpret_cast<const v4h*>(p.xl + at);
-#pragma unroll
-          for (int e = 0; e < 4; e++) v[e] = __builtin_fmaf(p.e, (float)xh[e] + (float)xl[e], p.of_sum * v[e]);
-          if constexpr (WHAT == kUpdate) {
-            v4h h, l;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              _Float16 hi, lo;
-              split_half(v[e], hi, lo);
-              h[e] = hi;
-              l[e] = lo;
-            }
-            *reinterpret_cast<v4h*>(p.x + at) = h;
-            *reinterpret_cast<v4h*>(p.xl + at) = l;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const int64_t turned = b * p.t_stride + (row + e) * p.ldt + q;
-              p.t[turned] = h[e];
-              if constexpr (SPLIT) p.tl[turned] = l[e];
-            }
-          } else {
-            if (q >= p.lo) continue;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              if (row + e >= p.hi) continue;
-              const int64_t o = b * p.n + (p.tall ? (row + e) * p.lo + q : q * p.hi + row + e);
-              T* param = static_cast<T*>(p.param);
-              float y = v[e] * p.from_x;
-              if constexpr (STEP) y = __builtin_fmaf(load_f(param, o), decay, -rate * y);
-              store_f(param, o, y);
-              if constexpr (STEP)
-                if (p.copy) store_f(p.copy, o, y);
-            }
-          }
-        }
+        for (int e = 0; e < 8; e++) y[e] = __builtin_fmaf(old[e], decay, -rate * y[e]);
       }
+      store_vec<8, false>(param, y);
+      if (STEP && copy) store_vec<8, false>(copy, y);
+    } else {
+      for (int e = 0; e < width - k; e++) {
+        if constexpr (STEP) y[e] = __builtin_fmaf(load_f(param, e), decay, -rate * y[e]);
+        store_f(param, e, y[e]);
+        if (STEP && copy) store_f(copy, e, y[e]);
+      }
+    }
+  };
+  const int64_t x_stride = p.ldx * p.ldt, a_stride = p.rows_p * p.rows_p;
+#pragma unroll
+  for (int i0 = 0; i0 < TP; i0 += kI) {
+    const int pp = wp * S::WP + 32 * i0, qq = wq * S::WQ;
+    if (pp >= np || qq >= nq) continue;  // (rows come in multiples of 64)
+    const int64_t row_p = p0 + pp, row_q = q0 + qq;
+    between();
+    // along P: rows of Q
+    if constexpr (WHAT != kGram) {
+      each_row(kQw, kPw, [&](int r, int c) {
+        float v[8];
+        if constexpr (WHAT == kSquare)
+          load_halves(p.a + (b * a_stride + (row_q + r) * p.rows_p) * L::kWide, nullptr, row_p + c, v);
+        else
+          load_halves(p.x + (b * x_stride + (row_q + r) * p.ldx) * L::kWide, SPLIT ? nullptr : p.xl + b * x_stride + (row_q + r) * p.ldx,
+                      row_p + c, v);
+        *reinterpret_cast<v4f*>(mine + spot(r, c, kPw)) = v4f{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<v4f*>(mine + spot(r, c + 4, kPw)) = v4f{v[4], v[5], v[6], v[7]};
+      });
+      between();
+    }
+    // lane l holds D[8 (e / 4) + 4 (l / 32) + e % 4][l % 32] of each 32 x 32 block
+#pragma unroll
+    for (int i = i0; i < i0 + kI; i++)
+#pragma unroll
+      for (int j = 0; j < TQ; j++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int row = 32 * j + (lane & 31), col = 32 * (i - i0) + 8 * r + 4 * (lane >> 5);
+          v4f* at = reinterpret_cast<v4f*>(mine + spot(row, col, kPw));
+          v4f v;
+#pragma unroll
+          for (int e = 0; e < 4; e++) v[e] = p.of_sum * acc[i][j][4 * r + e];
+          if constexpr (WHAT != kGram) {
+            const v4f with = *at;
+            const float times = WHAT == kSquare ? p.of_a : p.e;
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = __builtin_fmaf(times, with[e], v[e]);
+          }
+          if constexpr (WHAT == kSquare) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] += row_p + col + e == row_q + row ? p.on_diag : 0.f;
+          }
+          if (!(WHAT == kLast && p.tall)) *at = v;
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[i][j][4 * r + e] = v[e];
+        }
+    between();
+    if (WHAT != kLast || !p.tall) {
+      each_row(kQw, kPw, [&](int r, int c) {
+        float v[8];
+        get8(r, c, kPw, v);
+        if constexpr (WHAT == kLast)
+          finish(row_q + r, row_p + c, p.lo, p.hi, v);
+        else if constexpr (WHAT == kUpdate)
+          store_halves(p.x + (b * x_stride + (row_q + r) * p.ldx) * L::kWide, SPLIT ? nullptr : p.xl + b * x_stride + (row_q + r) * p.ldx,
+                       row_p + c, v);
+        else
+          store_halves(p.out + (b * a_stride + (row_q + r) * p.rows_p) * L::kWide, nullptr, row_p + c, v);
+      });
+    }
+    if (WHAT == kUpdate || (WHAT == kLast && p.tall) || ((WHAT == kGram || WHAT == kSquare) && pt != qt)) {  // along Q: rows of P
+      between();
+#pragma unroll
+      for (int i = i0; i < i0 + kI; i++)
+#pragma unroll
+        for (int j = 0; j < TQ; j++)
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            mine[spot(32 * (i - i0) + 8 * (e / 4) + 4 * (lane >> 5) + e % 4, 32 * j + (lane & 31), kQw)] = acc[i][j][e];
+      between();
+      each_row(kPw, kQw, [&](int r, int c) {
+        float v[8];
+        get8(r, c, kQw, v);
+        if constexpr (WHAT == kLast)
+          finish(row_p + r, row_q + c, p.hi, p.lo, v);
+        else if constexpr (WHAT == kUpdate)
+          store_halves(p.t + (b * x_stride + (row_p + r) * p.ldt) * L::kWide, nullptr, row_q + c, v);
+        else
+          store_halves(p.out + (b * a_stride + (row_p + r) * p.rows_p) * L::kWide, nullptr, row_q + c, v);
+      });
     }
   }
 }
 
-typedef Shape<128, 128, 2, 2> Tile;
+typedef Shape<256, 256, 2, 4, 2> Large;
+typedef Shape<128, 128, 2, 2, 2> Medium;
+typedef Shape<64, 64, 2, 2, 4> Small;
 
 // what the host has checked
 struct Plan {
@@ -444,29 +573,38 @@ struct Plan {
   float eps;
 };
 
-template <int WHAT, bool SPLIT, typename T = float, bool STEP = false>
-hipError_t launch_product(Args& p, int64_t batch, hipStream_t st) {
-  p.tiles_p = (int)((p.rows_p + Tile::kP - 1) / Tile::kP);
-  p.tiles_q = (int)((p.rows_q + Tile::kQ - 1) / Tile::kQ);
+template <int WHAT, bool SPLIT, class S, typename T, bool STEP>
+hipError_t launch_shape(Args& p, int64_t batch, hipStream_t st) {
+  p.tiles_p = (int)((p.rows_p + S::kP - 1) / S::kP);
+  p.tiles_q = (int)((p.rows_q + S::kQ - 1) / S::kQ);
   const int64_t tiles = WHAT == kGram || WHAT == kSquare ? (int64_t)p.tiles_p * (p.tiles_p + 1) / 2 : (int64_t)p.tiles_p * p.tiles_q;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  product_kernel<WHAT, SPLIT, Tile, T, STEP><<<dim3((unsigned)tiles, (unsigned)batch), Tile::kThreads, 0, st>>>(p);
+  product_kernel<WHAT, SPLIT, S, T, STEP><<<dim3((unsigned)tiles, (unsigned)batch), S::kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 
-template <typename G, bool MOMENTUM>
-void launch_start(const Source& s, const Plan& pl, Space& sp, bool split, float S, hipStream_t st) {
+template <int WHAT, bool SPLIT, typename T = float, bool STEP = false>
+hipError_t launch_product(Args& p, int64_t batch, hipStream_t st) {
+  const char* env = getenv("MXQ_W");
+  int v = env ? atoi(env) : 0;
+  if (v) v = (v / (WHAT == kGram ? 100 : WHAT == kSquare ? 10 : 1)) % 10;
+  if (v == 1) return launch_shape<WHAT, SPLIT, Small, T, STEP>(p, batch, st);
+  if (v == 2) return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, batch, st);
+  if (v == 3) return launch_shape<WHAT, SPLIT, Large, T, STEP>(p, batch, st);
+  return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, batch, st);
+}
+
+template <typename G, bool MOMENTUM, bool SPLIT>
+void launch_start(const Source& s, const Plan& pl, Space& sp, float S, hipStream_t st) {
   const int64_t per = 4 * kThreads;
   int64_t parts = (s.n + per - 1) / per;
   if (parts > kMaxParts) parts = kMaxParts;
   momentum_kernel<G, MOMENTUM><<<dim3((unsigned)parts, (unsigned)pl.batch), kThreads, 0, st>>>(s, sp.parts);
   const int64_t Rp = up64(pl.R), Cp = up64(pl.C);
   const bool tall = pl.R > pl.C;
-  // (without the low halves of the transpose where only X's are read)
-  _Float16 *same = tall ? sp.t : sp.x, *turn = tall ? sp.x : sp.t;
-  _Float16 *same_l = tall ? (split ? sp.tl : nullptr) : sp.xl, *turn_l = tall ? sp.xl : (split ? sp.tl : nullptr);
-  start_kernel<G, MOMENTUM><<<dim3((unsigned)(Rp / 64 * (Cp / 64)), (unsigned)pl.batch), kThreads, 0, st>>>(
-      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, same, same_l, turn, turn_l);
+  start_kernel<G, MOMENTUM, SPLIT><<<dim3((unsigned)(Rp / 64 * (Cp / 64)), (unsigned)pl.batch), kThreads, 0, st>>>(
+      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, tall ? sp.t : sp.x, tall ? nullptr : sp.xl, tall ? sp.x : sp.t,
+      tall ? sp.xl : nullptr);
 }
 
 template <bool SPLIT, typename T, bool STEP>
@@ -478,27 +616,24 @@ hipError_t iterate(const Plan& pl, Space& sp, float S, Args last, hipStream_t st
     const int left = pl.steps - 1 - i;
     const float e = (float)(pl.a * (left == 0 ? 0.4375 : left == 1 ? 0.71875 : 1.0));
     Args g{};
-    g.P = g.Q = sp.x, g.Pl = g.Ql = sp.xl, g.rows_p = g.rows_q = sp.Lp, g.K = sp.Hp;
-    g.of_sum = kScaleA / (S * S), g.out = sp.a, g.out_l = sp.al;
+    g.P = g.Q = sp.x, g.rows_p = g.rows_q = sp.Lp, g.K = sp.Hp;
+    g.of_sum = kScaleA / (S * S), g.out = sp.a;
     hipError_t err = launch_product<kGram, SPLIT>(g, pl.batch, st);
     if (err != hipSuccess) return err;
     Args q{};
-    q.P = q.Q = sp.a, q.Pl = q.Ql = sp.al, q.rows_p = q.rows_q = q.K = sp.Lp, q.a = sp.a, q.al = sp.al;
+    q.P = q.Q = sp.a, q.rows_p = q.rows_q = q.K = sp.Lp, q.a = sp.a;
     q.of_sum = (float)(pl.c * scale_b / ((double)kScaleA * kScaleA)), q.of_a = (float)(pl.b * scale_b / kScaleA);
-    q.on_diag = (float)((pl.a - e) * scale_b), q.out = sp.b, q.out_l = sp.bl;
+    q.on_diag = (float)((pl.a - e) * scale_b), q.out = sp.b;
     err = launch_product<kSquare, SPLIT>(q, pl.batch, st);
     if (err != hipSuccess) return err;
     Args u = last;
-    u.P = sp.t, u.Pl = sp.tl, u.Q = sp.b, u.Ql = sp.bl, u.rows_p = sp.Hp, u.rows_q = u.K = sp.Lp;
+    u.P = sp.t, u.Q = sp.b, u.rows_p = sp.Hp, u.rows_q = u.K = sp.Lp;
     u.of_sum = 1.f / scale_b, u.e = e;
-    u.x = sp.x, u.xl = sp.xl, u.t = sp.t2, u.tl = sp.tl2, u.ldx = sp.Hp, u.ldt = sp.Lp;
-    u.x_stride = u.t_stride = sp.Lp * sp.Hp;
+    u.x = sp.x, u.xl = sp.xl, u.t = sp.t2, u.ldx = sp.Hp, u.ldt = sp.Lp;
     if (left) {
       err = launch_product<kUpdate, SPLIT>(u, pl.batch, st);
       _Float16* v = sp.t;
       sp.t = sp.t2, sp.t2 = v;
-      v = sp.tl;
-      sp.tl = sp.tl2, sp.tl2 = v;
     } else {
       err = launch_product<kLast, SPLIT, T, STEP>(u, pl.batch, st);
     }
@@ -516,11 +651,11 @@ hipError_t run(const Plan& pl, const Source& s, mxq_dtype gdt, mxq_dtype odt, Ar
   int log = (int)std::floor(0.5 * std::log2((double)sp.lo * (double)sp.hi));
   const float S = std::ldexp(1.f, log < 15 ? log : 15);
   if (gdt == MXQ_DT_F32) {
-    if (STEP) launch_start<float, true>(s, pl, sp, split, S, st);
-    else launch_start<float, false>(s, pl, sp, split, S, st);
+    if (split) launch_start<float, STEP, true>(s, pl, sp, S, st);
+    else launch_start<float, STEP, false>(s, pl, sp, S, st);
   } else {
-    if (STEP) launch_start<uint16_t, true>(s, pl, sp, split, S, st);
-    else launch_start<uint16_t, false>(s, pl, sp, split, S, st);
+    if (split) launch_start<uint16_t, STEP, true>(s, pl, sp, S, st);
+    else launch_start<uint16_t, STEP, false>(s, pl, sp, S, st);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

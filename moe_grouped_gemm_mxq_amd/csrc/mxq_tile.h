@@ -44,6 +44,20 @@ __device__ __forceinline__ void wait_vmcnt() {
 }
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt((15) | (3 << 14) | (0x7 << 4)); }
 
+// Order of what follows a scheduling barrier: M matrix instructions, and between
+// them, evenly, V vector instructions, D LDS reads and G global loads.
+template <int M, int V, int D, int G, int m = 0>
+__device__ __forceinline__ void interleave() {
+  if constexpr (m < M) {
+    constexpr int d = (m + 1) * D / M - m * D / M, g = (m + 1) * G / M - m * G / M, v = (m + 1) * V / M - m * V / M;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+    if constexpr (g > 0) __builtin_amdgcn_sched_group_barrier(0x010, g, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    interleave<M, V, D, G, m + 1>();
+  }
+}
+
 // Logical tile order: workgroups are dealt to the XCDs round robin, so remap
 // blockIdx so that each XCD walks a contiguous run of the logical order (tiles
 // that share operand panels then share that XCD's L2).
