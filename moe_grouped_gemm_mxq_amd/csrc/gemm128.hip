@@ -289,17 +289,6 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
       load_lds4(sp + s * spitch, st + S::kCodesA + S::kCodesB + wave * 256);
     }
   };
-  auto load_stage = [&](uint8_t* st, int s) {
-#pragma unroll
-    for (int n = 0; n < S::kLoads; n++) load(st, s, n);
-  };
-  // The stage after s has landed; the loads of those after it may be in flight.
-  auto next_landed = [&](int s) {
-    if (NS > 2 && s + NS - 1 < t.nkb)
-      wait_vmcnt<(NS - 2) * S::kLoads>();
-    else
-      wait_vmcnt<0>();
-  };
   auto meet = [&]() {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -314,9 +303,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
   typedef FragOf<F32> Frag;
   // loads of each of the wave's TN row blocks of B, so that all are out by about half of the stage
   constexpr int kPer = (S::kLoads + TN / 2) / TN + 1;
-  // stage s, which is in st; meanwhile stage s + NS - 1 is loaded to next
+  // Stage s, which is in st, while stage s + NS - 1 is loaded to next (past the last
+  // one, the last again: every stage has the same loads in flight, and no branch
+  // parts them from the matrix instructions).
   auto stage = [&](const uint8_t* st, uint8_t* next, int s) {
-    const bool more = s + NS - 1 < t.nkb;
+    const int ahead_s = min(s + NS - 1, t.nkb - 1);
     const float* sa_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + wm * S::WM;
     const float* sb_of = reinterpret_cast<const float*>(st + S::kCodesA + S::kCodesB) + S::BM + wn * S::WN;
     typename Frag::type fm[TM];
@@ -351,38 +342,40 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
       block_products(fn, fm, d[i & 1]);
       // the loads a few at a time: a wave that issues all of them at once waits for
       // the queue, and its matrix instructions with it
-      if (more) {
 #pragma unroll
-        for (int n = i * kPer; n < (i + 1) * kPer && n < S::kLoads; n++) load(next, s + NS - 1, n);
-      }
+      for (int n = i * kPer; n < (i + 1) * kPer && n < S::kLoads; n++) load(next, ahead_s, n);
       if (i > 0) add(i - 1);
       if (i + 1 < TN) fn = Frag::of(raw);
       // one matrix instruction, then its share of the others: two waves that meet in
       // the same phase would otherwise wait for one another in both
-      constexpr int kMfma = TM * (F32 ? 4 : 1), kValu = (TM * (TILE128 ? 4 : 8) + (F32 ? 16 : 0) + kMfma - 1) / kMfma;
-#pragma unroll
-      for (int n = 0; n < kMfma; n++) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
-      }
+      interleave<TM * (F32 ? 4 : 1), TM * (TILE128 ? 4 : 8) + (F32 ? 16 : 0), 2, kPer>();
       __builtin_amdgcn_sched_barrier(0);
     }
     add(TN - 1);
-    next_landed(s);
+    wait_vmcnt<(NS - 2) * S::kLoads>();  // the next stage has landed
     wait_lgkmcnt0();
     meet();
   };
   if (t.nkb > 0) {
 #pragma unroll
     for (int s = 0; s < NS - 1; s++)
-      if (s < t.nkb) load_stage(stages[s], s);
-    next_landed(-1);
-    meet();
-    for (int s0 = 0; s0 < t.nkb; s0 += NS) {
 #pragma unroll
-      for (int u = 0; u < NS; u++)
-        if (s0 + u < t.nkb) stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
-    }
+      for (int n = 0; n < S::kLoads; n++) load(stages[s], min(s, t.nkb - 1), n);
+    wait_vmcnt<(NS - 2) * S::kLoads>();
+    meet();
+    // (left from within: a way round the loop after fewer than NS stages would have
+    // the compiler wait for loads that such a way would leave in flight)
+    auto all_stages = [&]() {
+      for (int s0 = 0;; s0 += NS) {
+#pragma unroll
+        for (int u = 0; u < NS; u++) {
+          stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
+          if (s0 + u + 1 >= t.nkb) return;
+        }
+      }
+    };
+    all_stages();
+    wait_vmcnt<0>();  // the loads still in flight land before the LDS goes away
   }
 
   // lane l holds C[m = l % 16][n = 4 (l / 16) .. + 3] of each 16 x 16 block

@@ -224,7 +224,8 @@ enum Product { kGram, kSquare, kUpdate, kLast };
 struct Args {
   const _Float16 *P, *Q;  // operands
   int64_t rows_p, rows_q, K;
-  int tiles_p, tiles_q;
+  int tiles_p, tiles_q;   // of one matrix
+  int first, parts;       // workgroup i does tile first + i, or of that many tiles a quarter each (parts = 2)
   // gram, square: A (read by square) and the result
   const _Float16* a;
   float of_sum, of_a, on_diag;  // result = of_sum * sum + of_a * A + on_diag on the diagonal
@@ -275,17 +276,20 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave % S::kWavesP, wq = wave / S::kWavesP;
-  const int64_t b = blockIdx.y;
-  int pt, qt;
+  const int quarters = p.parts * p.parts;
+  const int tile = p.first + xcd_remap(blockIdx.x / quarters, gridDim.x / quarters), quarter = blockIdx.x % quarters;
+  const int tiles = WHAT == kGram || WHAT == kSquare ? p.tiles_p * (p.tiles_p + 1) / 2 : p.tiles_p * p.tiles_q;
+  const int64_t b = tile / tiles;
+  int at = tile - (int)b * tiles, pt, qt;
   if constexpr (WHAT == kGram || WHAT == kSquare) {  // row pt of the upper triangle has tiles_p - pt tiles
-    int at = blockIdx.x;
     pt = 0;
     while (at >= p.tiles_p - pt) at -= p.tiles_p - pt++;
     qt = pt + at;
   } else {
-    raster(xcd_remap(blockIdx.x, p.tiles_p * p.tiles_q), p.tiles_p, p.tiles_q, pt, qt);
+    raster(at, p.tiles_p, p.tiles_q, pt, qt);
   }
-  const int64_t p0 = (int64_t)pt * S::kP, q0 = (int64_t)qt * S::kQ;
+  const int64_t p0 = (int64_t)(pt * p.parts + quarter / p.parts) * S::kP, q0 = (int64_t)(qt * p.parts + quarter % p.parts) * S::kQ;
+  if (p0 >= p.rows_p || q0 >= p.rows_q || ((WHAT == kGram || WHAT == kSquare) && p0 > q0)) return;
   const int np = (int)min<int64_t>(S::kP, p.rows_p - p0), nq = (int)min<int64_t>(S::kQ, p.rows_q - q0);
 
   const uint32_t ld = (uint32_t)p.K * 2 * L::kWide;
@@ -391,11 +395,18 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
     for (int n = 0; n < S::kLoads; n++) load(stages[s], min(s, ns - 1), n);
   wait_vmcnt<(NS - 2) * S::kLoads>();
   meet();
-  for (int s0 = 0; s0 < ns; s0 += NS) {
+  // (left from within: a way round the loop after fewer than NS stages would have the
+  // compiler wait for loads that such a way would leave in flight)
+  auto all_stages = [&]() {
+    for (int s0 = 0;; s0 += NS) {
 #pragma unroll
-    for (int u = 0; u < NS; u++)
-      if (s0 + u < ns) stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
-  }
+      for (int u = 0; u < NS; u++) {
+        stage(stages[u], stages[(u + NS - 1) % NS], s0 + u);
+        if (s0 + u + 1 >= ns) return;
+      }
+    }
+  };
+  all_stages();
   wait_vmcnt<0>();  // the LDS is used again below
   meet();
 
@@ -537,7 +548,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
           store_halves(p.out + (b * a_stride + (row_q + r) * p.rows_p) * L::kWide, nullptr, row_p + c, v);
       });
     }
-    if (WHAT == kUpdate || (WHAT == kLast && p.tall) || ((WHAT == kGram || WHAT == kSquare) && pt != qt)) {  // along Q: rows of P
+    if (WHAT == kUpdate || (WHAT == kLast && p.tall) || ((WHAT == kGram || WHAT == kSquare) && p0 != q0)) {  // along Q: rows of P
       between();
 #pragma unroll
       for (int i = i0; i < i0 + kI; i++)
@@ -573,25 +584,39 @@ struct Plan {
   float eps;
 };
 
+// tiles of side `side` of all matrices
+template <int WHAT>
+int64_t tiles_of(const Args& p, int64_t batch, int64_t side) {
+  const int64_t tp = (p.rows_p + side - 1) / side, tq = (p.rows_q + side - 1) / side;
+  return batch * (WHAT == kGram || WHAT == kSquare ? tp * (tp + 1) / 2 : tp * tq);
+}
+
+// `count` tiles of side `side` from `first` on, in workgroup tiles of shape S
 template <int WHAT, bool SPLIT, class S, typename T, bool STEP>
-hipError_t launch_shape(Args& p, int64_t batch, hipStream_t st) {
-  p.tiles_p = (int)((p.rows_p + S::kP - 1) / S::kP);
-  p.tiles_q = (int)((p.rows_q + S::kQ - 1) / S::kQ);
-  const int64_t tiles = WHAT == kGram || WHAT == kSquare ? (int64_t)p.tiles_p * (p.tiles_p + 1) / 2 : (int64_t)p.tiles_p * p.tiles_q;
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  product_kernel<WHAT, SPLIT, S, T, STEP><<<dim3((unsigned)tiles, (unsigned)batch), S::kThreads, 0, st>>>(p);
+hipError_t launch_shape(Args p, int64_t side, int64_t first, int64_t count, hipStream_t st) {
+  p.tiles_p = (int)((p.rows_p + side - 1) / side);
+  p.tiles_q = (int)((p.rows_q + side - 1) / side);
+  p.parts = (int)(side / S::kP);
+  p.first = (int)first;
+  if (first + count > INT32_MAX / 4) return hipErrorInvalidValue;
+  product_kernel<WHAT, SPLIT, S, T, STEP><<<(unsigned)(count * p.parts * p.parts), S::kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 
+// 64 x 64 tiles where 128 x 128 ones leave CUs without work (32 times 256 x 256 x 512, fp32 weights: gram 13.6 us against
+// 18.1 with 96 of them; update 23.5 against 19.9 with 256), 256 x 256 ones where there are two a CU (four times 4096 x 4096
+// x 7168: update 2.36 ms against 2.53), but for a last round that would leave more than half of the CUs idle.
 template <int WHAT, bool SPLIT, typename T = float, bool STEP = false>
-hipError_t launch_product(Args& p, int64_t batch, hipStream_t st) {
-  const char* env = getenv("MXQ_W");
-  int v = env ? atoi(env) : 0;
-  if (v) v = (v / (WHAT == kGram ? 100 : WHAT == kSquare ? 10 : 1)) % 10;
-  if (v == 1) return launch_shape<WHAT, SPLIT, Small, T, STEP>(p, batch, st);
-  if (v == 2) return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, batch, st);
-  if (v == 3) return launch_shape<WHAT, SPLIT, Large, T, STEP>(p, batch, st);
-  return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, batch, st);
+hipError_t launch_product(const Args& p, int64_t batch, hipStream_t st) {
+  const int64_t cus = device_cu_count(), large = tiles_of<WHAT>(p, batch, 256), medium = tiles_of<WHAT>(p, batch, 128);
+  if (large >= 2 * cus) {
+    const int64_t rest = 2 * (large % cus) <= cus ? large % cus : 0;
+    const hipError_t err = launch_shape<WHAT, SPLIT, Large, T, STEP>(p, 256, 0, large - rest, st);
+    if (err != hipSuccess || rest == 0) return err;
+    return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, 256, large - rest, rest, st);
+  }
+  if (medium >= cus) return launch_shape<WHAT, SPLIT, Medium, T, STEP>(p, 128, 0, medium, st);
+  return launch_shape<WHAT, SPLIT, Small, T, STEP>(p, 64, 0, tiles_of<WHAT>(p, batch, 64), st);
 }
 
 template <typename G, bool MOMENTUM, bool SPLIT>
