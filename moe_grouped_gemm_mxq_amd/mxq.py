@@ -620,24 +620,34 @@ def ceil128(v: int) -> int:
     return (v + BLOCK128 - 1) // BLOCK128 * BLOCK128
 
 
-def _here(t, name):
-    """The entry points work on the current device's memory and streams."""
-    if t.device.index != torch.cuda.current_device():
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_U8, _F32 = torch.uint8, torch.float32
+
+
+def _stream_here(stream, t, name):
+    """Handle of the stream, or of the current one of t's device, which the entry points need to be the current device."""
+    index = t.get_device()
+    if index != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if stream is None and _current_stream is not None:
+        return _current_stream(index)
+    return _stream(stream, t.device)
 
 
 def _copy128_shapes(R, C, tile, lead=(), ldq=None):
-    """Shapes of the row copy's and the colT copy's codes and scales."""
+    """Shapes of the row copy's codes and scales and of the colT copy's."""
     Rp = ceil128(R) if ldq is None else ldq
-    return {"q_row": (*lead, R, ceil128(C)), "s_row": (*lead, ceil128(C) // BLOCK128, -(-R // tile)),
-            "q_colT": (*lead, C, Rp), "s_colT": (*lead, Rp // BLOCK128, -(-C // tile))}
+    Cb = (C + BLOCK128 - 1) // BLOCK128
+    return ((*lead, R, Cb * BLOCK128), (*lead, Cb, -(-R // tile)), (*lead, C, Rp), (*lead, Rp // BLOCK128, -(-C // tile)))
 
 
-def _need_copies128(axis_mask, shapes, copies):
-    for bit, names in ((MXQ_AXIS_ROW, ("q_row", "s_row")), (MXQ_AXIS_COLT, ("q_colT", "s_colT"))):
-        for name in names:
-            if axis_mask & bit:
-                _need_array(copies[name], name, torch.uint8 if name[0] == "q" else torch.float32, shapes[name])
+def _need_copies128(axis_mask, shapes, q_row, s_row, q_colT, s_colT):
+    if axis_mask & MXQ_AXIS_ROW:
+        _need_array(q_row, "q_row", _U8, shapes[0])
+        _need_array(s_row, "s_row", _F32, shapes[1])
+    if axis_mask & MXQ_AXIS_COLT:
+        _need_array(q_colT, "q_colT", _U8, shapes[2])
+        _need_array(s_colT, "s_colT", _F32, shapes[3])
 
 
 def mxq_grouped128_cols_max(T: int, G: int) -> int:
@@ -647,79 +657,104 @@ def mxq_grouped128_cols_max(T: int, G: int) -> int:
 def mxq_quantize128(x, tile, axis_mask, q_row=None, s_row=None, q_colT=None, s_colT=None, stream=None):
     """x fp32 or bf16 [R][C] or [batch][R][C] (unit column stride) in blocks of tile x 128: q_row uint8 [R][ceil128(C)],
     s_row fp32 [C / 128][R / tile], q_colT [C][ceil128(R)], s_colT [R / 128][C / tile], each under [batch] for three dims."""
-    if isinstance(x, torch.Tensor) and x.dim() == 3:
-        nb, R, C = x.shape
-        batch_stride = x.stride(0)
-        # (the rows of one matrix where there is none)
-        dt, _, _, ldx = _matrix(x[0] if nb else x.new_empty((R, C)), "x")
-        lead = (nb,)
-    else:
-        dt, R, C, ldx = _matrix(x, "x")
-        nb, batch_stride, lead = 1, 0, ()
     if tile not in (1, 128):
         raise ValueError(f"tile must be 1 or 128, got {tile}")
-    _here(x, "x")
-    _need_copies128(axis_mask, _copy128_shapes(R, C, tile, lead),
-                    {"q_row": q_row, "s_row": s_row, "q_colT": q_colT, "s_colT": s_colT})
+    nb, batch_stride, lead = 1, 0, ()
+    if isinstance(x, torch.Tensor) and x.dim() == 3:
+        nb, R, C = x.shape
+        batch_stride, lead = x.stride(0), (nb,)
+        dt, _, _, ldx = _matrix(x[0] if nb else x.new_empty((R, C)), "x")
+    else:
+        dt, R, C, ldx = _matrix(x, "x")
+    _need_copies128(axis_mask, _copy128_shapes(R, C, tile, lead), q_row, s_row, q_colT, s_colT)
     _check(_lib.mxq_quantize128(x.data_ptr(), dt, nb, R, C, ldx, batch_stride, tile, axis_mask, _raw(q_row), _raw(s_row),
-                                _raw(q_colT), _raw(s_colT), _stream(stream, x.device)), "mxq_quantize128")
+                                _raw(q_colT), _raw(s_colT), _stream_here(stream, x, "x")), "mxq_quantize128")
 
 
 def mxq_quantize128_grouped(x, group_end, ldq, axis_mask, q_row=None, s_row=None, q_colT=None, s_colT=None, stream=None):
     """x fp32 or bf16 [T][C], rows in groups: q_colT uint8 [C][ldq], s_colT fp32 [ldq / 128][C], the blocks restarting with
     each group; q_row, s_row as mxq_quantize128's of all rows."""
     dt, T, C, ldx = _matrix(x, "x")
-    _need(group_end, torch.int32, "group_end", 1)
-    _need_array(group_end, "group_end", torch.int32, (group_end.numel(),))
-    _here(x, "x")
-    _need_copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq),
-                    {"q_row": q_row, "s_row": s_row, "q_colT": q_colT, "s_colT": s_colT})
-    _check(_lib.mxq_quantize128_grouped(x.data_ptr(), dt, T, C, ldx, group_end.data_ptr(), group_end.numel(), ldq or 0, axis_mask,
-                                        _raw(q_row), _raw(s_row), _raw(q_colT), _raw(s_colT), _stream(stream, x.device)),
+    G = _need_groups(group_end)
+    _need_copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq), q_row, s_row, q_colT, s_colT)
+    _check(_lib.mxq_quantize128_grouped(x.data_ptr(), dt, T, C, ldx, group_end.data_ptr(), G, ldq, axis_mask, _raw(q_row),
+                                        _raw(s_row), _raw(q_colT), _raw(s_colT), _stream_here(stream, x, "x")),
            "mxq_quantize128_grouped")
+
+
+def _need_groups(group_end):
+    _need(group_end, torch.int32, "group_end", 1)
+    _need_array(group_end, "group_end", torch.int32, group_end.shape)
+    return group_end.shape[0]
 
 
 def _need_operand128(codes, scales, name, lead=(), tiles=(1,)):
     """(rows, K, tile) of an operand's codes [lead.., rows, K] and scales [lead.., K / 128, rows / tile], tile one of `tiles`."""
-    _need(codes, torch.uint8, name)
+    try:
+        if codes.dtype is _U8 and scales.dtype is _F32 and codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous():
+            shape, rows_of = codes.shape, scales.shape
+            if len(shape) == 2 + len(lead) and (not lead or (shape[:-2] == lead and rows_of[:-2] == lead)):
+                rows, K = shape[-2:]
+                blocks, n = rows_of[-2:]
+                if blocks * BLOCK128 == K:
+                    for tile in tiles:
+                        if n == (rows + tile - 1) // tile:
+                            return rows, K, tile
+    except (AttributeError, ValueError):
+        pass
+    _need(codes, _U8, name)
     if codes.dim() != 2 + len(lead) or tuple(codes.shape[:-2]) != lead or not codes.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {(*lead, 'rows', 'K')}, got {tuple(codes.shape)}")
     rows, K = codes.shape[-2:]
-    _need(scales, torch.float32, "s" + name)
-    for tile in tiles:
-        if scales.is_contiguous() and tuple(scales.shape) == (*lead, K // BLOCK128, -(-rows // tile)):
-            return rows, K, tile
+    _need(scales, _F32, "s" + name)
     want = " or ".join(str((*lead, K // BLOCK128, -(-rows // tile))) for tile in tiles)
-    raise ValueError(f"s{name} must be a contiguous tensor of shape {want}, got {tuple(scales.shape)}")
+    raise ValueError(f"s{name} must be a contiguous tensor of shape {want}, got {tuple(scales.shape)} (K a multiple of 128: {K})")
+
+
+def _need_operands128(A, sA, B, sB):
+    M, K, _ = _need_operand128(A, sA, "A")
+    N, KB, tile = _need_operand128(B, sB, "B", tiles=(128, 1))
+    if KB != K:
+        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}")
+    return M, N, K, tile
 
 
 def mxq_gemm128(A, sA, B, sB, C, stream=None):
     """A uint8 [M][K], sA fp32 [K / 128][M]; B [N][K], sB [K / 128][N] or [K / 128][ceil(N / 128)] -> C fp32 or bf16 [M][N]."""
-    M, K, _ = _need_operand128(A, sA, "A")
-    N, KB, tile = _need_operand128(B, sB, "B", tiles=(128, 1))
+    M, N, K, tile = _need_operands128(A, sA, B, sB)
     cdt, rows, cols, ldc = _matrix(C, "C")
-    if KB != K or (rows, cols) != (M, N):
-        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
-    _here(A, "A")
+    if rows != M or cols != N:
+        raise ValueError(f"C must have shape {(M, N)}, got {tuple(C.shape)}")
+    _gemm128(A, sA, B, sB, tile, C, cdt, M, N, K, ldc, stream)
+
+
+def _gemm128(A, sA, B, sB, tile, C, cdt, M, N, K, ldc, stream):
     _check(_lib.mxq_gemm128(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), tile, C.data_ptr(), cdt, M, N, K, ldc,
-                            _stream(stream, A.device)), "mxq_gemm128")
+                            _stream_here(stream, A, "A")), "mxq_gemm128")
+
+
+def _need_grouped128(mode, A, sA, B, sB, group_end):
+    """(M, N, K, G, shape of C)."""
+    G = _need_groups(group_end)
+    M, K, _ = _need_operand128(A, sA, "A")
+    ragged_m = mode == MXQ_GG_RAGGED_M
+    N, KB, _ = _need_operand128(B, sB, "B", (G,), (128,)) if ragged_m else _need_operand128(B, sB, "B")
+    if KB != K:
+        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}")
+    return M, N, K, G, (M, N) if ragged_m else (G, M, N)
 
 
 def mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end, stream=None):
     """RAGGED_M: A [M][K], B [G][N][K] in 128 x 128 blocks, C [M][N].  RAGGED_K: A [M][K], B [N][K], C [G][M][N].  C fp32 or
     bf16."""
-    _need(group_end, torch.int32, "group_end", 1)
-    G = group_end.numel()
-    _need_array(group_end, "group_end", torch.int32, (G,))
-    M, K, _ = _need_operand128(A, sA, "A")
-    ragged_m = mode == MXQ_GG_RAGGED_M
-    N, KB, _ = _need_operand128(B, sB, "B", (G,), (128,)) if ragged_m else _need_operand128(B, sB, "B")
-    _need(C, C.dtype if C.dtype in _DTYPES else torch.float32, "C")
-    if KB != K or tuple(C.shape) != ((M, N) if ragged_m else (G, M, N)) or not C.is_contiguous():
-        raise ValueError(f"operand shapes disagree: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
-    _here(A, "A")
+    M, N, K, G, shape = _need_grouped128(mode, A, sA, B, sB, group_end)
+    _need_array(C, "C", C.dtype if isinstance(C, torch.Tensor) and C.dtype in _DTYPES else _F32, shape)
+    _grouped_gemm128(mode, A, sA, B, sB, C, M, N, K, group_end, G, stream)
+
+
+def _grouped_gemm128(mode, A, sA, B, sB, C, M, N, K, group_end, G, stream):
     _check(_lib.mxq_grouped_gemm128(mode, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), _DTYPES[C.dtype],
-                                    M, N, K, group_end.data_ptr(), G, _stream(stream, A.device)), "mxq_grouped_gemm128")
+                                    M, N, K, group_end.data_ptr(), G, _stream_here(stream, A, "A")), "mxq_grouped_gemm128")
 
 
 # ---- orthogonalised updates
@@ -756,9 +791,8 @@ def mxq_orthogonalize(x, cfg, out, workspace, stream=None):
     if out.shape != x.shape:
         raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
     _need(workspace, torch.uint8, "workspace", 1)
-    _here(x, "x")
     _check(_lib.mxq_orthogonalize(x.data_ptr(), dt, nb, R, C, ctypes.byref(cfg), out.data_ptr(), odt, workspace.data_ptr(),
-                                  workspace.numel(), _stream(stream, x.device)), "mxq_orthogonalize")
+                                  workspace.numel(), _stream_here(stream, x, "x")), "mxq_orthogonalize")
 
 
 def mxq_muon(param, grad, m, cfg, workspace, copy=None, control=None, stream=None):
@@ -773,9 +807,8 @@ def mxq_muon(param, grad, m, cfg, workspace, copy=None, control=None, stream=Non
     if control is not None:
         _need_array(control, "control", torch.int32, (4,))
     _need(workspace, torch.uint8, "workspace", 1)
-    _here(param, "param")
     _check(_lib.mxq_muon(param.data_ptr(), pdt, grad.data_ptr(), gdt, m.data_ptr(), _raw(copy), nb, R, C, ctypes.byref(cfg),
-                         _raw(control), workspace.data_ptr(), workspace.numel(), _stream(stream, param.device)), "mxq_muon")
+                         _raw(control), workspace.data_ptr(), workspace.numel(), _stream_here(stream, param, "param")), "mxq_muon")
 
 
 # ------------------------------------------------------------------ allocate-and-call helpers
@@ -1024,12 +1057,13 @@ def dispatch(x, slot, rows, dtype=None, stream=None):
     return combine_backward(x, slot, rows, dtype=dtype, stream=stream)[0]
 
 
-def _copies128(axis_mask, shapes, device, out):
-    """The requested copies, from `out` where it has them."""
+def _copies128(axis_mask, shapes, x, out):
+    """The requested copies, from `out` where it is given."""
     names = (("q_row", "s_row") if axis_mask & MXQ_AXIS_ROW else ()) + (("q_colT", "s_colT") if axis_mask & MXQ_AXIS_COLT else ())
     if out is not None:
         return {n: out[n] for n in names}
-    return {n: torch.empty(shapes[n], dtype=torch.uint8 if n[0] == "q" else torch.float32, device=device) for n in names}
+    of = dict(zip(("q_row", "s_row", "q_colT", "s_colT"), shapes()))
+    return {n: x.new_empty(of[n], dtype=_U8 if n[0] == "q" else _F32) for n in names}
 
 
 def quantize128(x, axis_mask=MXQ_AXIS_ROW, tile=1, out=None, stream=None):
@@ -1038,8 +1072,7 @@ def quantize128(x, axis_mask=MXQ_AXIS_ROW, tile=1, out=None, stream=None):
     if stream is not None:
         with _on(stream, x.device):
             return quantize128(x, axis_mask, tile, out)
-    *lead, R, C = x.shape
-    got = _copies128(axis_mask, _copy128_shapes(R, C, tile, tuple(lead)) if out is None else None, x.device, out)
+    got = _copies128(axis_mask, lambda: _copy128_shapes(*x.shape[-2:], tile, tuple(x.shape[:-2])), x, out)
     mxq_quantize128(x, tile, axis_mask, **got)
     return got
 
@@ -1050,12 +1083,12 @@ def quantize128_grouped(x, group_end, axis_mask=MXQ_AXIS_COLT, ldq=None, out=Non
     if stream is not None:
         with _on(stream, x.device):
             return quantize128_grouped(x, group_end, axis_mask, ldq, out)
-    T, C = x.shape
     if ldq is None:
-        ldq = out["q_colT"].shape[1] if out is not None and "q_colT" in out else mxq_grouped128_cols_max(T, group_end.numel())
-    got = _copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq) if out is None else None, x.device, out)
+        ldq = out["q_colT"].shape[1] if out is not None and "q_colT" in out else mxq_grouped128_cols_max(x.shape[0], group_end.numel())
+    got = _copies128(axis_mask, lambda: _copy128_shapes(*x.shape, 1, ldq=ldq), x, out)
     mxq_quantize128_grouped(x, group_end, ldq, axis_mask, **got)
-    return {**got, "ldq": ldq}
+    got["ldq"] = ldq
+    return got
 
 
 def gemm128(A, sA, B, sB, dtype=torch.bfloat16, stream=None):
@@ -1063,9 +1096,10 @@ def gemm128(A, sA, B, sB, dtype=torch.bfloat16, stream=None):
     if stream is not None:
         with _on(stream, A.device):
             return gemm128(A, sA, B, sB, dtype)
-    _type_code(dtype)
-    C = torch.empty((A.shape[0], B.shape[0]), dtype=dtype, device=A.device)
-    mxq_gemm128(A, sA, B, sB, C)
+    cdt = _type_code(dtype)
+    M, N, K, tile = _need_operands128(A, sA, B, sB)
+    C = sA.new_empty((M, N), dtype=dtype)
+    _gemm128(A, sA, B, sB, tile, C, cdt, M, N, K, N, None)
     return C
 
 
@@ -1075,9 +1109,9 @@ def grouped_gemm128(mode, A, sA, B, sB, group_end, dtype=torch.bfloat16, stream=
         with _on(stream, A.device):
             return grouped_gemm128(mode, A, sA, B, sB, group_end, dtype)
     _type_code(dtype)
-    shape = (A.shape[0], B.shape[1]) if mode == MXQ_GG_RAGGED_M else (group_end.numel(), A.shape[0], B.shape[0])
-    C = torch.empty(shape, dtype=dtype, device=A.device)
-    mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end)
+    M, N, K, G, shape = _need_grouped128(mode, A, sA, B, sB, group_end)
+    C = sA.new_empty(shape, dtype=dtype)
+    _grouped_gemm128(mode, A, sA, B, sB, C, M, N, K, group_end, G, None)
     return C
 
 
