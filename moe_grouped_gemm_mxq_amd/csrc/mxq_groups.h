@@ -155,4 +155,20 @@ __device__ __forceinline__ bool find_group_unit(const int32_t* __restrict__ grou
   return false;
 }
 
+// All units of the groups, under the same conditions.
+template <int UNIT>
+__device__ __forceinline__ int64_t group_units(const int32_t* __restrict__ group_end, int G, int64_t R) {
+  static_assert(UNIT >= 64, "the sum of a chunk's units must fit int32");
+  int64_t sum = 0;
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    int32_t start = 0, size = 0;
+    if (g0 + (int)(threadIdx.x & 63) < G) group_span(group_end, g0 + (threadIdx.x & 63), R, start, size);
+    int32_t units = (int32_t)(((uint32_t)size + (UNIT - 1)) / UNIT);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) units += __shfl_xor(units, off);
+    sum += __builtin_amdgcn_readfirstlane(units);
+  }
+  return sum;
+}
+
 }  // namespace mxq
