@@ -230,22 +230,12 @@ __device__ __forceinline__ void block_products(const AsBf16& n, const AsBf16 (&m
     for (int j = 0; j < TM; j++) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.f[s], m[j].f[s], d[j], 0, 0, 0);
 }
 
-__device__ __forceinline__ void store4(float* p, const v4f& v, int n) {
-  if (n >= 4) {
-    *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, v);
-  } else {
-    for (int e = 0; e < n; e++) p[e] = v[e];
-  }
-}
-__device__ __forceinline__ void store4(uint16_t* p, const v4f& v, int n) {
-  if (n >= 4) {
-    u32x2 w;
-    w[0] = bf16x2_of(v[0], v[1]);
-    w[1] = bf16x2_of(v[2], v[3]);
-    *reinterpret_cast<u32x2_any*>(p) = w;
-  } else {
-    for (int e = 0; e < n; e++) p[e] = bf16_of(v[e]);
-  }
+__device__ __forceinline__ void store4(float* p, const v4f& v) { *reinterpret_cast<v4f*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, const v4f& v) {
+  u32x2 w;
+  w[0] = bf16x2_of(v[0], v[1]);
+  w[1] = bf16x2_of(v[2], v[3]);
+  *reinterpret_cast<u32x2*>(p) = w;
 }
 
 // One stage is one block of 128 along K: codes and scales of the tile's rows,
@@ -393,7 +383,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
 #pragma unroll
   for (int j = 0; j < TM; j++)
 #pragma unroll
-    for (int i = 0; i < TN; i++) store4(mine + spot(j * 16 + (lane & 15), i * 16 + 4 * (lane >> 4)), acc[i][j], 4);
+    for (int i = 0; i < TN; i++) store4(mine + spot(j * 16 + (lane & 15), i * 16 + 4 * (lane >> 4)), acc[i][j]);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   Out* C = static_cast<Out*>(p.C) + t.c0 + t.m0 * p.ldc + t.n0;
   // past the caches where the lines are whole (dense 903 -> 897 us), not where rows share them (17.4 -> 19.9 us, N = 1237)
@@ -567,6 +557,9 @@ hipError_t launch_few(Problem p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// A launch has fewer than 2^32 threads, and few rows take 16 for each row of B.
+constexpr int64_t kMaxFewN = (1 << 28) - 64 * MXQ_MAX_GROUPS;
+
 // Waves a workgroup, and rows of B in it, from what they measured (us; bf16 C, N x K = 4096 x 7168 / 18432 x 7168 / 32
 // experts of 4096 x 7168 with 64 rows): 16 rows of B by 16 waves 8.2 / 33.4 / 102, 32 by 8 waves 11.4 / 35.2 / 97.
 template <int MODE, bool F32, bool TILE128>
@@ -605,7 +598,9 @@ hipError_t launch_gemm128(const Problem& p, bool f32, hipStream_t st) {
     // more, and with more than 16 where N alone fills the card, tiles are faster (N = 18432,
     // 64 rows: 44 us against 84; N = 4096: 26 against 20).
     const int64_t rows = MODE == kRaggedM ? 4 * p.M / p.G : p.M;
-    if (rows <= 16 || (rows <= 64 && p.N <= 32 * (int64_t)device_cu_count())) return f32 ? launch_few_of<MODE, true, TILE128>(p, rows, st) : launch_few_of<MODE, false, TILE128>(p, rows, st);
+    const bool few = rows <= 16 || (rows <= 64 && p.N <= 32 * (int64_t)device_cu_count());
+    if (few && p.N * p.G < kMaxFewN)
+      return f32 ? launch_few_of<MODE, true, TILE128>(p, rows, st) : launch_few_of<MODE, false, TILE128>(p, rows, st);
   }
   return f32 ? launch_tiles<MODE, true, TILE128>(p, st) : launch_tiles<MODE, false, TILE128>(p, st);
 }

@@ -172,7 +172,7 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
 // its rows do not hold.
 template <typename G, bool MOMENTUM, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, int64_t C, int64_t Rp, int64_t Cp, int nparts,
-                                                         float eps, float S, const double* __restrict__ parts,
+                                                         double eps, float S, const double* __restrict__ parts,
                                                          _Float16* __restrict__ same, _Float16* __restrict__ same_low,
                                                          _Float16* __restrict__ turn, _Float16* __restrict__ turn_low) {
   typedef Row<SPLIT> L;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
   if ((t & 63) == 0) waves[t >> 6] = sum;
   __syncthreads();
-  const float inv = (float)((double)S / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + (double)eps));
+  const double inv = (double)S / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + eps);  // (may be past fp32's range)
   const int64_t tiles_c = Cp / 64;
   const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
   const int64_t base = blockIdx.y * s.n, out = blockIdx.y * Rp * Cp;
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
       const int64_t i = base + r * C + c0 + c;
       update_of<G, MOMENTUM, false, 1>(static_cast<const G*>(s.grad) + i, MOMENTUM ? s.m + i : nullptr, s, scale, u);
     }
-    const float v = u[0] * inv;
+    const float v = (float)(u[0] * inv);
     tile[4 * k + (t >> 6)][c] = v;
     put(same, same_low, r, Cp, c0 + c, v);
   }
@@ -580,8 +580,7 @@ typedef Shape<64, 64, 2, 2, 4> Small;
 struct Plan {
   int64_t batch, R, C;
   int steps;
-  double a, b, c;
-  float eps;
+  double a, b, c, eps;
 };
 
 // tiles of side `side` of all matrices
@@ -724,7 +723,7 @@ mxq_status check(const char* who, int64_t batch, int64_t R, int64_t C, const mxq
 }
 
 Plan plan_of(int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz& ns) {
-  return Plan{batch, R, C, ns.steps, ns.a, ns.b, ns.c, (float)ns.eps};
+  return Plan{batch, R, C, ns.steps, ns.a, ns.b, ns.c, ns.eps};
 }
 
 }  // namespace
@@ -771,7 +770,7 @@ mxq_status mxq_muon(void* param, mxq_dtype param_dt, const void* grad, mxq_dtype
               "mxq_muon: tensors must be aligned to their elements");
   MXQ_REQUIRE(cfg->momentum >= 0 && cfg->momentum < 1, "mxq_muon: momentum must be in [0, 1)");
   MXQ_REQUIRE(cfg->nesterov == 0 || cfg->nesterov == 1, "mxq_muon: nesterov must be 0 or 1");
-  MXQ_REQUIRE(std::isfinite(cfg->weight_decay) && std::isfinite(cfg->scale), "mxq_muon: weight_decay and scale must be finite");
+  MXQ_REQUIRE(std::isfinite((float)cfg->weight_decay) && std::isfinite((float)cfg->scale), "mxq_muon: weight_decay and scale must be finite in fp32");
   MXQ_REQUIRE(aligned_to(control, 16), "mxq_muon: control must be 16-byte aligned");
   MXQ_REQUIRE_DEVICE();
   if (batch == 0) return ok();

@@ -29,6 +29,7 @@ constexpr int kLanes = 16;       // lanes of a row's block, eight elements each
 constexpr float kMaxCode = 448.f;
 constexpr uint32_t kAmaxFloor = 0x0D800000u;  // 2^-100
 constexpr uint32_t kInf = 0x7F800000u;
+constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of a launch: a grid has fewer than 2^32 threads
 
 // Eight consecutive elements as they lie in memory, zero from the n-th on.
 template <typename T>
@@ -157,20 +158,21 @@ struct Divisor {
 // Row copy with 1 x 128 blocks.  16 lanes take a block; the workgroup's 16
 // groups take 16 rows, so that their scales, which lie next to each other
 // (scales[block][row]), are written together.
+constexpr int kPerChunk = 4;  // blocks of a row that a workgroup takes
 template <typename T>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ldx,
                                                         int64_t x_stride, uint8_t* __restrict__ q,
-                                                        float* __restrict__ s, int64_t chunks, int per_chunk) {
+                                                        float* __restrict__ s, int64_t first, int64_t chunks) {
   const int64_t Cb = (C + kB - 1) / kB, Cp = Cb * kB;
-  const int64_t rt = blockIdx.x / chunks, chunk = blockIdx.x - rt * chunks;
+  const int64_t bid = first + blockIdx.x, rt = bid / chunks, chunk = bid - rt * chunks;
   const int64_t row = rt * 16 + threadIdx.x / kLanes;
   if (row >= R) return;
   const int c = (threadIdx.x % kLanes) * 8;
   const T* xr = x + blockIdx.y * x_stride + row * ldx;
   uint8_t* qr = q + ((int64_t)blockIdx.y * R + row) * Cp;
   float* sr = s + (int64_t)blockIdx.y * Cb * R + row;
-  const int64_t last = min((chunk + 1) * per_chunk, Cb);
-  for (int64_t b = chunk * per_chunk; b < last; b++) {
+  const int64_t last = min((chunk + 1) * kPerChunk, Cb);
+  for (int64_t b = chunk * kPerChunk; b < last; b++) {
     const int64_t col = b * kB + c;
     const Eight<T> v = load8(xr + col, (int)min<int64_t>(C - col, 8));
     const Divisor by(max16(largest_of(v)));
@@ -189,12 +191,12 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(const T* __restrict__ x,
                                                         int64_t x_stride, const int32_t* __restrict__ group_end,
                                                         int G, int64_t ldq, uint8_t* __restrict__ q_row,
                                                         float* __restrict__ s_row, uint8_t* __restrict__ q_colT,
-                                                        float* __restrict__ s_colT, int64_t tiles_c) {
+                                                        float* __restrict__ s_colT, int64_t first, int64_t tiles_c) {
   __shared__ uint2 turned[COLT ? kB * 16 : 1];
   __shared__ uint32_t part[4][kB];
   const int t = threadIdx.x, wave = t >> 6;
   const int c = t & 15, i = t >> 4;
-  const int64_t rt = blockIdx.x / tiles_c, ct = blockIdx.x - rt * tiles_c;
+  const int64_t bid = first + blockIdx.x, rt = bid / tiles_c, ct = bid - rt * tiles_c;
   const int64_t Cb = tiles_c, Cp = Cb * kB;
   const int64_t Rb = (R + kB - 1) / kB;
   int64_t row0 = rt * kB, out0 = rt * kB;  // first row, and its place along the transpose's rows
@@ -321,46 +323,41 @@ struct Args {
 };
 
 template <typename T, bool TILE128, bool ROW, bool COLT>
-void launch_tile(const T* x, const Args& a, dim3 grid, int64_t tiles_c, hipStream_t st) {
+void launch_tile(const T* x, const Args& a, dim3 grid, int64_t first, int64_t tiles_c, hipStream_t st) {
   if constexpr (!TILE128 && COLT) {
     if (a.group_end) {
       tile_kernel<T, TILE128, ROW, COLT, true><<<grid, kThreads, 0, st>>>(x, a.R, a.C, a.ldx, a.x_stride, a.group_end, a.G,
-                                                                          a.ldq, a.q_row, a.s_row, a.q_colT, a.s_colT, tiles_c);
+                                                                          a.ldq, a.q_row, a.s_row, a.q_colT, a.s_colT, first, tiles_c);
       return;
     }
   }
   tile_kernel<T, TILE128, ROW, COLT, false><<<grid, kThreads, 0, st>>>(x, a.R, a.C, a.ldx, a.x_stride, nullptr, 0, 0,
-                                                                       a.q_row, a.s_row, a.q_colT, a.s_colT, tiles_c);
+                                                                       a.q_row, a.s_row, a.q_colT, a.s_colT, first, tiles_c);
 }
 
 template <typename T>
 hipError_t launch(const T* x, int tile, bool row, bool col, const Args& a, hipStream_t st) {
-  const int64_t Cb = (a.C + kB - 1) / kB;
-  if (tile == 1 && !col) {
-    const int64_t tiles_r = (a.R + 15) / 16;
-    int per_chunk = 4;
-    const int64_t chunks = (Cb + per_chunk - 1) / per_chunk;
-    if (tiles_r * chunks > INT32_MAX) return hipErrorInvalidValue;
-    rows_kernel<T><<<dim3((unsigned)(tiles_r * chunks), (unsigned)a.batch), kThreads, 0, st>>>(
-        x, a.R, a.C, a.ldx, a.x_stride, a.q_row, a.s_row, chunks, per_chunk);
-    return hipGetLastError();
-  }
-  const int64_t tiles = ((a.R + kB - 1) / kB + (a.group_end ? a.G + 1 : 0)) * Cb;
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, (unsigned)a.batch);
-  if (tile == 1) {
-    if (row)
-      launch_tile<T, false, true, true>(x, a, grid, Cb, st);
+  const int64_t Cb = (a.C + kB - 1) / kB, chunks = (Cb + kPerChunk - 1) / kPerChunk;
+  const bool by_rows = tile == 1 && !col;
+  const int64_t all = by_rows ? (a.R + 15) / 16 * chunks : ((a.R + kB - 1) / kB + (a.group_end ? a.G + 1 : 0)) * Cb;
+  for (int64_t first = 0; first < all; first += kMaxGrid) {
+    const dim3 grid((unsigned)(all - first < kMaxGrid ? all - first : kMaxGrid), (unsigned)a.batch);
+    if (by_rows)
+      rows_kernel<T><<<grid, kThreads, 0, st>>>(x, a.R, a.C, a.ldx, a.x_stride, a.q_row, a.s_row, first, chunks);
+    else if (tile == 1 && row)
+      launch_tile<T, false, true, true>(x, a, grid, first, Cb, st);
+    else if (tile == 1)
+      launch_tile<T, false, false, true>(x, a, grid, first, Cb, st);
+    else if (row && col)
+      launch_tile<T, true, true, true>(x, a, grid, first, Cb, st);
+    else if (row)
+      launch_tile<T, true, true, false>(x, a, grid, first, Cb, st);
     else
-      launch_tile<T, false, false, true>(x, a, grid, Cb, st);
-  } else if (row && col) {
-    launch_tile<T, true, true, true>(x, a, grid, Cb, st);
-  } else if (row) {
-    launch_tile<T, true, true, false>(x, a, grid, Cb, st);
-  } else {
-    launch_tile<T, true, false, true>(x, a, grid, Cb, st);
+      launch_tile<T, true, false, true>(x, a, grid, first, Cb, st);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 hipError_t launch_any(const void* x, mxq_dtype dt, int tile, bool row, bool col, const Args& a, hipStream_t st) {
@@ -410,7 +407,8 @@ mxq_status mxq_quantize128(const void* x, mxq_dtype dt, int64_t batch, int64_t R
   MXQ_REQUIRE(batch >= 0 && batch <= 65535, "mxq_quantize128: batch must be in [0, 65535] (got %lld)", (long long)batch);
   const mxq_status s = check("mxq_quantize128", x, dt, R, C, ldx, axis_mask, a);
   if (s != MXQ_OK) return s;
-  MXQ_REQUIRE(batch <= 1 || R == 0 || x_stride >= (R - 1) * ldx + C,
+  // (R - 1) ldx + C may be past 64 bits
+  MXQ_REQUIRE(batch <= 1 || R == 0 || (x_stride >= C && (R == 1 || (x_stride - C) / (R - 1) >= ldx)),
               "mxq_quantize128: x_stride (%lld) smaller than one matrix", (long long)x_stride);
   MXQ_REQUIRE_DEVICE();
   if (batch == 0) return ok();

@@ -624,11 +624,15 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _U8, _F32 = torch.uint8, torch.float32
 
 
-def _stream_here(stream, t, name):
-    """Handle of the stream, or of the current one of t's device, which the entry points need to be the current device."""
+def _stream_here(stream, t, name, *others):
+    """Handle of the stream, or of the current one of t's device, which the entry points need to be the current device; the
+    others (or None) have to be there too."""
     index = t.get_device()
     if index != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+    for o in others:
+        if o is not None and o.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, another tensor on {o.device}")
     if stream is None and _current_stream is not None:
         return _current_stream(index)
     return _stream(stream, t.device)
@@ -668,7 +672,7 @@ def mxq_quantize128(x, tile, axis_mask, q_row=None, s_row=None, q_colT=None, s_c
         dt, R, C, ldx = _matrix(x, "x")
     _need_copies128(axis_mask, _copy128_shapes(R, C, tile, lead), q_row, s_row, q_colT, s_colT)
     _check(_lib.mxq_quantize128(x.data_ptr(), dt, nb, R, C, ldx, batch_stride, tile, axis_mask, _raw(q_row), _raw(s_row),
-                                _raw(q_colT), _raw(s_colT), _stream_here(stream, x, "x")), "mxq_quantize128")
+                                _raw(q_colT), _raw(s_colT), _stream_here(stream, x, "x", q_row, s_row, q_colT, s_colT)), "mxq_quantize128")
 
 
 def mxq_quantize128_grouped(x, group_end, ldq, axis_mask, q_row=None, s_row=None, q_colT=None, s_colT=None, stream=None):
@@ -678,8 +682,8 @@ def mxq_quantize128_grouped(x, group_end, ldq, axis_mask, q_row=None, s_row=None
     G = _need_groups(group_end)
     _need_copies128(axis_mask, _copy128_shapes(T, C, 1, ldq=ldq), q_row, s_row, q_colT, s_colT)
     _check(_lib.mxq_quantize128_grouped(x.data_ptr(), dt, T, C, ldx, group_end.data_ptr(), G, ldq, axis_mask, _raw(q_row),
-                                        _raw(s_row), _raw(q_colT), _raw(s_colT), _stream_here(stream, x, "x")),
-           "mxq_quantize128_grouped")
+                                        _raw(s_row), _raw(q_colT), _raw(s_colT),
+                                        _stream_here(stream, x, "x", group_end, q_row, s_row, q_colT, s_colT)), "mxq_quantize128_grouped")
 
 
 def _need_groups(group_end):
@@ -730,7 +734,7 @@ def mxq_gemm128(A, sA, B, sB, C, stream=None):
 
 def _gemm128(A, sA, B, sB, tile, C, cdt, M, N, K, ldc, stream):
     _check(_lib.mxq_gemm128(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), tile, C.data_ptr(), cdt, M, N, K, ldc,
-                            _stream_here(stream, A, "A")), "mxq_gemm128")
+                            _stream_here(stream, A, "A", sA, B, sB, C)), "mxq_gemm128")
 
 
 def _need_grouped128(mode, A, sA, B, sB, group_end):
@@ -754,7 +758,8 @@ def mxq_grouped_gemm128(mode, A, sA, B, sB, C, group_end, stream=None):
 
 def _grouped_gemm128(mode, A, sA, B, sB, C, M, N, K, group_end, G, stream):
     _check(_lib.mxq_grouped_gemm128(mode, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), _DTYPES[C.dtype],
-                                    M, N, K, group_end.data_ptr(), G, _stream_here(stream, A, "A")), "mxq_grouped_gemm128")
+                                    M, N, K, group_end.data_ptr(), G, _stream_here(stream, A, "A", sA, B, sB, C, group_end)),
+           "mxq_grouped_gemm128")
 
 
 # ---- orthogonalised updates
@@ -792,7 +797,7 @@ def mxq_orthogonalize(x, cfg, out, workspace, stream=None):
         raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
     _need(workspace, torch.uint8, "workspace", 1)
     _check(_lib.mxq_orthogonalize(x.data_ptr(), dt, nb, R, C, ctypes.byref(cfg), out.data_ptr(), odt, workspace.data_ptr(),
-                                  workspace.numel(), _stream_here(stream, x, "x")), "mxq_orthogonalize")
+                                  workspace.numel(), _stream_here(stream, x, "x", out, workspace)), "mxq_orthogonalize")
 
 
 def mxq_muon(param, grad, m, cfg, workspace, copy=None, control=None, stream=None):
@@ -808,7 +813,8 @@ def mxq_muon(param, grad, m, cfg, workspace, copy=None, control=None, stream=Non
         _need_array(control, "control", torch.int32, (4,))
     _need(workspace, torch.uint8, "workspace", 1)
     _check(_lib.mxq_muon(param.data_ptr(), pdt, grad.data_ptr(), gdt, m.data_ptr(), _raw(copy), nb, R, C, ctypes.byref(cfg),
-                         _raw(control), workspace.data_ptr(), workspace.numel(), _stream_here(stream, param, "param")), "mxq_muon")
+                         _raw(control), workspace.data_ptr(), workspace.numel(),
+                         _stream_here(stream, param, "param", grad, m, copy, control, workspace)), "mxq_muon")
 
 
 # ------------------------------------------------------------------ allocate-and-call helpers
@@ -1228,7 +1234,8 @@ class Muon:
     params fp32 or bf16, grads fp32 or bf16, m the momenta (fp32, zeros before the first step), copies: bf16 tensors that get
     the new parameters too, or None.  The tensors stay the caller's: they are read and written where they are, so a gradient
     that moves to other storage needs a new Muon.  The workspace is shared by the tensors, which are updated one after the
-    other on the step's stream."""
+    other on the step's stream, and by all steps: two that may run at once (on two streams, or in a graph that is replayed
+    while another step runs) need a Muon each."""
 
     def __init__(self, params, grads, m, copies=None):
         n = len(params)
