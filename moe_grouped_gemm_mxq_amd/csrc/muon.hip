@@ -8,8 +8,8 @@
 //   gram    A = X X^T, and square  B = b A + c A^2 + (a - e) I: symmetric, so only
 //           the tiles on and above the diagonal are computed and each is stored
 //           twice;
-//   update  X' = e X + B X, from rows of B and of X's transpose, stored both ways
-//           (each product reads both operands along their rows).
+//   update  X' = e X + B X, from rows of B and columns of X, which the LDS reads
+//           turn (four rows of sixteen numbers at a time), so that X is kept once.
 // Splitting a into e and a - e changes nothing but the rounding: e = a while the
 // iteration grows X, and less in the last two, where B is near its diagonal.
 //
@@ -59,9 +59,8 @@ struct Row {
 // Where a matrix's operands lie.
 struct Space {
   int64_t lo, hi, Lp, Hp;  // sides, and rounded up to 64 (zeros there)
-  _Float16* x;             // [batch][Lp] rows of Hp
-  _Float16* xl;            // what fp16 leaves of them, [batch][Lp][Hp], where the rows do not hold it
-  _Float16 *t, *t2;        // [batch][Hp] rows of Lp: the transpose, this iteration's and the next one's
+  _Float16 *x, *x2;        // [batch][Lp] rows of Hp: this iteration's X and the next one's
+  _Float16* xl;            // what fp16 leaves of X, [batch][Lp][Hp], where the rows do not hold it
   _Float16 *a, *b;         // [batch][Lp] rows of Lp
   double* parts;           // [batch][kMaxParts]
 };
@@ -79,9 +78,8 @@ int64_t lay_out(Space* sp, uint8_t* base, int64_t batch, int64_t R, int64_t C, b
   auto half = [&](int64_t n) { return reinterpret_cast<_Float16*>(take(batch * n * 2)); };
   Space s;
   s.lo = lo, s.hi = hi, s.Lp = Lp, s.Hp = Hp;
-  s.x = half(Lp * Hp * wide);
+  s.x = half(Lp * Hp * wide), s.x2 = half(Lp * Hp * wide);
   s.xl = split ? nullptr : half(Lp * Hp);
-  s.t = half(Lp * Hp * wide), s.t2 = half(Lp * Hp * wide);
   s.a = half(Lp * Lp * wide), s.b = half(Lp * Lp * wide);
   s.parts = reinterpret_cast<double*>(take(batch * kMaxParts * 8));
   if (sp) *sp = s;
@@ -167,14 +165,12 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
   lo = (_Float16)(v - (float)hi);
 }
 
-// u / (|u| + eps) times S, both ways round: 64 x 64 of [R][C], along its rows
-// (`same`) and turned through LDS (`turn`); low: where the low halves of X go that
-// its rows do not hold.
+// X = u / (|u| + eps) times S from 64 x 64 of u [R][C]; X's rows are u's columns
+// where it is tall.  low: where the low halves go that X's rows do not hold.
 template <typename G, bool MOMENTUM, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, int64_t C, int64_t Rp, int64_t Cp, int nparts,
-                                                         double eps, float S, const double* __restrict__ parts,
-                                                         _Float16* __restrict__ same, _Float16* __restrict__ same_low,
-                                                         _Float16* __restrict__ turn, _Float16* __restrict__ turn_low) {
+                                                         double eps, float S, const double* __restrict__ parts, int tall,
+                                                         _Float16* __restrict__ x, _Float16* __restrict__ low) {
   typedef Row<SPLIT> L;
   __shared__ float tile[64][65];
   __shared__ double waves[kThreads / 64];
@@ -189,38 +185,50 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
   const double inv = (double)S / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + eps);  // (may be past fp32's range)
   const int64_t tiles_c = Cp / 64;
   const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
-  const int64_t base = blockIdx.y * s.n, out = blockIdx.y * Rp * Cp;
-  const int c = t & 63;
-  auto put = [&](_Float16* rows, _Float16* low, int64_t row, int64_t width, int64_t k, float v) {
-    _Float16 hi, lo;
-    split_half(v, hi, lo);
-    rows[(out + row * width) * L::kWide + L::at(k)] = hi;
-    if constexpr (SPLIT) rows[(out + row * width) * L::kWide + L::at(k) + L::kLow] = lo;
-    else if (low) low[out + row * width + k] = lo;
-  };
-#pragma unroll 4
-  for (int k = 0; k < 16; k++) {
-    const int64_t r = r0 + 4 * k + (t >> 6);
-    float u[1] = {0.f};
-    if (run && r < R && c0 + c < C) {
+  const int64_t base = blockIdx.y * s.n;
+  const int c = (t & 15) * 4;
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const int64_t r = r0 + 16 * k + (t >> 4);
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+    if (run && r < R) {
       const int64_t i = base + r * C + c0 + c;
-      update_of<G, MOMENTUM, false, 1>(static_cast<const G*>(s.grad) + i, MOMENTUM ? s.m + i : nullptr, s, scale, u);
+      const G* g = static_cast<const G*>(s.grad) + i;
+      float* m = MOMENTUM ? s.m + i : nullptr;
+      if (c0 + c + 4 <= C) {
+        update_of<G, MOMENTUM, false, 4>(g, m, s, scale, u);
+      } else {
+        for (int e = 0; e < 4 && c0 + c + e < C; e++) update_of<G, MOMENTUM, false, 1>(g + e, MOMENTUM ? m + e : nullptr, s, scale, u + e);
+      }
     }
-    const float v = (float)(u[0] * inv);
-    tile[4 * k + (t >> 6)][c] = v;
-    put(same, same_low, r, Cp, c0 + c, v);
+#pragma unroll
+    for (int e = 0; e < 4; e++) tile[16 * k + (t >> 4)][c + e] = (float)(u[e] * inv);
   }
   __syncthreads();
-#pragma unroll 4
-  for (int k = 0; k < 16; k++) {
-    const int cc = 4 * k + (t >> 6);
-    put(turn, turn_low, c0 + cc, Rp, r0 + c, tile[c][cc]);
+  // rows of X, eight numbers a lane
+  const int64_t x0 = tall ? c0 : r0, k0 = tall ? r0 : c0, width = tall ? Rp : Cp, out = blockIdx.y * Rp * Cp;
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    const int row = 32 * k + (t >> 3), at = (t & 7) * 8;
+    v8h h, l;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      _Float16 hi, lo;
+      split_half(tall ? tile[at + e][row] : tile[row][at + e], hi, lo);
+      h[e] = hi;
+      l[e] = lo;
+    }
+    const int64_t begin = out + (x0 + row) * width;
+    *reinterpret_cast<v8h*>(x + begin * L::kWide + L::at(k0 + at)) = h;
+    if constexpr (SPLIT) *reinterpret_cast<v8h*>(x + begin * L::kWide + L::at(k0 + at) + L::kLow) = l;
+    else *reinterpret_cast<v8h*>(low + begin + k0 + at) = l;
   }
 }
 
 enum Product { kGram, kSquare, kUpdate, kLast };
 
-// D[p][q] = sum_k P[p][k] Q[q][k]; rows, columns and K of one matrix, in elements.
+// D[p][q] = sum_k P[p][k] Q[q][k] (gram, square), or sum_k P[k][p] Q[q][k] (update,
+// last); rows, columns and K of one matrix, in elements.
 struct Args {
   const _Float16 *P, *Q;  // operands
   int64_t rows_p, rows_q, K;
@@ -229,11 +237,10 @@ struct Args {
   // gram, square: A (read by square) and the result
   const _Float16* a;
   float of_sum, of_a, on_diag;  // result = of_sum * sum + of_a * A + on_diag on the diagonal
-  _Float16* out;
-  // update: X (read and written), its transpose
+  _Float16* out;  // (update: the next X)
+  // update, last: X's low halves where its rows do not hold them (read and written)
   float e;
-  _Float16 *x, *xl, *t;
-  int64_t ldx, ldt;
+  _Float16* xl;
   // last: the result's matrix
   void* param;
   uint16_t* copy;
@@ -249,6 +256,7 @@ struct Args {
 template <int BP, int BQ, int WAVES_P, int WAVES_Q, int STAGES>
 struct Shape {
   static constexpr int kP = BP, kQ = BQ, kWavesP = WAVES_P, kStages = STAGES;
+  static_assert(BP % 64 == 0 && BQ % 64 == 0, "operands' rows come in multiples of 64");
   static constexpr int kWaves = WAVES_P * WAVES_Q, kThreads = 64 * kWaves;
   static constexpr int WP = BP / WAVES_P, WQ = BQ / WAVES_Q;
   static constexpr int TP = WP / 32, TQ = WQ / 32;  // 32 x 32 blocks of a wave
@@ -263,9 +271,27 @@ __device__ __forceinline__ v8h load_half8(const uint8_t* st, int r0, int c, int 
   return *reinterpret_cast<const v8h*>(st + swz(r0 + (lane & 31), c + (lane >> 5)));
 }
 
+// The same where a stage holds rows of k, `row_bytes` of numbers p each, in chunks
+// of 64 bytes (32 numbers) of which row k has chunk c at turned_chunk(c, k): chunk
+// c, rows k0 + 8 (lane / 32) .. + 7, number lane % 32.  An instruction takes eight
+// bytes of a lane and gives lane i of sixteen the i-th numbers of four rows.
+template <int ROW_BYTES>
+__device__ __forceinline__ int turned_chunk(int c, int k) {  // four rows' chunks lie in different banks
+  return c ^ (ROW_BYTES >= 256 ? k & 3 : (k >> 1) & 1);
+}
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+template <int ROW_BYTES>
+__device__ __forceinline__ v8h load_turned8(const uint8_t* st, int k0, int c, int lane) {
+  const int k = (lane & 15) >> 2;
+  const uint8_t* at = st + (k0 + 8 * (lane >> 5) + k) * ROW_BYTES + turned_chunk<ROW_BYTES>(c, k) * 64 + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+  const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)at), b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(at + 4 * ROW_BYTES));
+  return __builtin_bit_cast(v8h, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // T: the last product's parameter (float or bf16's bits); STEP: it is updated
 // rather than overwritten.  A stage is a 128-byte line of every row of the tile:
-// 64 numbers, or the halves of 32.
+// 64 numbers, or the halves of 32; of a turned P as many rows of k.
 template <int WHAT, bool SPLIT, class S, typename T = float, bool STEP = false>
 __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
   typedef Row<SPLIT> L;
@@ -292,20 +318,31 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
   if (p0 >= p.rows_p || q0 >= p.rows_q || ((WHAT == kGram || WHAT == kSquare) && p0 > q0)) return;
   const int np = (int)min<int64_t>(S::kP, p.rows_p - p0), nq = (int)min<int64_t>(S::kQ, p.rows_q - q0);
 
-  const uint32_t ld = (uint32_t)p.K * 2 * L::kWide;
+  constexpr bool kTurn = WHAT == kUpdate || WHAT == kLast;
+  constexpr int kRowP = S::kP * 2 * L::kWide, kRowsP = 64 / L::kWide;  // a turned stage's rows
+  const uint32_t ld = (uint32_t)p.K * 2 * L::kWide, ldp = kTurn ? (uint32_t)p.rows_p * 2 * L::kWide : ld;
   uint32_t offP[S::kLoadsP], offQ[S::kLoadsQ];
 #pragma unroll
-  for (int j = 0; j < S::kLoadsP; j++)
-    offP[j] = (uint32_t)min((wave * S::kLoadsP + j) * 8 + (lane >> 3), np - 1) * ld + dma_chunk(j, lane) * 16;
+  for (int j = 0; j < S::kLoadsP; j++) {
+    if constexpr (kTurn) {  // past the tile: its last chunk
+      constexpr int lanes = kRowP / 16;  // of a row
+      const int k = (wave * S::kLoadsP + j) * (64 / lanes) + lane / lanes, pos = lane % lanes;
+      offP[j] = (uint32_t)k * ldp + min(turned_chunk<kRowP>(pos / 4, k), np * L::kWide / 32 - 1) * 64 + pos % 4 * 16;
+    } else {
+      offP[j] = (uint32_t)min((wave * S::kLoadsP + j) * 8 + (lane >> 3), np - 1) * ld + dma_chunk(j, lane) * 16;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < S::kLoadsQ; j++)
     offQ[j] = (uint32_t)min((wave * S::kLoadsQ + j) * 8 + (lane >> 3), nq - 1) * ld + dma_chunk(j, lane) * 16;
-  const uint8_t* const baseP = reinterpret_cast<const uint8_t*>(p.P) + (b * p.rows_p + p0) * ld;
+  const uint8_t* const baseP =
+      reinterpret_cast<const uint8_t*>(p.P) + (kTurn ? b * p.K * ldp + p0 * 2 * L::kWide : (b * p.rows_p + p0) * ld);
+  const int64_t stepP = kTurn ? (int64_t)kRowsP * ldp : 128;
   const uint8_t* const baseQ = reinterpret_cast<const uint8_t*>(p.Q) + (b * p.rows_q + q0) * ld;
   const int ns = (int)(ld / 128);
   auto load = [&](uint8_t* st, int s, int n) {
     if (n < S::kLoadsP)
-      load_lds16(baseP + (int64_t)s * 128 + offP[n], st + (wave * S::kLoadsP + n) * 1024);
+      load_lds16(baseP + s * stepP + offP[n], st + (wave * S::kLoadsP + n) * 1024);
     else
       load_lds16(baseQ + (int64_t)s * 128 + offQ[n - S::kLoadsP], st + S::kBytesP + (wave * S::kLoadsQ + n - S::kLoadsP) * 1024);
   };
@@ -323,7 +360,12 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
 
   auto read = [&](const uint8_t* st, int chunk, v8h (&fp)[TP], v8h (&fq)[TQ]) {
 #pragma unroll
-    for (int i = 0; i < TP; i++) fp[i] = load_half8(st, wp * S::WP + 32 * i, chunk, lane);
+    for (int i = 0; i < TP; i++) {
+      if constexpr (kTurn)  // (the halves of 32 numbers are chunks side by side)
+        fp[i] = load_turned8<kRowP>(st, 8 * (SPLIT ? chunk & 3 : chunk), (wp * TP + i) * L::kWide + (SPLIT ? chunk >> 2 : 0), lane);
+      else
+        fp[i] = load_half8(st, wp * S::WP + 32 * i, chunk, lane);
+    }
 #pragma unroll
     for (int j = 0; j < TQ; j++) fq[j] = load_half8(st + S::kBytesP, wq * S::WQ + 32 * j, chunk, lane);
   };
@@ -337,7 +379,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
   // one, the last again: every stage has the same loads in flight, and no branch
   // parts them from the matrix instructions).  Each part's numbers are read while the
   // part before it multiplies.
-  constexpr int kM = TP * TQ, kD = TP + TQ, kG = (S::kLoads + 1) / 2;
+  constexpr int kM = TP * TQ, kD = TP * (kTurn ? 2 : 1) + TQ, kG = (S::kLoads + 1) / 2;
   auto stage = [&](const uint8_t* st, uint8_t* next, int s) {
     const int ahead = min(s + NS - 1, ns - 1);
     auto load_half_of = [&](int which) {
@@ -487,7 +529,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
       }
     }
   };
-  const int64_t x_stride = p.ldx * p.ldt, a_stride = p.rows_p * p.rows_p;
+  const int64_t x_stride = p.rows_p * p.rows_q;  // (of a square matrix: gram, square)
+  auto row_of = [&](auto* of, int64_t row, int wide) { return of + (b * x_stride + row * p.rows_p) * wide; };
 #pragma unroll
   for (int i0 = 0; i0 < TP; i0 += kI) {
     const int pp = wp * S::WP + 32 * i0, qq = wq * S::WQ;
@@ -499,10 +542,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
       each_row(kQw, kPw, [&](int r, int c) {
         float v[8];
         if constexpr (WHAT == kSquare)
-          load_halves(p.a + (b * a_stride + (row_q + r) * p.rows_p) * L::kWide, nullptr, row_p + c, v);
+          load_halves(row_of(p.a, row_q + r, L::kWide), nullptr, row_p + c, v);
         else
-          load_halves(p.x + (b * x_stride + (row_q + r) * p.ldx) * L::kWide, SPLIT ? nullptr : p.xl + b * x_stride + (row_q + r) * p.ldx,
-                      row_p + c, v);
+          load_halves(row_of(p.P, row_q + r, L::kWide), SPLIT ? nullptr : row_of(p.xl, row_q + r, 1), row_p + c, v);
         *reinterpret_cast<v4f*>(mine + spot(r, c, kPw)) = v4f{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<v4f*>(mine + spot(r, c + 4, kPw)) = v4f{v[4], v[5], v[6], v[7]};
       });
@@ -541,14 +583,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
         get8(r, c, kPw, v);
         if constexpr (WHAT == kLast)
           finish(row_q + r, row_p + c, p.lo, p.hi, v);
-        else if constexpr (WHAT == kUpdate)
-          store_halves(p.x + (b * x_stride + (row_q + r) * p.ldx) * L::kWide, SPLIT ? nullptr : p.xl + b * x_stride + (row_q + r) * p.ldx,
-                       row_p + c, v);
         else
-          store_halves(p.out + (b * a_stride + (row_q + r) * p.rows_p) * L::kWide, nullptr, row_p + c, v);
+          store_halves(row_of(p.out, row_q + r, L::kWide), !SPLIT && WHAT == kUpdate ? row_of(p.xl, row_q + r, 1) : nullptr, row_p + c, v);
       });
     }
-    if (WHAT == kUpdate || (WHAT == kLast && p.tall) || ((WHAT == kGram || WHAT == kSquare) && p0 != q0)) {  // along Q: rows of P
+    if ((WHAT == kLast && p.tall) || ((WHAT == kGram || WHAT == kSquare) && p0 != q0)) {  // along Q: rows of P
       between();
 #pragma unroll
       for (int i = i0; i < i0 + kI; i++)
@@ -563,10 +602,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
         get8(r, c, kQw, v);
         if constexpr (WHAT == kLast)
           finish(row_p + r, row_q + c, p.hi, p.lo, v);
-        else if constexpr (WHAT == kUpdate)
-          store_halves(p.t + (b * x_stride + (row_p + r) * p.ldt) * L::kWide, nullptr, row_q + c, v);
         else
-          store_halves(p.out + (b * a_stride + (row_p + r) * p.rows_p) * L::kWide, nullptr, row_q + c, v);
+          store_halves(row_of(p.out, row_p + r, L::kWide), nullptr, row_q + c, v);
       });
     }
   }
@@ -625,10 +662,8 @@ void launch_start(const Source& s, const Plan& pl, Space& sp, float S, hipStream
   if (parts > kMaxParts) parts = kMaxParts;
   momentum_kernel<G, MOMENTUM><<<dim3((unsigned)parts, (unsigned)pl.batch), kThreads, 0, st>>>(s, sp.parts);
   const int64_t Rp = up64(pl.R), Cp = up64(pl.C);
-  const bool tall = pl.R > pl.C;
   start_kernel<G, MOMENTUM, SPLIT><<<dim3((unsigned)(Rp / 64 * (Cp / 64)), (unsigned)pl.batch), kThreads, 0, st>>>(
-      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, tall ? sp.t : sp.x, tall ? nullptr : sp.xl, tall ? sp.x : sp.t,
-      tall ? sp.xl : nullptr);
+      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, pl.R > pl.C, sp.x, sp.xl);
 }
 
 template <bool SPLIT, typename T, bool STEP>
@@ -651,13 +686,12 @@ hipError_t iterate(const Plan& pl, Space& sp, float S, Args last, hipStream_t st
     err = launch_product<kSquare, SPLIT>(q, pl.batch, st);
     if (err != hipSuccess) return err;
     Args u = last;
-    u.P = sp.t, u.Q = sp.b, u.rows_p = sp.Hp, u.rows_q = u.K = sp.Lp;
-    u.of_sum = 1.f / scale_b, u.e = e;
-    u.x = sp.x, u.xl = sp.xl, u.t = sp.t2, u.ldx = sp.Hp, u.ldt = sp.Lp;
+    u.P = sp.x, u.Q = sp.b, u.rows_p = sp.Hp, u.rows_q = u.K = sp.Lp;
+    u.of_sum = 1.f / scale_b, u.e = e, u.xl = sp.xl, u.out = sp.x2;
     if (left) {
       err = launch_product<kUpdate, SPLIT>(u, pl.batch, st);
-      _Float16* v = sp.t;
-      sp.t = sp.t2, sp.t2 = v;
+      _Float16* v = sp.x;
+      sp.x = sp.x2, sp.x2 = v;
     } else {
       err = launch_product<kLast, SPLIT, T, STEP>(u, pl.batch, st);
     }

@@ -165,7 +165,7 @@ def test_workspace():
         assert of(*bad) == 0
     for batch, R, C in ((1, 1, 1), (3, 70, 40), (4, 40, 70), (2, 4096, 7168)):
         lo, hi = (-(-min(R, C) // 64) * 64, -(-max(R, C) // 64) * 64)
-        for dt, halves in ((1, 4 * lo * hi + 2 * lo * lo), (0, 2 * (3 * lo * hi + 2 * lo * lo))):
+        for dt, halves in ((1, 3 * lo * hi + 2 * lo * lo), (0, 2 * (2 * lo * hi + 2 * lo * lo))):
             assert 0 <= of(batch, R, C, dt) - batch * (2 * halves + 2048) < 6 * 256
         assert of(batch, R, C, 0) == of(batch, C, R, 0)
     assert 0 <= of(0, 5, 5, 0) < 6 * 256
