@@ -610,7 +610,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
 }
 
 typedef Shape<256, 256, 2, 4, 2> Large;
-typedef Shape<128, 128, 2, 2, 2> Medium;
+typedef Shape<128, 128, 4, 2, 2> Medium;  // (eight waves: update of 32 times 256 x 256 x 512 14.4 us against 16.1 with four)
 typedef Shape<64, 64, 2, 2, 4> Small;
 
 // what the host has checked
@@ -639,8 +639,8 @@ hipError_t launch_shape(Args p, int64_t side, int64_t first, int64_t count, hipS
   return hipGetLastError();
 }
 
-// 64 x 64 tiles where 128 x 128 ones leave CUs without work (32 times 256 x 256 x 512, fp32 weights: gram 13.6 us against
-// 18.1 with 96 of them; update 23.5 against 19.9 with 256), 256 x 256 ones where there are two a CU (four times 4096 x 4096
+// 64 x 64 tiles where 128 x 128 ones leave CUs without work (32 times 256 x 256 x 512, fp32 weights: gram 10.4 us against
+// 18.1 with 96 of them; update 19.0 against 14.4 with 256), 256 x 256 ones where there are two a CU (four times 4096 x 4096
 // x 7168: update 2.36 ms against 2.53), but for a last round that would leave more than half of the CUs idle.
 template <int WHAT, bool SPLIT, typename T = float, bool STEP = false>
 hipError_t launch_product(const Args& p, int64_t batch, hipStream_t st) {
