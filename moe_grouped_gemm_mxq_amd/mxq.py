@@ -621,18 +621,21 @@ def ceil128(v: int) -> int:
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_device_count = functools.lru_cache(maxsize=None)(torch.cuda.device_count)
 _U8, _F32 = torch.uint8, torch.float32
 
 
 def _stream_here(stream, t, name, *others):
     """Handle of the stream, or of the current one of t's device, which the entry points need to be the current device; the
     others (or None) have to be there too."""
-    index = t.get_device()
-    if index != _current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    for o in others:
-        if o is not None and o.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, another tensor on {o.device}")
+    index = 0
+    if _device_count() != 1:  # (with one there is nothing to check, and small products wait for the host)
+        index = t.get_device()
+        if index != _current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+        for o in others:
+            if o is not None and o.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, another tensor on {o.device}")
     if stream is None and _current_stream is not None:
         return _current_stream(index)
     return _stream(stream, t.device)
@@ -1063,9 +1066,12 @@ def dispatch(x, slot, rows, dtype=None, stream=None):
     return combine_backward(x, slot, rows, dtype=dtype, stream=stream)[0]
 
 
+_COPY_NAMES = ((), ("q_row", "s_row"), ("q_colT", "s_colT"), ("q_row", "s_row", "q_colT", "s_colT"))
+
+
 def _copies128(axis_mask, shapes, x, out):
     """The requested copies, from `out` where it is given."""
-    names = (("q_row", "s_row") if axis_mask & MXQ_AXIS_ROW else ()) + (("q_colT", "s_colT") if axis_mask & MXQ_AXIS_COLT else ())
+    names = _COPY_NAMES[axis_mask & 3]
     if out is not None:
         return {n: out[n] for n in names}
     of = dict(zip(("q_row", "s_row", "q_colT", "s_colT"), shapes()))

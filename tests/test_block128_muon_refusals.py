@@ -238,6 +238,7 @@ def library(monkeypatch):
             return lambda *a: 4096 if name in ("mxq_orthogonalize_workspace", "mxq_grouped128_cols_max") else calls.append(name) or 0
 
     monkeypatch.setattr(mxq, "_lib", Library())
+    monkeypatch.setattr(mxq, "_device_count", lambda: 2)
     monkeypatch.setattr(mxq, "_current_device", lambda: 0)
     monkeypatch.setattr(mxq, "_current_stream", lambda index: 0)
     mxq.mxq_orthogonalize_workspace.cache_clear()
