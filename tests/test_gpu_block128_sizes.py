@@ -83,8 +83,9 @@ def test_ragged_m(case, dtype):
         at += m
 
 
-# (sizes, M, N): tiles of each shape, 1024 groups
-WEIGHTS = [([130, 0, 5, 300], 200, 300), ([1, 129, 0, 700], 700, 500), ([300, 0, 140], 2100, 1200), ([0, 257] * 512, 70, 64)]
+# (sizes, M, N): tiles of each shape, 37 groups of few tiles, 1024 of them
+WEIGHTS = [([130, 0, 5, 300], 200, 300), ([1, 129, 0, 700], 700, 500), ([300, 0, 140], 2100, 1200), ([7 * i % 190 for i in range(37)], 200, 340),
+           ([0, 257] * 512, 70, 64)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -103,7 +104,7 @@ def test_ragged_k(case, dtype):
     for g, m in enumerate(sizes):
         if m == 0:
             assert bool((got[g] == 0).all())
-        elif len(sizes) < 16 or g % 301 == 0 or g == len(sizes) - 1:
+        elif len(sizes) < 64 or g % 301 == 0 or g == len(sizes) - 1:
             k, b = slice(starts[g], starts[g + 1]), slice(starts[g] // 128, starts[g + 1] // 128)
             check(got[g][rows], A[rows][:, k], sA[b][:, rows], B[:, k], sB[b])
 
