@@ -60,7 +60,7 @@ def sizes_of(T, G, seed):
 
 
 # (T, G, N, K): tiles of each shape, few rows with many and few workgroups (rows a group up to 16, 32, 64), 1024 groups
-MOE = [(500, 3, 500, 256), (1000, 6, 2000, 384), (3000, 5, 4200, 256), (3000, 7, 2200, 128), (36, 9, 4100, 128), (60, 9, 4100, 256), (140, 9, 4100, 128),
+MOE = [(500, 3, 500, 256), (1000, 6, 2000, 384), (1300, 6, 2000, 384), (3000, 5, 4200, 256), (3000, 7, 2200, 128), (36, 9, 4100, 128), (60, 9, 4100, 256), (140, 9, 4100, 128),
        (36, 9, 300, 128), (60, 9, 300, 1152), (140, 9, 300, 256), (2000, 1024, 130, 128), (60000, 1024, 64, 128)]
 
 
@@ -84,7 +84,7 @@ def test_ragged_m(case, dtype):
 
 
 # (sizes, M, N): tiles of each shape, 37 groups of few tiles, 1024 of them
-WEIGHTS = [([130, 0, 5, 300], 200, 300), ([1, 129, 0, 700], 700, 500), ([300, 0, 140], 2100, 1200), ([7 * i % 190 for i in range(37)], 200, 340),
+WEIGHTS = [([130, 0, 5, 300], 200, 300), ([1, 129, 0, 700], 700, 500), ([1, 129, 0, 700], 1100, 500), ([300, 0, 140], 2100, 1200), ([7 * i % 190 for i in range(37)], 200, 340),
            ([0, 257] * 512, 70, 64)]
 
 
