@@ -434,7 +434,13 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm128_kernel(Problem p) {
 // 132 MB, where reading alone takes 25), so registers are kept few.  Of the
 // scales, lane (row, part) loads those of its row and of the part-th of the next
 // kU blocks, and the lanes of the other parts get them from it.
+//
+// A workgroup takes at most 64 rows of a group, sixteen (MB of them) after another
+// with B's rows from L2; longer groups have more workgroups (128 groups of 512 x
+// 2048, 512 rows: all in one group 102 us with one workgroup for all of its rows,
+// 16 so).
 constexpr int kU = 4;
+constexpr int kFewRows = 64;
 
 // a lane's 32 bytes of a block: 16 of either half, so that a load covers 64 bytes of each row
 __device__ __forceinline__ v8i load_lane32(const uint8_t* p) {
@@ -450,19 +456,28 @@ __global__ __launch_bounds__(64 * W, OCC) void few_rows_kernel(Problem p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int Kb = (int)(p.K / kB);
   const int64_t scales_n = TILE128 ? (p.N + kB - 1) / kB : p.N;
-  int64_t m_first = 0, m_rows = p.M;
+  int64_t m_first = 0;
+  int m_rows = (int)p.M;  // at most kFewRows
   const uint8_t* B = p.B;
   const float* sB = p.sB;
   int nt = blockIdx.x;
   if constexpr (MODE == kRaggedM) {
-    const int g = blockIdx.x / p.tiles_n;
-    nt = blockIdx.x - g * p.tiles_n;
-    int32_t start, size;
-    group_span(p.group_end, g, p.M, start, size);
-    m_first = start;
-    m_rows = size;
-    B += (int64_t)g * p.N * p.K;
-    sB += (int64_t)g * Kb * scales_n;
+    // the groups' rows past their first kFewRows, then a workgroup for each group's first ones, which need no search
+    const int unit = blockIdx.x / p.tiles_n, more = (int)(p.M / kFewRows);
+    nt = blockIdx.x - unit * p.tiles_n;
+    GroupUnit u;
+    if (unit < more) {
+      if (!find_group_unit<kFewRows, 1>(p.group_end, p.G, p.M, unit, u)) return;
+    } else {
+      u.g = unit - more;
+      u.local = 0;
+      group_span(p.group_end, u.g, p.M, u.start, u.size);
+      if (u.size == 0) return;
+    }
+    m_first = u.start + (int64_t)u.local * kFewRows;
+    m_rows = min(u.size - u.local * kFewRows, kFewRows);
+    B += (int64_t)u.g * p.N * p.K;
+    sB += (int64_t)u.g * Kb * scales_n;
   }
   const int64_t n0 = (int64_t)nt * (16 * NB);
   const uint8_t* b_row[NB];
@@ -473,7 +488,7 @@ __global__ __launch_bounds__(64 * W, OCC) void few_rows_kernel(Problem p) {
     sb_row[i] = sB + (TILE128 ? min(n0 + 16 * i, p.N - 1) / kB : min(n0 + 16 * i + in, p.N - 1));
   }
 
-  for (int64_t m0 = 0; m0 < m_rows; m0 += 16 * MB) {
+  for (int m0 = 0; m0 < m_rows; m0 += 16 * MB) {
     const uint8_t* a_row[MB];
     const float* sa_row[MB];
 #pragma unroll
@@ -541,7 +556,8 @@ __global__ __launch_bounds__(64 * W, OCC) void few_rows_kernel(Problem p) {
       float v = sums[0][ij][r];
 #pragma unroll
       for (int w = 1; w < W; w++) v += sums[w][ij][r];
-      const int64_t m = m0 + 16 * (ij % MB) + (r >> 4), n = n0 + 16 * (ij / MB) + (r & 15);
+      const int m = m0 + 16 * (ij % MB) + (r >> 4);
+      const int64_t n = n0 + 16 * (ij / MB) + (r & 15);
       if (m < m_rows && n < p.N) store_f(static_cast<Out*>(p.C), (m_first + m) * p.ldc + n, v);
     }
     if (m0 + 16 * MB < m_rows) __syncthreads();
@@ -573,15 +589,16 @@ hipError_t launch_shape(Problem p, hipStream_t st) {
 
 template <int MODE, bool F32, bool TILE128, int MB, int NB, int W, int OCC>
 hipError_t launch_few(Problem p, hipStream_t st) {
-  const int64_t tiles = (p.N + 16 * NB - 1) / (16 * NB), total = tiles * (MODE == kRaggedM ? p.G : 1);
+  const int64_t units = MODE == kRaggedM ? p.G + p.M / kFewRows : 1;
+  const int64_t tiles = (p.N + 16 * NB - 1) / (16 * NB), total = tiles * units;
   if (total > INT32_MAX) return hipErrorInvalidValue;
   p.tiles_n = (int)tiles;
   few_rows_kernel<MODE, F32, TILE128, MB, NB, W, OCC><<<(unsigned)total, 64 * W, 0, st>>>(p);
   return hipGetLastError();
 }
 
-// A launch has fewer than 2^32 threads, and few rows take 16 for each row of B.
-constexpr int64_t kMaxFewN = (1 << 28) - 64 * MXQ_MAX_GROUPS;
+// A launch has fewer than 2^32 threads, and few rows take 16 for each row of B, a quarter more where groups are uneven.
+constexpr int64_t kMaxFewN = 1 << 27;
 
 // Waves a workgroup, and rows of B in it, from what they measured (us; bf16 C, N x K = 4096 x 7168 / 18432 x 7168 / 32
 // experts of 4096 x 7168 with 64 rows): 16 rows of B by 16 waves 8.2 / 33.4 / 102, 32 by 8 waves 11.4 / 35.2 / 97.

@@ -122,7 +122,8 @@ struct GroupUnit {
 // All lanes of a wave call this with one u (no LDS, no barrier; a few hundred
 // cycles for up to 64 groups).  False where u is past the last unit, with
 // out.before all units.  A chunk of 64 groups holds fewer than 2^31 units for UNIT >= 64.
-template <int UNIT>
+// SKIP: only the units past each group's first SKIP ones are counted (local counts all).
+template <int UNIT, int SKIP = 0>
 __device__ __forceinline__ bool find_group_unit(const int32_t* __restrict__ group_end, int G, int64_t R, int64_t u,
                                                 GroupUnit& out) {
   static_assert(UNIT >= 64, "the sum of a chunk's units must fit int32");
@@ -131,7 +132,7 @@ __device__ __forceinline__ bool find_group_unit(const int32_t* __restrict__ grou
   for (int g0 = 0; g0 < G; g0 += 64) {
     int32_t start = 0, size = 0;
     if (g0 + lane < G) group_span(group_end, g0 + lane, R, start, size);
-    const int32_t units = (int32_t)(((uint32_t)size + (UNIT - 1)) / UNIT);
+    const int32_t units = max((int32_t)(((uint32_t)size + (UNIT - 1)) / UNIT) - SKIP, 0);
     int32_t upto = units;  // units of the chunk's groups up to this lane's
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -146,7 +147,7 @@ __device__ __forceinline__ bool find_group_unit(const int32_t* __restrict__ grou
       out.size = __builtin_amdgcn_readlane(size, at);
       const int32_t earlier = __builtin_amdgcn_readlane(upto - units, at);
       out.before = before + earlier;
-      out.local = (int32_t)(u - out.before);
+      out.local = (int32_t)(u - out.before) + SKIP;
       return true;
     }
     before += __builtin_amdgcn_readlane(upto, 63);

@@ -68,7 +68,19 @@ MOE = [(500, 3, 500, 256), (1000, 6, 2000, 384), (1300, 6, 2000, 384), (3000, 5,
 @pytest.mark.parametrize("case", MOE)
 def test_ragged_m(case, dtype):
     T, G, N, K = case
-    sizes = sizes_of(T, G, 5)
+    ragged_m(sizes_of(T, G, 5), N, K, dtype)
+
+
+# few rows a group on average, all or most of them in one or two
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [[0] * 30 + [64] + [0] * 9, [0, 65] + [0] * 38, [0] * 39 + [150], [129] + [1] * 37 + [0, 64], [0, 300, 1, 128, 0] * 8,
+                                   [64] * 20 + [65] * 20, [1] * 500 + [500] + [0] * 499])
+def test_few_rows_in_uneven_groups(sizes, dtype):
+    ragged_m(np.array(sizes), 200, 256, dtype)
+
+
+def ragged_m(sizes, N, K, dtype):
+    T, G = int(sizes.sum()), len(sizes)
     A, sA = operand(T + 9, K, 3)
     B, sB = operand(N, K, 4, 128, (G,))
     ends = torch.tensor(np.cumsum(sizes), dtype=torch.int32, device="cuda")
@@ -77,7 +89,7 @@ def test_ragged_m(case, dtype):
     assert bool((C[T:] == 7).all())
     at = 0
     for g, m in enumerate(sizes):
-        if m and (G < 16 or g % 97 == 0 or g == G - 1):
+        if m and (G < 64 or m > 1 and g % 97 == 0 or m > 300 or g == G - 1):
             rows = at + some(int(m))
             check(C[rows], A[rows], sA[:, rows], B[g], sB[g])
         at += m
