@@ -486,7 +486,13 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
     for (int e = 0; e < 4; e++) v[e] = a[e], v[e + 4] = c[e];
   };
   auto between = [&]() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
-  // eight halves of a row of an operand, from element k on
+  // eight halves of a row of an operand, from element k on; those of large matrices past the caches, which the operands
+  // need (four times 4096 x 4096 x 7168: update 1090 -> 1060 us; 32 times 256 x 256 x 512 174 -> 192 us in all if they were too)
+  const bool past = S::kP == 256 || (S::kP == 128 && p.parts == 2);
+  auto put = [&](v8h v, _Float16* to) {
+    if (past) __builtin_nontemporal_store(v, reinterpret_cast<v8h*>(to));
+    else *reinterpret_cast<v8h*>(to) = v;
+  };
   auto store_halves = [&](_Float16* row, _Float16* low, int64_t k, const float* v) {
     v8h h, l;
 #pragma unroll
@@ -496,15 +502,15 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Args p) {
       h[e] = hi;
       l[e] = lo;
     }
-    *reinterpret_cast<v8h*>(row + L::at(k)) = h;
-    if constexpr (SPLIT) *reinterpret_cast<v8h*>(row + L::at(k) + L::kLow) = l;
-    else if (low) *reinterpret_cast<v8h*>(low + k) = l;
+    put(h, row + L::at(k));
+    if constexpr (SPLIT) put(l, row + L::at(k) + L::kLow);
+    else if (low) put(l, low + k);
   };
   auto load_halves = [&](const _Float16* row, const _Float16* low, int64_t k, float* v) {
     const v8h h = *reinterpret_cast<const v8h*>(row + L::at(k));
     v8h l = {0, 0, 0, 0, 0, 0, 0, 0};
     if constexpr (SPLIT) l = *reinterpret_cast<const v8h*>(row + L::at(k) + L::kLow);
-    else if (low) l = *reinterpret_cast<const v8h*>(low + k);
+    else if (low) l = past ? __builtin_nontemporal_load(reinterpret_cast<const v8h*>(low + k)) : *reinterpret_cast<const v8h*>(low + k);
 #pragma unroll
     for (int e = 0; e < 8; e++) v[e] = (float)h[e] + (float)l[e];
   };
