@@ -25,8 +25,8 @@
 // most 1.25 throughout), A times 2^14, B times a power that its coefficients allow.
 //
 // What bounds it.  Large matrices: the matrix units and what feeds them; four 7168 x 4096 with fp32 weights 22.5 ms (three
-// products each: 1150 TFLOP/s, 66-73% of the cycles in matrix instructions), with bf16 weights 9.6 ms (900; 45-61%: of an
-// update's 1.09 ms about 0.2 are X read and written by all CUs at the same time).  An fp16 product of 8192^3 by the vendor's
+// products each: 1150 TFLOP/s, 66-73% of the cycles in matrix instructions), with bf16 weights 9.5 ms (900; 45-61%: of an
+// update's 1.06 ms about 0.2 are X read and written by all CUs at the same time).  An fp16 product of 8192^3 by the vendor's
 // library runs at 1400 TFLOP/s on such numbers.  Small ones (32 times 512 x 256: 174 us): 17 dependent launches of 8 to
 // 18 us, each some stages' latency and the traffic of its operands.
 #include <cmath>
