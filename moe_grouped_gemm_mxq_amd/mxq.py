@@ -18,6 +18,7 @@ rows r, r+32, r+64, r+96 of a 128-row group for one block).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -1239,9 +1240,9 @@ class Muon:
 
     params fp32 or bf16, grads fp32 or bf16, m the momenta (fp32, zeros before the first step), copies: bf16 tensors that get
     the new parameters too, or None.  The tensors stay the caller's: they are read and written where they are, so a gradient
-    that moves to other storage needs a new Muon.  The workspace is shared by the tensors, which are updated one after the
-    other on the step's stream, and by all steps: two that may run at once (on two streams, or in a graph that is replayed
-    while another step runs) need a Muon each."""
+    that moves to other storage needs a new Muon.  They are updated one after the other, in a workspace that each step
+    allocates on its stream: it goes back to that stream's pool when the step has been queued, or stays the graph's where
+    the step is captured (torch.cuda.graph), so a Muon need not outlive its steps."""
 
     def __init__(self, params, grads, m, copies=None):
         n = len(params)
@@ -1262,14 +1263,19 @@ class Muon:
                 raise ValueError(f"{name}all tensors must be on one device")
             need = max(need, mxq_orthogonalize_workspace(nb, R, C, pdt))
         self.tensors = list(zip(params, grads, m, copies))
-        self.workspace = torch.empty(need, dtype=torch.uint8, device=params[0].device) if n else None
+        self.workspace_bytes = need
 
     def step(self, *, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.1, scale="match_rms", grad_scale=1.0, steps=5,
              coefficients=NS_COEFFICIENTS, eps=1e-7, control=None, stream=None):
         """One step.  scale: a rule of muon_scale or a number.  control: an adamw_control tensor whose lr and grad_scale replace
         these (for graphs)."""
-        for param, grad, m, copy in self.tensors:
-            factor = muon_scale(param.shape, scale) if isinstance(scale, str) else scale
-            cfg = MuonConfig(newton_schulz(steps, coefficients, eps), lr, momentum, weight_decay, factor, grad_scale,
-                             int(bool(nesterov)))
-            mxq_muon(param, grad, m, cfg, self.workspace, copy, control, stream)
+        if not self.tensors:
+            return
+        device = self.tensors[0][0].device
+        with contextlib.nullcontext() if stream is None else _on(stream, device):
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+            for param, grad, m, copy in self.tensors:
+                factor = muon_scale(param.shape, scale) if isinstance(scale, str) else scale
+                cfg = MuonConfig(newton_schulz(steps, coefficients, eps), lr, momentum, weight_decay, factor, grad_scale,
+                                 int(bool(nesterov)))
+                mxq_muon(param, grad, m, cfg, workspace, copy, control)
