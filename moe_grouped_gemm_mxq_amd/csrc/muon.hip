@@ -20,9 +20,12 @@
 // rounding, where bf16 operands would be off by 1e-2 to 2e-1 (gradients of low
 // rank).  Results kept in fp32 take each product three times, high x high, high
 // x low and low x high, within 1e-5.
-// fp16's range is kept by powers of two: X is stored times S = 2^s, about the
-// root of lo x hi (its norm is at most 1 at the start and its singular values at
-// most 1.25 throughout), A times 2^14, B times a power that its coefficients allow.
+// fp16's range is kept by powers of two: X is stored times 2^15, A times 2^14, B
+// times a power that its coefficients allow.  X's singular values, and with them its
+// elements, stay within 1.25, so 1.25 x 2^15 is the largest number; any smaller power
+// would put more of the low halves of small elements under fp16's smallest step, and
+// they are what an outlier row or column leaves of the others (16 x 64 with a row and a
+// column 1000 times the rest, fp32 result: off by 5e-7, with 2^5 by 1.2e-5).
 //
 // What bounds it.  Large matrices: the matrix units and what feeds them; four 7168 x 4096 with fp32 weights 22.5 ms (three
 // products each: 1150 TFLOP/s, 66-73% of the cycles in matrix instructions), with bf16 weights 9.5 ms (900; 45-61%: of an
@@ -45,7 +48,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr float kScaleA = 16384.f;
+constexpr float kScaleX = 32768.f, kScaleA = 16384.f;
 constexpr int kMaxSide = 1 << 20;
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 256;  // partial sums of squares of a matrix
@@ -171,11 +174,11 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
   lo = (_Float16)(v - (float)hi);
 }
 
-// X = u / (|u| + eps) times S from 64 x 64 of u [R][C]; X's rows are u's columns
+// X = u / (|u| + eps) times kScaleX from 64 x 64 of u [R][C]; X's rows are u's columns
 // where it is tall.  low: where the low halves go that X's rows do not hold.
 template <typename G, bool MOMENTUM, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, int64_t C, int64_t Rp, int64_t Cp, int nparts,
-                                                         double eps, float S, const double* __restrict__ parts, int tall,
+                                                         double eps, const double* __restrict__ parts, int tall,
                                                          _Float16* __restrict__ x, _Float16* __restrict__ low) {
   typedef Row<SPLIT> L;
   __shared__ float tile[64][65];
@@ -188,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
   if ((t & 63) == 0) waves[t >> 6] = sum;
   __syncthreads();
-  const double inv = (double)S / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + eps);  // (may be past fp32's range)
+  const double inv = (double)kScaleX / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + eps);  // (may be past fp32's range)
   const int64_t tiles_c = Cp / 64;
   const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
   const int64_t base = blockIdx.y * s.n;
@@ -668,18 +671,18 @@ hipError_t launch_product(const Args& p, int64_t batch, hipStream_t st) {
 }
 
 template <typename G, bool MOMENTUM, bool SPLIT>
-void launch_start(const Source& s, const Plan& pl, Space& sp, float S, hipStream_t st) {
+void launch_start(const Source& s, const Plan& pl, Space& sp, hipStream_t st) {
   const int64_t per = 4 * kThreads;
   int64_t parts = (s.n + per - 1) / per;
   if (parts > kMaxParts) parts = kMaxParts;
   momentum_kernel<G, MOMENTUM><<<dim3((unsigned)parts, (unsigned)pl.batch), kThreads, 0, st>>>(s, sp.parts);
   const int64_t Rp = up64(pl.R), Cp = up64(pl.C);
   start_kernel<G, MOMENTUM, SPLIT><<<dim3((unsigned)(Rp / 64 * (Cp / 64)), (unsigned)pl.batch), kThreads, 0, st>>>(
-      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, S, sp.parts, pl.R > pl.C, sp.x, sp.xl);
+      s, pl.R, pl.C, Rp, Cp, (int)parts, pl.eps, sp.parts, pl.R > pl.C, sp.x, sp.xl);
 }
 
 template <bool SPLIT, typename T, bool STEP>
-hipError_t iterate(const Plan& pl, Space& sp, float S, Args last, hipStream_t st) {
+hipError_t iterate(const Plan& pl, Space& sp, Args last, hipStream_t st) {
   // B = b A + c A^2 + (a - e) I with A's eigenvalues in [0, 1.25^2]
   const double reach = std::fabs(pl.b) * 1.5625 + std::fabs(pl.c) * 1.5625 * 1.5625 + std::fabs(pl.a);
   const float scale_b = std::ldexp(1.f, 15 - (int)std::ceil(std::log2(reach > 1.0 ? reach : 1.0)));
@@ -688,7 +691,7 @@ hipError_t iterate(const Plan& pl, Space& sp, float S, Args last, hipStream_t st
     const float e = (float)(pl.a * (left == 0 ? 0.4375 : left == 1 ? 0.71875 : 1.0));
     Args g{};
     g.P = g.Q = sp.x, g.rows_p = g.rows_q = sp.Lp, g.K = sp.Hp;
-    g.of_sum = kScaleA / (S * S), g.out = sp.a;
+    g.of_sum = kScaleA / (kScaleX * kScaleX), g.out = sp.a;
     hipError_t err = launch_product<kGram, SPLIT>(g, pl.batch, st);
     if (err != hipSuccess) return err;
     Args q{};
@@ -718,20 +721,18 @@ hipError_t run(const Plan& pl, const Source& s, mxq_dtype gdt, mxq_dtype odt, Ar
   const bool split = odt == MXQ_DT_F32;
   Space sp;
   lay_out(&sp, workspace, pl.batch, pl.R, pl.C, split);
-  int log = (int)std::floor(0.5 * std::log2((double)sp.lo * (double)sp.hi));
-  const float S = std::ldexp(1.f, log < 15 ? log : 15);
   if (gdt == MXQ_DT_F32) {
-    if (split) launch_start<float, STEP, true>(s, pl, sp, S, st);
-    else launch_start<float, STEP, false>(s, pl, sp, S, st);
+    if (split) launch_start<float, STEP, true>(s, pl, sp, st);
+    else launch_start<float, STEP, false>(s, pl, sp, st);
   } else {
-    if (split) launch_start<uint16_t, STEP, true>(s, pl, sp, S, st);
-    else launch_start<uint16_t, STEP, false>(s, pl, sp, S, st);
+    if (split) launch_start<uint16_t, STEP, true>(s, pl, sp, st);
+    else launch_start<uint16_t, STEP, false>(s, pl, sp, st);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  last.n = pl.R * pl.C, last.lo = sp.lo, last.hi = sp.hi, last.tall = pl.R > pl.C, last.from_x = 1.f / S;
-  if (split) return iterate<true, float, STEP>(pl, sp, S, last, st);
-  return iterate<false, uint16_t, STEP>(pl, sp, S, last, st);
+  last.n = pl.R * pl.C, last.lo = sp.lo, last.hi = sp.hi, last.tall = pl.R > pl.C, last.from_x = 1.f / kScaleX;
+  if (split) return iterate<true, float, STEP>(pl, sp, last, st);
+  return iterate<false, uint16_t, STEP>(pl, sp, last, st);
 }
 
 // largest |a s + b s^3 + c s^5| for s in [0, 1.25]
