@@ -16,10 +16,12 @@
 // Precision.  The iteration multiplies small singular values by up to a = 3.4
 // each time, and rounding errors in their directions with them, so X itself is
 // kept in two fp16 numbers (22 bits).  The operands of the products are fp16: its
-// 11 bits put the result within about 1e-3 of itself (2-norm), under bf16's own
-// rounding, where bf16 operands would be off by 1e-2 to 2e-1 (gradients of low
-// rank).  Results kept in fp32 take each product three times, high x high, high
-// x low and low x high, within 1e-5.
+// 11 bits put five steps' result within 2e-3 of itself (2-norm) where there are 64
+// rows and more, about bf16's own rounding, and within 1e-2 where so few elements
+// make up the result that their roundings do not average out; bf16 operands would be
+// off by 1e-2 to 2e-1 (gradients of low rank).  Results kept in fp32 take each product
+// three times, high x high, high x low and low x high: as near as fp32 operands (2e-6
+// for noise, 6e-5 for low rank).
 // fp16's range is kept by powers of two: X is stored times 2^15, A times 2^14, B
 // times a power that its coefficients allow.  X's singular values, and with them its
 // elements, stay within 1.25, so 1.25 x 2^15 is the largest number; any smaller power

@@ -1,4 +1,4 @@
-"""How far orthogonalised matrices are from 64 bits."""
+"""How far orthogonalised matrices are from 64 bits, by the figures that include/mxq.h states."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +50,28 @@ def test_fp32_results_are_as_near_as_fp32s(shape, kind):
             e, single = off(a, want), off(in_fp32(u), want)
             print(shape, kind, seed, e, single, flush=True)
             assert e <= 4 * (single + 2.0 ** -20), (seed, e, single)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_bf16_results(shape, kind):
+    """2^-9 for 64 rows and columns and more without outliers, 2^-6 otherwise; and the rounding to bf16."""
+    stated = 2.0 ** -9 if min(shape[-2:]) >= 64 and not kind.startswith("outliers") else 2.0 ** -6
+    for seed in range(3):
+        x = matrices(kind, shape, seed)
+        got = wide(mxq().orthogonalize(x)).reshape(-1, *shape[-2:])
+        for a, u in zip(got, wide(x).reshape(-1, *shape[-2:])):
+            e = off(a, ref.orthogonalize(u))
+            print(shape, kind, seed, e, flush=True)
+            assert e <= stated + 2.0 ** -8, (seed, e)
+
+
+@pytest.mark.parametrize("steps,bf16,fp32", [(5, 2.0 ** -9, 2.0 ** -17), (8, 2.0 ** -8, 2.0 ** -17), (12, 2.0 ** -7, 2.0 ** -16), (32, 2.0 ** -5, 2.0 ** -13)])
+def test_errors_grow_with_the_steps(steps, bf16, fp32):
+    """The default coefficients do not converge: where the polynomial's slope is above 1, a step multiplies what is off."""
+    x = inputs("noise", (128, 256), 7)
+    want = ref.orthogonalize(wide(x), steps)
+    for dtype, stated, rounding in ((torch.bfloat16, bf16, 2.0 ** -8), (torch.float32, fp32, 2.0 ** -24)):
+        e = off(wide(mxq().orthogonalize(x, steps=steps, dtype=dtype)), want)
+        print(steps, dtype, e, flush=True)
+        assert e <= stated + rounding, (steps, dtype, e)
