@@ -524,9 +524,10 @@ mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, int32_t n_tensors, mxq_dty
 /* ------------------------------------------------------------------ FP8 with a scale for each block of 128
  * E4M3 codes with one fp32 scale for each block of 1 x 128 elements along the
  * reduction axis (activations, gradients) or of 128 x 128 (weights).  An
- * operand is `codes[rows][Kp]` (Kp = ceil128(K), codes past K 0x00) plus its
- * scales, block by block: `scales[Kp/128][rows]` (1 x 128) or
- * `scales[Kp/128][ceil(rows/128)]` (128 x 128).  R = 0 (M = 0) rows are valid. */
+ * operand is `codes[rows][Kp]` (Kp = ceil128(K), codes past K 0x00, or NaN in a
+ * block that holds a NaN) plus its scales, block by block:
+ * `scales[Kp/128][rows]` (1 x 128) or `scales[Kp/128][ceil(rows/128)]` (128 x 128).
+ * R = 0 (M = 0) rows are valid. */
 
 /* Row pitch (ldq) for a grouped token-axis copy of T rows in G groups: at
  * least T + 127 G, an upper bound of sum_g ceil128(m_g), rounded up to an odd
@@ -557,8 +558,9 @@ mxq_status mxq_quantize128(const void* x, mxq_dtype dt, int64_t batch, int64_t R
  * (group_end as for mxq_quantize_grouped):
  *   MXQ_AXIS_COLT: q_colT [C][ldq], s_colT [ldq/128][C]: blocks restart at each
  *     group start; group g occupies columns [P_g, P_g + ceil128(m_g)), P_g =
- *     sum_{j<g} ceil128(m_j), its tail zero.  Columns at and past P_G are not
- *     written.  ldq % 128 == 0; blocks that would fall past ldq are dropped.
+ *     sum_{j<g} ceil128(m_j), its tail zero (NaN in a block that holds a NaN).
+ *     Columns at and past P_G are not written.  ldq % 128 == 0; blocks that would
+ *     fall past ldq are dropped.
  *   MXQ_AXIS_ROW: as mxq_quantize128's, of all T rows.
  * 1 <= G <= MXQ_MAX_GROUPS. */
 mxq_status mxq_quantize128_grouped(const void* x, mxq_dtype dt, int64_t T, int64_t C, int64_t ldx,
