@@ -701,7 +701,7 @@ def _need_operand128(codes, scales, name, lead=(), tiles=(1,)):
     try:
         if codes.dtype is _U8 and scales.dtype is _F32 and codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous():
             shape, rows_of = codes.shape, scales.shape
-            if len(shape) == 2 + len(lead) and (not lead or (shape[:-2] == lead and rows_of[:-2] == lead)):
+            if len(shape) == len(rows_of) == 2 + len(lead) and (not lead or (shape[:-2] == lead and rows_of[:-2] == lead)):
                 rows, K = shape[-2:]
                 blocks, n = rows_of[-2:]
                 if blocks * BLOCK128 == K:
