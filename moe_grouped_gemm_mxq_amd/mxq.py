@@ -1261,7 +1261,10 @@ class Muon:
                 raise ValueError(f"{name}grad must have shape {tuple(p.shape)}, got {tuple(grads[i].shape)}")
             if any(t is not None and t.device != params[0].device for t in (p, grads[i], m[i], copies[i])):
                 raise ValueError(f"{name}all tensors must be on one device")
-            need = max(need, mxq_orthogonalize_workspace(nb, R, C, pdt))
+            room = mxq_orthogonalize_workspace(max(nb, 1), R, C, pdt)
+            if room == 0:  # (what a step refuses, before it has updated the tensors before)
+                raise ValueError(f"{name}matrices must have 1 to 2^20 rows and columns, in stacks of at most 65535, got {tuple(p.shape)}")
+            need = max(need, room)
         self.tensors = list(zip(params, grads, m, copies))
         self.workspace_bytes = need
 

@@ -21,3 +21,14 @@ def test_scales_of_more_dims(name, call, library):  # noqa: F811
     with pytest.raises(ValueError, match="must be"):
         call()
     assert not library
+
+
+@pytest.mark.parametrize("shape", [(0, 40), (40, 0), (3, 0, 40), (0, 0, 4), (2 ** 20 + 1, 1), (65536, 1, 1)])
+def test_weights_that_a_step_would_refuse(shape):
+    """Named when the Muon is made: a step that came upon them would have updated the weights before."""
+    mxq.mxq_orthogonalize_workspace.cache_clear()
+    first = [dev(4, 4), dev(2, 4, 5)]
+    with pytest.raises(ValueError, match=r"tensor 2: .*1 to 2\^20 .*65535"):
+        mxq.Muon(*([*first, dev(*shape)] for _ in range(3)))
+    assert len(mxq.Muon(first, first, first).tensors) == 2
+    assert len(mxq.Muon([dev(0, 4, 4)], [dev(0, 4, 4)], [dev(0, 4, 4)]).tensors) == 1  # (no experts here)
