@@ -596,7 +596,8 @@ mxq_status mxq_grouped_gemm128(mxq_gg_mode mode, const uint8_t* A, const float* 
  * Newton-Schulz iterations on matrices u [R][C]:
  *   X = u / (|u|_F + eps), then `steps` times X = a X + (b A + c A^2) X, A = X X^T
  * (the same for u and its transpose).  a s + b s^3 + c s^5 must stay within 1.25
- * in magnitude for s in [0, 1.25]; 3.4445, -4.7750, 2.0315 and 5 steps bring singular
+ * in magnitude for s in [0, 1.25], and within s for s in [1.25, 1.255], where
+ * roundings may put a singular value; 3.4445, -4.7750, 2.0315 and 5 steps bring singular
  * values from 1/500 of the norm up to between 0.68 and 1.21.
  * The products are taken on fp16 operands with fp32 sums, X being kept in 22 bits.
  * How far a result is from the exact one, in the 2-norm and relative to it, before

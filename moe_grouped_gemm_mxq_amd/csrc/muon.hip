@@ -753,6 +753,17 @@ double reach_of(double a, double b, double c) {
   return most;
 }
 
+// Largest |a + b s^2 + c s^4| for s in [1.25, 1.255]: by what an iteration multiplies a singular value that roundings
+// have put past 1.25.  Above 1 it would grow from there, and X leave fp16's range (a rank-1 matrix of 128 x 256 did so in
+// 8 steps with -4.125, 11.375, -6).
+double growth_past_reach(double a, double b, double c) {
+  auto at = [&](double t) { return std::fabs((c * t + b) * t + a); };
+  const double from = 1.25 * 1.25, to = 1.255 * 1.255;
+  double most = std::fmax(at(from), at(to));
+  if (c != 0 && -b / (2 * c) > from && -b / (2 * c) < to) most = std::fmax(most, at(-b / (2 * c)));
+  return most;
+}
+
 mxq_status check(const char* who, int64_t batch, int64_t R, int64_t C, const mxq_newton_schulz* ns, mxq_dtype gdt, mxq_dtype odt,
                  const void* workspace, int64_t bytes) {
   MXQ_REQUIRE(gdt == MXQ_DT_F32 || gdt == MXQ_DT_BF16, "%s: unknown type %d", who, (int)gdt);
@@ -764,6 +775,7 @@ mxq_status check(const char* who, int64_t batch, int64_t R, int64_t C, const mxq
   MXQ_REQUIRE(std::isfinite(ns->a) && std::isfinite(ns->b) && std::isfinite(ns->c), "%s: coefficients must be finite", who);
   MXQ_REQUIRE(std::fabs(ns->a) <= 64 && std::fabs(ns->b) <= 64 && std::fabs(ns->c) <= 64 && reach_of(ns->a, ns->b, ns->c) <= 1.25,
               "%s: coefficients must keep singular values in [0, 1.25] there", who);
+  MXQ_REQUIRE(growth_past_reach(ns->a, ns->b, ns->c) <= 1, "%s: coefficients must not let singular values grow from 1.25 on", who);
   MXQ_REQUIRE(std::isfinite(ns->eps) && ns->eps >= 0, "%s: eps must be finite and not negative", who);
   if (batch == 0) return MXQ_OK;
   MXQ_REQUIRE(workspace != nullptr && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned, not NULL", who);

@@ -1,9 +1,12 @@
 """Arguments of the block-128 and Muon binding that it has to refuse before anything runs."""
+import ctypes
+
+import numpy as np
 import pytest
-import torch
 
 from moe_grouped_gemm_mxq_amd import mxq
-from test_block128_muon_refusals import ENDS, SA, SB, SKB, SW, A, B, KB, U8, W, dev, library  # noqa: F401  (library: a fixture)
+from test_block128_muon_refusals import (DEVICE, ENDS, HAS_GPU, ORTHOGONALIZE, SA, SB, SKB, SW, A, B, KB, W, call, dev,  # noqa: F401
+                                         library, refused)  # (library: a fixture)
 
 
 def more(t):
@@ -32,3 +35,28 @@ def test_weights_that_a_step_would_refuse(shape):
         mxq.Muon(*([*first, dev(*shape)] for _ in range(3)))
     assert len(mxq.Muon(first, first, first).tensors) == 2
     assert len(mxq.Muon([dev(0, 4, 4)], [dev(0, 4, 4)], [dev(0, 4, 4)]).tensors) == 1  # (no experts here)
+
+
+# (the first: 1.25 goes to -1.25, and what is above it grows with a slope of 24; the other with one of 1.4)
+GROWING = [(-4.125, 11.375, -6.0), (1.0, -0.1201, 0.0768)]
+STEADY = [(3.4445, -4.7750, 2.0315), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (1.0, 0.0, 0.0), (-1.0, 0.0, 0.0), (0.0, 0.0, 0.0)]
+
+
+def orthogonalize_with(a, b, c):
+    cfg = mxq.newton_schulz(coefficients=(a, b, c))
+    return call("mxq_orthogonalize", ORTHOGONALIZE, dict(cfg=ctypes.byref(cfg)))
+
+
+@pytest.mark.parametrize("coefficients", GROWING)
+def test_coefficients_that_let_roundings_grow(coefficients):
+    s = np.linspace(0, 1.25, 100001)
+    a, b, c = coefficients
+    assert np.abs(a * s + b * s ** 3 + c * s ** 5).max() <= 1.25 and abs(a + b * 1.255 ** 2 + c * 1.255 ** 4) > 1
+    refused(orthogonalize_with(*coefficients), "grow")
+
+
+@pytest.mark.parametrize("coefficients", STEADY)
+def test_coefficients_that_do_not(coefficients):
+    if HAS_GPU:
+        pytest.skip("a GPU is present; this checks the no-device path")
+    assert orthogonalize_with(*coefficients) == DEVICE
