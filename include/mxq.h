@@ -612,7 +612,7 @@ mxq_status mxq_grouped_gemm128(mxq_gg_mode mode, const uint8_t* A, const float* 
  * (bf16) and 4e-6 (fp32) after 12 steps, by 1e-2 and 7e-6 after 32, matrices of a few
  * rows by up to 0.2 then (bf16).  A norm far below eps loses bits (u/eps is then small
  * in fp16).
- * A matrix with a NaN or an infinity becomes NaN. */
+ * A matrix with a NaN or an infinity becomes NaN; one of zeros stays zero, whatever eps. */
 #define MXQ_MAX_NS_STEPS 32
 typedef struct {
     double a, b, c; /* each at most 64 in magnitude */

@@ -193,7 +193,8 @@ __global__ __launch_bounds__(kThreads) void start_kernel(Source s, int64_t R, in
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
   if ((t & 63) == 0) waves[t >> 6] = sum;
   __syncthreads();
-  const double inv = (double)kScaleX / (sqrt((waves[0] + waves[1]) + (waves[2] + waves[3])) + eps);  // (may be past fp32's range)
+  const double squares = (waves[0] + waves[1]) + (waves[2] + waves[3]);
+  const double inv = squares == 0 ? 0 : (double)kScaleX / (sqrt(squares) + eps);  // (may be past fp32's range; zeros stay zeros without an eps)
   const int64_t tiles_c = Cp / 64;
   const int64_t r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
   const int64_t base = blockIdx.y * s.n;
