@@ -572,8 +572,10 @@ mxq_status mxq_quantize128_grouped(const void* x, mxq_dtype dt, int64_t T, int64
  * [K/128][N] for b_tile 1, [K/128][ceil(N/128)] for 128); C [M][ldc] of type cdt.
  * fp32 C: products exact, sums in fp32.  bf16 C: a block's products are summed by
  * the FP8 matrix instruction (each group of eight keeps about 13 bits below its
- * largest product), the blocks in fp32.  A product of two scales below 2^-126
- * loses bits as fp32 subnormals do.
+ * largest product: what terms that cancel leave is off by that much of the terms),
+ * the blocks in fp32.  A product of two scales below 2^-126 loses bits as fp32
+ * subnormals do, and one past fp32's range is infinite (NaN where the block's
+ * products add to 0); with b_tile 1 the same goes for the products' sum times sB.
  * K a positive multiple of 128 below MXQ_GEMM_MAX_ROW_BYTES; 0 <= M < 2^31,
  * 1 <= N < 2^31, ldc >= N.  A, B 16-byte aligned, scales 4-byte, C to its
  * elements. */

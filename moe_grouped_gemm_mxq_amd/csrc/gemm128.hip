@@ -12,9 +12,11 @@
 // units do while the matrix units work on the next block.
 //
 // Rounded to bf16, the partial products come from the FP8 matrix instruction,
-// whose sums of eight products keep about 13 bits below the largest, far below
-// the output's 8 bits.  An fp32 output takes the codes as bf16 numbers (exact) through the
-// bf16 instruction at half the rate: its products and sums are fp32's.
+// whose sums of eight products keep about 13 bits below the largest: off by at most
+// 2^-10 of it, where the output's rounding is 2^-8 of the sum of all.  (Terms that
+// cancel leave it the larger of the two; fp32 results avoid it.)  An fp32 output takes
+// the codes as bf16 numbers (exact) through the bf16 instruction at half the rate: its
+// products and sums are fp32's.
 #include <type_traits>
 
 #include "mxq_device.h"
@@ -624,7 +626,8 @@ int64_t tiles_of(const Problem& p, int mode, int64_t side) {
 // Measured (us; N x K = 4096 x 7168, rows 256 / 512 / 1024 / 1536 / 2048 / 4096): bf16 C: Small 26 / 35 / 62 / 82 / 116 / 225,
 // Deep 40 / 40 / 44 / 76 / 80 / 156, Medium 58 / 57 / 58 / 62 / 67 / 133, Large 92 / 91 / 90 / 89 / 90 / 106; fp32 C (256 / 512
 // / 1024 / 2048): Small 35 / 46 / 83 / 157, Deep 62 / 63 / 71 / 131, Medium 72 / 72 / 74 / 111.  So: Small while all of its tiles
-// are in work at once (two a CU), Deep while it is alone on a CU, Large where it fills three quarters of them.
+// are in work at once (two a CU), Deep while it is alone on a CU, Large where it fills three quarters of them.  What
+// bounds these sizes: one workgroup's stages follow one another (56 of Small's at 0.45 us), and K is not split.
 template <int MODE, bool F32, bool TILE128>
 hipError_t launch_tiles(const Problem& p, hipStream_t st) {
   const int64_t cus = device_cu_count();
