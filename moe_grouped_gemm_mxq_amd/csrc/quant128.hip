@@ -14,8 +14,9 @@
 // The division would cost about ten instructions an element where this takes four.
 //
 // Both kernels stream and are bound by HBM: 131072 x 4096 bf16 both ways, grouped, 0.43 ms (2.2 GB at 5.1 TB/s; 0.78 with
-// the elements held as fp32), 32 matrices 7168 x 4096 both ways in 128 x 128 blocks 0.72 ms (3.8 GB at 5.2 TB/s).  A copy
-// of 2 GB runs at 4.9-6.0 TB/s.
+// the elements held as fp32), 32 matrices 7168 x 4096 both ways in 128 x 128 blocks 0.72 ms (3.8 GB at 5.2 TB/s); rows
+// alone 131072 x 7168 0.53 ms from bf16, 0.94 from fp32 (2.8 and 4.7 GB at 5.3 and 5.0 TB/s).  A copy of 2 GB runs at
+// 4.9-6.0 TB/s.
 #include "mxq_device.h"
 #include "mxq_groups.h"
 #include "mxq_host.h"
