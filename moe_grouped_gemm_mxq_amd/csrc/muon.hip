@@ -742,14 +742,11 @@ hipError_t run(const Plan& pl, const Source& s, mxq_dtype gdt, mxq_dtype odt, Ar
 double reach_of(double a, double b, double c) {
   auto at = [&](double s) { return std::fabs(((c * s * s + b) * s * s + a) * s); };
   double most = at(1.25);
-  const double d = 9 * b * b - 20 * a * c;  // 5 c s^4 + 3 b s^2 + a = 0
-  if (c == 0) {
-    if (b != 0 && -a / (3 * b) > 0) most = std::fmax(most, at(std::fmin(1.25, std::sqrt(-a / (3 * b)))));
-  } else if (d >= 0) {
-    for (double sign : {-1.0, 1.0}) {
-      const double s2 = (-3 * b + sign * std::sqrt(d)) / (10 * c);
-      if (s2 > 0) most = std::fmax(most, at(std::fmin(1.25, std::sqrt(s2))));
-    }
+  const double d = 9 * b * b - 20 * a * c;  // 5 c t^2 + 3 b t + a = 0 for t = s^2
+  if (d >= 0) {
+    const double q = -0.5 * (3 * b + std::copysign(std::sqrt(d), b));  // (no difference of near numbers where c is tiny)
+    for (double t : {q / (5 * c), a / q})
+      if (t > 0) most = std::fmax(most, at(std::fmin(1.25, std::sqrt(t))));
   }
   return most;
 }

@@ -60,3 +60,13 @@ def test_coefficients_that_do_not(coefficients):
     if HAS_GPU:
         pytest.skip("a GPU is present; this checks the no-device path")
     assert orthogonalize_with(*coefficients) == DEVICE
+
+
+# 3 s - 1.5 s^3 reaches 1.63 at s = 0.82, whatever little is added
+@pytest.mark.parametrize("coefficients", [(3.0, -1.5, 0.0), (3.0, -1.5, 1e-3), (3.0, -1.5, 1e-18), (3.0, -1.5, -1e-18), (-3.0, 1.5, 1e-18), (-3.0, 1.5, -1e-300),
+                                          (3.0, -1e-18, -1.2), (3.0, 0.0, -1.2)])
+def test_coefficients_that_pass_the_bound_within(coefficients):
+    s = np.linspace(0, 1.25, 100001)
+    a, b, c = coefficients
+    assert np.abs(a * s + b * s ** 3 + c * s ** 5).max() > 1.25
+    refused(orthogonalize_with(*coefficients), "coefficients")
